@@ -27,6 +27,9 @@ FP8_OK, FP8_ERR_INVALID_ARG, FP8_ERR_UNSUPPORTED, FP8_ERR_ALIGNMENT, FP8_ERR_CUD
 FP8_E4M3, FP8_E5M2 = 0, 1
 FP8_GRAN_TENSOR, FP8_GRAN_TILE_1x128, FP8_GRAN_BLOCK_128x128, FP8_GRAN_MX_1x32 = 0, 1, 2, 3
 FP8_SCALE_CURRENT, FP8_SCALE_DELAYED = 0, 1
+FP4_NVFP4, FP4_MXFP4 = 0, 1
+FP8_DT_BF16, FP8_DT_F32 = 0, 1
+FP8_NORM_NONE, FP8_NORM_RMS, FP8_NORM_LAYER = 0, 1, 2
 
 
 class fp8_tensor_state_t(ctypes.Structure):
@@ -39,6 +42,24 @@ class fp8_tensor_state_t(ctypes.Structure):
         ("counters", ctypes.c_void_p),
         ("hist_len", ctypes.c_int32),
     ]
+
+
+class fp8_block_norm_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "width")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("stream_dt", "block_dt", "post", "pre")]
+    _fields_ += [("eps", ctypes.c_float)]
+    _fields_ += [("r", ctypes.c_void_p), ("ld_r", ctypes.c_int64), ("o", ctypes.c_void_p), ("ld_o", ctypes.c_int64)]
+    _fields_ += [("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("gate_rows", ctypes.c_int64)]
+    _fields_ += [(n, ctypes.c_void_p) for n in ("res_scale", "w_post", "b_post", "w_pre", "b_pre")]
+    _fields_ += [("r_out", ctypes.c_void_p), ("ld_r_out", ctypes.c_int64), ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64)]
+    _fields_ += [("hq", ctypes.c_void_p), ("hsf", ctypes.c_void_p), ("h_fmt", ctypes.c_int32), ("h_scale", ctypes.c_void_p)]
+    _fields_ += [("stat_post", ctypes.c_void_p), ("stat_pre", ctypes.c_void_p)]
+
+
+class fp8_block_norm_grad_t(ctypes.Structure):
+    _fields_ = [("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64), ("dr_out", ctypes.c_void_p), ("ld_dr_out", ctypes.c_int64)]
+    _fields_ += [("dr", ctypes.c_void_p), ("ld_dr", ctypes.c_int64), ("do_", ctypes.c_void_p), ("ld_do", ctypes.c_int64)]
+    _fields_ += [(n, ctypes.c_void_p) for n in ("dgate", "dres_scale", "dw_post", "db_post", "dw_pre", "db_pre")]
 
 
 class fp8_mm_problem_t(ctypes.Structure):
@@ -80,6 +101,7 @@ _I = ctypes.c_int
 _SP = ctypes.POINTER(fp8_tensor_state_t)
 _MP = ctypes.POINTER(fp8_mm_problem_t)
 
+_NP, _GP = ctypes.POINTER(fp8_block_norm_t), ctypes.POINTER(fp8_block_norm_grad_t)
 _SIGS = {
     "fp8_quantize": [_P, _I64, _I64, _I64, _I, _I, _I, _SP, _P, _P, _P, _P],
     "fp8_scaled_mm": [_P, _I, _P, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I64, _P],
@@ -95,6 +117,11 @@ _SIGS = {
     "fp8_linear_bwd_ws": [_P, _I64, _I64, _I64, _P, _SP, _P, _SP, _SP, _I, _P, _P, _P, _P, _P, _I64, _P],
     "fp8_linear_bwd_mn": [_P, _I64, _I64, _I64, _P, _SP, _P, _SP, _SP, _I, _P, _P, _P, _P, _I64, _P],
     "fp8_scaled_mm_t": [_P, _I, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P],
+    "fp4_quantize": [_P, _I64, _I64, _I64, _I, _I, _SP, _P, _P, _P, _P, _P],
+    "fp4_dequantize": [_P, _P, _I64, _I64, _I, _P, _P, _I, _I64, _P],
+    "fp4_scaled_mm": [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _I, _I64, _P],
+    "fp8_block_norm_fwd": [_NP, _P],
+    "fp8_block_norm_bwd": [_NP, _GP, _P, _I64, _P],
     "fp8_history_commit": [_SP, _P],
     "fp8_history_commit_many": [_SP, ctypes.c_int32, _P],
     "fp8_poll_device_error": [],
@@ -112,6 +139,12 @@ lib.fp8_linear_bwd_workspace_bytes.argtypes = [_I64, _I64, _I64]
 lib.fp8_linear_bwd_workspace_bytes.restype = ctypes.c_int64
 lib.fp8_scaled_mm_workspace_bytes.argtypes = [_I64, _I64, _I64]
 lib.fp8_scaled_mm_workspace_bytes.restype = ctypes.c_int64
+lib.fp4_row_bytes.argtypes = [_I64]
+lib.fp4_row_bytes.restype = ctypes.c_int64
+lib.fp4_scale_bytes.argtypes = [_I, _I64, _I64]
+lib.fp4_scale_bytes.restype = ctypes.c_int64
+lib.fp8_block_norm_bwd_workspace_bytes.argtypes = [_NP, _GP]
+lib.fp8_block_norm_bwd_workspace_bytes.restype = ctypes.c_int64
 lib.fp8_status_string.argtypes = [ctypes.c_int]
 lib.fp8_status_string.restype = ctypes.c_char_p
 
@@ -325,6 +358,87 @@ def fp8_linear_bwd_noalloc(dy, M, K, N, xqT_save, x_st, wq_kn, w_st, dy_st, mode
     arguments, no allocation by the call); see include/fp8gb.h for the size limit."""
     return _check(lib.fp8_linear_bwd_noalloc(_ptr(dy), M, K, N, _ptr(xqT_save), _state(x_st), _ptr(wq_kn),
                                              _state(w_st), _state(dy_st), mode, _ptr(dx), _ptr(dw), _stream(stream)))
+
+
+# ---- microscaled 4-bit operands --------------------------------------------------------
+def fp4_row_bytes(K) -> int:
+    """Bytes of one row of K 4-bit codes."""
+    n = lib.fp4_row_bytes(K)
+    if n < 0:
+        raise Fp8Error(FP8_ERR_INVALID_ARG, "fp4_row_bytes: negative size")
+    return n
+
+
+def fp4_scale_bytes(fmt, MN, K) -> int:
+    """Bytes of the scale atoms of a 4-bit operand [MN, K]."""
+    n = lib.fp4_scale_bytes(fmt, MN, K)
+    if n < 0:
+        raise Fp8Error(FP8_ERR_INVALID_ARG, "fp4_scale_bytes: negative size or unknown format")
+    return n
+
+
+def fp4_quantize(x, rows, cols, ld, fmt, mode, st, q, sf, qT=None, sfT=None, stream=None):
+    return _check(lib.fp4_quantize(_ptr(x), rows, cols, ld, fmt, mode, _state(st), _ptr(q), _ptr(sf), _ptr(qT),
+                                   _ptr(sfT), _stream(stream)))
+
+
+def fp4_dequantize(q, sf, MN, K, fmt, scale_inv, y, dt, ldy, stream=None):
+    return _check(lib.fp4_dequantize(_ptr(q), _ptr(sf), MN, K, fmt, _ptr(scale_inv), _ptr(y), dt, ldy,
+                                     _stream(stream)))
+
+
+def fp4_scaled_mm(A, sfa, B, sfb, M, N, K, fmt, scale_inv_a, scale_inv_b, C, dt, ldc, stream=None):
+    return _check(lib.fp4_scaled_mm(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), M, N, K, fmt, _ptr(scale_inv_a),
+                                    _ptr(scale_inv_b), _ptr(C), dt, ldc, _stream(stream)))
+
+
+# ---- the norms around a block ----------------------------------------------------------
+def _fill(c, names, given):
+    """Set the pointers and leading dimensions of an argument block; a matrix given as a tensor brings its own
+    row stride unless ld_<name> is given too."""
+    unknown = set(given) - set(names)
+    if unknown:
+        raise TypeError(f"{type(c).__name__} has no {', '.join(sorted(unknown))}")
+    fields = {n for n, _ in c._fields_}
+    for name, v in given.items():
+        if name in fields and dict(c._fields_)[name] is ctypes.c_void_p:
+            setattr(c, name, _ptr(v))
+            ld = "ld_" + name.rstrip("_")
+            if ld in fields and ld not in given and v is not None and not isinstance(v, int):
+                setattr(c, ld, v.stride(0))
+        else:
+            setattr(c, name, v)
+    c._keep = given  # the tensors stay alive with the block
+    return c
+
+
+def block_norm(tokens, width, stream_dt, block_dt, post=FP8_NORM_NONE, pre=FP8_NORM_RMS, eps=1e-5, **tensors):
+    """An fp8_block_norm_t: what a program keeps for the norms around one block. Keywords are the fields of
+    the C struct (r, o, gate, gate_rows, res_scale, w_post, ..., stat_pre; include/fp8gb.h)."""
+    c = fp8_block_norm_t(tokens=tokens, width=width, stream_dt=stream_dt, block_dt=block_dt, post=post, pre=pre, eps=eps)
+    return _fill(c, [n for n, _ in fp8_block_norm_t._fields_[7:]], tensors)
+
+
+def block_norm_grad(**tensors):
+    """An fp8_block_norm_grad_t; keywords are its fields, with ``do`` for ``do_``."""
+    if "do" in tensors:
+        tensors["do_"] = tensors.pop("do")
+    return _fill(fp8_block_norm_grad_t(), [n for n, _ in fp8_block_norm_grad_t._fields_], tensors)
+
+
+def fp8_block_norm_fwd(f, stream=None):
+    return _check(lib.fp8_block_norm_fwd(f, _stream(stream)))
+
+
+def fp8_block_norm_bwd(f, b, workspace, workspace_bytes, stream=None):
+    return _check(lib.fp8_block_norm_bwd(f, b, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def fp8_block_norm_bwd_workspace_bytes(f, b) -> int:
+    n = lib.fp8_block_norm_bwd_workspace_bytes(f, b)
+    if n < 0:
+        raise Fp8Error(FP8_ERR_INVALID_ARG, fp8_get_last_error_detail())
+    return n
 
 
 def fp8_history_commit(st, stream=None):

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/fp8gb.h"
+#include "api.h"
 #include "kernels.h"
 
 namespace fp8gb {
@@ -21,6 +22,8 @@ namespace {
 
 thread_local char g_detail[512] = "";
 std::atomic<unsigned long long> g_wait_limit_ns{4000000000ull};
+
+}  // namespace
 
 fp8_status_t fail(fp8_status_t s, const char* fmt, ...) {
   va_list ap;
@@ -34,6 +37,8 @@ fp8_status_t cuda_fail(cudaError_t e, const char* where) {
   return fail(FP8_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+namespace {
+
 constexpr int kMaxDev = 64;
 
 int current_device() {
@@ -42,7 +47,7 @@ int current_device() {
   return d;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
 QuantState to_qs(const fp8_tensor_state_t* st) {
   QuantState q{};
@@ -66,8 +71,6 @@ fp8_status_t check_state(const fp8_tensor_state_t* st, fp8_scaling_t mode, const
     return fail(FP8_ERR_INVALID_ARG, "%s: delayed scaling needs amax_history, hist_count and hist_len > 0", who);
   return FP8_OK;
 }
-
-}  // namespace
 
 int num_sms() {
   static int cache[kMaxDev] = {};

@@ -145,4 +145,71 @@ cudaError_t launch_gemm_group(const GemmArgs& g0, const GemmArgs& g1, void* ws, 
                               cudaStream_t stream, const char** why);
 int64_t gemm_group_workspace_bytes(const GemmArgs& g0, const GemmArgs& g1);
 
+// Microscaled 4-bit operands (fmt 0 NVFP4, 1 MXFP4). Quantise x [rows, cols] into (q, sf) with
+// groups along its rows and / or (qT, sfT) with groups down its columns; st.scale null: no tensor
+// scale.
+cudaError_t launch_quant4(int fmt, bool delayed, const void* x, int64_t rows, int64_t cols, int64_t ld,
+                          const QuantState& st, void* q, void* sf, void* qT, void* sfT, cudaStream_t stream);
+cudaError_t launch_dequant4(int fmt, bool f32, const void* q, const void* sf, int64_t mn, int64_t k,
+                            const float* scale_inv, void* y, int64_t ldy, cudaStream_t stream);
+struct Mm4Args {
+  const void* A;
+  const void* sfa;
+  const void* B;
+  const void* sfb;
+  int64_t M, N, K;
+  int fmt;
+  const float* da;
+  const float* db;
+  void* C;
+  bool f32;
+  int64_t ldc;
+};
+// C [M, N] = A B^T; M, N > 0.
+cudaError_t launch_mm4(const Mm4Args& g, cudaStream_t stream, const char** why);
+
+// The norms around a block: the fields of fp8_block_norm_t and fp8_block_norm_grad_t, checked;
+// norm kinds 0 none, 1 root mean square, 2 layer; h_fmt as above.
+struct NormFwd {
+  int64_t tokens, width;
+  bool stream_f32, block_f32;
+  int post, pre;
+  float eps;
+  const void* r;
+  const void* o;
+  const void* gate;
+  int64_t ld_r, ld_o, ld_gate, gate_rows;
+  const float* res_scale;
+  const float* w_post;
+  const float* b_post;
+  const float* w_pre;
+  const float* b_pre;
+  void* r_out;
+  void* h;
+  int64_t ld_r_out, ld_h;
+  uint8_t* hq;
+  uint8_t* hsf;
+  int h_fmt;
+  const float* h_scale;
+  float* stat_post;
+  float* stat_pre;
+};
+struct NormBwd {
+  const void* dh;
+  const void* dr_out;
+  void* dr;
+  void* dO;
+  int64_t ld_dh, ld_dr_out, ld_dr, ld_do;
+  float* dgate;
+  float* dres_scale;
+  float* dw_post;
+  float* db_post;
+  float* dw_pre;
+  float* db_pre;
+};
+// tokens, width > 0
+cudaError_t launch_norm_fwd(const NormFwd& f, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t stream);
+int64_t norm_bwd_workspace_bytes(const NormFwd& f);
+
 }  // namespace fp8gb

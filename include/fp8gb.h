@@ -406,6 +406,154 @@ fp8_status_t fp8_linear_bwd_noalloc(const void* dy_bf16, int64_t M, int64_t K, i
                                     fp8_tensor_state_t* dy_st, fp8_scaling_t mode,
                                     void* dx_bf16, void* dw_bf16, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Microscaled 4-bit operands
+ * ------------------------------------------------------------------------------------------
+ * The same fine-grained idea ([GUARD] "Real products..."), one step narrower; the pages stop at
+ * 8 bits. Elements are E2M1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6),
+ * rounded to nearest, ties to even, saturating; the groups run along the contraction:
+ *   FP4_NVFP4  one E4M3 scale per 16 elements and, optionally, one fp32 scale for the tensor.
+ *              With s the tensor's scale and d its inverse (1, 1 without one) and a the group's
+ *              max |x|: c = e4m3(fl32(fl32(a s) / 6)), r = fl32(s / c) (0 if c = 0),
+ *              code = e2m1(fl32(x r)); it stands for code * c * d. The tensor's scale follows
+ *              the library's rule with the format's largest value 6 * 448: s = fl32(2688 / amax),
+ *              d = fl32(amax / 2688), and 1, 1 where amax is zero, not finite or makes s overflow.
+ *   FP4_MXFP4  one power of two per 32 elements (UE8M0 byte e + 127), e the smallest integer with
+ *              6 * 2^e >= a (so nothing saturates; 0 for a = 0; at least -127),
+ *              code = e2m1(fl32(x 2^-e)).
+ * An infinity saturates (it counts as the largest finite bf16 in a). E2M1 has no NaN: a group
+ * that holds one gets the scale NaN (0x7F or 0xFF) and zero codes, so every result that it
+ * touches is NaN.
+ *
+ * Codes of an operand with MN rows and contraction K: MN rows of fp4_row_bytes(K) bytes, element
+ * k in the low (k even) or high nibble of byte k / 2, zero codes from K to the row's end. Scales:
+ * atoms of 512 bytes as for FP8_GRAN_MX_1x32, atom (m / 128, g / 4) at offset
+ * ((m / 128) * ceil(G / 4) + g / 4) * 512 for G = ceil(K / 16) (ceil(K / 32)) groups, the byte of
+ * (m, g) at 16 (m % 32) + 4 ((m / 32) % 4) + g % 4 in it; fp4_scale_bytes(fmt, MN, K) bytes in
+ * all. The quantiser writes the atoms whole: scales past the last row or group are 0 (NVFP4) or
+ * e = 0 (MXFP4). Any MN and K. Both buffers are caller-owned and 16-byte aligned. */
+typedef enum { FP4_NVFP4 = 0, FP4_MXFP4 = 1 } fp4_format_t;
+
+/* Element types of outputs that come in more than one. */
+typedef enum { FP8_DT_BF16 = 0, FP8_DT_F32 = 1 } fp8_dtype_t;
+
+/* Bytes of one row of codes (16 * ceil(K / 32)) and of an operand's scales; -1 for a negative
+ * size or an unknown format. */
+int64_t fp4_row_bytes(int64_t K);
+int64_t fp4_scale_bytes(fp4_format_t fmt, int64_t MN, int64_t K);
+
+/* Quantise a bf16 matrix x [rows, cols] (leading dimension ld >= cols) to 4 bits, in one pass:
+ *   q, sf    (MN = rows, K = cols): groups along x's rows, as an activation's forward operand;
+ *   qT, sfT  (MN = cols, K = rows): groups down its columns, codes transposed, as a weight [K, N]
+ *            or the operand of a gradient's other contraction.
+ * Either pair may be NULL, not both. st (NVFP4 only): the tensor's scale, from x's own amax (mode
+ * CURRENT; x is read twice) or from st's history (DELAYED; from the current amax while the history
+ * is empty); the call writes st->scale and st->scale_inv and sets st->amax_cur (CURRENT) or raises
+ * it to x's amax (DELAYED), as fp8_quantize does. st->counters are left alone. st == NULL: no
+ * tensor scale (mode CURRENT). x: 2-byte aligned (16-byte aligned with ld % 8 == 0 is faster). */
+fp8_status_t fp4_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_t ld, fp4_format_t fmt,
+                          fp8_scaling_t mode, const fp8_tensor_state_t* st, void* q, void* sf, void* qT,
+                          void* sfT, void* stream);
+
+/* y [MN, K] (leading dimension ldy >= K, bf16 or fp32) = the values the operand q, sf stands for:
+ * code * scale, times *scale_inv (device fp32; NULL: 1), rounded once. y aligned to its element. */
+fp8_status_t fp4_dequantize(const void* q, const void* sf, int64_t MN, int64_t K, fp4_format_t fmt,
+                            const float* scale_inv, void* y, fp8_dtype_t dt, int64_t ldy, void* stream);
+
+/* C [M, N] = A B^T of two 4-bit operands of one format, A with MN = M, B with MN = N, both along K:
+ *   C_ij = round( d_a d_b sum_g c_a[i,g] c_b[j,g] sum_{k in g} a_ik b_jk ),  fp32 accumulation,
+ * d_a and d_b the operands' inverse tensor scales (device fp32 each; NULL: 1), C bf16 or fp32 with
+ * leading dimension ldc >= N, 16-byte aligned, ldc a multiple of 8 (bf16) or 4 (fp32); elements of
+ * C's rows past N are not written. With operands quantised along the contraction this is the
+ * forward (x, W^T), the data gradient (dy, W) and the weight gradient (x^T, dy^T); a few rows of A
+ * (tokens being generated) take a kernel that streams B at the memory's rate. Any M, N, K >= 0
+ * (K == 0 writes zeros). The result does not depend on anything but the inputs (no atomics). */
+fp8_status_t fp4_scaled_mm(const void* A, const void* sfa, const void* B, const void* sfb, int64_t M, int64_t N,
+                           int64_t K, fp4_format_t fmt, const float* scale_inv_a, const float* scale_inv_b, void* C,
+                           fp8_dtype_t dt, int64_t ldc, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The norms around a block, with its gate and the residual's scale
+ * ------------------------------------------------------------------------------------------
+ * What stands between the output o of one block and the input h of the next on the residual
+ * stream r ([GUARD] "Real products...": norms stay in high precision), in one pass:
+ *     n  = norm_post(o) w_post + b_post        (the norm after the block)
+ *     r' = alpha r + gate n                    (its gate, the residual's scale)
+ *     h  = norm_pre(r') w_pre + b_pre          (the norm before the next block)
+ * norm = none, root mean square x / sqrt(mean(x^2) + eps), or layer (x - mean) / sqrt(var + eps).
+ * All arithmetic and statistics in fp32; h is computed from r' before r' is rounded to the
+ * stream's type. */
+typedef enum { FP8_NORM_NONE = 0, FP8_NORM_RMS = 1, FP8_NORM_LAYER = 2 } fp8_norm_t;
+
+/* Arguments of fp8_block_norm_fwd and what its backward reads. Device pointers, caller-owned.
+ * Matrices are [tokens, width] with leading dimensions in elements, aligned to their elements
+ * (16-byte aligned with rows of whole 16 bytes is faster); parameters and statistics are fp32. */
+typedef struct {
+  int64_t tokens, width;
+  int32_t stream_dt, block_dt; /* fp8_dtype_t of r, r_out and of o, gate, h */
+  int32_t post, pre;           /* fp8_norm_t */
+  float eps;
+  const void* r;               /* residual stream in */
+  int64_t ld_r;
+  const void* o;               /* block output; NULL: no block yet, r' = alpha r (post NONE, no gate) */
+  int64_t ld_o;
+  const void* gate;            /* [ceil(tokens / gate_rows), width]; row t takes row t / gate_rows. NULL: 1 */
+  int64_t ld_gate;
+  int64_t gate_rows;
+  const float* res_scale;      /* alpha, one fp32; NULL: 1 */
+  const float* w_post;         /* [width]; NULL: ones */
+  const float* b_post;         /* [width]; NULL: zeros */
+  const float* w_pre;
+  const float* b_pre;
+  void* r_out;                 /* r'; may be r itself (same leading dimension); NULL: not written */
+  int64_t ld_r_out;
+  void* h;                     /* NULL: not written */
+  int64_t ld_h;
+  void* hq;                    /* h as a 4-bit operand (MN = tokens, K = width), from the fp32 values; */
+  void* hsf;                   /* both NULL: not written. width % 32 == 0 */
+  int32_t h_fmt;               /* fp4_format_t of hq */
+  const float* h_scale;        /* NVFP4: h's tensor scale s (device fp32); NULL: 1 */
+  float* stat_post;            /* [tokens, 2]: mean (0 for RMS) and 1 / root; NULL: not written */
+  float* stat_pre;
+} fp8_block_norm_t;
+
+/* Gradients of the same: in dh (at h) and dr_out (at r'), either NULL for zero; out, each NULL for
+ * not wanted: dr, do_, dgate [groups, width], dres_scale [1], dw and db [width] (overwritten, fp32).
+ *     g = dr_out + norm_pre'(dh; r');  dr = alpha g;  dres_scale = sum g r;  dgate = sum over the
+ *     rows of a gate's group of g n;  do = norm_post'(gate g; o);  dw, db: sums over the tokens. */
+typedef struct {
+  const void* dh;     /* block_dt */
+  int64_t ld_dh;
+  const void* dr_out; /* stream_dt */
+  int64_t ld_dr_out;
+  void* dr;           /* stream_dt; may be dr_out itself (same leading dimension) */
+  int64_t ld_dr;
+  void* do_;          /* block_dt */
+  int64_t ld_do;
+  float* dgate;
+  float* dres_scale;
+  float* dw_post;
+  float* db_post;
+  float* dw_pre;
+  float* db_pre;
+} fp8_block_norm_grad_t;
+
+/* Forward. Refused (FP8_ERR_INVALID_ARG): a missing r, no output, gate without gate_rows > 0, norm
+ * parameters without a norm, post norm or gate without o, unknown types or kinds, eps < 0 or not
+ * finite; FP8_ERR_UNSUPPORTED: tokens or width >= 2^31, hq with width % 32 != 0. */
+fp8_status_t fp8_block_norm_fwd(const fp8_block_norm_t* f, void* stream);
+
+/* Backward from f's inputs (r is read for dres_scale only), its r_out (as written by the forward),
+ * stat_post and stat_pre (required where there is that norm). workspace: device, 16-byte aligned,
+ * at least fp8_block_norm_bwd_workspace_bytes(f, b) bytes, contents irrelevant before and after;
+ * calls that may overlap need their own. Sums over the tokens are taken in a fixed order (the
+ * same inputs give the same bits on one device). */
+fp8_status_t fp8_block_norm_bwd(const fp8_block_norm_t* f, const fp8_block_norm_grad_t* b, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the backward needs on the current device; negative on an error. */
+int64_t fp8_block_norm_bwd_workspace_bytes(const fp8_block_norm_t* f, const fp8_block_norm_grad_t* b);
+
 /* Push st->amax_cur into the history: amax_history[hist_count % hist_len] = amax_cur;
  * hist_count += 1; amax_cur = 0 (the next step's delayed casts start a new running maximum).
  * [GUARD] "Real products...": amax history tracking. */

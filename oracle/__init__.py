@@ -20,7 +20,8 @@ Sources (the three web pages on FP8 mixed-precision training):
 
 Modules: ``fp8`` (formats, cast), ``quant`` (amax, scales, counters, tile/block,
 delayed state), ``gemm`` (scaled matmuls and the error bound), ``linear``
-(forward/backward compositions and the delayed-scaling training loop).
+(forward/backward compositions and the delayed-scaling training loop), ``fp4`` (microscaled
+4-bit operands), ``norm`` (the norms around a block).
 
 Parity status per function is stated in each module header.  Functions whose
 definition the pages leave open follow a stated reading; the delayed-scaling state
