@@ -176,6 +176,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// 3-D tiled load of one box into shared memory (single CTA).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // 2-D tiled load into this CTA's shared memory whose transaction bytes are signalled on an
 // mbarrier of either CTA of the pair (shared::cluster address `bar_cluster`).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int32_t c0,
@@ -324,6 +332,35 @@ __device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, u
       "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
+}
+
+// D[tmem] (+)= (A sfa) (B sfb)^T for 4-bit (E2M1) operands of 64 K, fp32 accumulation. FMT 0: one E4M3 scale
+// per 16 K (scale_vec::4X, the four bytes of each row's scale word); FMT 1: one UE8M0 scale per 32 K
+// (scale_vec::2X, the two bytes that the descriptor's scale-factor ids pick: 0 or 2). PAIR: the CTA-pair form.
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void mma_f4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                       uint32_t sfb, uint32_t accumulate) {
+#define FP8GB_MMA_F4(group, kind, vec)                                                                     \
+  asm volatile(                                                                                            \
+      "{\n\t.reg .pred p;\n\t"                                                                             \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                          \
+      "tcgen05.mma." group ".kind::" kind ".block_scale.scale_vec::" vec " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" \
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)               \
+      : "memory")
+  if constexpr (FMT == 0 && PAIR)
+    FP8GB_MMA_F4("cta_group::2", "mxf4nvf4", "4X");
+  else if constexpr (FMT == 0)
+    FP8GB_MMA_F4("cta_group::1", "mxf4nvf4", "4X");
+  else if constexpr (PAIR)
+    FP8GB_MMA_F4("cta_group::2", "mxf4", "2X");
+  else
+    FP8GB_MMA_F4("cta_group::1", "mxf4", "2X");
+#undef FP8GB_MMA_F4
+}
+
+// Instruction descriptor of mma_f4: both operands E2M1, K-major; scale type E4M3 (FMT 0) or UE8M0.
+__host__ __device__ constexpr uint32_t idesc_f4(int fmt, uint32_t M, uint32_t N) {
+  return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (static_cast<uint32_t>(fmt) << 23) | ((M >> 4) << 24);
 }
 
 // Instruction descriptor for kind::mxf8f6f4 with UE8M0 scales, fp32 accumulator, both operands
