@@ -173,22 +173,42 @@ def _check(status: int) -> int:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:  # None or a raw device address
         return t
-    return t.data_ptr()
+
+
+def _no_torch_stream():
+    return None
+
+
+def _find_current_stream():
+    """A function that returns the raw handle of torch's current stream on the current device (None without a GPU).
+    torch's raw-handle getter takes 0.2 us a call where torch.cuda.current_stream() takes 3, as much as a launch."""
+    try:
+        import torch
+    except ImportError:
+        return _no_torch_stream
+    if not torch.cuda.is_available():
+        return _no_torch_stream
+    try:
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    except AttributeError:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    torch.cuda.init()
+    return lambda: raw(device())
+
+
+_current_stream = None
 
 
 def _stream(s):
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
-        return None
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -200,3 +200,16 @@ def test_dequantize(g, fmt, mn, k, dt, pad):
         got = y.float().cpu().numpy()
         assert np.array_equal(np.isnan(got[:, :k]), np.isnan(want)) and np.array_equal(np.nan_to_num(got[:, :k]), np.nan_to_num(want))
         assert (got[:, k:] == 7.0).all()
+
+
+def test_history_amax_ignores_nan(g):
+    x = values_of(31, 140, 150)
+    x[3, 4] = np.nan
+    x[100, 149] = np.nan
+    x = f32_from_bf16_bits(bf16_bits_from_f32(x))
+    st = g.TensorState(4)
+    for _ in range(2):  # from an empty history, and from one
+        out = quantize(g, x, fp4.NV, "both", st, g.FP8_SCALE_DELAYED)
+        assert st.snapshot()["amax_cur"] == np.nanmax(np.abs(x))
+        check(out, x, fp4.NV, np.float32(2688) / np.float32(np.nanmax(np.abs(x))))
+        g.fp8_history_commit(st)
