@@ -193,6 +193,7 @@ struct NormFwd {
   const float* h_scale;
   float* stat_post;
   float* stat_pre;
+  WaitCtl w;  // (backward)
 };
 struct NormBwd {
   const void* dh;
