@@ -27,88 +27,167 @@ __device__ __forceinline__ float load(const bf16* p) { return __bfloat162float(*
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// VEC consecutive elements. stream: data read or written once (kept out of L1, evicted first from
-// L2); otherwise parameters, which every row reads.
-template <int VEC>
-__device__ __forceinline__ void load_stream(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 4) {
-    const float4 t = __ldcs(reinterpret_cast<const float4*>(p));
-    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-  } else {
-    v[0] = __ldcs(p);
-  }
-}
-__device__ __forceinline__ void unpack4(uint2 t, float (&v)[4]) {
-  v[0] = __uint_as_float(t.x << 16), v[1] = __uint_as_float(t.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(t.y << 16), v[3] = __uint_as_float(t.y & 0xFFFF0000u);
-}
-template <int VEC>
-__device__ __forceinline__ void load_stream(const bf16* p, float (&v)[VEC]) {
-  if constexpr (VEC == 4)
-    unpack4(__ldcs(reinterpret_cast<const uint2*>(p)), v);
-  else
-    v[0] = __uint_as_float(static_cast<uint32_t>(__ldcs(reinterpret_cast<const uint16_t*>(p))) << 16);
-}
-template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 4) {
-    const float4 t = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-  } else {
-    v[0] = __ldg(p);
-  }
-}
-template <int VEC>
-__device__ __forceinline__ void load_param(const bf16* p, float (&v)[VEC]) {
-  if constexpr (VEC == 4)
-    unpack4(__ldg(reinterpret_cast<const uint2*>(p)), v);
-  else
-    v[0] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+// Two fp32 values in one 64-bit register: the arithmetic below works on both at once.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
   return r;
 }
-template <int VEC>
-__device__ __forceinline__ void store_stream(float* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 4)
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-  else
-    __stcs(p, v[0]);
+__device__ __forceinline__ Pair both(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 split(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
+  return r;
 }
-template <int VEC>
-__device__ __forceinline__ void store_stream(bf16* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 4)
-    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3])));
-  else
-    *p = __float2bfloat16_rn(v[0]);
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float sum2(Pair p) {
+  const float2 t = split(p);
+  return t.x + t.y;
+}
+__device__ __forceinline__ Pair pair_of(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t pack2(Pair p) {
+  const float2 t = split(p);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(t.y), "f"(t.x));
+  return r;
 }
 
-// Sums of two values over the warps of a CTA (all of them; `warps` of them), the same bits on every
-// thread. red: 2 x 32 values that consecutive sums take in turn, so one barrier each is enough: who
-// writes a half again has passed the barrier after everyone's read of it.
-__device__ __forceinline__ float2 warp_sum2(float2 s) {
+// How a row lies in its warps' registers: a warp holds 32 E consecutive columns, a lane E of them. VEC 4: items of 4
+// consecutive columns, item i of a lane 128 i columns after its first; VEC 1: element e 32 e columns after it. Either
+// way a warp's access is contiguous and an item's place a constant offset. `left`: columns from the lane's first one
+// to the row's end; what lies past it reads as `pad` and is not written.
+template <int VEC, int E>
+struct Row {
+  static_assert(E % 4 == 0 && (VEC == 1 || VEC == 4), "items");
+  static __device__ __forceinline__ int first(int warp, int lane) { return warp * 32 * E + lane * VEC; }
+
+  // stream: rows, read once (kept out of L1); otherwise parameters, which every row reads
+  template <bool STREAM>
+  static __device__ __forceinline__ void load(const float* p, int left, Pair (&x)[E / 2], float pad = 0.0f) {
+    if constexpr (VEC == 4) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
-    s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+      for (int i = 0; i < E / 4; ++i) {
+        x[2 * i] = x[2 * i + 1] = both(pad);
+        if (128 * i < left) {
+          const float4* at = reinterpret_cast<const float4*>(p + 128 * i);
+          const float4 t = STREAM ? __ldcs(at) : __ldg(at);
+          x[2 * i] = pair(t.x, t.y);
+          x[2 * i + 1] = pair(t.z, t.w);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        float lo = pad, hi = pad;
+        if (64 * e < left) lo = STREAM ? __ldcs(p + 64 * e) : __ldg(p + 64 * e);
+        if (64 * e + 32 < left) hi = STREAM ? __ldcs(p + 64 * e + 32) : __ldg(p + 64 * e + 32);
+        x[e] = pair(lo, hi);
+      }
+    }
   }
+  template <bool STREAM>
+  static __device__ __forceinline__ void load(const bf16* p, int left, Pair (&x)[E / 2], float pad = 0.0f) {
+    if constexpr (VEC == 4) {
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        x[2 * i] = x[2 * i + 1] = both(pad);
+        if (128 * i < left) {
+          const uint2* at = reinterpret_cast<const uint2*>(p + 128 * i);
+          const uint2 t = STREAM ? __ldcs(at) : __ldg(at);
+          x[2 * i] = pair_of(t.x);
+          x[2 * i + 1] = pair_of(t.y);
+        }
+      }
+    } else {
+      auto one = [&](int at) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + at;
+        return at < left ? __uint_as_float(static_cast<uint32_t>(STREAM ? __ldcs(q) : __ldg(q)) << 16) : pad;
+      };
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) x[e] = pair(one(64 * e), one(64 * e + 32));
+    }
+  }
+  static __device__ __forceinline__ void store(float* p, int left, const Pair (&x)[E / 2]) {
+#pragma unroll
+    for (int e = 0; e < E / 2; e += VEC == 4 ? 2 : 1) {
+      const float2 a = split(x[e]);
+      if constexpr (VEC == 4) {
+        const float2 b = split(x[e + 1]);
+        if (64 * e < left) __stcs(reinterpret_cast<float4*>(p + 64 * e), make_float4(a.x, a.y, b.x, b.y));
+      } else {
+        if (64 * e < left) __stcs(p + 64 * e, a.x);
+        if (64 * e + 32 < left) __stcs(p + 64 * e + 32, a.y);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(bf16* p, int left, const Pair (&x)[E / 2]) {
+#pragma unroll
+    for (int e = 0; e < E / 2; e += VEC == 4 ? 2 : 1) {
+      if constexpr (VEC == 4) {
+        if (64 * e < left) __stcs(reinterpret_cast<uint2*>(p + 64 * e), make_uint2(pack2(x[e]), pack2(x[e + 1])));
+      } else {
+        const uint32_t w = pack2(x[e]);
+        if (64 * e < left) reinterpret_cast<uint16_t*>(p)[64 * e] = static_cast<uint16_t>(w);
+        if (64 * e + 32 < left) reinterpret_cast<uint16_t*>(p)[64 * e + 32] = static_cast<uint16_t>(w >> 16);
+      }
+    }
+  }
+};
+
+// Sums over the warps of a CTA (all of them; `warps` of them), in warp order, the same bits on every thread. red: two
+// halves that consecutive sums take in turn, so one barrier each is enough: who writes a half again has passed the
+// barrier after everyone's read of it. A CTA of one warp needs none.
+struct Red {
+  __align__(16) float v[2][2][32];
+};
+__device__ __forceinline__ float warp_sum(float s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   return s;
 }
-__device__ __forceinline__ float2 cta_sum2(float2 s, float2 (*red)[32], int& turn, int warps) {
-  s = warp_sum2(s);
+__device__ __forceinline__ float red_sum(const float* r, int warps) {
+  float s = r[0];
+  for (int w = 1; w < warps; ++w) s += r[w];
+  return s;
+}
+__device__ __forceinline__ float cta_sum(float s, Red& red, int& turn, int warps) {
+  s = warp_sum(s);
   if (warps == 1) return s;
-  float2* r = red[turn];
+  float* r = red.v[turn][0];
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
   __syncthreads();
-  s = r[0];
-  for (int w = 1; w < warps; ++w) {
-    s.x += r[w].x;
-    s.y += r[w].y;
+  return red_sum(r, warps);
+}
+__device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn, int warps) {
+  s.x = warp_sum(s.x);
+  s.y = warp_sum(s.y);
+  if (warps == 1) return s;
+  float *rx = red.v[turn][0], *ry = red.v[turn][1];
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) {
+    rx[threadIdx.x >> 5] = s.x;
+    ry[threadIdx.x >> 5] = s.y;
   }
-  return s;
+  __syncthreads();
+  return make_float2(red_sum(rx, warps), red_sum(ry, warps));
 }
 
 __device__ __forceinline__ float affine(float z, const float* w, const float* b, int64_t c) {

@@ -23,7 +23,7 @@ constexpr int kPart = 6;
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha,
                                                            int64_t rows_per) {
-  __shared__ float2 red[2][32];
+  __shared__ Red red;
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
         a += dz;
         q = fmaf(dz, zpre(c), q);
       }
-      s1 = cta_sum2(make_float2(a, q), red, turn, kThreads / 32);
+      s1 = cta_sum(make_float2(a, q), red, turn, kThreads / 32);
     }
     auto grad = [&](int64_t c) {
       float g = dro != nullptr ? load(dro + c) : 0.0f;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
         a += dz;
         q = fmaf(dz, (load(o + c) - post.x) * post.y, q);
       }
-      s2 = cta_sum2(make_float2(a, q), red, turn, kThreads / 32);
+      s2 = cta_sum(make_float2(a, q), red, turn, kThreads / 32);
     }
     const bool whole = f.gate != nullptr && grp * f.gate_rows >= t0 && (min((grp + 1) * f.gate_rows, f.tokens) <= t1);
     const bool last = f.gate != nullptr && (t + 1 == t1 || (t + 1) / f.gate_rows != grp);
@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
 // A row in the registers of a CTA, the next rows on their way to shared memory
 // ---------------------------------------------------------------------------------------
 // Every input is read once, from a ring of rows that asynchronous bulk copies fill ahead (RING: rows of whole
-// 16 bytes) or from global memory. A thread holds the same I items of VEC columns of every row, so the column
-// sums stay in its registers over all of the CTA's tokens.
-//   pass 1: dz and z of the norm before the next block; its two row sums; dw_pre, db_pre
+// 16 bytes) or from global memory. A thread holds the same E columns of every row, so the column sums stay in its
+// registers over all of the CTA's tokens.
+//   pass 1: dz and z of the norm before the next block; its row sums; dw_pre, db_pre
 //   pass 2: g, so dr and dalpha; dn, dgate, dw_post, db_post; dz and z of the norm after the block; its row sums
 //   pass 3: do
 constexpr int kMaxStages = 4;
@@ -144,39 +144,61 @@ struct Ring {
   int dh, r_out, dr_out, o, r;  // each tensor's place in a row; -1: not there
 };
 
-template <int VEC>
-__device__ __forceinline__ void store_part(float* p, const float (&v)[VEC]) {  // (D % 4 == 0 where VEC == 4)
-  if constexpr (VEC == 4)
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  else
-    *p = v[0];
-}
-
-// VEC elements of a row at column c: from the ring's copy, or from global memory.
-template <bool RING, int VEC, typename T>
-__device__ __forceinline__ void item(const uint8_t* held, int at, const void* base, int64_t ld, int64_t t, int c, float (&v)[VEC]) {
+// A row's columns from the ring's copy, or from global memory.
+template <bool RING, int VEC, int E, typename T>
+__device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* base, int64_t ld, int64_t t, int c, int left, Pair (&x)[E / 2]) {
   if constexpr (RING) {
     const T* p = reinterpret_cast<const T*>(held + at) + c;
-    if constexpr (sizeof(T) == 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-      unpack4(*reinterpret_cast<const uint2*>(p), v);
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      x[2 * i] = x[2 * i + 1] = both(0.0f);
+      if (128 * i < left) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p + 128 * i);
+          x[2 * i] = pair(q.x, q.y);
+          x[2 * i + 1] = pair(q.z, q.w);
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(p + 128 * i);
+          x[2 * i] = pair_of(q.x);
+          x[2 * i + 1] = pair_of(q.y);
+        }
+      }
     }
   } else {
-    load_stream<VEC>(static_cast<const T*>(base) + t * ld + c, v);
+    Row<VEC, E>::template load<true>(static_cast<const T*>(base) + t * ld + c, left, x);
+  }
+}
+
+// Column sums to the workspace or to dgate (aligned to 4 bytes only).
+template <int VEC, int E, bool WIDE>
+__device__ __forceinline__ void leave(float* p, int left, const Pair (&x)[E / 2]) {
+  if constexpr (VEC == 4 && !WIDE) {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const float2 a = split(x[2 * i]), b = split(x[2 * i + 1]);
+      if (128 * i < left) {
+        p[128 * i] = a.x;
+        p[128 * i + 1] = a.y;
+        p[128 * i + 2] = b.x;
+        p[128 * i + 3] = b.y;
+      }
+    }
+  } else {
+    Row<VEC, E>::store(p, left, x);
   }
 }
 
 // WHAT: 0 weights' sums only, 1 the gate's too, 2 the gate's and the biases', 3 the biases'.
-template <typename TS, typename TB, int VEC, int I, bool RING, int WHAT>
+template <typename TS, typename TB, int VEC, int E, bool RING, int WHAT>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per, const Ring ring) {
+  using R = Row<VEC, E>;
   constexpr bool GATE = WHAT == 1 || WHAT == 2, BIAS = WHAT >= 2;
+  constexpr int H = E / 2;
   extern __shared__ __align__(16) uint8_t rows_smem[];
-  __shared__ float2 red[2][32];
+  __shared__ Red red;
   __shared__ double red_alpha[16];
   __shared__ __align__(8) uint64_t bars[kMaxStages];
-  const int D = static_cast<int>(f.width), step = blockDim.x * VEC, c0 = threadIdx.x * VEC, warps = blockDim.x >> 5;
+  const int D = static_cast<int>(f.width), warps = blockDim.x >> 5, c = R::first(threadIdx.x >> 5, threadIdx.x & 31), left = D - c;
   const int64_t t0 = blockIdx.x * rows_per, t1 = min(t0 + rows_per, f.tokens);
   const uint32_t bar0 = smem_u32(bars);
   if constexpr (RING) {
@@ -189,8 +211,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
   pdl_wait();
   pdl_trigger();
 
-  auto fetch = [&](int64_t t) {  // (thread 0) row t's inputs into its stage
-    const int s = static_cast<int>((t - t0) % ring.stages);
+  auto fetch = [&](int64_t t, int s) {  // (thread 0) row t's inputs into stage s
     const uint32_t dst = smem_u32(rows_smem) + s * ring.bytes, bar = bar0 + 8 * s;
     const uint32_t nb = D * sizeof(TB), ns = D * sizeof(TS);
     mbar_arrive_expect_tx(bar, ring.bytes);
@@ -201,150 +222,210 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     if (ring.r >= 0) bulk_load(dst + ring.r, static_cast<const TS*>(f.r) + t * f.ld_r, ns, bar);
   };
   if (RING && threadIdx.x == 0)
-    for (int s = 0; s < ring.stages && t0 + s < t1; ++s) fetch(t0 + s);
+    for (int s = 0; s < ring.stages && t0 + s < t1; ++s) fetch(t0 + s, s);
 
-  int turn = 0;
+  int turn = 0, stage = 0;
+  uint32_t phase = 0;
   const float alpha = f.res_scale != nullptr ? __ldg(f.res_scale) : 1.0f, inv = 1.0f / static_cast<float>(D);
-  float aw_pre[I][VEC], aw_post[I][VEC], ag[GATE ? I : 1][VEC], ab_pre[BIAS ? I : 1][VEC], ab_post[BIAS ? I : 1][VEC];
+  Pair aw_pre[H], aw_post[H], ag[GATE ? H : 1], ab_pre[BIAS ? H : 1], ab_post[BIAS ? H : 1];
+  const Pair zero = both(0.0f);
 #pragma unroll
-  for (int i = 0; i < I; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      aw_pre[i][j] = aw_post[i][j] = 0.0f;
-      if constexpr (GATE) ag[i][j] = 0.0f;
-      if constexpr (BIAS) ab_pre[i][j] = ab_post[i][j] = 0.0f;
-    }
+  for (int i = 0; i < H; ++i) {
+    aw_pre[i] = aw_post[i] = zero;
+    if constexpr (GATE) ag[i] = zero;
+    if constexpr (BIAS) ab_pre[i] = ab_post[i] = zero;
+  }
   // sum g r cancels (its terms have both signs), so the rounding of its running sum is kept: hi + lo
   float al_hi = 0.0f, al_lo = 0.0f;
   const bool back = b.dh != nullptr, normed = back && f.pre != kNone, block = f.o != nullptr;
   float* mine = part + static_cast<int64_t>(blockIdx.x) * kPart * D;
+  int64_t grp = 0, grp_end = f.tokens;  // the gate's row, and the first token past its group
+  if (f.gate != nullptr) {
+    grp = t0 / f.gate_rows;
+    grp_end = (grp + 1) * f.gate_rows;
+  }
+  const int64_t grp0 = grp;
   bool ok = true;
   for (int64_t t = t0; t < t1; ++t) {
     const uint8_t* held = nullptr;
     if constexpr (RING) {
-      const int s = static_cast<int>((t - t0) % ring.stages);
-      ok = mbar_wait(bar0 + 8 * s, static_cast<uint32_t>((t - t0) / ring.stages) & 1u, f.w, DEV_ERR_WAIT_PRODUCER);
+      ok = mbar_wait(bar0 + 8 * stage, phase, f.w, DEV_ERR_WAIT_PRODUCER);
       ok = __syncthreads_or(!ok) == 0;
       if (!ok) break;  // a wait ran out: the CTA stops together
-      held = rows_smem + s * ring.bytes;
+      held = rows_smem + stage * ring.bytes;
+    }
+    if (f.gate != nullptr && t == grp_end) {
+      ++grp;
+      grp_end += f.gate_rows;
     }
     const float2 pre = normed ? __ldg(reinterpret_cast<const float2*>(f.stat_pre) + t) : make_float2(0.0f, 1.0f);
     const float2 post = f.post != kNone ? __ldg(reinterpret_cast<const float2*>(f.stat_post) + t) : make_float2(0.0f, 1.0f);
-    const int64_t grp = f.gate != nullptr ? t / f.gate_rows : 0;
-    const TB* gate = f.gate != nullptr ? static_cast<const TB*>(f.gate) + grp * f.ld_gate : nullptr;
-    float dz[I][VEC], z[I][VEC];
-    float2 s1 = make_float2(0.0f, 0.0f);
+    Pair dz[H], z[H];
+    float m1 = 0.0f, q1 = 0.0f;
+    if (back) {
+      row_of<RING, VEC, E, TB>(held, ring.dh, b.dh, b.ld_dh, t, c, left, dz);
+      if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int c = c0 + i * step;
+        for (int i = 0; i < H; ++i) ab_pre[i] = add2(ab_pre[i], dz[i]);
+      }
+      if (normed) {
+        row_of<RING, VEC, E, TS>(held, ring.r_out, f.r_out, f.ld_r_out, t, c, left, z);
+        const Pair m = both(-pre.x), rstd = both(pre.y);
+        if (f.pre == kLayer) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) dz[i][j] = z[i][j] = 0.0f;
-      if (c < D && back) {
-        float dy[VEC], w[VEC];
-        item<RING, VEC, TB>(held, ring.dh, b.dh, b.ld_dh, t, c, dy);
-        if (normed) item<RING, VEC, TS>(held, ring.r_out, f.r_out, f.ld_r_out, t, c, z[i]);
-        if (f.w_pre != nullptr) load_param<VEC>(f.w_pre + c, w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          z[i][j] = normed ? (z[i][j] - pre.x) * pre.y : 0.0f;
-          aw_pre[i][j] = fmaf(dy[j], z[i][j], aw_pre[i][j]);
-          if constexpr (BIAS) ab_pre[i][j] += dy[j];
-          dz[i][j] = f.w_pre != nullptr ? dy[j] * w[j] : dy[j];
-          s1.x += dz[i][j];
-          s1.y = fmaf(dz[i][j], z[i][j], s1.y);
+          for (int i = 0; i < H; ++i) z[i] = add2(z[i], m);
         }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          z[i] = mul2(z[i], rstd);
+          aw_pre[i] = fma2(dz[i], z[i], aw_pre[i]);
+        }
+        if (f.w_pre != nullptr) {
+          Pair w[H];
+          R::template load<false>(f.w_pre + c, left, w);
+#pragma unroll
+          for (int i = 0; i < H; ++i) dz[i] = mul2(dz[i], w[i]);
+        }
+        Pair sq = zero;
+#pragma unroll
+        for (int i = 0; i < H; ++i) sq = fma2(dz[i], z[i], sq);
+        if (f.pre == kLayer) {
+          Pair sm = zero;
+#pragma unroll
+          for (int i = 0; i < H; ++i) sm = add2(sm, dz[i]);
+          const float2 s = cta_sum(make_float2(sum2(sm), sum2(sq)), red, turn, warps);
+          m1 = s.x * inv;
+          q1 = s.y * inv;
+        } else {
+          q1 = cta_sum(sum2(sq), red, turn, warps) * inv;
+        }
+        const Pair q = both(-q1), mm = both(-m1);
+#pragma unroll
+        for (int i = 0; i < H; ++i) dz[i] = mul2(add2(fma2(z[i], q, dz[i]), mm), rstd);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < H; ++i) dz[i] = zero;
+    }
+    // dz: the norm's share of g, the gradient at r'
+    if (b.dr_out != nullptr) {
+      row_of<RING, VEC, E, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, left, z);
+#pragma unroll
+      for (int i = 0; i < H; ++i) dz[i] = add2(dz[i], z[i]);
+    }
+    if constexpr (VEC == 4) {  // nothing past the row
+#pragma unroll
+      for (int i = 0; i < H; ++i)
+        if (64 * (i & ~1) >= left) dz[i] = zero;
+    } else {
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float2 v = split(dz[i]);
+        dz[i] = pair(64 * i < left ? v.x : 0.0f, 64 * i + 32 < left ? v.y : 0.0f);
       }
     }
-    if (normed) s1 = cta_sum2(s1, red, turn, warps);
-    const float m1 = f.pre == kLayer && normed ? s1.x * inv : 0.0f, q1 = normed ? s1.y * inv : 0.0f;
-    float2 s2 = make_float2(0.0f, 0.0f);
-    float row_alpha = 0.0f;
+    if (b.dres_scale != nullptr) {
+      row_of<RING, VEC, E, TS>(held, ring.r, f.r, f.ld_r, t, c, left, z);
+      Pair s = zero;
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int c = c0 + i * step;
-      if (c < D) {
-        float g[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) g[j] = 0.0f;
-        if (b.dr_out != nullptr) item<RING, VEC, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) g[j] = fmaf(dz[i][j] - z[i][j] * q1 - m1, pre.y, g[j]);
-        if (b.dres_scale != nullptr) {
-          float r[VEC];
-          item<RING, VEC, TS>(held, ring.r, f.r, f.ld_r, t, c, r);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) row_alpha = fmaf(g[j], r[j], row_alpha);
-        }
-        if (b.dr != nullptr) {
-          float v[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] = g[j] * alpha;
-          store_stream<VEC>(static_cast<TS*>(b.dr) + t * b.ld_dr + c, v);
-        }
-        if (block) {
-          float x[VEC], gv[VEC], w[VEC], bp[VEC];
-          item<RING, VEC, TB>(held, ring.o, f.o, f.ld_o, t, c, x);
-          if (gate != nullptr) load_param<VEC>(gate + c, gv);
-          if (f.w_post != nullptr) load_param<VEC>(f.w_post + c, w);
-          if (GATE && f.b_post != nullptr) load_param<VEC>(f.b_post + c, bp);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float zo = (x[j] - post.x) * post.y;
-            if constexpr (GATE) {
-              float n = f.w_post != nullptr ? zo * w[j] : zo;
-              if (f.b_post != nullptr) n += bp[j];
-              ag[i][j] = fmaf(g[j], n, ag[i][j]);
-            }
-            const float dn = gate != nullptr ? g[j] * gv[j] : g[j];
-            aw_post[i][j] = fmaf(dn, zo, aw_post[i][j]);
-            if constexpr (BIAS) ab_post[i][j] += dn;
-            z[i][j] = zo;
-            dz[i][j] = f.w_post != nullptr ? dn * w[j] : dn;
-            s2.x += dz[i][j];
-            s2.y = fmaf(dz[i][j], zo, s2.y);
-          }
-        }
-      }
-    }
-    {  // two-sum
-      const float sum = __fadd_rn(al_hi, row_alpha), part2 = __fsub_rn(sum, al_hi);
-      al_lo += __fadd_rn(__fsub_rn(al_hi, __fsub_rn(sum, part2)), __fsub_rn(row_alpha, part2));
+      for (int i = 0; i < H; ++i) s = fma2(dz[i], z[i], s);
+      const float a = sum2(s), sum = __fadd_rn(al_hi, a), took = __fsub_rn(sum, al_hi);  // two-sum
+      al_lo += __fadd_rn(__fsub_rn(al_hi, __fsub_rn(sum, took)), __fsub_rn(a, took));
       al_hi = sum;
     }
-    if (block && f.post != kNone && b.dO != nullptr && warps > 1)
-      s2 = cta_sum2(s2, red, turn, warps);
-    else {
-      s2 = warp_sum2(s2);  // (a CTA of one warp, or not needed)
-      if constexpr (RING) __syncthreads();
+    if (b.dr != nullptr) {
+      const Pair a = both(alpha);
+#pragma unroll
+      for (int i = 0; i < H; ++i) z[i] = mul2(dz[i], a);
+      R::store(static_cast<TS*>(b.dr) + t * b.ld_dr + c, left, z);
     }
-    // a barrier of this row is behind every read of its stage: the next row may land there
-    if (RING && threadIdx.x == 0 && t + ring.stages < t1) fetch(t + ring.stages);
-    if (b.dO != nullptr) {
-      const float m2 = f.post == kLayer ? s2.x * inv : 0.0f, q2 = f.post != kNone ? s2.y * inv : 0.0f;
+    float m2 = 0.0f, q2 = 0.0f;
+    if (block) {
+      row_of<RING, VEC, E, TB>(held, ring.o, f.o, f.ld_o, t, c, left, z);
+      if (f.post != kNone) {
+        if (f.post == kLayer) {
+          const Pair m = both(-post.x);
 #pragma unroll
-      for (int i = 0; i < I; ++i) {
-        const int c = c0 + i * step;
-        if (c < D) {
-          float v[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] = (dz[i][j] - z[i][j] * q2 - m2) * post.y;
-          store_stream<VEC>(static_cast<TB*>(b.dO) + t * b.ld_do + c, v);
+          for (int i = 0; i < H; ++i) z[i] = add2(z[i], m);
         }
+        const Pair rstd = both(post.y);
+#pragma unroll
+        for (int i = 0; i < H; ++i) z[i] = mul2(z[i], rstd);
       }
-    }
-    if constexpr (GATE) {
-      if (t + 1 == t1 || (t + 1) / f.gate_rows != grp) {
-        const bool whole = grp * f.gate_rows >= t0 && min((grp + 1) * f.gate_rows, f.tokens) <= t1;
-        float* to = whole ? b.dgate + grp * D : mine + (grp == t0 / f.gate_rows ? 4 : 5) * static_cast<int64_t>(D);
+      Pair w[H];
+      if (f.w_post != nullptr) R::template load<false>(f.w_post + c, left, w);
+      if (f.gate != nullptr) {
+        if constexpr (GATE) {
+          if (f.b_post != nullptr) {
+            Pair bp[H];
+            R::template load<false>(f.b_post + c, left, bp);
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-          const int c = c0 + i * step;
+            for (int i = 0; i < H; ++i) ag[i] = fma2(dz[i], f.w_post != nullptr ? fma2(z[i], w[i], bp[i]) : add2(z[i], bp[i]), ag[i]);
+          } else if (f.w_post != nullptr) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            if (c < D) to[c + j] = ag[i][j];
-            ag[i][j] = 0.0f;
+            for (int i = 0; i < H; ++i) ag[i] = fma2(dz[i], mul2(z[i], w[i]), ag[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < H; ++i) ag[i] = fma2(dz[i], z[i], ag[i]);
           }
         }
+        Pair g[H];
+        R::template load<false>(static_cast<const TB*>(f.gate) + grp * f.ld_gate + c, left, g);
+#pragma unroll
+        for (int i = 0; i < H; ++i) dz[i] = mul2(dz[i], g[i]);
+      }
+      // dz: dn
+#pragma unroll
+      for (int i = 0; i < H; ++i) aw_post[i] = fma2(dz[i], z[i], aw_post[i]);
+      if constexpr (BIAS) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) ab_post[i] = add2(ab_post[i], dz[i]);
+      }
+      if (f.w_post != nullptr) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) dz[i] = mul2(dz[i], w[i]);
+      }
+    }
+    if (block && f.post != kNone && b.dO != nullptr) {
+      Pair sq = zero;
+#pragma unroll
+      for (int i = 0; i < H; ++i) sq = fma2(dz[i], z[i], sq);
+      if (f.post == kLayer) {
+        Pair sm = zero;
+#pragma unroll
+        for (int i = 0; i < H; ++i) sm = add2(sm, dz[i]);
+        const float2 s = cta_sum(make_float2(sum2(sm), sum2(sq)), red, turn, warps);
+        m2 = s.x * inv;
+        q2 = s.y * inv;
+      } else {
+        q2 = cta_sum(sum2(sq), red, turn, warps) * inv;
+      }
+      if (RING && warps == 1) __syncwarp();
+    } else if constexpr (RING) {
+      __syncthreads();
+    }
+    if constexpr (RING) {
+      // a barrier of this row is behind every read of its stage: a later row may land there
+      if (threadIdx.x == 0 && t + ring.stages < t1) fetch(t + ring.stages, stage);
+      if (++stage == ring.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (b.dO != nullptr) {
+      if (f.post != kNone) {
+        const Pair q = both(-q2), mm = both(-m2), rstd = both(post.y);
+#pragma unroll
+        for (int i = 0; i < H; ++i) dz[i] = mul2(add2(fma2(z[i], q, dz[i]), mm), rstd);
+      }
+      R::store(static_cast<TB*>(b.dO) + t * b.ld_do + c, left, dz);
+    }
+    if constexpr (GATE) {
+      if (t + 1 == t1 || t + 1 == grp_end) {
+        const bool whole = grp_end - f.gate_rows >= t0 && min(grp_end, f.tokens) <= t1;
+        leave<VEC, E, false>((whole ? b.dgate + grp * D : mine + (grp == grp0 ? 4 : 5) * static_cast<int64_t>(D)) + c, left, ag);
+#pragma unroll
+        for (int i = 0; i < H; ++i) ag[i] = zero;
       }
     }
   }
@@ -353,18 +434,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     while (globaltimer_ns() - w0 < 200000ull) {
     }
   }
-  auto leave = [&](int k, const float(&a)[I][VEC]) {
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int c = c0 + i * step;
-      if (c < D) store_part<VEC>(mine + k * static_cast<int64_t>(D) + c, a[i]);
-    }
-  };
-  if (b.dw_pre != nullptr) leave(0, aw_pre);
-  if (b.dw_post != nullptr) leave(2, aw_post);
+  if (b.dw_pre != nullptr) leave<VEC, E, true>(mine + c, left, aw_pre);
+  if (b.dw_post != nullptr) leave<VEC, E, true>(mine + 2 * static_cast<int64_t>(D) + c, left, aw_post);
   if constexpr (BIAS) {
-    leave(1, ab_pre);
-    leave(3, ab_post);
+    leave<VEC, E, true>(mine + D + c, left, ab_pre);
+    leave<VEC, E, true>(mine + 3 * static_cast<int64_t>(D) + c, left, ab_post);
   }
   if (b.dres_scale != nullptr) {
     double a = static_cast<double>(al_hi) + static_cast<double>(al_lo);
@@ -439,11 +513,11 @@ struct BwdPlan {
   int64_t rows_per;
 };
 
-int items_of(int64_t width) { return width <= 2048 ? 2 : 4; }  // of 4 columns per thread
+int columns_of(int64_t width) { return width <= 2048 ? 8 : 16; }  // per thread
 
 BwdPlan bwd_plan(int64_t tokens, int64_t width) {
   BwdPlan p;
-  const int64_t per = 32 * 4 * items_of(width);
+  const int64_t per = 32 * columns_of(width);
   p.threads = width <= 8192 ? static_cast<int>((width + per - 1) / per) * 32 : kThreads;
   p.per_sm = p.threads >= 512 ? 1 : p.threads >= 256 ? 2 : 4;
   const int64_t most = static_cast<int64_t>(p.per_sm) * num_sms();
@@ -454,30 +528,30 @@ BwdPlan bwd_plan(int64_t tokens, int64_t width) {
 
 constexpr int kRingBytes = 216 * 1024;  // of an SM's shared memory
 
-template <typename TS, typename TB, int VEC, int I, bool RING, int WHAT>
+template <typename TS, typename TB, int VEC, int E, bool RING, int WHAT>
 cudaError_t launch_kernel(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
   if constexpr (RING) {
     static bool done[64] = {};  // the limit is per device; setting it twice is harmless
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
-      e = cudaFuncSetAttribute(norm_bwd_kernel<TS, TB, VEC, I, RING, WHAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+      e = cudaFuncSetAttribute(norm_bwd_kernel<TS, TB, VEC, E, RING, WHAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
       if (e == cudaSuccess && dev < 64) done[dev] = true;
     }
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(norm_bwd_kernel<TS, TB, VEC, I, RING, WHAT>, dim3(pl.ctas), dim3(pl.threads), RING ? ring.stages * ring.bytes : 0, stream, f, b, part,
+  return launch_pdl(norm_bwd_kernel<TS, TB, VEC, E, RING, WHAT>, dim3(pl.ctas), dim3(pl.threads), RING ? ring.stages * ring.bytes : 0, stream, f, b, part,
                     part_alpha, pl.rows_per, ring);
 }
 
-template <typename TS, typename TB, int VEC, int I, bool RING>
+template <typename TS, typename TB, int VEC, int E, bool RING>
 cudaError_t launch_what(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
   const bool bias = b.db_pre != nullptr || b.db_post != nullptr;
   if (b.dgate != nullptr)
-    return bias ? launch_kernel<TS, TB, VEC, I, RING, 2>(f, b, pl, part, part_alpha, ring, stream)
-                : launch_kernel<TS, TB, VEC, I, RING, 1>(f, b, pl, part, part_alpha, ring, stream);
-  return bias ? launch_kernel<TS, TB, VEC, I, RING, 3>(f, b, pl, part, part_alpha, ring, stream)
-              : launch_kernel<TS, TB, VEC, I, RING, 0>(f, b, pl, part, part_alpha, ring, stream);
+    return bias ? launch_kernel<TS, TB, VEC, E, RING, 2>(f, b, pl, part, part_alpha, ring, stream)
+                : launch_kernel<TS, TB, VEC, E, RING, 1>(f, b, pl, part, part_alpha, ring, stream);
+  return bias ? launch_kernel<TS, TB, VEC, E, RING, 3>(f, b, pl, part, part_alpha, ring, stream)
+              : launch_kernel<TS, TB, VEC, E, RING, 0>(f, b, pl, part, part_alpha, ring, stream);
 }
 
 template <typename TS, typename TB>
@@ -505,14 +579,14 @@ cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t st
     place(b.dres_scale != nullptr, f.r, f.ld_r, ss, ring.r);
     vec = vec && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) && rows_aligned(b.dr, b.ld_dr, ss, 4 * ss) && rows_aligned(b.dO, b.ld_do, bs, 4 * bs) &&
           rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16);
-    const bool two = items_of(f.width) == 2;
+    const bool eight = columns_of(f.width) == 8;
     if (vec) {
       const int64_t room = kRingBytes / pl.per_sm / ring.bytes;
       ring.stages = static_cast<int>(room < 1 ? 1 : room < kMaxStages ? room : kMaxStages);
-      e = two ? launch_what<TS, TB, 4, 2, true>(f, b, pl, part, part_alpha, ring, stream)
-              : launch_what<TS, TB, 4, 4, true>(f, b, pl, part, part_alpha, ring, stream);
+      e = eight ? launch_what<TS, TB, 4, 8, true>(f, b, pl, part, part_alpha, ring, stream)
+              : launch_what<TS, TB, 4, 16, true>(f, b, pl, part, part_alpha, ring, stream);
     } else {
-      e = two ? launch_what<TS, TB, 1, 8, false>(f, b, pl, part, part_alpha, ring, stream)
+      e = eight ? launch_what<TS, TB, 1, 8, false>(f, b, pl, part, part_alpha, ring, stream)
               : launch_what<TS, TB, 1, 16, false>(f, b, pl, part, part_alpha, ring, stream);
     }
   }

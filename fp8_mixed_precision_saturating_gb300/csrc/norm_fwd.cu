@@ -9,28 +9,28 @@ using namespace norms;
 
 // Mean and 1 / root of a row whose element c is value(c).
 template <typename F>
-__device__ __forceinline__ float2 row_stat(int kind, int64_t width, float eps, float2 (*red)[32], int& turn, F value) {
+__device__ __forceinline__ float2 row_stat(int kind, int64_t width, float eps, Red& red, int& turn, F value) {
   float2 st = make_float2(0.0f, 1.0f);
   if (kind == kNone) return st;
   const float n = static_cast<float>(width);
   if (kind == kLayer) {
     float a = 0.0f;
     for (int64_t c = threadIdx.x; c < width; c += kThreads) a += value(c);
-    st.x = cta_sum2(make_float2(a, 0.0f), red, turn, kThreads / 32).x / n;
+    st.x = cta_sum(a, red, turn, kThreads / 32) / n;
   }
   float a = 0.0f;
   for (int64_t c = threadIdx.x; c < width; c += kThreads) {
     const float z = value(c) - st.x;
     a = fmaf(z, z, a);
   }
-  st.y = 1.0f / sqrtf(cta_sum2(make_float2(a, 0.0f), red, turn, kThreads / 32).x / n + eps);
+  st.y = 1.0f / sqrtf(cta_sum(a, red, turn, kThreads / 32) / n + eps);
   return st;
 }
 
 // Any width and alignment: one CTA per token, the row read again for every pass over it.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f) {
-  __shared__ float2 red[2][32];
+  __shared__ Red red;
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -96,40 +96,69 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f)
 // ---------------------------------------------------------------------------------------
 // A row in the registers of its warps
 // ---------------------------------------------------------------------------------------
-// The row's elements are read once and stay in registers through both statistics. `blockDim.x / 32` warps share
-// a row, a lane holds I items of VEC consecutive elements (item i of thread x starts at column
-// (i blockDim.x + x) VEC, so every access of a warp is contiguous); a warp that holds a whole row needs no
-// barrier, and blockDim.y such rows share a CTA. The parameters come from L1, where the streamed rows do not
-// displace them.
-template <int VEC, int I>
-__device__ __forceinline__ float2 held_stat(int kind, int width, float eps, const float (&v)[I][VEC], float2 (*red)[32], int& turn) {
+// The row's elements are read once and stay in registers through both statistics; the parameters come from L1,
+// where the streamed rows do not displace them. `blockDim.x / 32` warps share a row; a warp that holds a whole row
+// needs no barrier, and blockDim.y such rows share a CTA.
+template <int VEC, int E>
+__device__ __forceinline__ float2 held_stat(int kind, int width, float eps, const Pair (&v)[E / 2], int left, Red& red, int& turn) {
   float2 st = make_float2(0.0f, 1.0f);
   if (kind == kNone) return st;
   const int warps = blockDim.x >> 5;
   const float n = static_cast<float>(width);
+  Pair q = both(0.0f);
   if (kind == kLayer) {
-    float a = 0.0f;
+    Pair a = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < I; ++i)  // (elements past the row are zero)
+    for (int i = 0; i < E / 2; ++i) a = add2(a, v[i]);  // (zero past the row)
+    st.x = cta_sum(sum2(a), red, turn, warps) / n;
+    const Pair m = both(-st.x);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a += v[i][j];
-    st.x = cta_sum2(make_float2(a, 0.0f), red, turn, warps).x / n;
-  }
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const bool in = static_cast<int>(i * blockDim.x + threadIdx.x) * VEC < width;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float z = in ? v[i][j] - st.x : 0.0f;
-      a = fmaf(z, z, a);
+    for (int i = 0; i < E / 2; ++i) {
+      Pair z = add2(v[i], m);
+      if constexpr (VEC == 4) {
+        if (64 * (i & ~1) >= left) z = both(0.0f);
+      } else {
+        const float2 t = split(z);
+        z = pair(64 * i < left ? t.x : 0.0f, 64 * i + 32 < left ? t.y : 0.0f);
+      }
+      q = fma2(z, z, q);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) q = fma2(v[i], v[i], q);
   }
-  st.y = 1.0f / sqrtf(cta_sum2(make_float2(a, 0.0f), red, turn, warps).x / n + eps);
+  st.y = 1.0f / sqrtf(cta_sum(sum2(q), red, turn, warps) / n + eps);
   return st;
 }
 
-// An item of h as 4-bit codes, with its group's scale (the group is 16 or 32 neighbouring elements, held by
+// x <- ((x - mean) rstd) w + b, the mean taken off before the scaling so that a large one does not cancel
+template <int VEC, int E>
+__device__ __forceinline__ void held_affine(Pair (&x)[E / 2], int kind, float2 st, const float* w, const float* b, int c, int left) {
+  if (kind == kNone) return;
+  const Pair rstd = both(st.y);
+  if (kind == kLayer) {
+    const Pair m = both(-st.x);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = mul2(add2(x[i], m), rstd);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], rstd);
+  }
+  if (w != nullptr) {
+    Pair p[E / 2];
+    Row<VEC, E>::template load<false>(w + c, left, p);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], p[i]);
+  }
+  if (b != nullptr) {
+    Pair p[E / 2];
+    Row<VEC, E>::template load<false>(b + c, left, p);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = add2(x[i], p[i]);
+  }
+}
+
+// VEC consecutive elements of h as 4-bit codes, with their group's scale (16 or 32 neighbouring elements, held by
 // neighbouring lanes, all of them in the row: width % 32 == 0).
 template <int FMT, int VEC>
 __device__ __forceinline__ void emit_codes(const NormFwd& f, const float (&h)[VEC], int64_t t, int c, float s, int64_t pitch, int64_t atoms) {
@@ -142,12 +171,11 @@ __device__ __forceinline__ void emit_codes(const NormFwd& f, const float (&h)[VE
   for (int o = 1; o < LANES; o <<= 1) a = max(a, __shfl_xor_sync(mask, a, o));
   float mul;
   const uint32_t b = fp4::group_scale<FMT>(a, s, mul);
-  const bool nan = b == fp4::F4<FMT>::kScaleNaN;
   float w[8] = {};
 #pragma unroll
   for (int j = 0; j < VEC; ++j) w[j] = __fmul_rn(h[j], mul);
   uint32_t codes = fp4::cvt8_e2m1(w);
-  if (nan) codes = 0;
+  if (b == fp4::F4<FMT>::kScaleNaN) codes = 0;
   if constexpr (VEC == 4) {
     *reinterpret_cast<uint16_t*>(f.hq + t * pitch + c / 2) = static_cast<uint16_t>(codes);
   } else {
@@ -162,9 +190,30 @@ __device__ __forceinline__ void emit_codes(const NormFwd& f, const float (&h)[VE
   }
 }
 
-template <typename TS, typename TB, int VEC, int I>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_ctas) {
-  __shared__ float2 red[2][32];
+template <int FMT, int VEC, int E>
+__device__ __forceinline__ void emit_row(const NormFwd& f, const Pair (&h)[E / 2], int64_t t, int c, int left) {
+  const float s = f.h_scale != nullptr ? __ldg(f.h_scale) : 1.0f;
+  const int64_t atoms = fp4::atoms_along(FMT, f.width), pitch = fp4::row_bytes(f.width);
+#pragma unroll
+  for (int i = 0; i < E / VEC; ++i) {
+    if (32 * VEC * i < left) {
+      float v[VEC];
+      if constexpr (VEC == 4) {
+        const float2 a = split(h[2 * i]), b = split(h[2 * i + 1]);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+      } else {
+        const float2 a = split(h[i / 2]);
+        v[0] = i & 1 ? a.y : a.x;
+      }
+      emit_codes<FMT, VEC>(f, v, t, c + 32 * VEC * i, s, pitch, atoms);
+    }
+  }
+}
+
+template <typename TS, typename TB, int VEC, int E>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_ctas, uint32_t gate_rows) {
+  using R = Row<VEC, E>;
+  __shared__ Red red;
   pdl_wait();
   pdl_trigger();
   if (static_cast<int>(blockIdx.x) >= row_ctas) {
@@ -176,89 +225,63 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_
       *reinterpret_cast<uint32_t*>(f.hsf + fp4::scale_offset(f.tokens + i / atoms, i % atoms * 4, atoms)) = f.h_fmt == 0 ? 0u : 0x7F7F7F7Fu;
     return;
   }
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= f.tokens) return;  // (a row of one warp: no barrier follows)
   int turn = 0;
-  const int D = static_cast<int>(f.width), step = blockDim.x * VEC, c0 = threadIdx.x * VEC;
+  const int D = static_cast<int>(f.width), c = R::first(threadIdx.x >> 5, threadIdx.x & 31), left = D - c;
   const float alpha = f.res_scale != nullptr ? __ldg(f.res_scale) : 1.0f;
-  const TS* r = static_cast<const TS*>(f.r) + t * f.ld_r;
-  float x[I][VEC], n[I][VEC];
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) x[i][j] = n[i][j] = 0.0f;
-    if (c0 + i * step < D) load_stream<VEC>(r + c0 + i * step, x[i]);
-  }
+  Pair x[E / 2];
+  R::template load<true>(static_cast<const TS*>(f.r) + t * f.ld_r + c, left, x);
   if (f.o != nullptr) {
-    const TB* o = static_cast<const TB*>(f.o) + t * f.ld_o;
-    const TB* gate = f.gate != nullptr ? static_cast<const TB*>(f.gate) + t / f.gate_rows * f.ld_gate : nullptr;
-#pragma unroll
-    for (int i = 0; i < I; ++i)
-      if (c0 + i * step < D) load_stream<VEC>(o + c0 + i * step, n[i]);
-    const float2 post = held_stat<VEC, I>(f.post, D, f.eps, n, red, turn);
+    Pair n[E / 2];
+    R::template load<true>(static_cast<const TB*>(f.o) + t * f.ld_o + c, left, n);
+    const float2 post = held_stat<VEC, E>(f.post, D, f.eps, n, left, red, turn);
     if (threadIdx.x == 0 && f.stat_post != nullptr) reinterpret_cast<float2*>(f.stat_post)[t] = post;
+    held_affine<VEC, E>(n, f.post, post, f.w_post, f.b_post, c, left);
+    const Pair a = both(alpha);
+    if (f.gate != nullptr) {
+      Pair g[E / 2];
+      R::template load<false>(static_cast<const TB*>(f.gate) + (t / gate_rows) * f.ld_gate + c, left, g);
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int c = c0 + i * step;
-      if (c >= D) break;
-      float w[VEC], b[VEC], g[VEC];
-      if (f.w_post != nullptr) load_param<VEC>(f.w_post + c, w);
-      if (f.b_post != nullptr) load_param<VEC>(f.b_post + c, b);
-      if (gate != nullptr) load_param<VEC>(gate + c, g);
+      for (int i = 0; i < E / 2; ++i) x[i] = fma2(g[i], n[i], mul2(x[i], a));
+    } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float z = (n[i][j] - post.x) * post.y;
-        if (f.w_post != nullptr) z *= w[j];
-        if (f.b_post != nullptr) z += b[j];
-        const float v = x[i][j] * alpha;
-        x[i][j] = gate != nullptr ? fmaf(g[j], z, v) : v + z;
-      }
+      for (int i = 0; i < E / 2; ++i) x[i] = fma2(x[i], a, n[i]);
     }
   } else {
     if (threadIdx.x == 0 && f.stat_post != nullptr) reinterpret_cast<float2*>(f.stat_post)[t] = make_float2(0.0f, 1.0f);
 #pragma unroll
-    for (int i = 0; i < I; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) x[i][j] *= alpha;
+    for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], both(alpha));
   }
-  if (f.r_out != nullptr) {  // (r may be r_out: every thread has read what it writes)
-    TS* out = static_cast<TS*>(f.r_out) + t * f.ld_r_out;
+  if constexpr (VEC == 4) {  // (an item past the row holds what its norm made of nothing)
 #pragma unroll
-    for (int i = 0; i < I; ++i)
-      if (c0 + i * step < D) store_stream<VEC>(out + c0 + i * step, x[i]);
+    for (int i = 0; i < E / 2; ++i)
+      if (64 * (i & ~1) >= left) x[i] = both(0.0f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 v = split(x[i]);
+      x[i] = pair(64 * i < left ? v.x : 0.0f, 64 * i + 32 < left ? v.y : 0.0f);
+    }
   }
-  const float2 pre = held_stat<VEC, I>(f.pre, D, f.eps, x, red, turn);
+  // (r may be r_out: every thread has read what it writes)
+  if (f.r_out != nullptr) R::store(static_cast<TS*>(f.r_out) + t * f.ld_r_out + c, left, x);
+  const float2 pre = held_stat<VEC, E>(f.pre, D, f.eps, x, left, red, turn);
   if (threadIdx.x == 0 && f.stat_pre != nullptr) reinterpret_cast<float2*>(f.stat_pre)[t] = pre;
   if (f.h == nullptr && f.hq == nullptr) return;
-  TB* h = static_cast<TB*>(f.h) + t * f.ld_h;
-  const float hs = f.hq != nullptr && f.h_scale != nullptr ? __ldg(f.h_scale) : 1.0f;
-  const int64_t atoms = fp4::atoms_along(f.h_fmt, D), pitch = fp4::row_bytes(D);
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = c0 + i * step;
-    if (c >= D) break;
-    float w[VEC], b[VEC], y[VEC];
-    if (f.w_pre != nullptr) load_param<VEC>(f.w_pre + c, w);
-    if (f.b_pre != nullptr) load_param<VEC>(f.b_pre + c, b);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      y[j] = (x[i][j] - pre.x) * pre.y;
-      if (f.w_pre != nullptr) y[j] *= w[j];
-      if (f.b_pre != nullptr) y[j] += b[j];
-    }
-    if (f.h != nullptr) store_stream<VEC>(h + c, y);
-    if (f.hq != nullptr) {
-      if (f.h_fmt == 0)
-        emit_codes<0, VEC>(f, y, t, c, hs, pitch, atoms);
-      else
-        emit_codes<1, VEC>(f, y, t, c, hs, pitch, atoms);
-    }
+  held_affine<VEC, E>(x, f.pre, pre, f.w_pre, f.b_pre, c, left);
+  if (f.h != nullptr) R::store(static_cast<TB*>(f.h) + t * f.ld_h + c, left, x);
+  if (f.hq != nullptr) {
+    if (f.h_fmt == 0)
+      emit_row<0, VEC, E>(f, x, t, c, left);
+    else
+      emit_row<1, VEC, E>(f, x, t, c, left);
   }
 }
 
-template <typename TS, typename TB, int VEC, int I>
+template <typename TS, typename TB, int VEC, int E>
 cudaError_t launch_rows(const NormFwd& f, cudaStream_t stream) {
-  const int warps = static_cast<int>((f.width + 32 * VEC * I - 1) / (32 * VEC * I));
+  const int warps = static_cast<int>((f.width + 32 * E - 1) / (32 * E));
   const int rows = warps == 1 ? 4 : 1;
   const int64_t row_ctas = (f.tokens + rows - 1) / rows;
   int64_t fill = 0;
@@ -266,8 +289,9 @@ cudaError_t launch_rows(const NormFwd& f, cudaStream_t stream) {
     const int64_t words = ((128 - (f.tokens & 127)) & 127) * fp4::atoms_along(f.h_fmt, f.width);
     fill = (words + 32 * warps * rows - 1) / (32 * warps * rows);
   }
-  return launch_pdl(norm_fwd_kernel<TS, TB, VEC, I>, dim3(static_cast<unsigned>(row_ctas + fill)), dim3(32 * warps, rows), 0, stream, f,
-                    static_cast<int>(row_ctas));
+  const uint32_t gate_rows = static_cast<uint32_t>(f.gate == nullptr || f.gate_rows > f.tokens ? f.tokens : f.gate_rows);
+  return launch_pdl(norm_fwd_kernel<TS, TB, VEC, E>, dim3(static_cast<unsigned>(row_ctas + fill)), dim3(32 * warps, rows), 0, stream, f,
+                    static_cast<int>(row_ctas), gate_rows);
 }
 
 template <typename TS, typename TB>
@@ -279,8 +303,8 @@ cudaError_t fwd_as(const NormFwd& f, cudaStream_t stream) {
   // 32 elements per lane keep enough loads in flight for the memory's rate; with no more rows than a few per
   // SM the latency counts instead, and a row is spread over four times the lanes
   const bool few = f.tokens <= 2ll * num_sms();
-  if (f.width <= 256 || (few && f.width <= 4096)) return vec ? launch_rows<TS, TB, 4, 2>(f, stream) : launch_rows<TS, TB, 1, 8>(f, stream);
-  if (f.width <= 16384) return vec ? launch_rows<TS, TB, 4, 8>(f, stream) : launch_rows<TS, TB, 1, 32>(f, stream);
+  if (f.width <= 256 || (few && f.width <= 4096)) return vec ? launch_rows<TS, TB, 4, 8>(f, stream) : launch_rows<TS, TB, 1, 8>(f, stream);
+  if (f.width <= 16384) return vec ? launch_rows<TS, TB, 4, 32>(f, stream) : launch_rows<TS, TB, 1, 32>(f, stream);
   const int64_t most = 8ll * num_sms();
   return launch_pdl(norm_fwd_any_kernel<TS, TB>, dim3(static_cast<unsigned>(f.tokens < most ? f.tokens : most)), dim3(kThreads), 0, stream, f);
 }
