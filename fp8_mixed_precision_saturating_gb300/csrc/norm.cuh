@@ -72,53 +72,68 @@ __device__ __forceinline__ uint32_t pack2(Pair p) {
 // How a row lies in its warps' registers: a warp holds 32 E consecutive columns, a lane E of them. VEC 4: items of 4
 // consecutive columns, item i of a lane 128 i columns after its first; VEC 1: element e 32 e columns after it. Either
 // way a warp's access is contiguous and an item's place a constant offset. `left`: columns from the lane's first one
-// to the row's end; what lies past it reads as `pad` and is not written.
-template <int VEC, int E>
+// to the row's end; what lies past it reads as zero and is not written. FULL: nothing lies past it (whole warps), so
+// nothing is checked.
+template <int VEC, int E, bool FULL>
 struct Row {
+  static __device__ __forceinline__ bool in(int at, int left) { return FULL || at < left; }
   static_assert(E % 4 == 0 && (VEC == 1 || VEC == 4), "items");
   static __device__ __forceinline__ int first(int warp, int lane) { return warp * 32 * E + lane * VEC; }
 
+  // what lies past the row becomes zero
+  static __device__ __forceinline__ void clear(Pair (&x)[E / 2], int left) {
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        if constexpr (VEC == 4) {
+          if (64 * (i & ~1) >= left) x[i] = both(0.0f);
+        } else {
+          const float2 v = split(x[i]);
+          x[i] = pair(64 * i < left ? v.x : 0.0f, 64 * i + 32 < left ? v.y : 0.0f);
+        }
+      }
+    }
+  }
+
   // stream: rows, read once (kept out of L1); otherwise parameters, which every row reads
   template <bool STREAM>
-  static __device__ __forceinline__ void load(const float* p, int left, Pair (&x)[E / 2], float pad = 0.0f) {
+  static __device__ __forceinline__ void load(const float* p, int left, Pair (&x)[E / 2]) {
     if constexpr (VEC == 4) {
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
-        x[2 * i] = x[2 * i + 1] = both(pad);
-        if (128 * i < left) {
-          const float4* at = reinterpret_cast<const float4*>(p + 128 * i);
-          const float4 t = STREAM ? __ldcs(at) : __ldg(at);
-          x[2 * i] = pair(t.x, t.y);
-          x[2 * i + 1] = pair(t.z, t.w);
-        }
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float4* at = reinterpret_cast<const float4*>(p + 128 * i);
+        if (in(128 * i, left)) t = STREAM ? __ldcs(at) : __ldg(at);
+        x[2 * i] = pair(t.x, t.y);
+        x[2 * i + 1] = pair(t.z, t.w);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        float lo = pad, hi = pad;
-        if (64 * e < left) lo = STREAM ? __ldcs(p + 64 * e) : __ldg(p + 64 * e);
-        if (64 * e + 32 < left) hi = STREAM ? __ldcs(p + 64 * e + 32) : __ldg(p + 64 * e + 32);
+        float lo = 0.0f, hi = 0.0f;
+        if (in(64 * e, left)) lo = STREAM ? __ldcs(p + 64 * e) : __ldg(p + 64 * e);
+        if (in(64 * e + 32, left)) hi = STREAM ? __ldcs(p + 64 * e + 32) : __ldg(p + 64 * e + 32);
         x[e] = pair(lo, hi);
       }
     }
   }
   template <bool STREAM>
-  static __device__ __forceinline__ void load(const bf16* p, int left, Pair (&x)[E / 2], float pad = 0.0f) {
+  static __device__ __forceinline__ void load(const bf16* p, int left, Pair (&x)[E / 2]) {
     if constexpr (VEC == 4) {
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
-        x[2 * i] = x[2 * i + 1] = both(pad);
-        if (128 * i < left) {
-          const uint2* at = reinterpret_cast<const uint2*>(p + 128 * i);
-          const uint2 t = STREAM ? __ldcs(at) : __ldg(at);
-          x[2 * i] = pair_of(t.x);
-          x[2 * i + 1] = pair_of(t.y);
-        }
+        uint2 t = make_uint2(0u, 0u);
+        const uint2* at = reinterpret_cast<const uint2*>(p + 128 * i);
+        if (in(128 * i, left)) t = STREAM ? __ldcs(at) : __ldg(at);
+        x[2 * i] = pair_of(t.x);
+        x[2 * i + 1] = pair_of(t.y);
       }
     } else {
       auto one = [&](int at) {
         const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + at;
-        return at < left ? __uint_as_float(static_cast<uint32_t>(STREAM ? __ldcs(q) : __ldg(q)) << 16) : pad;
+        uint32_t v = 0;
+        if (in(at, left)) v = STREAM ? __ldcs(q) : __ldg(q);
+        return __uint_as_float(v << 16);
       };
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) x[e] = pair(one(64 * e), one(64 * e + 32));
@@ -130,10 +145,10 @@ struct Row {
       const float2 a = split(x[e]);
       if constexpr (VEC == 4) {
         const float2 b = split(x[e + 1]);
-        if (64 * e < left) __stcs(reinterpret_cast<float4*>(p + 64 * e), make_float4(a.x, a.y, b.x, b.y));
+        if (in(64 * e, left)) __stcs(reinterpret_cast<float4*>(p + 64 * e), make_float4(a.x, a.y, b.x, b.y));
       } else {
-        if (64 * e < left) __stcs(p + 64 * e, a.x);
-        if (64 * e + 32 < left) __stcs(p + 64 * e + 32, a.y);
+        if (in(64 * e, left)) __stcs(p + 64 * e, a.x);
+        if (in(64 * e + 32, left)) __stcs(p + 64 * e + 32, a.y);
       }
     }
   }
@@ -141,11 +156,11 @@ struct Row {
 #pragma unroll
     for (int e = 0; e < E / 2; e += VEC == 4 ? 2 : 1) {
       if constexpr (VEC == 4) {
-        if (64 * e < left) __stcs(reinterpret_cast<uint2*>(p + 64 * e), make_uint2(pack2(x[e]), pack2(x[e + 1])));
+        if (in(64 * e, left)) __stcs(reinterpret_cast<uint2*>(p + 64 * e), make_uint2(pack2(x[e]), pack2(x[e + 1])));
       } else {
         const uint32_t w = pack2(x[e]);
-        if (64 * e < left) reinterpret_cast<uint16_t*>(p)[64 * e] = static_cast<uint16_t>(w);
-        if (64 * e + 32 < left) reinterpret_cast<uint16_t*>(p)[64 * e + 32] = static_cast<uint16_t>(w >> 16);
+        if (in(64 * e, left)) reinterpret_cast<uint16_t*>(p)[64 * e] = static_cast<uint16_t>(w);
+        if (in(64 * e + 32, left)) reinterpret_cast<uint16_t*>(p)[64 * e + 32] = static_cast<uint16_t>(w >> 16);
       }
     }
   }

@@ -135,7 +135,10 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
 // 16 bytes) or from global memory. A thread holds the same E columns of every row, so the column sums stay in its
 // registers over all of the CTA's tokens.
 //   pass 1: dz and z of the norm before the next block; its row sums; dw_pre, db_pre
-//   pass 2: g, so dr and dalpha; dn, dgate, dw_post, db_post; dz and z of the norm after the block; its row sums
+//   pass 2: g, so dr and dalpha; dz and z of the norm after the block; its row sums
+// dgate, dw_post and db_post are all made of sum g z and sum g over the rows that share a gate: with n = z w + b and
+// dn = gate g,  dgate = w sum g z + b sum g,  dw_post = sum over the gates of gate sum g z,  db_post likewise. So the
+// rows add to those two sums alone, and they are spent where the gate's row changes.
 //   pass 3: do
 constexpr int kMaxStages = 4;
 
@@ -145,38 +148,38 @@ struct Ring {
 };
 
 // A row's columns from the ring's copy, or from global memory.
-template <bool RING, int VEC, int E, typename T>
+template <bool RING, int VEC, int E, bool FULL, typename T>
 __device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* base, int64_t ld, int64_t t, int c, int left, Pair (&x)[E / 2]) {
   if constexpr (RING) {
     const T* p = reinterpret_cast<const T*>(held + at) + c;
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
-      x[2 * i] = x[2 * i + 1] = both(0.0f);
-      if (128 * i < left) {
-        if constexpr (sizeof(T) == 4) {
-          const float4 q = *reinterpret_cast<const float4*>(p + 128 * i);
-          x[2 * i] = pair(q.x, q.y);
-          x[2 * i + 1] = pair(q.z, q.w);
-        } else {
-          const uint2 q = *reinterpret_cast<const uint2*>(p + 128 * i);
-          x[2 * i] = pair_of(q.x);
-          x[2 * i + 1] = pair_of(q.y);
-        }
+      const bool in = FULL || 128 * i < left;
+      if constexpr (sizeof(T) == 4) {
+        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in) q = *reinterpret_cast<const float4*>(p + 128 * i);
+        x[2 * i] = pair(q.x, q.y);
+        x[2 * i + 1] = pair(q.z, q.w);
+      } else {
+        uint2 q = make_uint2(0u, 0u);
+        if (in) q = *reinterpret_cast<const uint2*>(p + 128 * i);
+        x[2 * i] = pair_of(q.x);
+        x[2 * i + 1] = pair_of(q.y);
       }
     }
   } else {
-    Row<VEC, E>::template load<true>(static_cast<const T*>(base) + t * ld + c, left, x);
+    Row<VEC, E, FULL>::template load<true>(static_cast<const T*>(base) + t * ld + c, left, x);
   }
 }
 
 // Column sums to the workspace or to dgate (aligned to 4 bytes only).
-template <int VEC, int E, bool WIDE>
+template <int VEC, int E, bool FULL, bool WIDE>
 __device__ __forceinline__ void leave(float* p, int left, const Pair (&x)[E / 2]) {
   if constexpr (VEC == 4 && !WIDE) {
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
       const float2 a = split(x[2 * i]), b = split(x[2 * i + 1]);
-      if (128 * i < left) {
+      if (FULL || 128 * i < left) {
         p[128 * i] = a.x;
         p[128 * i + 1] = a.y;
         p[128 * i + 2] = b.x;
@@ -184,26 +187,27 @@ __device__ __forceinline__ void leave(float* p, int left, const Pair (&x)[E / 2]
       }
     }
   } else {
-    Row<VEC, E>::store(p, left, x);
+    Row<VEC, E, FULL>::store(p, left, x);
   }
 }
 
-// WHAT: 0 weights' sums only, 1 the gate's too, 2 the gate's and the biases', 3 the biases'.
-template <typename TS, typename TB, int VEC, int E, bool RING, int WHAT>
+// SUM: sum dh and sum g are wanted (a bias's gradient, or the gate's where there is a bias).
+template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING, bool SUM>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per, const Ring ring) {
-  using R = Row<VEC, E>;
-  constexpr bool GATE = WHAT == 1 || WHAT == 2, BIAS = WHAT >= 2;
+  using R = Row<VEC, E, FULL>;
   constexpr int H = E / 2;
   extern __shared__ __align__(16) uint8_t rows_smem[];
   __shared__ Red red;
   __shared__ double red_alpha[16];
   __shared__ __align__(8) uint64_t bars[kMaxStages];
+  __shared__ volatile int failed[2];  // rows in turn, so that no wait of the next row is taken for this one's
   const int D = static_cast<int>(f.width), warps = blockDim.x >> 5, c = R::first(threadIdx.x >> 5, threadIdx.x & 31), left = D - c;
   const int64_t t0 = blockIdx.x * rows_per, t1 = min(t0 + rows_per, f.tokens);
   const uint32_t bar0 = smem_u32(bars);
   if constexpr (RING) {
     if (threadIdx.x == 0) {
       for (int s = 0; s < ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+      failed[0] = failed[1] = 0;
       fence_mbar_init();
     }
     __syncthreads();
@@ -227,14 +231,14 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
   int turn = 0, stage = 0;
   uint32_t phase = 0;
   const float alpha = f.res_scale != nullptr ? __ldg(f.res_scale) : 1.0f, inv = 1.0f / static_cast<float>(D);
-  Pair aw_pre[H], aw_post[H], ag[GATE ? H : 1], ab_pre[BIAS ? H : 1], ab_post[BIAS ? H : 1];
+  Pair aw_pre[H], agz[H], ab_pre[SUM ? H : 1], ag[SUM ? H : 1];
   const Pair zero = both(0.0f);
 #pragma unroll
   for (int i = 0; i < H; ++i) {
-    aw_pre[i] = aw_post[i] = zero;
-    if constexpr (GATE) ag[i] = zero;
-    if constexpr (BIAS) ab_pre[i] = ab_post[i] = zero;
+    aw_pre[i] = agz[i] = zero;
+    if constexpr (SUM) ab_pre[i] = ag[i] = zero;
   }
+  bool spent = false;  // this CTA's rows of dw_post and db_post hold earlier gates' shares
   // sum g r cancels (its terms have both signs), so the rounding of its running sum is kept: hi + lo
   float al_hi = 0.0f, al_lo = 0.0f;
   const bool back = b.dh != nullptr, normed = back && f.pre != kNone, block = f.o != nullptr;
@@ -245,13 +249,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     grp_end = (grp + 1) * f.gate_rows;
   }
   const int64_t grp0 = grp;
-  bool ok = true;
+  bool stop = false;
   for (int64_t t = t0; t < t1; ++t) {
     const uint8_t* held = nullptr;
     if constexpr (RING) {
-      ok = mbar_wait(bar0 + 8 * stage, phase, f.w, DEV_ERR_WAIT_PRODUCER);
-      ok = __syncthreads_or(!ok) == 0;
-      if (!ok) break;  // a wait ran out: the CTA stops together
+      // a wait that ran out is looked at behind this row's barrier, so that the CTA stops together
+      if (!mbar_wait(bar0 + 8 * stage, phase, f.w, DEV_ERR_WAIT_PRODUCER)) failed[(t - t0) & 1] = 1;
       held = rows_smem + stage * ring.bytes;
     }
     if (f.gate != nullptr && t == grp_end) {
@@ -263,13 +266,13 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     Pair dz[H], z[H];
     float m1 = 0.0f, q1 = 0.0f;
     if (back) {
-      row_of<RING, VEC, E, TB>(held, ring.dh, b.dh, b.ld_dh, t, c, left, dz);
-      if constexpr (BIAS) {
+      row_of<RING, VEC, E, FULL, TB>(held, ring.dh, b.dh, b.ld_dh, t, c, left, dz);
+      if constexpr (SUM) {
 #pragma unroll
         for (int i = 0; i < H; ++i) ab_pre[i] = add2(ab_pre[i], dz[i]);
       }
       if (normed) {
-        row_of<RING, VEC, E, TS>(held, ring.r_out, f.r_out, f.ld_r_out, t, c, left, z);
+        row_of<RING, VEC, E, FULL, TS>(held, ring.r_out, f.r_out, f.ld_r_out, t, c, left, z);
         const Pair m = both(-pre.x), rstd = both(pre.y);
         if (f.pre == kLayer) {
 #pragma unroll
@@ -309,23 +312,13 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     }
     // dz: the norm's share of g, the gradient at r'
     if (b.dr_out != nullptr) {
-      row_of<RING, VEC, E, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, left, z);
+      row_of<RING, VEC, E, FULL, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, left, z);
 #pragma unroll
       for (int i = 0; i < H; ++i) dz[i] = add2(dz[i], z[i]);
     }
-    if constexpr (VEC == 4) {  // nothing past the row
-#pragma unroll
-      for (int i = 0; i < H; ++i)
-        if (64 * (i & ~1) >= left) dz[i] = zero;
-    } else {
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const float2 v = split(dz[i]);
-        dz[i] = pair(64 * i < left ? v.x : 0.0f, 64 * i + 32 < left ? v.y : 0.0f);
-      }
-    }
+    R::clear(dz, left);
     if (b.dres_scale != nullptr) {
-      row_of<RING, VEC, E, TS>(held, ring.r, f.r, f.ld_r, t, c, left, z);
+      row_of<RING, VEC, E, FULL, TS>(held, ring.r, f.r, f.ld_r, t, c, left, z);
       Pair s = zero;
 #pragma unroll
       for (int i = 0; i < H; ++i) s = fma2(dz[i], z[i], s);
@@ -341,7 +334,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     }
     float m2 = 0.0f, q2 = 0.0f;
     if (block) {
-      row_of<RING, VEC, E, TB>(held, ring.o, f.o, f.ld_o, t, c, left, z);
+      row_of<RING, VEC, E, FULL, TB>(held, ring.o, f.o, f.ld_o, t, c, left, z);
       if (f.post != kNone) {
         if (f.post == kLayer) {
           const Pair m = both(-post.x);
@@ -352,36 +345,21 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
 #pragma unroll
         for (int i = 0; i < H; ++i) z[i] = mul2(z[i], rstd);
       }
-      Pair w[H];
-      if (f.w_post != nullptr) R::template load<false>(f.w_post + c, left, w);
+#pragma unroll
+      for (int i = 0; i < H; ++i) agz[i] = fma2(dz[i], z[i], agz[i]);
+      if constexpr (SUM) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) ag[i] = add2(ag[i], dz[i]);
+      }
       if (f.gate != nullptr) {
-        if constexpr (GATE) {
-          if (f.b_post != nullptr) {
-            Pair bp[H];
-            R::template load<false>(f.b_post + c, left, bp);
-#pragma unroll
-            for (int i = 0; i < H; ++i) ag[i] = fma2(dz[i], f.w_post != nullptr ? fma2(z[i], w[i], bp[i]) : add2(z[i], bp[i]), ag[i]);
-          } else if (f.w_post != nullptr) {
-#pragma unroll
-            for (int i = 0; i < H; ++i) ag[i] = fma2(dz[i], mul2(z[i], w[i]), ag[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < H; ++i) ag[i] = fma2(dz[i], z[i], ag[i]);
-          }
-        }
         Pair g[H];
         R::template load<false>(static_cast<const TB*>(f.gate) + grp * f.ld_gate + c, left, g);
 #pragma unroll
         for (int i = 0; i < H; ++i) dz[i] = mul2(dz[i], g[i]);
       }
-      // dz: dn
-#pragma unroll
-      for (int i = 0; i < H; ++i) aw_post[i] = fma2(dz[i], z[i], aw_post[i]);
-      if constexpr (BIAS) {
-#pragma unroll
-        for (int i = 0; i < H; ++i) ab_post[i] = add2(ab_post[i], dz[i]);
-      }
       if (f.w_post != nullptr) {
+        Pair w[H];
+        R::template load<false>(f.w_post + c, left, w);
 #pragma unroll
         for (int i = 0; i < H; ++i) dz[i] = mul2(dz[i], w[i]);
       }
@@ -400,12 +378,14 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
       } else {
         q2 = cta_sum(sum2(sq), red, turn, warps) * inv;
       }
-      if (RING && warps == 1) __syncwarp();
+      if (RING && warps == 1) __syncthreads();  // (its sum needs no barrier, its stage does)
     } else if constexpr (RING) {
       __syncthreads();
     }
     if constexpr (RING) {
       // a barrier of this row is behind every read of its stage: a later row may land there
+      stop = failed[(t - t0) & 1] != 0;
+      if (stop) break;
       if (threadIdx.x == 0 && t + ring.stages < t1) fetch(t + ring.stages, stage);
       if (++stage == ring.stages) {
         stage = 0;
@@ -420,26 +400,63 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
       }
       R::store(static_cast<TB*>(b.dO) + t * b.ld_do + c, left, dz);
     }
-    if constexpr (GATE) {
-      if (t + 1 == t1 || t + 1 == grp_end) {
+    if (block && (t + 1 == t1 || (f.gate != nullptr && t + 1 == grp_end))) {
+      if (b.dgate != nullptr) {
         const bool whole = grp_end - f.gate_rows >= t0 && min(grp_end, f.tokens) <= t1;
-        leave<VEC, E, false>((whole ? b.dgate + grp * D : mine + (grp == grp0 ? 4 : 5) * static_cast<int64_t>(D)) + c, left, ag);
+        Pair v[H];
 #pragma unroll
-        for (int i = 0; i < H; ++i) ag[i] = zero;
+        for (int i = 0; i < H; ++i) v[i] = agz[i];
+        if (f.w_post != nullptr) {
+          R::template load<false>(f.w_post + c, left, v);
+#pragma unroll
+          for (int i = 0; i < H; ++i) v[i] = mul2(v[i], agz[i]);
+        }
+        if constexpr (SUM) {
+          if (f.b_post != nullptr) {
+            Pair p[H];
+            R::template load<false>(f.b_post + c, left, p);
+#pragma unroll
+            for (int i = 0; i < H; ++i) v[i] = fma2(p[i], ag[i], v[i]);
+          }
+        }
+        leave<VEC, E, FULL, false>((whole ? b.dgate + grp * D : mine + (grp == grp0 ? 4 : 5) * static_cast<int64_t>(D)) + c, left, v);
+      }
+      auto spend = [&](int k, Pair(&a)[H]) {  // gate times the sum, onto what earlier gates left
+        Pair v[H];
+        float* p = mine + k * static_cast<int64_t>(D) + c;
+        if (f.gate != nullptr) {
+          R::template load<false>(static_cast<const TB*>(f.gate) + grp * f.ld_gate + c, left, v);
+#pragma unroll
+          for (int i = 0; i < H; ++i) a[i] = mul2(a[i], v[i]);
+        }
+        if (spent) {
+          R::template load<true>(p, left, v);
+#pragma unroll
+          for (int i = 0; i < H; ++i) a[i] = add2(a[i], v[i]);
+        }
+        leave<VEC, E, FULL, true>(p, left, a);
+#pragma unroll
+        for (int i = 0; i < H; ++i) a[i] = zero;
+      };
+      if (b.dw_post != nullptr) spend(2, agz);
+      if constexpr (SUM) {
+        if (b.db_post != nullptr) spend(3, ag);
+      }
+      spent = true;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        agz[i] = zero;
+        if constexpr (SUM) ag[i] = zero;
       }
     }
   }
-  if (RING && !ok && threadIdx.x == 0) {  // copies in flight land (microseconds) before the CTA can exit
+  if (RING && threadIdx.x == 0 && stop) {  // copies in flight land (microseconds) before the CTA can exit
     const unsigned long long w0 = globaltimer_ns();
     while (globaltimer_ns() - w0 < 200000ull) {
     }
   }
-  if (b.dw_pre != nullptr) leave<VEC, E, true>(mine + c, left, aw_pre);
-  if (b.dw_post != nullptr) leave<VEC, E, true>(mine + 2 * static_cast<int64_t>(D) + c, left, aw_post);
-  if constexpr (BIAS) {
-    leave<VEC, E, true>(mine + D + c, left, ab_pre);
-    leave<VEC, E, true>(mine + 3 * static_cast<int64_t>(D) + c, left, ab_post);
-  }
+  if (b.dw_pre != nullptr) leave<VEC, E, FULL, true>(mine + c, left, aw_pre);
+  if constexpr (SUM) leave<VEC, E, FULL, true>(mine + D + c, left, ab_pre);
   if (b.dres_scale != nullptr) {
     double a = static_cast<double>(al_hi) + static_cast<double>(al_lo);
 #pragma unroll
@@ -455,7 +472,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
 
 // Column sums over CTAs' partial rows: 32 columns per CTA; its 8 warps take consecutive ranges of the
 // partial rows, and their sums are added in warp order. blockIdx.y 0 .. 3: the parameters (and alpha);
-// 3 + p for p >= 1: the gate group that CTAs p - 1 and p share, if CTA p - 1 holds its first token.
+// from 4 on: the gate groups that several CTAs share.
 __global__ void __launch_bounds__(kThreads) norm_bwd_reduce_kernel(const NormFwd f, const NormBwd b, const float* part,
                                                                    const double* part_alpha, int64_t rows_per, int ctas) {
   __shared__ float sums[8][32];
@@ -499,12 +516,15 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_reduce_kernel(const NormFwd
     }
     return;
   }
-  const int p = static_cast<int>(blockIdx.y) - 3;
-  const int64_t first = p * rows_per;  // CTA p's first token
-  const int64_t grp = first / f.gate_rows, ga = grp * f.gate_rows, ge = min(ga + f.gate_rows, f.tokens);
-  if (ga == first || ga / rows_per != p - 1) return;
-  const int last = static_cast<int>((ge - 1) / rows_per);
-  add(p - 1, last + 1, [=](int q) { return static_cast<int64_t>(q) * kPart + (q * rows_per / f.gate_rows == grp ? 4 : 5); }, b.dgate + grp * D);
+  // by groups where they are fewer than the CTAs, else by the CTAs' borders
+  const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
+  const bool by_group = groups < ctas;
+  for (int64_t i = blockIdx.y - 4; i < (by_group ? groups : ctas - 1); i += gridDim.y - 4) {
+    const int64_t grp = by_group ? i : (i + 1) * rows_per / f.gate_rows, ga = grp * f.gate_rows, ge = min(ga + f.gate_rows, f.tokens);
+    const int first = static_cast<int>(ga / rows_per), last = static_cast<int>((ge - 1) / rows_per);
+    if (first == last || (!by_group && first != i)) continue;  // one CTA's alone, or another border's
+    add(first, last + 1, [=](int q) { return static_cast<int64_t>(q) * kPart + (q * rows_per / f.gate_rows == grp ? 4 : 5); }, b.dgate + grp * D);
+  }
 }
 
 // The split of the tokens, from the sizes alone: CTAs of a row each, enough per SM for some 512 threads.
@@ -528,30 +548,27 @@ BwdPlan bwd_plan(int64_t tokens, int64_t width) {
 
 constexpr int kRingBytes = 216 * 1024;  // of an SM's shared memory
 
-template <typename TS, typename TB, int VEC, int E, bool RING, int WHAT>
+template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING, bool SUM>
 cudaError_t launch_kernel(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
   if constexpr (RING) {
     static bool done[64] = {};  // the limit is per device; setting it twice is harmless
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
-      e = cudaFuncSetAttribute(norm_bwd_kernel<TS, TB, VEC, E, RING, WHAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+      e = cudaFuncSetAttribute(norm_bwd_kernel<TS, TB, VEC, E, FULL, RING, SUM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
       if (e == cudaSuccess && dev < 64) done[dev] = true;
     }
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(norm_bwd_kernel<TS, TB, VEC, E, RING, WHAT>, dim3(pl.ctas), dim3(pl.threads), RING ? ring.stages * ring.bytes : 0, stream, f, b, part,
+  return launch_pdl(norm_bwd_kernel<TS, TB, VEC, E, FULL, RING, SUM>, dim3(pl.ctas), dim3(pl.threads), RING ? ring.stages * ring.bytes : 0, stream, f, b, part,
                     part_alpha, pl.rows_per, ring);
 }
 
-template <typename TS, typename TB, int VEC, int E, bool RING>
-cudaError_t launch_what(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
-  const bool bias = b.db_pre != nullptr || b.db_post != nullptr;
-  if (b.dgate != nullptr)
-    return bias ? launch_kernel<TS, TB, VEC, E, RING, 2>(f, b, pl, part, part_alpha, ring, stream)
-                : launch_kernel<TS, TB, VEC, E, RING, 1>(f, b, pl, part, part_alpha, ring, stream);
-  return bias ? launch_kernel<TS, TB, VEC, E, RING, 3>(f, b, pl, part, part_alpha, ring, stream)
-              : launch_kernel<TS, TB, VEC, E, RING, 0>(f, b, pl, part, part_alpha, ring, stream);
+template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING>
+cudaError_t launch_sums(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
+  if (b.db_pre != nullptr || b.db_post != nullptr || (b.dgate != nullptr && f.b_post != nullptr))
+    return launch_kernel<TS, TB, VEC, E, FULL, RING, true>(f, b, pl, part, part_alpha, ring, stream);
+  return launch_kernel<TS, TB, VEC, E, FULL, RING, false>(f, b, pl, part, part_alpha, ring, stream);
 }
 
 template <typename TS, typename TB>
@@ -583,16 +600,23 @@ cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t st
     if (vec) {
       const int64_t room = kRingBytes / pl.per_sm / ring.bytes;
       ring.stages = static_cast<int>(room < 1 ? 1 : room < kMaxStages ? room : kMaxStages);
-      e = eight ? launch_what<TS, TB, 4, 8, true>(f, b, pl, part, part_alpha, ring, stream)
-              : launch_what<TS, TB, 4, 16, true>(f, b, pl, part, part_alpha, ring, stream);
+      const bool full = f.width % (eight ? 256 : 512) == 0;
+      e = eight ? (full ? launch_sums<TS, TB, 4, 8, true, true>(f, b, pl, part, part_alpha, ring, stream)
+                        : launch_sums<TS, TB, 4, 8, false, true>(f, b, pl, part, part_alpha, ring, stream))
+                : (full ? launch_sums<TS, TB, 4, 16, true, true>(f, b, pl, part, part_alpha, ring, stream)
+                        : launch_sums<TS, TB, 4, 16, false, true>(f, b, pl, part, part_alpha, ring, stream));
     } else {
-      e = eight ? launch_what<TS, TB, 1, 8, false>(f, b, pl, part, part_alpha, ring, stream)
-              : launch_what<TS, TB, 1, 16, false>(f, b, pl, part, part_alpha, ring, stream);
+      e = eight ? launch_sums<TS, TB, 1, 8, false, false>(f, b, pl, part, part_alpha, ring, stream)
+              : launch_sums<TS, TB, 1, 16, false, false>(f, b, pl, part, part_alpha, ring, stream);
     }
   }
   if (e != cudaSuccess) return e;
-  const bool split = b.dgate != nullptr && pl.ctas > 1;
-  const dim3 grid(static_cast<unsigned>((f.width + 31) / 32), 4u + (split ? static_cast<unsigned>(pl.ctas - 1) : 0u));
+  int64_t shared = 0;  // gate groups that may be shared
+  if (b.dgate != nullptr && pl.ctas > 1) {
+    const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
+    shared = groups < pl.ctas ? groups : pl.ctas - 1;
+  }
+  const dim3 grid(static_cast<unsigned>((f.width + 31) / 32), static_cast<unsigned>(4 + (shared < 32 ? shared : 32)));
   return launch_pdl(norm_bwd_reduce_kernel, grid, dim3(kThreads), 0, stream, f, b, part, part_alpha, pl.rows_per, pl.ctas);
 }
 

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f)
 // The row's elements are read once and stay in registers through both statistics; the parameters come from L1,
 // where the streamed rows do not displace them. `blockDim.x / 32` warps share a row; a warp that holds a whole row
 // needs no barrier, and blockDim.y such rows share a CTA.
-template <int VEC, int E>
+template <int VEC, int E, bool FULL>
 __device__ __forceinline__ float2 held_stat(int kind, int width, float eps, const Pair (&v)[E / 2], int left, Red& red, int& turn) {
   float2 st = make_float2(0.0f, 1.0f);
   if (kind == kNone) return st;
@@ -112,17 +112,12 @@ __device__ __forceinline__ float2 held_stat(int kind, int width, float eps, cons
     for (int i = 0; i < E / 2; ++i) a = add2(a, v[i]);  // (zero past the row)
     st.x = cta_sum(sum2(a), red, turn, warps) / n;
     const Pair m = both(-st.x);
+    Pair z[E / 2];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      Pair z = add2(v[i], m);
-      if constexpr (VEC == 4) {
-        if (64 * (i & ~1) >= left) z = both(0.0f);
-      } else {
-        const float2 t = split(z);
-        z = pair(64 * i < left ? t.x : 0.0f, 64 * i + 32 < left ? t.y : 0.0f);
-      }
-      q = fma2(z, z, q);
-    }
+    for (int i = 0; i < E / 2; ++i) z[i] = add2(v[i], m);
+    Row<VEC, E, FULL>::clear(z, left);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) q = fma2(z[i], z[i], q);
   } else {
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) q = fma2(v[i], v[i], q);
@@ -132,7 +127,7 @@ __device__ __forceinline__ float2 held_stat(int kind, int width, float eps, cons
 }
 
 // x <- ((x - mean) rstd) w + b, the mean taken off before the scaling so that a large one does not cancel
-template <int VEC, int E>
+template <int VEC, int E, bool FULL>
 __device__ __forceinline__ void held_affine(Pair (&x)[E / 2], int kind, float2 st, const float* w, const float* b, int c, int left) {
   if (kind == kNone) return;
   const Pair rstd = both(st.y);
@@ -146,13 +141,13 @@ __device__ __forceinline__ void held_affine(Pair (&x)[E / 2], int kind, float2 s
   }
   if (w != nullptr) {
     Pair p[E / 2];
-    Row<VEC, E>::template load<false>(w + c, left, p);
+    Row<VEC, E, FULL>::template load<false>(w + c, left, p);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], p[i]);
   }
   if (b != nullptr) {
     Pair p[E / 2];
-    Row<VEC, E>::template load<false>(b + c, left, p);
+    Row<VEC, E, FULL>::template load<false>(b + c, left, p);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) x[i] = add2(x[i], p[i]);
   }
@@ -210,9 +205,9 @@ __device__ __forceinline__ void emit_row(const NormFwd& f, const Pair (&h)[E / 2
   }
 }
 
-template <typename TS, typename TB, int VEC, int E>
+template <typename TS, typename TB, int VEC, int E, bool FULL>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_ctas, uint32_t gate_rows) {
-  using R = Row<VEC, E>;
+  using R = Row<VEC, E, FULL>;
   __shared__ Red red;
   pdl_wait();
   pdl_trigger();
@@ -235,9 +230,9 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_
   if (f.o != nullptr) {
     Pair n[E / 2];
     R::template load<true>(static_cast<const TB*>(f.o) + t * f.ld_o + c, left, n);
-    const float2 post = held_stat<VEC, E>(f.post, D, f.eps, n, left, red, turn);
+    const float2 post = held_stat<VEC, E, FULL>(f.post, D, f.eps, n, left, red, turn);
     if (threadIdx.x == 0 && f.stat_post != nullptr) reinterpret_cast<float2*>(f.stat_post)[t] = post;
-    held_affine<VEC, E>(n, f.post, post, f.w_post, f.b_post, c, left);
+    held_affine<VEC, E, FULL>(n, f.post, post, f.w_post, f.b_post, c, left);
     const Pair a = both(alpha);
     if (f.gate != nullptr) {
       Pair g[E / 2];
@@ -253,23 +248,13 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], both(alpha));
   }
-  if constexpr (VEC == 4) {  // (an item past the row holds what its norm made of nothing)
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i)
-      if (64 * (i & ~1) >= left) x[i] = both(0.0f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 v = split(x[i]);
-      x[i] = pair(64 * i < left ? v.x : 0.0f, 64 * i + 32 < left ? v.y : 0.0f);
-    }
-  }
+  R::clear(x, left);  // (past the row: what the norm made of nothing)
   // (r may be r_out: every thread has read what it writes)
   if (f.r_out != nullptr) R::store(static_cast<TS*>(f.r_out) + t * f.ld_r_out + c, left, x);
-  const float2 pre = held_stat<VEC, E>(f.pre, D, f.eps, x, left, red, turn);
+  const float2 pre = held_stat<VEC, E, FULL>(f.pre, D, f.eps, x, left, red, turn);
   if (threadIdx.x == 0 && f.stat_pre != nullptr) reinterpret_cast<float2*>(f.stat_pre)[t] = pre;
   if (f.h == nullptr && f.hq == nullptr) return;
-  held_affine<VEC, E>(x, f.pre, pre, f.w_pre, f.b_pre, c, left);
+  held_affine<VEC, E, FULL>(x, f.pre, pre, f.w_pre, f.b_pre, c, left);
   if (f.h != nullptr) R::store(static_cast<TB*>(f.h) + t * f.ld_h + c, left, x);
   if (f.hq != nullptr) {
     if (f.h_fmt == 0)
@@ -279,7 +264,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_
   }
 }
 
-template <typename TS, typename TB, int VEC, int E>
+template <typename TS, typename TB, int VEC, int E, bool FULL>
 cudaError_t launch_rows(const NormFwd& f, cudaStream_t stream) {
   const int warps = static_cast<int>((f.width + 32 * E - 1) / (32 * E));
   const int rows = warps == 1 ? 4 : 1;
@@ -290,7 +275,7 @@ cudaError_t launch_rows(const NormFwd& f, cudaStream_t stream) {
     fill = (words + 32 * warps * rows - 1) / (32 * warps * rows);
   }
   const uint32_t gate_rows = static_cast<uint32_t>(f.gate == nullptr || f.gate_rows > f.tokens ? f.tokens : f.gate_rows);
-  return launch_pdl(norm_fwd_kernel<TS, TB, VEC, E>, dim3(static_cast<unsigned>(row_ctas + fill)), dim3(32 * warps, rows), 0, stream, f,
+  return launch_pdl(norm_fwd_kernel<TS, TB, VEC, E, FULL>, dim3(static_cast<unsigned>(row_ctas + fill)), dim3(32 * warps, rows), 0, stream, f,
                     static_cast<int>(row_ctas), gate_rows);
 }
 
@@ -300,11 +285,18 @@ cudaError_t fwd_as(const NormFwd& f, cudaStream_t stream) {
   const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.ld_r_out, ss, 4 * ss) &&
                    rows_aligned(f.o, f.ld_o, bs, 4 * bs) && rows_aligned(f.h, f.ld_h, bs, 4 * bs) && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) &&
                    rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16) && rows_aligned(f.b_pre, 0, 4, 16);
-  // 32 elements per lane keep enough loads in flight for the memory's rate; with no more rows than a few per
-  // SM the latency counts instead, and a row is spread over four times the lanes
+  // 16 elements per lane keep enough loads in flight for the memory's rate; with no more rows than a few per SM the
+  // latency counts instead, and a row is spread over twice the lanes
   const bool few = f.tokens <= 2ll * num_sms();
-  if (f.width <= 256 || (few && f.width <= 4096)) return vec ? launch_rows<TS, TB, 4, 8>(f, stream) : launch_rows<TS, TB, 1, 8>(f, stream);
-  if (f.width <= 16384) return vec ? launch_rows<TS, TB, 4, 32>(f, stream) : launch_rows<TS, TB, 1, 32>(f, stream);
+  if (f.width <= 256 || (few && f.width <= 4096)) {
+    if (!vec) return launch_rows<TS, TB, 1, 8, false>(f, stream);
+    return f.width % 256 == 0 ? launch_rows<TS, TB, 4, 8, true>(f, stream) : launch_rows<TS, TB, 4, 8, false>(f, stream);
+  }
+  if (f.width <= 8192) {
+    if (!vec) return launch_rows<TS, TB, 1, 16, false>(f, stream);
+    return f.width % 512 == 0 ? launch_rows<TS, TB, 4, 16, true>(f, stream) : launch_rows<TS, TB, 4, 16, false>(f, stream);
+  }
+  if (f.width <= 16384 && vec) return launch_rows<TS, TB, 4, 32, false>(f, stream);
   const int64_t most = 8ll * num_sms();
   return launch_pdl(norm_fwd_any_kernel<TS, TB>, dim3(static_cast<unsigned>(f.tokens < most ? f.tokens : most)), dim3(kThreads), 0, stream, f);
 }
