@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {  // the whole warp walks the stages, one lane issues
       const uint32_t idesc = idesc_f4(FMT, 256, 256);
       int stage = 0, i = 0;
       uint32_t phase = 0;
@@ -195,26 +195,30 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
       for (int t = first; ok && t < p.tiles; t += step, ++i) {
         // the tile before has been read as far as the two accumulators share columns (and the one before it, whose
         // accumulator this is, altogether)
-        if (i > 0 && !mbar_wait(bar_free, (i - 1) & 1, p.w, DEV_ERR_WAIT_MMA)) break;
+        ok = i == 0 || mbar_wait(bar_free, (i - 1) & 1, p.w, DEV_ERR_WAIT_MMA);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         const uint32_t d = tmem + (i & 1 ? C::ACC1 : 0);
-        for (int k = 0; k < p.stages_k; ++k) {
-          if (!mbar_wait(bar_full + 8 * stage, phase, p.w, DEV_ERR_WAIT_MMA)) {
-            ok = false;
-            break;
-          }
+        for (int k = 0; ok && k < p.stages_k; ++k) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * stage, phase, p.w, DEV_ERR_WAIT_MMA));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = base + stage * 2 * kOpBytes, sf = base + C::OFF_SF + stage * C::SF_BYTES;
-          stage_mma<FMT, true, 2>(d, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == 0);
-          mma_commit_pair(bar_empty + 8 * stage, 0x3);
+          if (elect_one()) {
+            const uint32_t sa = base + stage * 2 * kOpBytes, sf = base + C::OFF_SF + stage * C::SF_BYTES;
+            stage_mma<FMT, true, 2>(d, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == 0);
+            mma_commit_pair(bar_empty + 8 * stage, 0x3);
+          }
+          __syncwarp();
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) mma_commit_pair(bar_done + 8 * (i & 1), 0x3);
+        if (ok && elect_one()) mma_commit_pair(bar_done + 8 * (i & 1), 0x3);
+        __syncwarp();
       }
-      mma_commit_pair(bar_final, 0x1);
+      if (elect_one()) mma_commit_pair(bar_final, 0x1);
+      __syncwarp();
       if (!wait_drain(bar_final, 0, 1000000000ull)) atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
     }
   } else {
