@@ -155,35 +155,34 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const uint32_t full_lead = mapa_shared(bar_full, 0);
-      for (int t = first; ok && t < p.tiles; t += step) {
-        int mb, nb;
-        tile_at(t, p, mb, nb);
-        for (int k = 0; k < p.stages_k; ++k) {
-          if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER)) {
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t full_lead = mapa_shared(bar_full, 0);
+    for (int t = first; ok && t < p.tiles; t += step) {
+      int mb, nb;
+      tile_at(t, p, mb, nb);
+      for (int k = 0; k < p.stages_k; ++k) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, phase ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
+        if (!ok) break;
+        if (elect_one()) {
           const uint32_t sa = base + stage * 2 * kOpBytes, sf = base + C::OFF_SF + stage * C::SF_BYTES, fb = full_lead + 8 * stage;
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * C::TX_BYTES);  // both CTAs' bytes
           tma_load_2d_pair(sa, &tmA, fb, k * 128, mb * 256 + static_cast<int>(rank) * 128);
           tma_load_2d_pair(sa + kOpBytes, &tmB, fb, k * 128, nb * 256 + static_cast<int>(rank) * 128);
           tma_load_3d_pair(sf, &tmSA, fb, 0, k * C::KA, mb * 2 + static_cast<int>(rank));
           tma_load_3d_pair(sf + 512 * C::KA, &tmSB, fb, 0, k * C::KA, nb * 2);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {  // let the loads in flight land (microseconds) before the CTA can exit
-        const unsigned long long t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
+    }
+    if (!ok) {  // let the loads in flight land (microseconds) before the CTA can exit
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {
       }
     }
   } else if (warp == 1) {
@@ -390,11 +389,11 @@ __global__ void __launch_bounds__(192)
 
   bool good = true;  // (epilogue warps)
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t issued = 0;
-      for (int k = k0; k < k1; ++k, ++issued) {
-        const int stage = issued % C::STAGES;
-        if (!mbar_wait(bar_empty + 8 * stage, ((issued / C::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER)) break;
+    int issued = 0;
+    for (int k = k0; k < k1; ++k, ++issued) {
+      const int stage = issued % C::STAGES;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, ((issued / C::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER))) break;
+      if (elect_one()) {
         const uint32_t sa = base + stage * C::OP_BYTES, sf = base + C::OFF_SF + stage * C::SF_BYTES, fb = bar_full + 8 * stage;
         mbar_arrive_expect_tx(fb, C::TX_BYTES);
         tma_load_2d(sa, &tmW, fb, k * 128, nb * 128);
@@ -402,25 +401,27 @@ __global__ void __launch_bounds__(192)
         tma_load_3d(sf, &tmSW, fb, 0, k * C::KA, nb);
         tma_load_3d(sf + 512 * C::KA, &tmSX, fb, 0, k * C::KA, mb * BN / 128);
       }
-      // every load that was issued lands before the CTA can exit, also after a wait that ran out
-      for (uint32_t s = issued > C::STAGES ? issued - C::STAGES : 0; s < issued; ++s)
-        wait_drain(bar_full + 8 * (s % C::STAGES), (s / C::STAGES) & 1, 1000000000ull);
+      __syncwarp();
     }
+    // every load that was issued lands before the CTA can exit, also after a wait that ran out
+    for (int s = issued > C::STAGES ? issued - C::STAGES : 0; s < issued; ++s)
+      wait_drain(bar_full + 8 * (s % C::STAGES), (s / C::STAGES) & 1, 1000000000ull);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f4(FMT, 128, BN);
-      for (int k = k0; k < k1; ++k) {
-        const uint32_t n = k - k0;
-        const int stage = n % C::STAGES;
-        if (!mbar_wait(bar_full + 8 * stage, (n / C::STAGES) & 1, p.w, DEV_ERR_WAIT_MMA)) break;
-        tc_fence_after();
+    const uint32_t idesc = idesc_f4(FMT, 128, BN);
+    for (int k = k0; k < k1; ++k) {
+      const int n = k - k0, stage = n % C::STAGES;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * stage, (n / C::STAGES) & 1, p.w, DEV_ERR_WAIT_MMA))) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint32_t sa = base + stage * C::OP_BYTES, sf = base + C::OFF_SF + stage * C::SF_BYTES;
         stage_mma<FMT, false, C::NB>(tmem, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == k0);
         mma_commit(bar_empty + 8 * stage);
       }
-      mma_commit(bar_done);
-      if (!wait_drain(bar_done, 0, 4000000000ull)) atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
+      __syncwarp();
     }
+    if (elect_one()) mma_commit(bar_done);
+    __syncwarp();
+    if (!wait_drain(bar_done, 0, 4000000000ull)) atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
   } else {
     good = mbar_wait(bar_done, 0, p.w, DEV_ERR_WAIT_EPILOGUE);
     __syncwarp();
