@@ -14,6 +14,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "kernels.h"
@@ -69,6 +70,73 @@ __device__ __forceinline__ void stage_mma(uint32_t d, uint32_t sa, uint32_t sb, 
   }
 }
 
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cta.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Every thread's share of a reduction over the CTAs first, first + step, ... (n of them, at most MOST) of the cluster:
+// items begin, begin + stride, ... below end, four fp32 values each at at(item) in every CTA's shared memory, summed in
+// CTA order and handed to out(item, sum). The loads of U items are in flight together, and this CTA's own values (its
+// place among the n is `own`) are read as local ones: two pairs' 128 x 256 tiles took 3.1 us when they went the
+// remote way too.
+template <int MOST, int U, typename At, typename Out>
+__device__ __forceinline__ void cluster_sum(int begin, int end, int stride, int first, int step, int n, int own, At at, Out out) {
+  for (int i = begin; i < end; i += U * stride) {
+    float4 v[U][MOST];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < MOST; ++r)
+        if (r < n && i + u * stride < end)
+          v[u][r] = r == own ? ld_shared_f32x4(at(i + u * stride)) : ld_cluster_f32x4(mapa_shared(at(i + u * stride), static_cast<uint32_t>(first + r * step)));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float4 s = v[u][0];
+#pragma unroll
+      for (int r = 1; r < MOST; ++r)
+        if (r < n) s = make_float4(__fadd_rn(s.x, v[u][r].x), __fadd_rn(s.y, v[u][r].y), __fadd_rn(s.z, v[u][r].z), __fadd_rn(s.w, v[u][r].w));
+      if (i + u * stride < end) out(i + u * stride, s);
+    }
+  }
+}
+
+// Four neighbouring results times d, `left` of them inside the row (rows and columns in fours are aligned).
+template <typename T>
+__device__ __forceinline__ void put4(T* p, float4 s, float d, int left) {
+  const float v[4] = {__fmul_rn(s.x, d), __fmul_rn(s.y, d), __fmul_rn(s.z, d), __fmul_rn(s.w, d)};
+  if (left >= 4) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    else
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < left) {
+        if constexpr (sizeof(T) == 2)
+          p[j] = __float2bfloat16_rn(v[j]);
+        else
+          p[j] = v[j];
+      }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void put(T* p, float v) {
+  if constexpr (sizeof(T) == 2)
+    *p = __float2bfloat16_rn(v);
+  else
+    *p = v;
+}
+
 // ---------------------------------------------------------------------------------------
 // Many rows: persistent CTA pairs, tiles of 256 x 256
 // ---------------------------------------------------------------------------------------
@@ -76,6 +144,9 @@ __device__ __forceinline__ void stage_mma(uint32_t d, uint32_t sa, uint32_t sb, 
 // tensor core computes every column). Two accumulators of 256 columns and the scale columns do not fit in
 // 512, so the second accumulator starts before the first one ends: the next tile's MMAs may begin once the
 // columns that the two share have been read, which the epilogue does first.
+// With too few tiles for the GPU, the pairs of a larger cluster take consecutive ranges of one tile's K (SPLIT): each
+// CTA writes its 128 x 256 fp32 partial tile where its operands were, and then sums a share of the rows over the
+// pairs, in order, and stores it (the same bits every time; no workspace, no atomics).
 template <int FMT>
 struct Pair {
   static constexpr int KA = kAtoms<FMT>;
@@ -89,6 +160,10 @@ struct Pair {
   static constexpr int OFF_SF = STAGES * 2 * kOpBytes;
   static constexpr int OFF_STG = OFF_SF + STAGES * SF_BYTES;
   static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * kStg;
+  // SPLIT: the partial tile lies where the operands were
+  static constexpr int TILE_PITCH = 260 * 4;  // bytes of a row: lanes' 16 bytes in different banks
+  static_assert(128 * TILE_PITCH <= OFF_SF, "partial tile");
+  static constexpr int MOST_SPLITS = 4;
   static constexpr int NBAR = 2 * STAGES + 4;  // full, empty, tile done [2], shared columns read, final
   static constexpr int OFF_SLOT = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM = OFF_SLOT + 16 + 1024;
@@ -98,7 +173,9 @@ struct Pair {
 };
 
 struct PairParams {
-  int M, N, tiles, num_m, num_n, stages_k, group_m;
+  int M, N, tiles, num_m, num_n, stages_k, group_m, splits;
+  void* C;
+  int64_t ldc;
   const float* da;
   const float* db;
   WaitCtl w;
@@ -111,11 +188,12 @@ __device__ __forceinline__ void tile_at(int t, const PairParams& p, int& mb, int
   mb = g * p.group_m + (l - nb * rows);
 }
 
-template <int FMT, bool F32>
+template <int FMT, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
     mm4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSA,
                     const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ PairParams p) {
   using C = Pair<FMT>;
+  using T = std::conditional_t<F32, float, __nv_bfloat16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(smem);
@@ -123,8 +201,12 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
   const uint32_t bar_full = base + C::OFF_BAR, bar_empty = bar_full + 8 * C::STAGES, bar_done = bar_empty + 8 * C::STAGES;
   const uint32_t bar_free = bar_done + 16, bar_final = bar_free + 8;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
-  const uint32_t rank = cluster_ctarank();
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // SPLIT: pair `part` of the cluster's `splits` takes K stages [k0, k1) of the cluster's one tile
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
+  const int part = static_cast<int>(crank >> 1);
+  const int first = SPLIT ? blockIdx.x / (2 * p.splits) : blockIdx.x >> 1, step = SPLIT ? p.tiles : gridDim.x >> 1;
+  const int k0 = SPLIT ? p.stages_k * part / p.splits : 0, k1 = SPLIT ? p.stages_k * (part + 1) / p.splits : p.stages_k;
+  const uint16_t pair_mask = static_cast<uint16_t>(0x3u << lead);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -158,11 +240,11 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const uint32_t full_lead = mapa_shared(bar_full, 0);
+    const uint32_t full_lead = mapa_shared(bar_full, lead);
     for (int t = first; ok && t < p.tiles; t += step) {
       int mb, nb;
       tile_at(t, p, mb, nb);
-      for (int k = 0; k < p.stages_k; ++k) {
+      for (int k = k0; k < k1; ++k) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, phase ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
         if (!ok) break;
         if (elect_one()) {
@@ -198,14 +280,14 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         const uint32_t d = tmem + (i & 1 ? C::ACC1 : 0);
-        for (int k = 0; ok && k < p.stages_k; ++k) {
+        for (int k = k0; ok && k < k1; ++k) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * stage, phase, p.w, DEV_ERR_WAIT_MMA));
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t sa = base + stage * 2 * kOpBytes, sf = base + C::OFF_SF + stage * C::SF_BYTES;
-            stage_mma<FMT, true, 2>(d, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == 0);
-            mma_commit_pair(bar_empty + 8 * stage, 0x3);
+            stage_mma<FMT, true, 2>(d, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == k0);
+            mma_commit_pair(bar_empty + 8 * stage, pair_mask);
           }
           __syncwarp();
           if (++stage == C::STAGES) {
@@ -213,18 +295,40 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
             phase ^= 1u;
           }
         }
-        if (ok && elect_one()) mma_commit_pair(bar_done + 8 * (i & 1), 0x3);
+        if (ok && elect_one()) mma_commit_pair(bar_done + 8 * (i & 1), pair_mask);
         __syncwarp();
       }
-      if (elect_one()) mma_commit_pair(bar_final, 0x1);
+      if (elect_one()) mma_commit_pair(bar_final, static_cast<uint16_t>(1u << lead));
       __syncwarp();
       if (!wait_drain(bar_final, 0, 1000000000ull)) atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
     }
+  } else if constexpr (SPLIT) {
+    // this CTA's partial tile: rows of 256 fp32 (every load has landed and every MMA is done)
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const bool good = mbar_wait(bar_done, 0, p.w, DEV_ERR_WAIT_EPILOGUE);
+    __syncwarp();
+    tc_fence_after();
+    if (good) {
+      uint8_t* row = smem + (q * 32 + lane) * C::TILE_PITCH + half * 512;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(acc + c, r);
+        tmem_ld_wait();
+        reg_fence(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(row + 4 * c + 16 * j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
   } else {
     const int ew = warp - 2, q = warp & 3, half = ew >> 2;
     uint8_t* stg = smem + C::OFF_STG + ew * kStg;
     const float d = __fmul_rn(p.da != nullptr ? __ldg(p.da) : 1.0f, p.db != nullptr ? __ldg(p.db) : 1.0f);
-    const uint32_t free_lead = mapa_shared(bar_free, 0);
+    const uint32_t free_lead = mapa_shared(bar_free, lead);
     int i = 0;
     for (int t = first; t < p.tiles; t += step, ++i) {
       int mb, nb;
@@ -250,6 +354,18 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(free_lead);
         }
+        const int chunk0 = nb * 256 + chunk * 64;
+        if (chunk0 + 64 > p.N && (p.N & (F32 ? 3 : 7)) != 0) {
+          // the row's end inside 16 bytes: a tiled store would write zeros up to the end of those, so plain stores
+          if (row0 + lane < p.M) {
+            T* out = static_cast<T*>(p.C) + (row0 + lane) * p.ldc + chunk0;
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (chunk0 + j < p.N) put(out + j, __fmul_rn(__uint_as_float(r[j]), d));
+          }
+          __syncwarp();
+          continue;
+        }
         constexpr int PARTS = F32 ? 2 : 1;  // 128 bytes of a row per store: 64 bf16 or 32 fp32
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) {
@@ -273,7 +389,7 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          const int col0 = nb * 256 + chunk * 64 + 32 * h;
+          const int col0 = chunk0 + 32 * h;
           if (lane == 0 && row0 < p.M && col0 < p.N) {  // (the rest is clipped at M and N)
             tma_store_2d(&tmC, smem_u32(stg), col0, row0);
             bulk_commit_group();
@@ -286,7 +402,22 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no commit or load of the pair targets a CTA that has left
+  cluster_sync_all();  // no commit or load of the pair targets a CTA that has left; SPLIT: the partial tiles are there
+  if constexpr (SPLIT) {
+    const float d = __fmul_rn(p.da != nullptr ? __ldg(p.da) : 1.0f, p.db != nullptr ? __ldg(p.db) : 1.0f);
+    int mb, nb;
+    tile_at(first, p, mb, nb);
+    const int row0 = mb * 256 + static_cast<int>(rank) * 128, live = max(0, min(128, p.M - row0));
+    const int r0 = live * part / p.splits, r1 = live * (part + 1) / p.splits;
+    cluster_sum<C::MOST_SPLITS, 4>(r0 * 64 + static_cast<int>(threadIdx.x), r1 * 64, C::THREADS, static_cast<int>(rank), 2, p.splits, part,
+                                   [&](int i) { return base + (i >> 6) * C::TILE_PITCH + 16 * (i & 63); },
+                                   [&](int i, float4 s) {
+                                     const int n = nb * 256 + 4 * (i & 63);
+                                     put4(static_cast<T*>(p.C) + (row0 + (i >> 6)) * p.ldc + n, s, d, p.N - n);
+                                   });
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while its tile is being read
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -304,19 +435,19 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
 template <int FMT, int BN>
 struct Split {
   static constexpr int KA = kAtoms<FMT>;
-  static constexpr int NB = BN > 128 ? 2 : 1;
+  static_assert(BN <= 128, "one scale block of A");
   static constexpr int X_BYTES = BN * 128;
   static constexpr int OP_BYTES = kOpBytes + X_BYTES;
-  static constexpr int SF_BYTES = 512 * KA * (1 + NB);
+  static constexpr int SF_BYTES = 512 * KA * 2;
   static constexpr int TX_BYTES = OP_BYTES + SF_BYTES;
   // up to 64 rows of A two CTAs share an SM (their loads overlap each other's start and end)
-  static constexpr int BUDGET = BN <= 64 ? 108 * 1024 : 216 * 1024;
-  static constexpr int FIT = BUDGET / (TX_BYTES);
+  static constexpr int PER_SM = BN <= 64 ? 2 : 1;
+  static constexpr int FIT = 220 * 1024 / PER_SM / TX_BYTES;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int THREADS = 192;
   static constexpr int ACC_COLS = BN;
-  static constexpr int SFA = ACC_COLS, SFB = SFA + 4 * KA, COLS = SFB + 4 * KA * NB;
-  static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int SFA = ACC_COLS, SFB = SFA + 4 * KA, COLS = SFB + 4 * KA;
+  static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
   static constexpr int OFF_SF = STAGES * OP_BYTES;
   static constexpr int OFF_BAR = OFF_SF + STAGES * SF_BYTES;
   static constexpr int NBAR = 2 * STAGES + 1;
@@ -334,20 +465,6 @@ struct SplitParams {
   const float* db;
   WaitCtl w;
 };
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-template <typename T>
-__device__ __forceinline__ void put(T* p, float v) {
-  if constexpr (sizeof(T) == 2)
-    *p = __float2bfloat16_rn(v);
-  else
-    *p = v;
-}
 
 template <int FMT, int BN, typename T>
 __global__ void __launch_bounds__(192)
@@ -414,7 +531,7 @@ __global__ void __launch_bounds__(192)
       tc_fence_after();
       if (elect_one()) {
         const uint32_t sa = base + stage * C::OP_BYTES, sf = base + C::OFF_SF + stage * C::SF_BYTES;
-        stage_mma<FMT, false, C::NB>(tmem, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == k0);
+        stage_mma<FMT, false, 1>(tmem, sa, sa + kOpBytes, sf, sf + 512 * C::KA, tmem + C::SFA, tmem + C::SFB, idesc, k == k0);
         mma_commit(bar_empty + 8 * stage);
       }
       __syncwarp();
@@ -429,20 +546,19 @@ __global__ void __launch_bounds__(192)
   }
   const float d = __fmul_rn(p.da != nullptr ? __ldg(p.da) : 1.0f, p.db != nullptr ? __ldg(p.db) : 1.0f);
   T* out = static_cast<T*>(p.C);
+  const int live = min(BN, p.M - mb * BN);  // rows of A in this tile
   if (splits == 1) {
     if (warp >= 2 && good) {
       const int q = warp & 3, n = nb * 128 + q * 32 + lane;
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
+      for (int c = 0; c < live; c += 16) {
         uint32_t r[16];
         tmem_ld16(acc + c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int m = mb * BN + c + j;
-          if (m < p.M && n < p.N) put(out + m * p.ldc + n, __fmul_rn(__uint_as_float(r[j]), d));
-        }
+        for (int j = 0; j < 16; ++j)
+          if (c + j < live && n < p.N) put(out + (mb * BN + c + j) * p.ldc + n, __fmul_rn(__uint_as_float(r[j]), d));
       }
     }
   } else {
@@ -452,7 +568,7 @@ __global__ void __launch_bounds__(192)
       const int q = warp & 3;
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
+      for (int c = 0; c < live; c += 16) {
         uint32_t r[16];
         tmem_ld16(acc + c, r);
         tmem_ld_wait();
@@ -462,14 +578,12 @@ __global__ void __launch_bounds__(192)
     }
     __syncwarp();
     cluster_sync_all();
-    const int live = min(BN, p.M - mb * BN);  // rows of A in this tile
     const int c0 = live * rank / splits, c1 = live * (rank + 1) / splits;
-    for (int i = c0 * 128 + static_cast<int>(threadIdx.x); i < c1 * 128; i += C::THREADS) {
-      const int m = mb * BN + (i >> 7), n = nb * 128 + (i & 127);
-      float s = 0.0f;
-      for (int r = 0; r < splits; ++r) s = __fadd_rn(s, ld_cluster_f32(mapa_shared(base + 4 * i, r)));
-      if (n < p.N) put(out + m * p.ldc + n, __fmul_rn(s, d));
-    }
+    cluster_sum<8, 2>(c0 * 32 + static_cast<int>(threadIdx.x), c1 * 32, C::THREADS, 0, 1, splits, rank, [&](int i) { return base + 16 * i; },
+                      [&](int i, float4 s) {
+                        const int n = nb * 128 + 4 * (i & 31);
+                        put4(out + (mb * BN + (i >> 5)) * p.ldc + n, s, d, p.N - n);
+                      });
     __syncwarp();
     cluster_sync_all();  // no CTA leaves while its tile is being read
   }
@@ -497,42 +611,40 @@ bool scales_map(CUtensorMap* m, const void* sf, int fmt, int64_t mn, int64_t k, 
                         fmt == 0 ? 4 : 2, static_cast<uint32_t>(blocks));
 }
 
-// Once per device and kernel: the shared-memory limit, and how many clusters of `cluster` CTAs are resident at
-// once (0: not asked).
+// Once per device and kernel: the shared-memory limit; and per cluster size (up to 8), how many clusters are resident
+// at once.
 template <auto Kernel>
 cudaError_t prepare(int smem, int threads, int cluster, int* resident) {
   static bool done[64] = {};
-  static int count[64] = {};
+  static int count[64][9] = {};
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
-  if (dev >= 64 || !done[dev]) {
+  if (!done[dev]) {
     e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int n = 0;
-    if (cluster > 1) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(cluster);
-      cfg.blockDim = dim3(threads);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(Kernel), &cfg);
-      if (e != cudaSuccess) return e;
-    }
-    if (dev >= 64) {
-      *resident = n;
-      return cudaSuccess;
-    }
     done[dev] = true;
-    count[dev] = n;
   }
-  *resident = count[dev];
+  if (count[dev][cluster] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(Kernel), &cfg);
+    if (e != cudaSuccess) return e;
+    if (n <= 0) return cudaErrorInvalidConfiguration;
+    count[dev][cluster] = n;
+  }
+  *resident = count[dev][cluster];
   return cudaSuccess;
 }
 
@@ -553,13 +665,12 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-template <int FMT, bool F32>
-cudaError_t launch_pair(const Mm4Args& g, cudaStream_t stream, const char** why) {
+template <int FMT, bool F32, bool SPLIT>
+cudaError_t launch_pair(const Mm4Args& g, int splits, cudaStream_t stream, const char** why) {
   using C = Pair<FMT>;
   int clusters = 0;
-  const cudaError_t e = prepare<mm4_pair_kernel<FMT, F32>>(C::SMEM, C::THREADS, 2, &clusters);
+  const cudaError_t e = prepare<mm4_pair_kernel<FMT, F32, SPLIT>>(C::SMEM, C::THREADS, 2 * splits, &clusters);
   if (e != cudaSuccess) return e;
-  if (clusters <= 0) return cudaErrorInvalidConfiguration;
   CUtensorMap a, b, sa, sb, c;
   if (!codes_map(&a, g.A, g.M, g.K, 128) || !codes_map(&b, g.B, g.N, g.K, 128) || !scales_map(&sa, g.sfa, FMT, g.M, g.K, 1) ||
       !scales_map(&sb, g.sfb, FMT, g.N, g.K, 2) ||
@@ -576,22 +687,29 @@ cudaError_t launch_pair(const Mm4Args& g, cudaStream_t stream, const char** why)
   p.tiles = p.num_m * p.num_n;
   p.stages_k = static_cast<int>((g.K + kStageK - 1) / kStageK);
   p.group_m = 16;
+  p.splits = splits;
+  p.C = g.C;
+  p.ldc = g.ldc;
   p.da = g.da;
   p.db = g.db;
   p.w = wait_ctl();
-  const int slots = p.tiles < clusters ? p.tiles : clusters;
-  return launch_cluster(mm4_pair_kernel<FMT, F32>, dim3(2 * slots), C::THREADS, C::SMEM, 2, stream, a, b, sa, sb, c, p);
+  if constexpr (SPLIT) {
+    return launch_cluster(mm4_pair_kernel<FMT, F32, true>, dim3(2 * splits * p.tiles), C::THREADS, C::SMEM, 2 * splits, stream, a, b, sa, sb, c, p);
+  } else {
+    const int slots = p.tiles < clusters ? p.tiles : clusters;
+    return launch_cluster(mm4_pair_kernel<FMT, F32, false>, dim3(2 * slots), C::THREADS, C::SMEM, 2, stream, a, b, sa, sb, c, p);
+  }
 }
 
 template <int FMT, int BN, typename T>
 cudaError_t launch_split(const Mm4Args& g, int splits, cudaStream_t stream, const char** why) {
   using C = Split<FMT, BN>;
   int n = 0;
-  const cudaError_t e = prepare<mm4_split_kernel<FMT, BN, T>>(C::SMEM, C::THREADS, 1, &n);
+  const cudaError_t e = prepare<mm4_split_kernel<FMT, BN, T>>(C::SMEM, C::THREADS, splits, &n);
   if (e != cudaSuccess) return e;
   CUtensorMap w, x, sw, sx;
   if (!codes_map(&w, g.B, g.N, g.K, 128) || !codes_map(&x, g.A, g.M, g.K, BN) || !scales_map(&sw, g.sfb, FMT, g.N, g.K, 1) ||
-      !scales_map(&sx, g.sfa, FMT, g.M, g.K, C::NB)) {
+      !scales_map(&sx, g.sfa, FMT, g.M, g.K, 1)) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
@@ -609,20 +727,65 @@ cudaError_t launch_split(const Mm4Args& g, int splits, cudaStream_t stream, cons
   return launch_cluster(mm4_split_kernel<FMT, BN, T>, grid, C::THREADS, C::SMEM, splits, stream, w, x, sw, sx, p);
 }
 
+// How a product is run: CTA pairs (bn == 0), or clusters of `splits` with tiles of 128 x bn.
+struct Plan {
+  int bn, splits;
+};
+
+// The cheapest plan. Up to 64 rows of A the weights' bytes and the latency decide: one CTA per SM (more of them measured
+// slower: 1 x 4096 x 4096 took 3.9 us in 128 CTAs, 4.4 in 256), at least two stages each. Above, the measured times of
+// a stage and of what comes before and after the stages (us, GB300): a pair does 256 x 256 x 256 in 0.27, a CTA
+// 128 x 128 x 256 in 0.31; summing the parts of a split tile takes 3.6 on pairs (128 KB per CTA), 1.2 otherwise, where
+// the single CTA's unsplit epilogue takes 2.
+template <int FMT, typename T>
+cudaError_t choose(int64_t M, int64_t N, int64_t K, Plan* plan) {
+  const int64_t stages = (K + kStageK - 1) / kStageK, sms = num_sms();
+  const int64_t cols = (N + 127) / 128;
+  if (M <= 64) {
+    plan->bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    int64_t s = sms / cols;
+    s = s < stages / 2 ? s : stages / 2;
+    plan->splits = static_cast<int>(s < 1 ? 1 : s > 8 ? 8 : s);
+    return cudaSuccess;
+  }
+  float best = 0.0f;
+  auto offer = [&](int bn, int splits, float us) {
+    if (plan->splits != 0 && us >= best) return;
+    best = us;
+    *plan = {bn, splits};
+  };
+  *plan = {0, 0};
+  const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), small = (M + 127) / 128 * cols;
+  for (int s = 1; s <= Pair<FMT>::MOST_SPLITS && s <= stages; ++s) {
+    int clusters = 0;
+    const cudaError_t e = s == 1 ? prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, false>>(Pair<FMT>::SMEM, Pair<FMT>::THREADS, 2, &clusters)
+                                 : prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, true>>(Pair<FMT>::SMEM, Pair<FMT>::THREADS, 2 * s, &clusters);
+    if (e != cudaSuccess) return e;
+    if (s > 1 && tiles > clusters) break;
+    offer(0, s, 4.3f + 0.27f * static_cast<float>((stages + s - 1) / s * ((tiles + clusters - 1) / clusters)) + (s > 1 ? 3.6f : 0.0f));
+  }
+  for (int s = 1; s <= 8 && s <= stages && small <= sms; ++s) {
+    int clusters = 0;
+    const cudaError_t e = prepare<mm4_split_kernel<FMT, 128, T>>(Split<FMT, 128>::SMEM, Split<FMT, 128>::THREADS, s, &clusters);
+    if (e != cudaSuccess) return e;
+    if (s > 1 && small > clusters) break;
+    offer(128, s, 4.0f + 0.31f * static_cast<float>((stages + s - 1) / s) + (s > 1 ? 1.2f : 2.0f));
+  }
+  return cudaSuccess;
+}
+
 template <int FMT, typename T>
 cudaError_t launch_as(const Mm4Args& g, cudaStream_t stream, const char** why) {
-  const int64_t tiles256 = (g.M + 255) / 256 * ((g.N + 255) / 256), stages = (g.K + kStageK - 1) / kStageK;
-  if (g.M > 128 && tiles256 >= 76) return launch_pair<FMT, sizeof(T) == 4>(g, stream, why);
-  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
-  const int64_t tiles = (g.N + 127) / 128 * ((g.M + bn - 1) / bn);
-  int splits = 1;
-  const int64_t room = (bn <= 64 ? 2ll : 1ll) * num_sms();
-  while (splits < 8 && tiles * (splits + 1) <= room && stages / (splits + 1) >= 2) ++splits;
-  switch (bn) {
-    case 16: return launch_split<FMT, 16, T>(g, splits, stream, why);
-    case 32: return launch_split<FMT, 32, T>(g, splits, stream, why);
-    case 64: return launch_split<FMT, 64, T>(g, splits, stream, why);
-    default: return launch_split<FMT, 128, T>(g, splits, stream, why);
+  Plan p{0, 0};
+  const cudaError_t e = choose<FMT, T>(g.M, g.N, g.K, &p);
+  if (e != cudaSuccess) return e;
+  switch (p.bn) {
+    case 0:
+      return p.splits > 1 ? launch_pair<FMT, sizeof(T) == 4, true>(g, p.splits, stream, why) : launch_pair<FMT, sizeof(T) == 4, false>(g, 1, stream, why);
+    case 16: return launch_split<FMT, 16, T>(g, p.splits, stream, why);
+    case 32: return launch_split<FMT, 32, T>(g, p.splits, stream, why);
+    case 64: return launch_split<FMT, 64, T>(g, p.splits, stream, why);
+    default: return launch_split<FMT, 128, T>(g, p.splits, stream, why);
   }
 }
 

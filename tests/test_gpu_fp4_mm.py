@@ -69,6 +69,18 @@ def test_exact(g, fmt, m, n, k):
     assert np.array_equal(product(g, a, b, m, n, k, fmt, False), to_bf16(want))
 
 
+@pytest.mark.parametrize("n", [2561, 2564, 2568, 2815, 2816])
+@pytest.mark.parametrize("m", [2049, 2304])
+@pytest.mark.parametrize("f32", [False, True])
+def test_exact_many_tiles(g, m, n, f32):
+    """Enough 256 x 256 tiles for every pair of SMs to take several, rows ending inside 16 bytes of the output."""
+    k = 300
+    rng = np.random.default_rng(m + n)
+    a, b = operand(rng, fp4.NV, m, k, True), operand(rng, fp4.NV, n, k, True)
+    want, _ = fp4.scaled_mm(a[2], b[2])
+    assert np.array_equal(product(g, a, b, m, n, k, fp4.NV, f32), want if f32 else to_bf16(want))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("m,n,k", [(1, 768, 3000), (20, 520, 1536), (130, 300, 777), (520, 1030, 2050), (1500, 640, 512)])
