@@ -166,35 +166,46 @@ struct Row {
   }
 };
 
-// Sums over the warps of a CTA (all of them; `warps` of them), in warp order, the same bits on every thread. red: two
-// halves that consecutive sums take in turn, so one barrier each is enough: who writes a half again has passed the
-// barrier after everyone's read of it. A CTA of one warp needs none.
+// Sums over the warps of a CTA (up to 16), in a fixed order, the same bits on every thread. v: two halves that
+// consecutive sums take in turn, so one barrier each is enough: who writes a half again has passed the barrier after
+// everyone's read of it. Places of warps that are not there hold zero (clear), so a sum reads all sixteen without a
+// loop. A CTA of one warp needs neither.
 struct Red {
-  __align__(16) float v[2][2][32];
+  __align__(16) float v[2][2][16];
+  __device__ __forceinline__ void clear() {  // before the first sum's barrier, by the first 64 threads or fewer
+    for (int i = threadIdx.x; i < 64; i += blockDim.x)
+      if ((i & 15) >= static_cast<int>(blockDim.x >> 5)) v[0][0][i] = 0.0f;
+  }
 };
 __device__ __forceinline__ float warp_sum(float s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   return s;
 }
-__device__ __forceinline__ float red_sum(const float* r, int warps) {
-  float s = r[0];
-  for (int w = 1; w < warps; ++w) s += r[w];
-  return s;
+__device__ __forceinline__ float red_sum(const float* r) {
+  const float4* q = reinterpret_cast<const float4*>(r);
+  Pair a = both(0.0f), b = both(0.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 t = q[i];
+    a = add2(a, pair(t.x, t.y));
+    b = add2(b, pair(t.z, t.w));
+  }
+  return sum2(add2(a, b));
 }
-__device__ __forceinline__ float cta_sum(float s, Red& red, int& turn, int warps) {
+__device__ __forceinline__ float cta_sum(float s, Red& red, int& turn) {
   s = warp_sum(s);
-  if (warps == 1) return s;
+  if (blockDim.x == 32) return s;
   float* r = red.v[turn][0];
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
   __syncthreads();
-  return red_sum(r, warps);
+  return red_sum(r);
 }
-__device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn, int warps) {
+__device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn) {
   s.x = warp_sum(s.x);
   s.y = warp_sum(s.y);
-  if (warps == 1) return s;
+  if (blockDim.x == 32) return s;
   float *rx = red.v[turn][0], *ry = red.v[turn][1];
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) {
@@ -202,7 +213,15 @@ __device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn, int war
     ry[threadIdx.x >> 5] = s.y;
   }
   __syncthreads();
-  return make_float2(red_sum(rx, warps), red_sum(ry, warps));
+  return make_float2(red_sum(rx), red_sum(ry));
+}
+
+// 1 / sqrt(a): the approximation of the special function unit and one Newton step, within 2 units in the last place
+// (a division and a square root take some forty instructions of every warp of a row)
+__device__ __forceinline__ float inv_sqrt(float a) {
+  const float y = rsqrtf(a);
+  const float e = fmaf(-a * y, y, 1.0f);  // 1 - a y^2
+  return a > 0.0f && a < 3.402823466e38f ? fmaf(0.5f * y, e, y) : y;
 }
 
 __device__ __forceinline__ float affine(float z, const float* w, const float* b, int64_t c) {

@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
                                                            int64_t rows_per) {
   __shared__ Red red;
   int turn = 0;
+  red.clear();
   pdl_wait();
   pdl_trigger();
   const float alpha = f.res_scale != nullptr ? *f.res_scale : 1.0f;
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
         a += dz;
         q = fmaf(dz, zpre(c), q);
       }
-      s1 = cta_sum(make_float2(a, q), red, turn, kThreads / 32);
+      s1 = cta_sum(make_float2(a, q), red, turn);
     }
     auto grad = [&](int64_t c) {
       float g = dro != nullptr ? load(dro + c) : 0.0f;
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
         a += dz;
         q = fmaf(dz, (load(o + c) - post.x) * post.y, q);
       }
-      s2 = cta_sum(make_float2(a, q), red, turn, kThreads / 32);
+      s2 = cta_sum(make_float2(a, q), red, turn);
     }
     const bool whole = f.gate != nullptr && grp * f.gate_rows >= t0 && (min((grp + 1) * f.gate_rows, f.tokens) <= t1);
     const bool last = f.gate != nullptr && (t + 1 == t1 || (t + 1) / f.gate_rows != grp);
@@ -172,7 +173,7 @@ __device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* 
   }
 }
 
-// Column sums to the workspace or to dgate (aligned to 4 bytes only).
+// Column sums to the workspace (WIDE; they stay in L2 for the kernel that adds them up) or to dgate (aligned to 4 bytes only).
 template <int VEC, int E, bool FULL, bool WIDE>
 __device__ __forceinline__ void leave(float* p, int left, const Pair (&x)[E / 2]) {
   if constexpr (VEC == 4 && !WIDE) {
@@ -186,8 +187,19 @@ __device__ __forceinline__ void leave(float* p, int left, const Pair (&x)[E / 2]
         p[128 * i + 3] = b.y;
       }
     }
+  } else if constexpr (VEC == 4) {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const float2 a = split(x[2 * i]), b = split(x[2 * i + 1]);
+      if (FULL || 128 * i < left) *reinterpret_cast<float4*>(p + 128 * i) = make_float4(a.x, a.y, b.x, b.y);
+    }
   } else {
-    Row<VEC, E, FULL>::store(p, left, x);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 a = split(x[i]);
+      if (64 * i < left) p[64 * i] = a.x;
+      if (64 * i + 32 < left) p[64 * i + 32] = a.y;
+    }
   }
 }
 
@@ -204,6 +216,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
   const int D = static_cast<int>(f.width), warps = blockDim.x >> 5, c = R::first(threadIdx.x >> 5, threadIdx.x & 31), left = D - c;
   const int64_t t0 = blockIdx.x * rows_per, t1 = min(t0 + rows_per, f.tokens);
   const uint32_t bar0 = smem_u32(bars);
+  if (warps > 1) red.clear();
   if constexpr (RING) {
     if (threadIdx.x == 0) {
       for (int s = 0; s < ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -296,25 +309,36 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
           Pair sm = zero;
 #pragma unroll
           for (int i = 0; i < H; ++i) sm = add2(sm, dz[i]);
-          const float2 s = cta_sum(make_float2(sum2(sm), sum2(sq)), red, turn, warps);
+          const float2 s = cta_sum(make_float2(sum2(sm), sum2(sq)), red, turn);
           m1 = s.x * inv;
           q1 = s.y * inv;
         } else {
-          q1 = cta_sum(sum2(sq), red, turn, warps) * inv;
+          q1 = cta_sum(sum2(sq), red, turn) * inv;
         }
-        const Pair q = both(-q1), mm = both(-m1);
+        const Pair q = both(-q1);
 #pragma unroll
-        for (int i = 0; i < H; ++i) dz[i] = mul2(add2(fma2(z[i], q, dz[i]), mm), rstd);
+        for (int i = 0; i < H; ++i) dz[i] = fma2(z[i], q, dz[i]);
+        if (f.pre == kLayer) {
+          const Pair mm = both(-m1);
+#pragma unroll
+          for (int i = 0; i < H; ++i) dz[i] = add2(dz[i], mm);
+        }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < H; ++i) dz[i] = zero;
     }
-    // dz: the norm's share of g, the gradient at r'
-    if (b.dr_out != nullptr) {
-      row_of<RING, VEC, E, FULL, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, left, z);
+    // dz, times rstd: the norm's share of g, the gradient at r'
+    {
+      const Pair rstd = both(pre.y);
+      if (b.dr_out != nullptr) {
+        row_of<RING, VEC, E, FULL, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, left, z);
 #pragma unroll
-      for (int i = 0; i < H; ++i) dz[i] = add2(dz[i], z[i]);
+        for (int i = 0; i < H; ++i) dz[i] = fma2(dz[i], rstd, z[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < H; ++i) dz[i] = mul2(dz[i], rstd);
+      }
     }
     R::clear(dz, left);
     if (b.dres_scale != nullptr) {
@@ -372,11 +396,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
         Pair sm = zero;
 #pragma unroll
         for (int i = 0; i < H; ++i) sm = add2(sm, dz[i]);
-        const float2 s = cta_sum(make_float2(sum2(sm), sum2(sq)), red, turn, warps);
+        const float2 s = cta_sum(make_float2(sum2(sm), sum2(sq)), red, turn);
         m2 = s.x * inv;
         q2 = s.y * inv;
       } else {
-        q2 = cta_sum(sum2(sq), red, turn, warps) * inv;
+        q2 = cta_sum(sum2(sq), red, turn) * inv;
       }
       if (RING && warps == 1) __syncthreads();  // (its sum needs no barrier, its stage does)
     } else if constexpr (RING) {
@@ -394,9 +418,14 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     }
     if (b.dO != nullptr) {
       if (f.post != kNone) {
-        const Pair q = both(-q2), mm = both(-m2), rstd = both(post.y);
+        const Pair q = both(-q2), rstd = both(post.y);
+        if (f.post == kLayer) {
+          const Pair mm = both(-m2);
 #pragma unroll
-        for (int i = 0; i < H; ++i) dz[i] = mul2(add2(fma2(z[i], q, dz[i]), mm), rstd);
+          for (int i = 0; i < H; ++i) dz[i] = add2(dz[i], mm);
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) dz[i] = mul2(fma2(z[i], q, dz[i]), rstd);
       }
       R::store(static_cast<TB*>(b.dO) + t * b.ld_do + c, left, dz);
     }
@@ -470,36 +499,63 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
   }
 }
 
-// Column sums over CTAs' partial rows: 32 columns per CTA; its 8 warps take consecutive ranges of the
-// partial rows, and their sums are added in warp order. blockIdx.y 0 .. 3: the parameters (and alpha);
-// from 4 on: the gate groups that several CTAs share.
-__global__ void __launch_bounds__(kThreads) norm_bwd_reduce_kernel(const NormFwd f, const NormBwd b, const float* part,
-                                                                   const double* part_alpha, int64_t rows_per, int ctas) {
-  __shared__ float sums[8][32];
+// Column sums over CTAs' partial rows: 32 V columns per CTA (V = 4 where rows are whole 16 bytes); its 16 warps take
+// consecutive ranges of the partial rows, and their sums are added in warp order. blockIdx.y 0 .. 3: the parameters
+// (and alpha); from 4 on: the gate groups that several CTAs share.
+constexpr int kReduceWarps = 16;
+
+template <int V>
+struct Cols {
+  float v[V];
+};
+
+template <int V>
+__global__ void __launch_bounds__(32 * kReduceWarps) norm_bwd_reduce_kernel(const NormFwd f, const NormBwd b, const float* part,
+                                                                            const double* part_alpha, int64_t rows_per, int ctas) {
+  __shared__ Cols<V> sums[kReduceWarps][32];
   pdl_wait();
   pdl_trigger();
-  const int64_t D = f.width, c = blockIdx.x * 32ll + (threadIdx.x & 31);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t D = f.width, c = (blockIdx.x * 32ll + lane) * V;
+  auto fetch = [&](int64_t row) {
+    Cols<V> x;
+    if constexpr (V == 4) {
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(part + row * D + c));
+      x.v[0] = t.x, x.v[1] = t.y, x.v[2] = t.z, x.v[3] = t.w;
+    } else {
+      x.v[0] = __ldcg(part + row * D + c);
+    }
+    return x;
+  };
   auto add = [&](int q0, int q1, auto place, float* out) {  // out[c] = sum over q of the partial row place(q)
-    float s = 0.0f;
-    const int n = q1 - q0, e = q0 + n * (warp + 1) / 8;
+    Cols<V> s = {};
+    const int n = q1 - q0, e = q0 + n * (warp + 1) / kReduceWarps;
     if (c < D) {
-      int q = q0 + n * warp / 8;
+      int q = q0 + n * warp / kReduceWarps;
       for (; q + 8 <= e; q += 8) {
-        float v[8];
+        Cols<V> x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = __ldcs(part + place(q + u) * D + c);
+        for (int u = 0; u < 8; ++u) x[u] = fetch(place(q + u));
 #pragma unroll
-        for (int u = 0; u < 8; ++u) s += v[u];
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int j = 0; j < V; ++j) s.v[j] += x[u].v[j];
       }
-      for (; q < e; ++q) s += __ldcs(part + place(q) * D + c);
+      for (; q < e; ++q) {
+        const Cols<V> x = fetch(place(q));
+#pragma unroll
+        for (int j = 0; j < V; ++j) s.v[j] += x.v[j];
+      }
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < D) {
 #pragma unroll
-      for (int w = 1; w < 8; ++w) s += sums[w][lane];
-      out[c] = s;
+      for (int w = 1; w < kReduceWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s.v[j] += sums[w][lane].v[j];
+#pragma unroll
+      for (int j = 0; j < V; ++j) out[c + j] = s.v[j];
     }
     __syncthreads();
   };
@@ -523,7 +579,9 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_reduce_kernel(const NormFwd
     const int64_t grp = by_group ? i : (i + 1) * rows_per / f.gate_rows, ga = grp * f.gate_rows, ge = min(ga + f.gate_rows, f.tokens);
     const int first = static_cast<int>(ga / rows_per), last = static_cast<int>((ge - 1) / rows_per);
     if (first == last || (!by_group && first != i)) continue;  // one CTA's alone, or another border's
-    add(first, last + 1, [=](int q) { return static_cast<int64_t>(q) * kPart + (q * rows_per / f.gate_rows == grp ? 4 : 5); }, b.dgate + grp * D);
+    // the group is the last one of the CTA that holds its first token, unless it is that CTA's first too
+    const int slot = first * rows_per / f.gate_rows == grp ? 4 : 5;
+    add(first, last + 1, [=](int q) { return static_cast<int64_t>(q) * kPart + (q == first ? slot : 4); }, b.dgate + grp * D);
   }
 }
 
@@ -539,7 +597,7 @@ BwdPlan bwd_plan(int64_t tokens, int64_t width) {
   BwdPlan p;
   const int64_t per = 32 * columns_of(width);
   p.threads = width <= 8192 ? static_cast<int>((width + per - 1) / per) * 32 : kThreads;
-  p.per_sm = p.threads >= 512 ? 1 : p.threads >= 256 ? 2 : 4;
+  p.per_sm = p.threads > 292 ? 1 : p.threads > 195 ? 2 : p.threads > 146 ? 3 : 4;  // (some 112 registers each)
   const int64_t most = static_cast<int64_t>(p.per_sm) * num_sms();
   p.rows_per = (tokens + most - 1) / most;
   p.ctas = static_cast<int>((tokens + p.rows_per - 1) / p.rows_per);
@@ -616,8 +674,10 @@ cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t st
     const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
     shared = groups < pl.ctas ? groups : pl.ctas - 1;
   }
-  const dim3 grid(static_cast<unsigned>((f.width + 31) / 32), static_cast<unsigned>(4 + (shared < 32 ? shared : 32)));
-  return launch_pdl(norm_bwd_reduce_kernel, grid, dim3(kThreads), 0, stream, f, b, part, part_alpha, pl.rows_per, pl.ctas);
+  const int cols = f.width % 4 == 0 ? 128 : 32;
+  const dim3 grid(static_cast<unsigned>((f.width + cols - 1) / cols), static_cast<unsigned>(4 + (shared < 32 ? shared : 32)));
+  return launch_pdl(cols == 128 ? norm_bwd_reduce_kernel<4> : norm_bwd_reduce_kernel<1>, grid, dim3(32 * kReduceWarps), 0, stream, f, b, part, part_alpha,
+                    pl.rows_per, pl.ctas);
 }
 
 }  // namespace

@@ -12,18 +12,18 @@ template <typename F>
 __device__ __forceinline__ float2 row_stat(int kind, int64_t width, float eps, Red& red, int& turn, F value) {
   float2 st = make_float2(0.0f, 1.0f);
   if (kind == kNone) return st;
-  const float n = static_cast<float>(width);
+  const float inv = 1.0f / static_cast<float>(width);
   if (kind == kLayer) {
     float a = 0.0f;
     for (int64_t c = threadIdx.x; c < width; c += kThreads) a += value(c);
-    st.x = cta_sum(a, red, turn, kThreads / 32) / n;
+    st.x = cta_sum(a, red, turn) * inv;
   }
   float a = 0.0f;
   for (int64_t c = threadIdx.x; c < width; c += kThreads) {
     const float z = value(c) - st.x;
     a = fmaf(z, z, a);
   }
-  st.y = 1.0f / sqrtf(cta_sum(a, red, turn, kThreads / 32) / n + eps);
+  st.y = inv_sqrt(fmaf(cta_sum(a, red, turn), inv, eps));
   return st;
 }
 
@@ -32,6 +32,7 @@ template <typename TS, typename TB>
 __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f) {
   __shared__ Red red;
   int turn = 0;
+  red.clear();
   pdl_wait();
   pdl_trigger();
   const float alpha = f.res_scale != nullptr ? *f.res_scale : 1.0f;
@@ -103,14 +104,13 @@ template <int VEC, int E, bool FULL>
 __device__ __forceinline__ float2 held_stat(int kind, int width, float eps, const Pair (&v)[E / 2], int left, Red& red, int& turn) {
   float2 st = make_float2(0.0f, 1.0f);
   if (kind == kNone) return st;
-  const int warps = blockDim.x >> 5;
-  const float n = static_cast<float>(width);
+  const float inv = 1.0f / static_cast<float>(width);
   Pair q = both(0.0f);
   if (kind == kLayer) {
     Pair a = both(0.0f);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) a = add2(a, v[i]);  // (zero past the row)
-    st.x = cta_sum(sum2(a), red, turn, warps) / n;
+    st.x = cta_sum(sum2(a), red, turn) * inv;
     const Pair m = both(-st.x);
     Pair z[E / 2];
 #pragma unroll
@@ -122,7 +122,7 @@ __device__ __forceinline__ float2 held_stat(int kind, int width, float eps, cons
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) q = fma2(v[i], v[i], q);
   }
-  st.y = 1.0f / sqrtf(cta_sum(sum2(q), red, turn, warps) / n + eps);
+  st.y = inv_sqrt(fmaf(cta_sum(sum2(q), red, turn), inv, eps));
   return st;
 }
 
@@ -209,6 +209,7 @@ template <typename TS, typename TB, int VEC, int E, bool FULL>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_ctas, uint32_t gate_rows) {
   using R = Row<VEC, E, FULL>;
   __shared__ Red red;
+  if (blockDim.x > 32) red.clear();
   pdl_wait();
   pdl_trigger();
   if (static_cast<int>(blockIdx.x) >= row_ctas) {
