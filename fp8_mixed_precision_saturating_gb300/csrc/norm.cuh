@@ -139,6 +139,17 @@ struct Row {
       for (int e = 0; e < E / 2; ++e) x[e] = pair(one(64 * e), one(64 * e + 32));
     }
   }
+  // parameters that a CTA keeps in shared memory, from the row's first column on
+  static __device__ __forceinline__ void load_shared(uint32_t fp32_at, int c, int left, Pair (&x)[E / 2]) {
+    static_assert(VEC == 4, "rows of whole 16 bytes");
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (in(128 * i, left)) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w) : "r"(fp32_at + 4 * c + 512 * i));
+      x[2 * i] = pair(t.x, t.y);
+      x[2 * i + 1] = pair(t.z, t.w);
+    }
+  }
   static __device__ __forceinline__ void store(float* p, int left, const Pair (&x)[E / 2]) {
 #pragma unroll
     for (int e = 0; e < E / 2; e += VEC == 4 ? 2 : 1) {
@@ -166,10 +177,45 @@ struct Row {
   }
 };
 
+constexpr int kMaxStages = 4;            // rows that a ring in shared memory holds
+constexpr int kRingBytes = 216 * 1024;   // of an SM's shared memory for its CTAs' rings
+
+// A row's columns from the ring's copy, or from global memory.
+template <bool RING, int VEC, int E, bool FULL, typename T>
+__device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* base, int64_t ld, int64_t t, int c, int left, Pair (&x)[E / 2]) {
+  if constexpr (RING) {
+    const T* p = reinterpret_cast<const T*>(held + at) + c;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const bool in = FULL || 128 * i < left;
+      if constexpr (sizeof(T) == 4) {
+        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in) q = *reinterpret_cast<const float4*>(p + 128 * i);
+        x[2 * i] = pair(q.x, q.y);
+        x[2 * i + 1] = pair(q.z, q.w);
+      } else {
+        uint2 q = make_uint2(0u, 0u);
+        if (in) q = *reinterpret_cast<const uint2*>(p + 128 * i);
+        x[2 * i] = pair_of(q.x);
+        x[2 * i + 1] = pair_of(q.y);
+      }
+    }
+  } else {
+    Row<VEC, E, FULL>::template load<true>(static_cast<const T*>(base) + t * ld + c, left, x);
+  }
+}
+
 // Sums over the warps of a CTA (up to 16), in a fixed order, the same bits on every thread. v: two halves that
 // consecutive sums take in turn, so one barrier each is enough: who writes a half again has passed the barrier after
 // everyone's read of it. Places of warps that are not there hold zero (clear), so a sum reads all sixteen without a
 // loop. A CTA of one warp needs neither.
+// Several teams of threads (threadIdx.y), each with its own row and Red, may share a CTA: the barrier is the team's.
+__device__ __forceinline__ void team_sync() {
+  if (blockDim.y == 1)
+    __syncthreads();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+}
 struct Red {
   __align__(16) float v[2][2][16];
   __device__ __forceinline__ void clear() {  // before the first sum's barrier, by the first 64 threads or fewer
@@ -199,7 +245,7 @@ __device__ __forceinline__ float cta_sum(float s, Red& red, int& turn) {
   float* r = red.v[turn][0];
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
-  __syncthreads();
+  team_sync();
   return red_sum(r);
 }
 __device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn) {
@@ -212,7 +258,7 @@ __device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn) {
     rx[threadIdx.x >> 5] = s.x;
     ry[threadIdx.x >> 5] = s.y;
   }
-  __syncthreads();
+  team_sync();
   return make_float2(red_sum(rx), red_sum(ry));
 }
 

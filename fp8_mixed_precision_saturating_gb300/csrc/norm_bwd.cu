@@ -141,37 +141,10 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
 // dn = gate g,  dgate = w sum g z + b sum g,  dw_post = sum over the gates of gate sum g z,  db_post likewise. So the
 // rows add to those two sums alone, and they are spent where the gate's row changes.
 //   pass 3: do
-constexpr int kMaxStages = 4;
-
 struct Ring {
   int stages, bytes;            // rows held, bytes of one
   int dh, r_out, dr_out, o, r;  // each tensor's place in a row; -1: not there
 };
-
-// A row's columns from the ring's copy, or from global memory.
-template <bool RING, int VEC, int E, bool FULL, typename T>
-__device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* base, int64_t ld, int64_t t, int c, int left, Pair (&x)[E / 2]) {
-  if constexpr (RING) {
-    const T* p = reinterpret_cast<const T*>(held + at) + c;
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const bool in = FULL || 128 * i < left;
-      if constexpr (sizeof(T) == 4) {
-        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in) q = *reinterpret_cast<const float4*>(p + 128 * i);
-        x[2 * i] = pair(q.x, q.y);
-        x[2 * i + 1] = pair(q.z, q.w);
-      } else {
-        uint2 q = make_uint2(0u, 0u);
-        if (in) q = *reinterpret_cast<const uint2*>(p + 128 * i);
-        x[2 * i] = pair_of(q.x);
-        x[2 * i + 1] = pair_of(q.y);
-      }
-    }
-  } else {
-    Row<VEC, E, FULL>::template load<true>(static_cast<const T*>(base) + t * ld + c, left, x);
-  }
-}
 
 // Column sums to the workspace (WIDE; they stay in L2 for the kernel that adds them up) or to dgate (aligned to 4 bytes only).
 template <int VEC, int E, bool FULL, bool WIDE>
@@ -603,8 +576,6 @@ BwdPlan bwd_plan(int64_t tokens, int64_t width) {
   p.ctas = static_cast<int>((tokens + p.rows_per - 1) / p.rows_per);
   return p;
 }
-
-constexpr int kRingBytes = 216 * 1024;  // of an SM's shared memory
 
 template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING, bool SUM>
 cudaError_t launch_kernel(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
