@@ -43,6 +43,28 @@ __device__ __forceinline__ float ue8m0_value(uint32_t byte) {
   return byte == 0u ? __uint_as_float(1u << 22) : byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
+// fl32(a / 6) for finite a >= 0 where the quotient is normal (below, both round to a zero scale): a product with the
+// reciprocal and one residual correction round as the division does (Markstein, 1990), in three instructions.
+__device__ __forceinline__ float sixth(float a) {
+  const float r = 1.0f / 6.0f, q = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-6.0f, q, a), r, q);
+}
+
+// NVFP4's scale byte and factor as group_scale gives them, with the quotients s / 1, s / 1.125, ..., s / 1.875 in
+// `table` (filled by quotient): an E4M3 value is one of those eight times a power of two, so fl32(s / c) is an entry
+// times an exact power. A division per group of 16 would be a third of a quantiser's instructions.
+__device__ __forceinline__ float quotient(float s, int i) { return __fdiv_rn(s, 1.0f + 0.125f * static_cast<float>(i)); }
+__device__ __forceinline__ uint32_t group_scale_nv(uint32_t abits, float s, const float* table, float& mul) {
+  mul = 0.0f;
+  if (abits > 0x7F800000u) return 0x7Fu;
+  const float t = sixth(fminf(__fmul_rn(__uint_as_float(abits), s), 3.402823466e38f));
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(t));
+  const uint32_t v = __float_as_uint(e4m3_value(c));
+  if (v != 0u) mul = __fmul_rn(table[(v >> 20) & 7u], __uint_as_float((254u << 23) - (v & 0x7F800000u)));
+  return c;
+}
+
 // The scale byte of a group whose largest magnitude is `a` (fp32 bits `abits`, NaN if the group
 // holds one), and the fp32 factor its elements are multiplied by before the cast (0 when they
 // are all coded as zero: a zero scale).

@@ -38,31 +38,34 @@ __global__ void __launch_bounds__(512) amax4_kernel(const uint16_t* x, int64_t r
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5), w0 = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
   uint32_t m = 0;
-  if (vec) {  // rows of 16-byte chunks; a contiguous matrix is one long row
+  if (vec) {  // whole 16-byte chunks, 8 of a lane's in flight; a contiguous matrix is one long row
     if (ld == cols) {
       cols *= rows;
       rows = 1;
     }
-    const int64_t per = (cols / 8 + 127) / 128, n = rows * per;  // 128 chunks (4 per lane) at a time
-    for (int64_t i = w0; i < n; i += warps) {
-      const int64_t r = per == 1 ? i : i / per, c = (i - r * per) * 128 + lane;
-      const uint4* row = reinterpret_cast<const uint4*>(x + r * ld);
-      uint4 v[4];
+    const int64_t n = cols / 8;
+    auto span = [&](const uint4* row, int64_t c) {  // 256 chunks of a row from c on
+      uint4 v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = c + 32 * j < cols / 8 ? __ldg(row + c + 32 * j) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 8; ++j) v[j] = c + 32 * j < n ? __ldg(row + c + 32 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m = absmax_v(m, v[j]);
-    }
+      for (int j = 0; j < 8; ++j) m = absmax_v(m, v[j]);
+    };
+    if (rows == 1)
+      for (int64_t i = w0; i * 256 < n; i += warps) span(reinterpret_cast<const uint4*>(x), i * 256 + lane);
+    else
+      for (int64_t r = w0; r < rows; r += warps)
+        for (int64_t c = 0; c < n; c += 256) span(reinterpret_cast<const uint4*>(x + r * ld), c + lane);
     m = fold2(m);
   } else {
-    const int64_t per = (cols + 255) / 256, n = rows * per;
-    for (int64_t i = w0; i < n; i += warps) {
-      const int64_t r = i / per, c = (i - r * per) * 256 + lane;
-      uint32_t v[8];
+    for (int64_t r = w0; r < rows; r += warps) {
+      for (int64_t c0 = 0; c0 < cols; c0 += 256) {
+        uint32_t v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = c + 32 * j < cols ? x[r * ld + c + 32 * j] & 0x7FFFu : 0u;
+        for (int j = 0; j < 8; ++j) v[j] = c0 + lane + 32 * j < cols ? x[r * ld + c0 + lane + 32 * j] & 0x7FFFu : 0u;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = v[j] <= 0x7F80u ? max(m, v[j]) : m;
+        for (int j = 0; j < 8; ++j) m = v[j] <= 0x7F80u ? max(m, v[j]) : m;
+      }
     }
   }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -77,14 +80,18 @@ __global__ void __launch_bounds__(512) amax4_kernel(const uint16_t* x, int64_t r
 
 // 16 elements (8 words of two bf16) times mul -> 16 codes.
 __device__ __forceinline__ uint2 cast16(const uint32_t (&w)[8], float mul) {
+  unsigned long long mm;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(mm) : "f"(mul));
   uint32_t c[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __fmul_rn(__uint_as_float(w[4 * h + i] << 16), mul);
-      v[2 * i + 1] = __fmul_rn(__uint_as_float(w[4 * h + i] & 0xFFFF0000u), mul);
+      const uint32_t t = w[4 * h + i];
+      asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%2, %3};\n\tmul.rn.f32x2 a, a, %4;\n\tmov.b64 {%0, %1}, a;\n\t}"
+          : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
+          : "f"(__uint_as_float(t << 16)), "f"(__uint_as_float(t & 0xFFFF0000u)), "l"(mm));
     }
     c[h] = fp4::cvt8_e2m1(v);
   }
@@ -99,15 +106,17 @@ constexpr int kTile = 128, kPitch = 272;  // bytes per tile row: 16 more than 25
 
 template <int FMT, bool ROWS, bool COLS, bool VEC>
 __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows, int cols, int64_t ld, QuantState st, int delayed,
-                                                     uint8_t* q, uint8_t* sf, uint8_t* qT, uint8_t* sfT, int tiles_x) {
+                                                     uint8_t* q, uint8_t* sf, uint8_t* qT, uint8_t* sfT, int tiles_x, int backwards) {
   constexpr int G = fp4::F4<FMT>::kGroup, ATOMS = FMT == 0 ? 2 : 1;
   __shared__ __align__(16) uint8_t tile[kTile * kPitch];
   __shared__ __align__(16) uint8_t s_sf[512 * ATOMS], s_sfT[512 * ATOMS];
   __shared__ __align__(16) uint8_t s_qT[COLS ? kTile * 64 : 16];
+  __shared__ float table[8];  // (NVFP4) the tensor's scale over the eight E4M3 significands
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ty = blockIdx.x / tiles_x, tx = blockIdx.x - ty * tiles_x;
+  // behind a pass for the tensor's amax the tiles are taken from the end: what that pass read last is still in L2
+  const int b = backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x, ty = b / tiles_x, tx = b - ty * tiles_x;
   const int r0 = ty * kTile, c0 = tx * kTile;
   if constexpr (VEC) {
     uint4 v[8];
@@ -135,6 +144,10 @@ __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows
     }
   }
   const float s = FMT == 0 ? tensor_scale(st, delayed != 0, blockIdx.x == 0 && tid == 0) : 1.0f;
+  if (FMT == 0 && tid < 8) table[tid] = fp4::quotient(s, tid);
+  auto group = [&](uint32_t bf16_bits, float& mul) {
+    return FMT == 0 ? fp4::group_scale_nv(bf16_bits << 16, s, table, mul) : fp4::group_scale<FMT>(bf16_bits << 16, s, mul);
+  };
   __syncthreads();
   uint32_t am = 0;  // largest magnitude of the tile (NaN included; delayed scaling records it)
   if constexpr (ROWS) {
@@ -156,7 +169,7 @@ __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows
       if constexpr (FMT == 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       am = max(am, m);
       float mul;
-      const uint32_t c = fp4::group_scale<FMT>(m << 16, s, mul);
+      const uint32_t c = group(m, mul);
       uint2 o = cast16(w, mul);
       if (c == fp4::F4<FMT>::kScaleNaN) o = make_uint2(0u, 0u);
       const int byte = c0 / 2 + 8 * g;
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows
         const uint32_t a = e ? m >> 16 : m & 0xFFFFu;
         am = max(am, a);
         float mul;
-        const uint32_t c = fp4::group_scale<FMT>(a << 16, s, mul);
+        const uint32_t c = group(a, mul);
         const int col = col0 + 2 * h + e, group = FMT == 0 ? warp : warp >> 1;
         s_sfT[(group >> 2) * 512 + 16 * (col & 31) + 4 * (col >> 5) + (group & 3)] = static_cast<uint8_t>(c);
 #pragma unroll
@@ -279,7 +292,16 @@ __global__ void __launch_bounds__(256) dequant4_kernel(const uint8_t* q, const u
     float v[8];
     fp4::e2m1_values(code[j], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], c), d);
+    for (int i = 0; i < 8; i += 2) {
+      // code * c is exact in fp32 (5 significant bits), so the tensor's scale brings the only rounding but the output's
+      asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+          : "+f"(v[i]), "+f"(v[i + 1])
+          : "f"(c));
+      if (scale_inv != nullptr)
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "+f"(v[i]), "+f"(v[i + 1])
+            : "f"(d));
+    }
     if constexpr (VEC) {
       T* at = y + m * ldy + k0;
       if (k0 + 8 <= k) {
@@ -337,9 +359,9 @@ cudaError_t launch_tiles(const void* x, int64_t rows, int64_t cols, int64_t ld, 
   const dim3 grid(static_cast<unsigned>(tx * ty));
   if (vec)
     return launch_pdl(quant4_kernel<FMT, ROWS, COLS, true>, grid, dim3(256), 0, stream, xb, static_cast<int>(rows), static_cast<int>(cols), ld, st,
-                      delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx));
+                      delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx), st.scale != nullptr && !delayed ? 1 : 0);
   return launch_pdl(quant4_kernel<FMT, ROWS, COLS, false>, grid, dim3(256), 0, stream, xb, static_cast<int>(rows), static_cast<int>(cols), ld, st,
-                    delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx));
+                    delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx), st.scale != nullptr && !delayed ? 1 : 0);
 }
 
 template <int FMT>
