@@ -139,13 +139,13 @@ struct Row {
       for (int e = 0; e < E / 2; ++e) x[e] = pair(one(64 * e), one(64 * e + 32));
     }
   }
-  // parameters that a CTA keeps in shared memory, from the row's first column on
-  static __device__ __forceinline__ void load_shared(uint32_t fp32_at, int c, int left, Pair (&x)[E / 2]) {
+  // fp32 parameters that a CTA keeps in shared memory; fp32_at: the lane's first column's address
+  static __device__ __forceinline__ void load_shared(uint32_t fp32_at, int left, Pair (&x)[E / 2]) {
     static_assert(VEC == 4, "rows of whole 16 bytes");
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
       float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (in(128 * i, left)) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w) : "r"(fp32_at + 4 * c + 512 * i));
+      if (in(128 * i, left)) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(t.x), "=f"(t.y), "=f"(t.z), "=f"(t.w) : "r"(fp32_at + 512 * i));
       x[2 * i] = pair(t.x, t.y);
       x[2 * i + 1] = pair(t.z, t.w);
     }
@@ -209,13 +209,6 @@ __device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* 
 // consecutive sums take in turn, so one barrier each is enough: who writes a half again has passed the barrier after
 // everyone's read of it. Places of warps that are not there hold zero (clear), so a sum reads all sixteen without a
 // loop. A CTA of one warp needs neither.
-// Several teams of threads (threadIdx.y), each with its own row and Red, may share a CTA: the barrier is the team's.
-__device__ __forceinline__ void team_sync() {
-  if (blockDim.y == 1)
-    __syncthreads();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
-}
 struct Red {
   __align__(16) float v[2][2][16];
   __device__ __forceinline__ void clear() {  // before the first sum's barrier, by the first 64 threads or fewer
@@ -245,7 +238,7 @@ __device__ __forceinline__ float cta_sum(float s, Red& red, int& turn) {
   float* r = red.v[turn][0];
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
-  team_sync();
+  __syncthreads();
   return red_sum(r);
 }
 __device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn) {
@@ -258,8 +251,52 @@ __device__ __forceinline__ float2 cta_sum(float2 s, Red& red, int& turn) {
     rx[threadIdx.x >> 5] = s.x;
     ry[threadIdx.x >> 5] = s.y;
   }
-  team_sync();
+  __syncthreads();
   return make_float2(red_sum(rx), red_sum(ry));
+}
+
+// The same for a team of threads (threadIdx.y) of 2 to WARPS warps that has its own row and its own Red.
+template <int WARPS>
+__device__ __forceinline__ float team_red(const float* r) {
+  const float4* q = reinterpret_cast<const float4*>(r);
+  Pair a = both(0.0f), b = both(0.0f);
+#pragma unroll
+  for (int i = 0; i < WARPS / 4; ++i) {
+    const float4 t = q[i];
+    a = add2(a, pair(t.x, t.y));
+    b = add2(b, pair(t.z, t.w));
+  }
+  return sum2(add2(a, b));
+}
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory"); }
+template <int WARPS>
+__device__ __forceinline__ float team_sum(float s, Red& red, int& turn) {
+  s = warp_sum(s);
+  float* r = red.v[turn][0];
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
+  team_sync();
+  return team_red<WARPS>(r);
+}
+template <int WARPS>
+__device__ __forceinline__ float2 team_sum(float2 s, Red& red, int& turn) {
+  s.x = warp_sum(s.x);
+  s.y = warp_sum(s.y);
+  float *rx = red.v[turn][0], *ry = red.v[turn][1];
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) {
+    rx[threadIdx.x >> 5] = s.x;
+    ry[threadIdx.x >> 5] = s.y;
+  }
+  team_sync();
+  return make_float2(team_red<WARPS>(rx), team_red<WARPS>(ry));
+}
+
+// A parameter vector kept in shared memory in fp32, by all threads of a CTA (thread tid of n): p[i] * q[i], ones where
+// there is none.
+template <typename T>
+__device__ __forceinline__ void keep_product(float* to, const float* p, const T* q, int width, int tid, int n) {
+  for (int i = tid; i < width; i += n) to[i] = (p != nullptr ? __ldg(p + i) : 1.0f) * (q != nullptr ? load(q + i) : 1.0f);
 }
 
 // 1 / sqrt(a): the approximation of the special function unit and one Newton step, within 2 units in the last place
