@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8gb.so")
-SOURCES = ["api.cu", "quant.cu", "gemm.cu", "api4.cu", "quant4.cu", "gemm4.cu", "norm_fwd.cu", "norm_fwd_ring.cu", "norm_bwd.cu"]
+SOURCES = ["api.cu", "quant.cu", "gemm.cu", "api4.cu", "quant4.cu", "gemm4.cu", "norm_fwd.cu", "norm_fwd_ring.cu", "norm_bwd.cu", "norm_bwd_ring.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

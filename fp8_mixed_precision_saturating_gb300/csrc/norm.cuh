@@ -292,11 +292,37 @@ __device__ __forceinline__ float2 team_sum(float2 s, Red& red, int& turn) {
   return make_float2(team_red<WARPS>(rx), team_red<WARPS>(ry));
 }
 
-// A parameter vector kept in shared memory in fp32, by all threads of a CTA (thread tid of n): p[i] * q[i], ones where
-// there is none.
+// A parameter vector kept in shared memory in fp32, by all threads of a CTA (thread tid of n): p[i] * q[i], `none`
+// where there is no p and ones where there is no q. width % 4 == 0.
 template <typename T>
-__device__ __forceinline__ void keep_product(float* to, const float* p, const T* q, int width, int tid, int n) {
-  for (int i = tid; i < width; i += n) to[i] = (p != nullptr ? __ldg(p + i) : 1.0f) * (q != nullptr ? load(q + i) : 1.0f);
+__device__ __forceinline__ void keep_product(float* to, const float* p, float none, const T* q, int width, int tid, int n) {
+  const bool wide = (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (reinterpret_cast<uintptr_t>(q) & (4 * sizeof(T) - 1)) == 0;
+  for (int i = 4 * tid; i < width; i += 4 * n) {
+    float a[4] = {none, none, none, none}, b[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if (wide) {
+      if (p != nullptr) {
+        const float4 t = __ldg(reinterpret_cast<const float4*>(p + i));
+        a[0] = t.x, a[1] = t.y, a[2] = t.z, a[3] = t.w;
+      }
+      if (q != nullptr) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 t = __ldg(reinterpret_cast<const float4*>(q + i));
+          b[0] = t.x, b[1] = t.y, b[2] = t.z, b[3] = t.w;
+        } else {
+          const uint2 t = __ldg(reinterpret_cast<const uint2*>(q + i));
+          const float2 u = split(pair_of(t.x)), v = split(pair_of(t.y));
+          b[0] = u.x, b[1] = u.y, b[2] = v.x, b[3] = v.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (p != nullptr) a[j] = p[i + j];
+        if (q != nullptr) b[j] = load(q + i + j);
+      }
+    }
+    *reinterpret_cast<float4*>(to + i) = make_float4(a[0] * b[0], a[1] * b[1], a[2] * b[2], a[3] * b[3]);
+  }
 }
 
 // 1 / sqrt(a): the approximation of the special function unit and one Newton step, within 2 units in the last place

@@ -5,18 +5,12 @@
 //                  dw = sum_t dy z,  db = sum_t dy
 //   g = dr_out + norm_pre'(dh; r');  dr = alpha g;  dalpha = sum g r
 //   dn = gate g;  dgate = sum over the gate's rows of g n;  do = norm_post'(dn; o)
-#include "norm.cuh"
+#include "norm_bwd.cuh"
 
 namespace fp8gb {
 namespace {
 
 using namespace norms;
-
-// CTA p takes the consecutive tokens [p R, (p + 1) R) and leaves its share of every column sum in
-// its own rows of the workspace: 4 rows for the parameters, then 2 for the gate gradient of the
-// groups that it shares with its neighbours (its first group, its last). A group inside one CTA's
-// tokens is written out by that CTA alone. A second kernel adds the shares up in CTA order.
-constexpr int kPart = 6;
 
 // Any width and alignment: the row read again for every pass over it, the column sums in the
 // workspace (which its CTA alone touches).
@@ -130,92 +124,31 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
 }
 
 // ---------------------------------------------------------------------------------------
-// A row in the registers of a CTA, the next rows on their way to shared memory
+// A row in the registers of a CTA
 // ---------------------------------------------------------------------------------------
-// Every input is read once, from a ring of rows that asynchronous bulk copies fill ahead (RING: rows of whole
-// 16 bytes) or from global memory. A thread holds the same E columns of every row, so the column sums stay in its
-// registers over all of the CTA's tokens.
+// Every input is read once. A thread holds the same E columns of every row, so the column sums stay in its registers
+// over all of the CTA's tokens.
 //   pass 1: dz and z of the norm before the next block; its row sums; dw_pre, db_pre
 //   pass 2: g, so dr and dalpha; dz and z of the norm after the block; its row sums
 // dgate, dw_post and db_post are all made of sum g z and sum g over the rows that share a gate: with n = z w + b and
 // dn = gate g,  dgate = w sum g z + b sum g,  dw_post = sum over the gates of gate sum g z,  db_post likewise. So the
 // rows add to those two sums alone, and they are spent where the gate's row changes.
 //   pass 3: do
-struct Ring {
-  int stages, bytes;            // rows held, bytes of one
-  int dh, r_out, dr_out, o, r;  // each tensor's place in a row; -1: not there
-};
-
-// Column sums to the workspace (WIDE; they stay in L2 for the kernel that adds them up) or to dgate (aligned to 4 bytes only).
-template <int VEC, int E, bool FULL, bool WIDE>
-__device__ __forceinline__ void leave(float* p, int left, const Pair (&x)[E / 2]) {
-  if constexpr (VEC == 4 && !WIDE) {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const float2 a = split(x[2 * i]), b = split(x[2 * i + 1]);
-      if (FULL || 128 * i < left) {
-        p[128 * i] = a.x;
-        p[128 * i + 1] = a.y;
-        p[128 * i + 2] = b.x;
-        p[128 * i + 3] = b.y;
-      }
-    }
-  } else if constexpr (VEC == 4) {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const float2 a = split(x[2 * i]), b = split(x[2 * i + 1]);
-      if (FULL || 128 * i < left) *reinterpret_cast<float4*>(p + 128 * i) = make_float4(a.x, a.y, b.x, b.y);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 a = split(x[i]);
-      if (64 * i < left) p[64 * i] = a.x;
-      if (64 * i + 32 < left) p[64 * i + 32] = a.y;
-    }
-  }
-}
-
 // SUM: sum dh and sum g are wanted (a bias's gradient, or the gate's where there is a bias).
-template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING, bool SUM>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per, const Ring ring) {
+template <typename TS, typename TB, int VEC, int E, bool SUM>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per) {
+  constexpr bool FULL = false;
   using R = Row<VEC, E, FULL>;
   constexpr int H = E / 2;
-  extern __shared__ __align__(16) uint8_t rows_smem[];
   __shared__ Red red;
   __shared__ double red_alpha[16];
-  __shared__ __align__(8) uint64_t bars[kMaxStages];
-  __shared__ volatile int failed[2];  // rows in turn, so that no wait of the next row is taken for this one's
   const int D = static_cast<int>(f.width), warps = blockDim.x >> 5, c = R::first(threadIdx.x >> 5, threadIdx.x & 31), left = D - c;
   const int64_t t0 = blockIdx.x * rows_per, t1 = min(t0 + rows_per, f.tokens);
-  const uint32_t bar0 = smem_u32(bars);
   if (warps > 1) red.clear();
-  if constexpr (RING) {
-    if (threadIdx.x == 0) {
-      for (int s = 0; s < ring.stages; ++s) mbar_init(bar0 + 8 * s, 1);
-      failed[0] = failed[1] = 0;
-      fence_mbar_init();
-    }
-    __syncthreads();
-  }
   pdl_wait();
   pdl_trigger();
 
-  auto fetch = [&](int64_t t, int s) {  // (thread 0) row t's inputs into stage s
-    const uint32_t dst = smem_u32(rows_smem) + s * ring.bytes, bar = bar0 + 8 * s;
-    const uint32_t nb = D * sizeof(TB), ns = D * sizeof(TS);
-    mbar_arrive_expect_tx(bar, ring.bytes);
-    if (ring.dh >= 0) bulk_load(dst + ring.dh, static_cast<const TB*>(b.dh) + t * b.ld_dh, nb, bar);
-    if (ring.r_out >= 0) bulk_load(dst + ring.r_out, static_cast<const TS*>(f.r_out) + t * f.ld_r_out, ns, bar);
-    if (ring.dr_out >= 0) bulk_load(dst + ring.dr_out, static_cast<const TS*>(b.dr_out) + t * b.ld_dr_out, ns, bar);
-    if (ring.o >= 0) bulk_load(dst + ring.o, static_cast<const TB*>(f.o) + t * f.ld_o, nb, bar);
-    if (ring.r >= 0) bulk_load(dst + ring.r, static_cast<const TS*>(f.r) + t * f.ld_r, ns, bar);
-  };
-  if (RING && threadIdx.x == 0)
-    for (int s = 0; s < ring.stages && t0 + s < t1; ++s) fetch(t0 + s, s);
-
-  int turn = 0, stage = 0;
-  uint32_t phase = 0;
+  int turn = 0;
   const float alpha = f.res_scale != nullptr ? __ldg(f.res_scale) : 1.0f, inv = 1.0f / static_cast<float>(D);
   Pair aw_pre[H], agz[H], ab_pre[SUM ? H : 1], ag[SUM ? H : 1];
   const Pair zero = both(0.0f);
@@ -235,14 +168,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     grp_end = (grp + 1) * f.gate_rows;
   }
   const int64_t grp0 = grp;
-  bool stop = false;
   for (int64_t t = t0; t < t1; ++t) {
-    const uint8_t* held = nullptr;
-    if constexpr (RING) {
-      // a wait that ran out is looked at behind this row's barrier, so that the CTA stops together
-      if (!mbar_wait(bar0 + 8 * stage, phase, f.w, DEV_ERR_WAIT_PRODUCER)) failed[(t - t0) & 1] = 1;
-      held = rows_smem + stage * ring.bytes;
-    }
     if (f.gate != nullptr && t == grp_end) {
       ++grp;
       grp_end += f.gate_rows;
@@ -252,13 +178,13 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     Pair dz[H], z[H];
     float m1 = 0.0f, q1 = 0.0f;
     if (back) {
-      row_of<RING, VEC, E, FULL, TB>(held, ring.dh, b.dh, b.ld_dh, t, c, left, dz);
+      R::template load<true>(static_cast<const TB*>(b.dh) + t * b.ld_dh + c, left, dz);
       if constexpr (SUM) {
 #pragma unroll
         for (int i = 0; i < H; ++i) ab_pre[i] = add2(ab_pre[i], dz[i]);
       }
       if (normed) {
-        row_of<RING, VEC, E, FULL, TS>(held, ring.r_out, f.r_out, f.ld_r_out, t, c, left, z);
+        R::template load<true>(static_cast<const TS*>(f.r_out) + t * f.ld_r_out + c, left, z);
         const Pair m = both(-pre.x), rstd = both(pre.y);
         if (f.pre == kLayer) {
 #pragma unroll
@@ -305,7 +231,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     {
       const Pair rstd = both(pre.y);
       if (b.dr_out != nullptr) {
-        row_of<RING, VEC, E, FULL, TS>(held, ring.dr_out, b.dr_out, b.ld_dr_out, t, c, left, z);
+        R::template load<true>(static_cast<const TS*>(b.dr_out) + t * b.ld_dr_out + c, left, z);
 #pragma unroll
         for (int i = 0; i < H; ++i) dz[i] = fma2(dz[i], rstd, z[i]);
       } else {
@@ -315,7 +241,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     }
     R::clear(dz, left);
     if (b.dres_scale != nullptr) {
-      row_of<RING, VEC, E, FULL, TS>(held, ring.r, f.r, f.ld_r, t, c, left, z);
+      R::template load<true>(static_cast<const TS*>(f.r) + t * f.ld_r + c, left, z);
       Pair s = zero;
 #pragma unroll
       for (int i = 0; i < H; ++i) s = fma2(dz[i], z[i], s);
@@ -331,7 +257,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
     }
     float m2 = 0.0f, q2 = 0.0f;
     if (block) {
-      row_of<RING, VEC, E, FULL, TB>(held, ring.o, f.o, f.ld_o, t, c, left, z);
+      R::template load<true>(static_cast<const TB*>(f.o) + t * f.ld_o + c, left, z);
       if (f.post != kNone) {
         if (f.post == kLayer) {
           const Pair m = both(-post.x);
@@ -374,19 +300,6 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
         q2 = s.y * inv;
       } else {
         q2 = cta_sum(sum2(sq), red, turn) * inv;
-      }
-      if (RING && warps == 1) __syncthreads();  // (its sum needs no barrier, its stage does)
-    } else if constexpr (RING) {
-      __syncthreads();
-    }
-    if constexpr (RING) {
-      // a barrier of this row is behind every read of its stage: a later row may land there
-      stop = failed[(t - t0) & 1] != 0;
-      if (stop) break;
-      if (threadIdx.x == 0 && t + ring.stages < t1) fetch(t + ring.stages, stage);
-      if (++stage == ring.stages) {
-        stage = 0;
-        phase ^= 1u;
       }
     }
     if (b.dO != nullptr) {
@@ -450,11 +363,6 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
         agz[i] = zero;
         if constexpr (SUM) ag[i] = zero;
       }
-    }
-  }
-  if (RING && threadIdx.x == 0 && stop) {  // copies in flight land (microseconds) before the CTA can exit
-    const unsigned long long w0 = globaltimer_ns();
-    while (globaltimer_ns() - w0 < 200000ull) {
     }
   }
   if (b.dw_pre != nullptr) leave<VEC, E, FULL, true>(mine + c, left, aw_pre);
@@ -558,105 +466,53 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_bwd_reduce_kernel(cons
   }
 }
 
-// The split of the tokens, from the sizes alone: CTAs of a row each, enough per SM for some 512 threads.
-struct BwdPlan {
-  int ctas, threads, per_sm;
-  int64_t rows_per;
-};
-
-int columns_of(int64_t width) { return width <= 2048 ? 8 : 16; }  // per thread
-
-BwdPlan bwd_plan(int64_t tokens, int64_t width) {
-  BwdPlan p;
-  const int64_t per = 32 * columns_of(width);
-  p.threads = width <= 8192 ? static_cast<int>((width + per - 1) / per) * 32 : kThreads;
-  p.per_sm = p.threads > 292 ? 1 : p.threads > 195 ? 2 : p.threads > 146 ? 3 : 4;  // (some 112 registers each)
-  const int64_t most = static_cast<int64_t>(p.per_sm) * num_sms();
-  p.rows_per = (tokens + most - 1) / most;
-  p.ctas = static_cast<int>((tokens + p.rows_per - 1) / p.rows_per);
-  return p;
-}
-
-template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING, bool SUM>
-cudaError_t launch_kernel(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
-  if constexpr (RING) {
-    static bool done[64] = {};  // the limit is per device; setting it twice is harmless
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
-      e = cudaFuncSetAttribute(norm_bwd_kernel<TS, TB, VEC, E, FULL, RING, SUM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-      if (e == cudaSuccess && dev < 64) done[dev] = true;
-    }
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(norm_bwd_kernel<TS, TB, VEC, E, FULL, RING, SUM>, dim3(pl.ctas), dim3(pl.threads), RING ? ring.stages * ring.bytes : 0, stream, f, b, part,
-                    part_alpha, pl.rows_per, ring);
-}
-
-template <typename TS, typename TB, int VEC, int E, bool FULL, bool RING>
-cudaError_t launch_sums(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, const Ring& ring, cudaStream_t stream) {
-  if (b.db_pre != nullptr || b.db_post != nullptr || (b.dgate != nullptr && f.b_post != nullptr))
-    return launch_kernel<TS, TB, VEC, E, FULL, RING, true>(f, b, pl, part, part_alpha, ring, stream);
-  return launch_kernel<TS, TB, VEC, E, FULL, RING, false>(f, b, pl, part, part_alpha, ring, stream);
+template <typename TS, typename TB, int VEC, int E>
+cudaError_t launch_rows(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, cudaStream_t stream) {
+  if (sums_wanted(f, b))
+    return launch_pdl(norm_bwd_kernel<TS, TB, VEC, E, true>, dim3(pl.parts), dim3(pl.threads), 0, stream, f, b, part, part_alpha, pl.rows_per);
+  return launch_pdl(norm_bwd_kernel<TS, TB, VEC, E, false>, dim3(pl.parts), dim3(pl.threads), 0, stream, f, b, part, part_alpha, pl.rows_per);
 }
 
 template <typename TS, typename TB>
 cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t stream) {
   const BwdPlan pl = bwd_plan(f.tokens, f.width);
   double* part_alpha = static_cast<double*>(ws);
-  float* part = reinterpret_cast<float*>(part_alpha + pl.ctas + (pl.ctas & 1));
+  float* part = reinterpret_cast<float*>(part_alpha + pl.parts + (pl.parts & 1));
   const int64_t ss = sizeof(TS), bs = sizeof(TB);
-  cudaError_t e;
-  if (f.width > 8192) {
-    e = launch_pdl(norm_bwd_any_kernel<TS, TB>, dim3(pl.ctas), dim3(kThreads), 0, stream, f, b, part, part_alpha, pl.rows_per);
+  bool taken = false;
+  cudaError_t e = launch_norm_bwd_ring(f, b, pl, part, part_alpha, stream, &taken);
+  if (e != cudaSuccess) return e;
+  if (taken) {
+  } else if (f.width > 8192) {
+    e = launch_pdl(norm_bwd_any_kernel<TS, TB>, dim3(pl.parts), dim3(kThreads), 0, stream, f, b, part, part_alpha, pl.rows_per);
   } else {
-    Ring ring{0, 0, -1, -1, -1, -1, -1};
-    bool vec = f.width * bs % 16 == 0 && f.width * ss % 16 == 0;
-    auto place = [&](bool there, const void* p, int64_t ld, int64_t size, int& at) {
-      if (!there) return;
-      at = ring.bytes;
-      ring.bytes += static_cast<int>(f.width * size);
-      vec = vec && rows_aligned(p, ld, size, 16);
-    };
-    place(b.dh != nullptr, b.dh, b.ld_dh, bs, ring.dh);
-    place(b.dh != nullptr && f.pre != kNone, f.r_out, f.ld_r_out, ss, ring.r_out);
-    place(b.dr_out != nullptr, b.dr_out, b.ld_dr_out, ss, ring.dr_out);
-    place(f.o != nullptr, f.o, f.ld_o, bs, ring.o);
-    place(b.dres_scale != nullptr, f.r, f.ld_r, ss, ring.r);
-    vec = vec && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) && rows_aligned(b.dr, b.ld_dr, ss, 4 * ss) && rows_aligned(b.dO, b.ld_do, bs, 4 * bs) &&
-          rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16);
-    const bool eight = columns_of(f.width) == 8;
-    if (vec) {
-      const int64_t room = kRingBytes / pl.per_sm / ring.bytes;
-      ring.stages = static_cast<int>(room < 1 ? 1 : room < kMaxStages ? room : kMaxStages);
-      const bool full = f.width % (eight ? 256 : 512) == 0;
-      e = eight ? (full ? launch_sums<TS, TB, 4, 8, true, true>(f, b, pl, part, part_alpha, ring, stream)
-                        : launch_sums<TS, TB, 4, 8, false, true>(f, b, pl, part, part_alpha, ring, stream))
-                : (full ? launch_sums<TS, TB, 4, 16, true, true>(f, b, pl, part, part_alpha, ring, stream)
-                        : launch_sums<TS, TB, 4, 16, false, true>(f, b, pl, part, part_alpha, ring, stream));
-    } else {
-      e = eight ? launch_sums<TS, TB, 1, 8, false, false>(f, b, pl, part, part_alpha, ring, stream)
-              : launch_sums<TS, TB, 1, 16, false, false>(f, b, pl, part, part_alpha, ring, stream);
-    }
+    const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.ld_r_out, ss, 4 * ss) &&
+                     rows_aligned(f.o, f.ld_o, bs, 4 * bs) && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) && rows_aligned(b.dh, b.ld_dh, bs, 4 * bs) &&
+                     rows_aligned(b.dr_out, b.ld_dr_out, ss, 4 * ss) && rows_aligned(b.dr, b.ld_dr, ss, 4 * ss) && rows_aligned(b.dO, b.ld_do, bs, 4 * bs) &&
+                     rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16);
+    if (columns_of(f.width) == 8)
+      e = vec ? launch_rows<TS, TB, 4, 8>(f, b, pl, part, part_alpha, stream) : launch_rows<TS, TB, 1, 8>(f, b, pl, part, part_alpha, stream);
+    else
+      e = vec ? launch_rows<TS, TB, 4, 16>(f, b, pl, part, part_alpha, stream) : launch_rows<TS, TB, 1, 16>(f, b, pl, part, part_alpha, stream);
   }
   if (e != cudaSuccess) return e;
   int64_t shared = 0;  // gate groups that may be shared
-  if (b.dgate != nullptr && pl.ctas > 1) {
+  if (b.dgate != nullptr && pl.parts > 1) {
     const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
-    shared = groups < pl.ctas ? groups : pl.ctas - 1;
+    shared = groups < pl.parts ? groups : pl.parts - 1;
   }
   const int cols = f.width % 4 == 0 ? 128 : 32;
   const dim3 grid(static_cast<unsigned>((f.width + cols - 1) / cols), static_cast<unsigned>(4 + (shared < 32 ? shared : 32)));
   return launch_pdl(cols == 128 ? norm_bwd_reduce_kernel<4> : norm_bwd_reduce_kernel<1>, grid, dim3(32 * kReduceWarps), 0, stream, f, b, part, part_alpha,
-                    pl.rows_per, pl.ctas);
+                    pl.rows_per, pl.parts);
 }
 
 }  // namespace
 
 int64_t norm_bwd_workspace_bytes(const NormFwd& f) {
   if (f.tokens == 0 || f.width == 0) return 0;
-  const int64_t ctas = bwd_plan(f.tokens, f.width).ctas;
-  return ctas * kPart * f.width * 4 + (ctas + 1) / 2 * 16;
+  const int64_t parts = bwd_plan(f.tokens, f.width).parts;
+  return parts * kPart * f.width * 4 + (parts + 1) / 2 * 16;
 }
 
 cudaError_t launch_norm_bwd(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t stream) {

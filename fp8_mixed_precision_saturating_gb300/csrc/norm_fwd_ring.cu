@@ -90,13 +90,11 @@ __global__ void __launch_bounds__(MOST, 1) norm_fwd_ring_kernel(const NormFwd f,
   float* par = reinterpret_cast<float*>(smem + teams * stages * bytes);  // w_post, w_pre, b_post, b_pre
   {
     const TB* one = grouped ? nullptr : gate;
-    keep_product(par, f.w_post, one, D, tid, threads);
-    keep_product(par + D, f.w_pre, static_cast<const TB*>(nullptr), D, tid, threads);
+    keep_product(par, f.w_post, 1.0f, one, D, tid, threads);
+    keep_product(par + D, f.w_pre, 1.0f, static_cast<const TB*>(nullptr), D, tid, threads);
     if constexpr (BIAS) {
-      for (int i = tid; i < D; i += threads) {
-        par[2 * D + i] = f.b_post != nullptr ? f.b_post[i] * (one != nullptr ? load(one + i) : 1.0f) : 0.0f;
-        par[3 * D + i] = f.b_pre != nullptr ? f.b_pre[i] : 0.0f;
-      }
+      keep_product(par + 2 * D, f.b_post, 0.0f, one, D, tid, threads);
+      keep_product(par + 3 * D, f.b_pre, 0.0f, static_cast<const TB*>(nullptr), D, tid, threads);
     }
   }
   if (f.hq != nullptr) fill_scales(f, blockIdx.x * static_cast<int64_t>(threads) + tid, static_cast<int64_t>(gridDim.x) * threads);
