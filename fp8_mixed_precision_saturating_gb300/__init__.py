@@ -12,6 +12,7 @@ built (``python -c "import __graft_entry__ as g; g.build()"``).
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,7 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libfp8gb.so is missing at {LIB_PATH}: build it first (fp8_mixed_precision_saturating_gb300._build.build())")
 
 lib = ctypes.CDLL(LIB_PATH)
+_fastcall = None
 
 # enums (include/fp8gb.h)
 FP8_OK, FP8_ERR_INVALID_ARG, FP8_ERR_UNSUPPORTED, FP8_ERR_ALIGNMENT, FP8_ERR_CUDA, FP8_ERR_TIMEOUT = range(6)
@@ -197,6 +199,8 @@ def _find_current_stream():
     except AttributeError:
         return lambda: torch.cuda.current_stream().cuda_stream
     torch.cuda.init()
+    if _fastcall is not None:
+        _fastcall.use_torch(raw, device)
     return lambda: raw(device())
 
 
@@ -482,3 +486,17 @@ def fp8_set_wait_limit_ns(ns: int):
 def fp8_selftest_wait_timeout(limit_ns: int, stream=None) -> int:
     """Returns the raw status (FP8_ERR_TIMEOUT is the expected result)."""
     return lib.fp8_selftest_wait_timeout(limit_ns, _stream(stream))
+
+
+# ---------------------------------------------------------------------------------------
+# the same calls in C (csrc/fastcall.c), where the host could build them
+# ---------------------------------------------------------------------------------------
+try:
+    _fastcall = importlib.import_module(__name__ + "._fastcall")
+except ImportError:
+    pass
+if _fastcall is not None:
+    _NAMES = ("fp4_quantize", "fp4_dequantize", "fp4_scaled_mm", "fp8_block_norm_fwd", "fp8_block_norm_bwd")
+    _fastcall.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NAMES), _check, _stream)
+    _by_ctypes = {n: globals()[n] for n in _NAMES}  # (what a host without Python.h calls)
+    globals().update({n: getattr(_fastcall, n) for n in _NAMES})

@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,6 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8gb.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "api4.cu", "quant4.cu", "gemm4.cu", "norm_fwd.cu", "norm_fwd_ring.cu", "norm_bwd.cu", "norm_bwd_ring.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
@@ -31,8 +33,27 @@ def _inputs():
     return files
 
 
+def python_header() -> str | None:
+    """The folder of Python.h, where the host has it and a C compiler."""
+    d = sysconfig.get_paths()["include"]
+    return d if os.path.exists(os.path.join(d, "Python.h")) and shutil.which("gcc") else None
+
+
+def build_fastcall():
+    """_fastcall.so: the binding's calls in C (csrc/fastcall.c); without Python.h the ctypes wrappers are used alone."""
+    include = python_header()
+    if include is None:
+        return
+    tmp = FASTCALL + ".tmp"
+    r = subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE, os.path.join(CSRC, "fastcall.c"), "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on fastcall.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or (python_header() and not os.path.exists(FASTCALL)):
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -64,6 +85,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    build_fastcall()
     os.replace(tmp, LIB)
     return LIB
 

@@ -732,6 +732,34 @@ struct Plan {
   int bn, splits;
 };
 
+// How many clusters of each number of splits the current device holds at once, asked once.
+template <int FMT, typename T>
+struct Clusters {
+  int pair[Pair<FMT>::MOST_SPLITS + 1], one[9];  // CTA pairs; single CTAs with 128-wide tiles
+  static cudaError_t of(const Clusters** out) {
+    static Clusters all[64];
+    static bool done[64] = {};
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!done[dev]) {
+      using P = Pair<FMT>;
+      using S = Split<FMT, 128>;
+      for (int s = 1; s <= P::MOST_SPLITS && e == cudaSuccess; ++s)
+        e = s == 1 ? prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, false>>(P::SMEM, P::THREADS, 2, &all[dev].pair[s])
+                   : prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, true>>(P::SMEM, P::THREADS, 2 * s, &all[dev].pair[s]);
+      for (int s = 1; s <= 8 && e == cudaSuccess; ++s) e = prepare<mm4_split_kernel<FMT, 128, T>>(S::SMEM, S::THREADS, s, &all[dev].one[s]);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+    *out = &all[dev];
+    return cudaSuccess;
+  }
+};
+
 // The cheapest plan. Up to 64 rows of A the weights' bytes and the latency decide: one CTA per SM (more of them measured
 // slower: 1 x 4096 x 4096 took 3.9 us in 128 CTAs, 4.4 in 256), at least two stages each. Above, the measured times of
 // a stage and of what comes before and after the stages (us, GB300): a pair does 256 x 256 x 256 in 0.27, a CTA
@@ -748,6 +776,9 @@ cudaError_t choose(int64_t M, int64_t N, int64_t K, Plan* plan) {
     plan->splits = static_cast<int>(s < 1 ? 1 : s > 8 ? 8 : s);
     return cudaSuccess;
   }
+  const Clusters<FMT, T>* fit = nullptr;
+  const cudaError_t e = Clusters<FMT, T>::of(&fit);
+  if (e != cudaSuccess) return e;
   float best = 0.0f;
   auto offer = [&](int bn, int splits, float us) {
     if (plan->splits != 0 && us >= best) return;
@@ -756,21 +787,10 @@ cudaError_t choose(int64_t M, int64_t N, int64_t K, Plan* plan) {
   };
   *plan = {0, 0};
   const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), small = (M + 127) / 128 * cols;
-  for (int s = 1; s <= Pair<FMT>::MOST_SPLITS && s <= stages; ++s) {
-    int clusters = 0;
-    const cudaError_t e = s == 1 ? prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, false>>(Pair<FMT>::SMEM, Pair<FMT>::THREADS, 2, &clusters)
-                                 : prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, true>>(Pair<FMT>::SMEM, Pair<FMT>::THREADS, 2 * s, &clusters);
-    if (e != cudaSuccess) return e;
-    if (s > 1 && tiles > clusters) break;
-    offer(0, s, 4.3f + 0.27f * static_cast<float>((stages + s - 1) / s * ((tiles + clusters - 1) / clusters)) + (s > 1 ? 3.6f : 0.0f));
-  }
-  for (int s = 1; s <= 8 && s <= stages && small <= sms; ++s) {
-    int clusters = 0;
-    const cudaError_t e = prepare<mm4_split_kernel<FMT, 128, T>>(Split<FMT, 128>::SMEM, Split<FMT, 128>::THREADS, s, &clusters);
-    if (e != cudaSuccess) return e;
-    if (s > 1 && small > clusters) break;
+  for (int s = 1; s <= Pair<FMT>::MOST_SPLITS && s <= stages && (s == 1 || tiles <= fit->pair[s]); ++s)
+    offer(0, s, 4.3f + 0.27f * static_cast<float>((stages + s - 1) / s * ((tiles + fit->pair[s] - 1) / fit->pair[s])) + (s > 1 ? 3.6f : 0.0f));
+  for (int s = 1; s <= 8 && s <= stages && small <= (s == 1 ? sms : fit->one[s]); ++s)
     offer(128, s, 4.0f + 0.31f * static_cast<float>((stages + s - 1) / s) + (s > 1 ? 1.2f : 2.0f));
-  }
   return cudaSuccess;
 }
 
