@@ -258,6 +258,96 @@ __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows
   }
 }
 
+// Along the rows alone, from 16-byte aligned rows: no tile and no barrier. A lane takes 16 neighbouring elements of 4
+// rows 32 apart (their scale words are neighbours in an atom), a warp 512 columns; all loads are in flight at once.
+template <int FMT>
+__global__ void __launch_bounds__(256) quant4_rows_kernel(const uint16_t* x, int rows, int cols, int64_t ld, QuantState st, int delayed, uint8_t* q,
+                                                          uint8_t* sf, int pieces, int backwards) {
+  __shared__ float table[8];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const float s = FMT == 0 ? tensor_scale(st, delayed != 0, blockIdx.x == 0 && tid == 0) : 1.0f;
+  const int b = backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const int64_t item = b * 8ll + (tid >> 5), line = item / pieces;  // (128-row block, row in 32), piece of 512 columns
+  const int c0 = static_cast<int>(item - line * pieces) * 512 + 16 * lane;
+  const int64_t m0 = (line >> 5) * 128 + (line & 31);
+  uint4 v[4][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[j][h] = make_uint4(0, 0, 0, 0);
+      const int c = c0 + 8 * h;
+      if (m0 + 32 * j < rows) {
+        const uint16_t* row = x + (m0 + 32 * j) * ld;
+        if (c + 8 <= cols) {
+          v[j][h] = __ldcs(reinterpret_cast<const uint4*>(row + c));
+        } else if (c < cols) {  // a row's last elements: what follows them is not read
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v[j][h]);
+#pragma unroll
+          for (int i = 0; i < 7; ++i)
+            if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+        }
+      }
+    }
+  if constexpr (FMT == 0) {
+    if (tid < 8) table[tid] = fp4::quotient(s, tid);
+    __syncthreads();
+  }
+  const int64_t pitch = fp4::row_bytes(cols), atoms = fp4::atoms_along(FMT, cols);
+  uint32_t am = 0, scales = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w[8] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w, v[j][1].x, v[j][1].y, v[j][1].z, v[j][1].w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    if constexpr (FMT == 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    am = max(am, m);
+    float mul;
+    const uint32_t c = FMT == 0 ? fp4::group_scale_nv(m << 16, s, table, mul) : fp4::group_scale<FMT>(m << 16, s, mul);
+    uint2 o = cast16(w, mul);
+    if (c == fp4::F4<FMT>::kScaleNaN) o = make_uint2(0u, 0u);
+    if (m0 + 32 * j < rows && c0 / 2 < pitch) *reinterpret_cast<uint2*>(q + (m0 + 32 * j) * pitch + c0 / 2) = o;
+    scales |= c << (8 * j);
+  }
+  // four groups' lanes hold a byte of each of the four rows; afterwards each of them holds a row's word of four groups
+  constexpr int STEP = FMT == 0 ? 1 : 2;  // lanes per group
+  const int at = (lane / STEP) & 3;
+  const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, scales, STEP);
+  uint32_t t = at & 1 ? __byte_perm(o1, scales, 0x7351) : __byte_perm(scales, o1, 0x6240);  // rows {1, 3} or {0, 2} of two groups
+  const uint32_t o2 = __shfl_xor_sync(0xFFFFFFFFu, t, 2 * STEP);
+  t = at & 2 ? __byte_perm(o2, t, 0x7632) : __byte_perm(t, o2, 0x5410);
+  const int64_t atom = (c0 / fp4::F4<FMT>::kGroup) >> 2;
+  if (m0 < (rows + 127ll) / 128 * 128 && atom < atoms && lane % STEP == 0)
+    *reinterpret_cast<uint32_t*>(sf + ((m0 >> 7) * atoms + atom) * 512 + 16 * (m0 & 31) + 4 * at) = t;
+  if (FMT == 0 && delayed && st.scale != nullptr && *st.hist_count > 0) {
+    __shared__ uint32_t s_am;
+    if (tid == 0) s_am = 0;
+    if (__syncthreads_or(am > 0x7F80u)) {  // a CTA with a NaN looks at its elements again, without it
+      am = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w[4] = {v[j][h].x, v[j][h].y, v[j][h].z, v[j][h].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+            if (lo <= 0x7F80u) am = max(am, lo);
+            if (hi <= 0x7F80u) am = max(am, hi);
+          }
+        }
+    }
+    am = __reduce_max_sync(0xFFFFFFFFu, am);
+    if (lane == 0) atomicMax(&s_am, am);
+    __syncthreads();
+    if (tid == 0) atomic_max_amax(st.amax_cur, s_am);
+  }
+}
+
 // A warp takes 256 elements of 4 rows 32 apart (their scale words are 16 bytes of an atom), a lane 8 of each.
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) dequant4_kernel(const uint8_t* q, const uint8_t* sf, int64_t mn, int64_t k, const float* scale_inv, T* y,
@@ -368,7 +458,14 @@ template <int FMT>
 cudaError_t launch_ways(const void* x, int64_t rows, int64_t cols, int64_t ld, const QuantState& st, bool delayed, bool vec, void* q, void* sf,
                         void* qT, void* sfT, cudaStream_t stream) {
   if (q != nullptr && qT != nullptr) return launch_tiles<FMT, true, true>(x, rows, cols, ld, st, delayed, vec, q, sf, qT, sfT, stream);
-  if (q != nullptr) return launch_tiles<FMT, true, false>(x, rows, cols, ld, st, delayed, vec, q, sf, qT, sfT, stream);
+  if (q != nullptr && vec) {
+    const int64_t pieces = (cols + 511) / 512, grid = ((rows + 127) / 128 * 32 * pieces + 7) / 8;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;  // (more than the memory holds)
+    return launch_pdl(quant4_rows_kernel<FMT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, static_cast<const uint16_t*>(x),
+                      static_cast<int>(rows), static_cast<int>(cols), ld, st, delayed ? 1 : 0, static_cast<uint8_t*>(q), static_cast<uint8_t*>(sf),
+                      static_cast<int>(pieces), st.scale != nullptr && !delayed ? 1 : 0);
+  }
+  if (q != nullptr) return launch_tiles<FMT, true, false>(x, rows, cols, ld, st, delayed, false, q, sf, qT, sfT, stream);
   return launch_tiles<FMT, false, true>(x, rows, cols, ld, st, delayed, vec, q, sf, qT, sfT, stream);
 }
 
