@@ -98,7 +98,7 @@ __device__ __forceinline__ uint2 cast16(const uint32_t (&w)[8], float mul) {
   return make_uint2(c[0], c[1]);
 }
 
-// One 128 x 128 tile of x per CTA, read once into shared memory (zero past the matrix, which gives the padding's
+// Both ways, or rows that are not aligned: one 128 x 128 tile of x per CTA, read once into shared memory (zero past the matrix, which gives the padding's
 // codes and scales their values without a branch), then quantised along its rows (ROWS) and down its columns
 // (COLS). Either way the tile is 64 bytes of each of 128 operand rows and whole scale atoms (2 for NVFP4, 1 for
 // MXFP4), so codes leave in 64-byte pieces and scales in 512-byte ones.
@@ -348,6 +348,109 @@ __global__ void __launch_bounds__(256) quant4_rows_kernel(const uint16_t* x, int
   }
 }
 
+// Down the columns alone, from 16-byte aligned rows: 128 rows by 128 columns per CTA, read straight into registers (a
+// warp takes 16 rows, a lane 4 columns; MXFP4: 32 rows of half the columns, a lane 2); only codes and scales pass
+// through shared memory, to leave in 64- and 512-byte pieces.
+template <int FMT>
+__global__ void __launch_bounds__(256) quant4_cols_kernel(const uint16_t* x, int rows, int cols, int64_t ld, QuantState st, int delayed, uint8_t* qT,
+                                                          uint8_t* sfT, int tiles_x, int backwards) {
+  constexpr int G = fp4::F4<FMT>::kGroup, ATOMS = FMT == 0 ? 2 : 1, PAIRS = FMT == 0 ? 2 : 1;  // pairs of columns per lane
+  __shared__ __align__(16) uint8_t s_sfT[512 * ATOMS];
+  __shared__ __align__(16) uint8_t s_qT[kTile * 64];
+  __shared__ float table[8];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x, ty = b / tiles_x, tx = b - ty * tiles_x;
+  const int r0 = ty * kTile, c0 = tx * kTile;
+  const int k0 = FMT == 0 ? 16 * warp : 32 * (warp >> 1), col0 = FMT == 0 ? 4 * lane : 64 * (warp & 1) + 2 * lane;
+  uint32_t v[G][PAIRS];
+  {
+    const uint16_t* at = x + (r0 + k0) * ld + c0 + col0;
+    const bool whole = c0 + col0 + 2 * PAIRS <= cols;
+#pragma unroll
+    for (int i = 0; i < G; ++i, at += ld) {
+      const bool in = r0 + k0 + i < rows;
+#pragma unroll
+      for (int h = 0; h < PAIRS; ++h) v[i][h] = 0;
+      if (in && whole) {
+        if constexpr (FMT == 0) {
+          const uint2 t = __ldcs(reinterpret_cast<const uint2*>(at));
+          v[i][0] = t.x;
+          v[i][PAIRS - 1] = t.y;
+        } else {
+          v[i][0] = __ldcs(reinterpret_cast<const uint32_t*>(at));
+        }
+      } else if (in) {  // the last columns
+#pragma unroll
+        for (int e = 0; e < 2 * PAIRS; ++e)
+          if (c0 + col0 + e < cols) v[i][e >> 1] |= static_cast<uint32_t>(at[e]) << (16 * (e & 1));
+      }
+    }
+  }
+  const float s = FMT == 0 ? tensor_scale(st, delayed != 0, blockIdx.x == 0 && tid == 0) : 1.0f;
+  if constexpr (FMT == 0) {
+    if (tid < 8) table[tid] = fp4::quotient(s, tid);
+    __syncthreads();
+  }
+  uint32_t am = 0;
+#pragma unroll
+  for (int h = 0; h < PAIRS; ++h) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < G; ++i) m = __vmaxu2(m, v[i][h] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t a = e ? m >> 16 : m & 0xFFFFu;
+      am = max(am, a);
+      float mul;
+      const uint32_t c = FMT == 0 ? fp4::group_scale_nv(a << 16, s, table, mul) : fp4::group_scale<FMT>(a << 16, s, mul);
+      const int col = col0 + 2 * h + e, grp = k0 / G;
+      s_sfT[(grp >> 2) * 512 + 16 * (col & 31) + 4 * (col >> 5) + (grp & 3)] = static_cast<uint8_t>(c);
+#pragma unroll
+      for (int t = 0; t < G / 16; ++t) {
+        uint32_t w[8];  // the column's elements two by two
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = __byte_perm(v[16 * t + 2 * k][h], v[16 * t + 2 * k + 1][h], e ? 0x7632 : 0x5410);
+        uint2 o = cast16(w, mul);
+        if (c == fp4::F4<FMT>::kScaleNaN) o = make_uint2(0u, 0u);
+        // 8-byte piece k0 / 16 + t of the column's 64 bytes, moved by its column so that lanes use other banks
+        *reinterpret_cast<uint2*>(s_qT + 64 * col + 8 * (((k0 >> 4) + t) ^ ((col >> 2) & 7))) = o;
+      }
+    }
+  }
+  if (FMT == 0 && delayed && st.scale != nullptr && *st.hist_count > 0) {
+    __shared__ uint32_t s_am;
+    if (tid == 0) s_am = 0;
+    if (__syncthreads_or(am > 0x7F80u)) {  // a CTA with a NaN looks at its elements again, without it
+      am = 0;
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int h = 0; h < PAIRS; ++h) {
+          const uint32_t lo = v[i][h] & 0x7FFFu, hi = (v[i][h] >> 16) & 0x7FFFu;
+          if (lo <= 0x7F80u) am = max(am, lo);
+          if (hi <= 0x7F80u) am = max(am, hi);
+        }
+    }
+    am = __reduce_max_sync(0xFFFFFFFFu, am);
+    if (lane == 0) atomicMax(&s_am, am);
+    __syncthreads();
+    if (tid == 0) atomic_max_amax(st.amax_cur, s_am);
+  }
+  __syncthreads();
+  const int64_t atoms = fp4::atoms_along(FMT, rows), pitch = fp4::row_bytes(rows);
+  if (tid < 32 * ATOMS && ty * ATOMS + (tid >> 5) < atoms)
+    reinterpret_cast<uint4*>(sfT + (tx * atoms + ty * ATOMS) * 512)[tid] = reinterpret_cast<const uint4*>(s_sfT)[tid];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int col = 64 * i + (tid >> 2), piece = tid & 3, sw = (col >> 2) & 7, byte = r0 / 2 + 16 * piece;
+    const uint2 lo = *reinterpret_cast<const uint2*>(s_qT + 64 * col + 8 * ((2 * piece) ^ sw));
+    const uint2 hi = *reinterpret_cast<const uint2*>(s_qT + 64 * col + 8 * ((2 * piece + 1) ^ sw));
+    if (c0 + col < cols && byte < pitch) *reinterpret_cast<uint4*>(qT + (c0 + col) * pitch + byte) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+}
+
 // A warp takes 256 elements of 4 rows 32 apart (their scale words are 16 bytes of an atom), a lane 8 of each.
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) dequant4_kernel(const uint8_t* q, const uint8_t* sf, int64_t mn, int64_t k, const float* scale_inv, T* y,
@@ -447,9 +550,11 @@ cudaError_t launch_tiles(const void* x, int64_t rows, int64_t cols, int64_t ld, 
   auto* xb = static_cast<const uint16_t*>(x);
   auto b = [](void* p) { return static_cast<uint8_t*>(p); };
   const dim3 grid(static_cast<unsigned>(tx * ty));
-  if (vec)
-    return launch_pdl(quant4_kernel<FMT, ROWS, COLS, true>, grid, dim3(256), 0, stream, xb, static_cast<int>(rows), static_cast<int>(cols), ld, st,
-                      delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx), st.scale != nullptr && !delayed ? 1 : 0);
+  if constexpr (ROWS && COLS) {
+    if (vec)
+      return launch_pdl(quant4_kernel<FMT, ROWS, COLS, true>, grid, dim3(256), 0, stream, xb, static_cast<int>(rows), static_cast<int>(cols), ld, st,
+                        delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx), st.scale != nullptr && !delayed ? 1 : 0);
+  }
   return launch_pdl(quant4_kernel<FMT, ROWS, COLS, false>, grid, dim3(256), 0, stream, xb, static_cast<int>(rows), static_cast<int>(cols), ld, st,
                     delayed ? 1 : 0, b(q), b(sf), b(qT), b(sfT), static_cast<int>(tx), st.scale != nullptr && !delayed ? 1 : 0);
 }
@@ -466,7 +571,14 @@ cudaError_t launch_ways(const void* x, int64_t rows, int64_t cols, int64_t ld, c
                       static_cast<int>(pieces), st.scale != nullptr && !delayed ? 1 : 0);
   }
   if (q != nullptr) return launch_tiles<FMT, true, false>(x, rows, cols, ld, st, delayed, false, q, sf, qT, sfT, stream);
-  return launch_tiles<FMT, false, true>(x, rows, cols, ld, st, delayed, vec, q, sf, qT, sfT, stream);
+  if (vec) {
+    const int64_t tx = (cols + kTile - 1) / kTile, grid = tx * ((rows + kTile - 1) / kTile);
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;  // (more than the memory holds)
+    return launch_pdl(quant4_cols_kernel<FMT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, static_cast<const uint16_t*>(x),
+                      static_cast<int>(rows), static_cast<int>(cols), ld, st, delayed ? 1 : 0, static_cast<uint8_t*>(qT), static_cast<uint8_t*>(sfT),
+                      static_cast<int>(tx), st.scale != nullptr && !delayed ? 1 : 0);
+  }
+  return launch_tiles<FMT, false, true>(x, rows, cols, ld, st, delayed, false, q, sf, qT, sfT, stream);
 }
 
 template <int FMT, typename T>
