@@ -380,10 +380,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
   }
 }
 
-// Column sums over CTAs' partial rows: 32 V columns per CTA (V = 4 where rows are whole 16 bytes); its 16 warps take
-// consecutive ranges of the partial rows, and their sums are added in warp order. blockIdx.y 0 .. 3: the parameters
-// (and alpha); from 4 on: the gate groups that several CTAs share.
-constexpr int kReduceWarps = 16;
+// Column sums over the parts' rows: 8 V columns per CTA (V = 4 where rows are whole 16 bytes). Its 16 warps take
+// consecutive ranges of the parts, the four quarters of a warp every fourth one, so that some 1200 parts are three rounds of
+// loads for a lane; the sums are added in this order whatever runs first. blockIdx.y 0 .. 3: the parameters (and alpha); from 4
+// on: the gate groups that several parts share.
+constexpr int kReduceWarps = 16, kBatch = 8;
 
 template <int V>
 struct Cols {
@@ -392,12 +393,12 @@ struct Cols {
 
 template <int V>
 __global__ void __launch_bounds__(32 * kReduceWarps) norm_bwd_reduce_kernel(const NormFwd f, const NormBwd b, const float* part,
-                                                                            const double* part_alpha, int64_t rows_per, int ctas) {
-  __shared__ Cols<V> sums[kReduceWarps][32];
+                                                                            const double* part_alpha, int64_t rows_per, int parts) {
+  __shared__ Cols<V> sums[kReduceWarps][8];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t D = f.width, c = (blockIdx.x * 32ll + lane) * V;
+  const int64_t D = f.width, c = (blockIdx.x * 8ll + (lane & 7)) * V;
   auto fetch = [&](int64_t row) {
     Cols<V> x;
     if constexpr (V == 4) {
@@ -412,25 +413,24 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_bwd_reduce_kernel(cons
     Cols<V> s = {};
     const int n = q1 - q0, e = q0 + n * (warp + 1) / kReduceWarps;
     if (c < D) {
-      int q = q0 + n * warp / kReduceWarps;
-      for (; q + 8 <= e; q += 8) {
-        Cols<V> x[8];
+      for (int q = q0 + n * warp / kReduceWarps + (lane >> 3); q < e; q += 4 * kBatch) {
+        Cols<V> x[kBatch];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = fetch(place(q + u));
+        for (int u = 0; u < kBatch; ++u) x[u] = fetch(place(min(q + 4 * u, e - 1)));  // (past the range: its last row, not added)
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-          for (int j = 0; j < V; ++j) s.v[j] += x[u].v[j];
-      }
-      for (; q < e; ++q) {
-        const Cols<V> x = fetch(place(q));
-#pragma unroll
-        for (int j = 0; j < V; ++j) s.v[j] += x.v[j];
+          for (int j = 0; j < V; ++j) s.v[j] += q + 4 * u < e ? x[u].v[j] : 0.0f;
       }
     }
-    sums[warp][lane] = s;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      s.v[j] += __shfl_xor_sync(0xFFFFFFFFu, s.v[j], 8);
+      s.v[j] += __shfl_xor_sync(0xFFFFFFFFu, s.v[j], 16);
+    }
+    if (lane < 8) sums[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < D) {
+    if (warp == 0 && lane < 8 && c < D) {
 #pragma unroll
       for (int w = 1; w < kReduceWarps; ++w)
 #pragma unroll
@@ -443,24 +443,24 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_bwd_reduce_kernel(cons
   if (blockIdx.y < 4) {
     const int k = blockIdx.y;
     float* out = k == 0 ? b.dw_pre : k == 1 ? b.db_pre : k == 2 ? b.dw_post : b.db_post;
-    if (out != nullptr) add(0, ctas, [=](int q) { return static_cast<int64_t>(q) * kPart + k; }, out);
+    if (out != nullptr) add(0, parts, [=](int q) { return static_cast<int64_t>(q) * kPart + k; }, out);
     if (k == 0 && b.dres_scale != nullptr && blockIdx.x == 0 && warp == 0) {
       double s = 0.0;
-      for (int p = lane; p < ctas; p += 32) s += part_alpha[p];
+      for (int p = lane; p < parts; p += 32) s += part_alpha[p];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
       if (lane == 0) *b.dres_scale = static_cast<float>(s);
     }
     return;
   }
-  // by groups where they are fewer than the CTAs, else by the CTAs' borders
+  // by groups where they are fewer than the parts, else by the parts' borders
   const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
-  const bool by_group = groups < ctas;
-  for (int64_t i = blockIdx.y - 4; i < (by_group ? groups : ctas - 1); i += gridDim.y - 4) {
+  const bool by_group = groups < parts;
+  for (int64_t i = blockIdx.y - 4; i < (by_group ? groups : parts - 1); i += gridDim.y - 4) {
     const int64_t grp = by_group ? i : (i + 1) * rows_per / f.gate_rows, ga = grp * f.gate_rows, ge = min(ga + f.gate_rows, f.tokens);
     const int first = static_cast<int>(ga / rows_per), last = static_cast<int>((ge - 1) / rows_per);
-    if (first == last || (!by_group && first != i)) continue;  // one CTA's alone, or another border's
-    // the group is the last one of the CTA that holds its first token, unless it is that CTA's first too
+    if (first == last || (!by_group && first != i)) continue;  // one part's alone, or another border's
+    // the group is the last one of the part that holds its first token, unless it is that part's first too
     const int slot = first * rows_per / f.gate_rows == grp ? 4 : 5;
     add(first, last + 1, [=](int q) { return static_cast<int64_t>(q) * kPart + (q == first ? slot : 4); }, b.dgate + grp * D);
   }
@@ -501,9 +501,9 @@ cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t st
     const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
     shared = groups < pl.parts ? groups : pl.parts - 1;
   }
-  const int cols = f.width % 4 == 0 ? 128 : 32;
+  const int cols = f.width % 4 == 0 ? 32 : 8;
   const dim3 grid(static_cast<unsigned>((f.width + cols - 1) / cols), static_cast<unsigned>(4 + (shared < 32 ? shared : 32)));
-  return launch_pdl(cols == 128 ? norm_bwd_reduce_kernel<4> : norm_bwd_reduce_kernel<1>, grid, dim3(32 * kReduceWarps), 0, stream, f, b, part, part_alpha,
+  return launch_pdl(cols == 32 ? norm_bwd_reduce_kernel<4> : norm_bwd_reduce_kernel<1>, grid, dim3(32 * kReduceWarps), 0, stream, f, b, part, part_alpha,
                     pl.rows_per, pl.parts);
 }
 

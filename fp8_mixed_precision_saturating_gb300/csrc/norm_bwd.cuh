@@ -20,6 +20,8 @@ struct BwdPlan {
   int64_t rows_per;
 };
 
+constexpr int kMostTeams = 15;  // (a CTA of several parts keeps a named barrier for each, besides its own)
+
 inline int columns_of(int64_t width) { return width <= 2048 ? 8 : 16; }
 
 inline BwdPlan bwd_plan(int64_t tokens, int64_t width) {
@@ -27,7 +29,7 @@ inline BwdPlan bwd_plan(int64_t tokens, int64_t width) {
   const int64_t per = 32 * columns_of(width);
   p.threads = width <= 8192 ? static_cast<int>((width + per - 1) / per) * 32 : kThreads;
   p.per_sm = (columns_of(width) == 8 ? 640 : 512) / p.threads;
-  p.per_sm = p.per_sm < 1 ? 1 : p.per_sm > 8 ? 8 : p.per_sm;
+  p.per_sm = p.per_sm < 1 ? 1 : p.per_sm > kMostTeams ? kMostTeams : p.per_sm;
   const int64_t most = static_cast<int64_t>(p.per_sm) * num_sms();
   p.rows_per = (tokens + most - 1) / most;
   p.parts = static_cast<int>((tokens + p.rows_per - 1) / p.rows_per);
