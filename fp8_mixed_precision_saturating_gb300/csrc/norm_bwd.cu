@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
 template <typename TS, typename TB, int VEC, int E, bool SUM>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per) {
   // EARLY: all of a row's loads at once, an input that is not there as a row of no columns, so that no branch parts
-  // them (16384 x 52 bf16: 26.3 -> 17.1 us; 4099 x 1537, fp32 stream: 50.9 -> 45.5). With 16 columns a lane the registers
+  // them (16384 x 52 bf16: 26.3 -> 17.1 us; 4099 x 1537 in 8 columns a lane, fp32 stream: 50.9 -> 45.5). With 16 columns a lane the registers
   // are short, and single 16-bit elements take one each (4099 x 1537 bf16: 54.3 -> 62.8).
   constexpr bool FULL = false, EARLY = E == 8 && (VEC == 4 || sizeof(TS) == 4);
   using R = Row<VEC, E, FULL>;
