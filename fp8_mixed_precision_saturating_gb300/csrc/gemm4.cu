@@ -147,6 +147,9 @@ __device__ __forceinline__ void put(T* p, float v) {
 // With too few tiles for the GPU, the pairs of a larger cluster take consecutive ranges of one tile's K (SPLIT): each
 // CTA writes its 128 x 256 fp32 partial tile where its operands were, and then sums a share of the rows over the
 // pairs, in order, and stores it (the same bits every time; no workspace, no atomics).
+// 16384 x 14336 x 4096, NVFP4 to bf16: 285 us (6.8 PFLOP/s; 314 where the power limit holds the clock down), bound by the tensor
+// pipe, active 73 % of the time; with a lane index instead of an elected lane issuing it took 511. 1536 x 1000 x 16379: 24
+// tiles, K in 2: 18 us (on single CTAs 24.6), of which the sum is 3.6.
 template <int FMT>
 struct Pair {
   static constexpr int KA = kAtoms<FMT>;
@@ -432,6 +435,8 @@ __global__ void __launch_bounds__(Pair<FMT>::THREADS, 1)
 // MMA of 16 columns and the whole CTA's intake is B. The CTAs of a cluster take consecutive ranges of K; each
 // writes its fp32 tile to its own shared memory, and each then sums a share of the columns over all of them, in
 // rank order (the same bits every time), and stores it. No workspace, no atomics.
+// 1 x 14336 x 4096 NVFP4 in 6.5 us (33 MB of weights: 5.1 TB/s), 23 x 6144 x 1536 MXFP4 in 4.0 (latency: launch, first
+// load, the sum over the cluster).
 template <int FMT, int BN>
 struct Split {
   static constexpr int KA = kAtoms<FMT>;

@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f,
 // dn = gate g,  dgate = w sum g z + b sum g,  dw_post = sum over the gates of gate sum g z,  db_post likewise. So the
 // rows add to those two sums alone, and they are spent where the gate's row changes.
 //   pass 3: do
-// SUM: sum dh and sum g are wanted (a bias's gradient, or the gate's where there is a bias).
+// SUM: sum dh and sum g are wanted (a bias's gradient, or the gate's where there is a bias). Bound by the latency of a
+// row's loads and sums, with 15 to 20 warps on an SM: 16384 x 52 bf16 17 us, 4099 x 1537 47.6.
 template <typename TS, typename TB, int VEC, int E, bool SUM>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per) {
   // EARLY: all of a row's loads at once, an input that is not there as a row of no columns, so that no branch parts
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
 
 // Column sums over the parts' rows: 8 V columns per CTA (V = 4 where rows are whole 16 bytes). Its 16 warps take
 // consecutive ranges of the parts, the four quarters of a warp every fourth one, so that some 1200 parts are three rounds of
-// loads for a lane; the sums are added in this order whatever runs first. blockIdx.y 0 .. 3: the parameters (and alpha); from 4
+// loads for a lane; the sums are added in this order whatever runs first. Bound by the latency of those rounds: 6 us for 456
+// parts of 1536 columns with 9 gate groups, behind 28 us for the parts (a warp a range, its lanes over columns: 10). blockIdx.y 0 .. 3: the parameters (and alpha); from 4
 // on: the gate groups that several parts share.
 constexpr int kReduceWarps = 16, kBatch = 8;
 

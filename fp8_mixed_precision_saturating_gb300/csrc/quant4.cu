@@ -101,7 +101,8 @@ __device__ __forceinline__ uint2 cast16(const uint32_t (&w)[8], float mul) {
 // Both ways, or rows that are not aligned: one 128 x 128 tile of x per CTA, read once into shared memory (zero past the matrix, which gives the padding's
 // codes and scales their values without a branch), then quantised along its rows (ROWS) and down its columns
 // (COLS). Either way the tile is 64 bytes of each of 128 operand rows and whole scale atoms (2 for NVFP4, 1 for
-// MXFP4), so codes leave in 64-byte pieces and scales in 512-byte ones.
+// MXFP4), so codes leave in 64-byte pieces and scales in 512-byte ones. 4099 x 1536 both ways in 7.9 us, 2.6 TB/s: one wave of
+// 396 tiles, bound by its latency; 512 threads per tile were no faster (76.3 -> 79.9 us for a 4096 x 14336 weight).
 constexpr int kTile = 128, kPitch = 272;  // bytes per tile row: 16 more than 256, so rows start in other banks
 
 template <int FMT, bool ROWS, bool COLS, bool VEC>
@@ -260,6 +261,8 @@ __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows
 
 // Along the rows alone, from 16-byte aligned rows: no tile and no barrier. A lane takes 16 neighbouring elements of 4
 // rows 32 apart (their scale words are neighbours in an atom), a warp 512 columns; all loads are in flight at once.
+// 16384 x 4096: 30.1 us, 5.7 TB/s (through the tile 33.0); issue slots 64 % used, so the instructions per element (largest
+// of the group, scale, multiply, conversion) count beside the memory.
 template <int FMT>
 __global__ void __launch_bounds__(256) quant4_rows_kernel(const uint16_t* x, int rows, int cols, int64_t ld, QuantState st, int delayed, uint8_t* q,
                                                           uint8_t* sf, int pieces, int backwards) {
@@ -350,7 +353,8 @@ __global__ void __launch_bounds__(256) quant4_rows_kernel(const uint16_t* x, int
 
 // Down the columns alone, from 16-byte aligned rows: 128 rows by 128 columns per CTA, read straight into registers (a
 // warp takes 16 rows, a lane 4 columns; MXFP4: 32 rows of half the columns, a lane 2); only codes and scales pass
-// through shared memory, to leave in 64- and 512-byte pieces.
+// through shared memory, to leave in 64- and 512-byte pieces. 4096 x 14336: 30.2 us, 5.0 TB/s (through the tile 31.9;
+// 256 rows per CTA 32.9).
 template <int FMT>
 __global__ void __launch_bounds__(256) quant4_cols_kernel(const uint16_t* x, int rows, int cols, int64_t ld, QuantState st, int delayed, uint8_t* qT,
                                                           uint8_t* sfT, int tiles_x, int backwards) {
@@ -451,7 +455,8 @@ __global__ void __launch_bounds__(256) quant4_cols_kernel(const uint16_t* x, int
   }
 }
 
-// A warp takes 256 elements of 4 rows 32 apart (their scale words are 16 bytes of an atom), a lane 8 of each.
+// A warp takes 256 elements of 4 rows 32 apart (their scale words are 16 bytes of an atom), a lane 8 of each. 16384 x 4096
+// to bf16: 26.2 us, 6.6 TB/s, the memory's rate; 1536 x 4099 (rows that are not aligned) 5.7 us.
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) dequant4_kernel(const uint8_t* q, const uint8_t* sf, int64_t mn, int64_t k, const float* scale_inv, T* y,
                                                        int64_t ldy, int pieces) {
