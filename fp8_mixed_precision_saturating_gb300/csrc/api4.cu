@@ -14,7 +14,7 @@ using namespace fp8gb;
 
 namespace {
 
-constexpr int64_t kMaxDim = (1ll << 31) - 1;
+constexpr int64_t kMaxDim = (1ll << 31) - 1025;  // the end of a tile that a dimension ends in is still a 32-bit number
 
 bool known(fp4_format_t f) { return f == FP4_NVFP4 || f == FP4_MXFP4; }
 bool known(fp8_dtype_t t) { return t == FP8_DT_BF16 || t == FP8_DT_F32; }
@@ -55,7 +55,7 @@ fp8_status_t check_norm(const fp8_block_norm_t* f, const char* who) {
     return fail(FP8_ERR_INVALID_ARG, "%s: unknown type", who);
   if (!known_norm(f->post) || !known_norm(f->pre)) return fail(FP8_ERR_INVALID_ARG, "%s: unknown norm", who);
   if (!(f->eps >= 0.0f) || !std::isfinite(f->eps)) return fail(FP8_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
-  if (f->tokens > kMaxDim || f->width > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31", who);
+  if (f->tokens > kMaxDim || f->width > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31 - 1024", who);
   if (f->gate != nullptr && f->gate_rows <= 0) return fail(FP8_ERR_INVALID_ARG, "%s: a gate needs gate_rows > 0", who);
   if (f->post == FP8_NORM_NONE && (f->w_post != nullptr || f->b_post != nullptr))
     return fail(FP8_ERR_INVALID_ARG, "%s: w_post or b_post without a norm after the block", who);
@@ -139,7 +139,7 @@ fp8_status_t fp4_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_
   if (st == nullptr && mode == FP8_SCALE_DELAYED)
     return fail(FP8_ERR_INVALID_ARG, "%s: delayed scaling needs a state", who);
   if (st != nullptr) FP8GB_TRY(check_state(st, mode, who));
-  if (rows > kMaxDim || cols > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31", who);
+  if (rows > kMaxDim || cols > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31 - 1024", who);
   if (!aligned16(q) || !aligned16(sf) || !aligned16(qT) || !aligned16(sfT))
     return fail(FP8_ERR_ALIGNMENT, "%s: the codes and scales must be 16-byte aligned", who);
   if (!aligned_to(x_bf16, 2)) return fail(FP8_ERR_ALIGNMENT, "%s: x is not aligned to its elements", who);
@@ -158,7 +158,7 @@ fp8_status_t fp4_dequantize(const void* q, const void* sf, int64_t MN, int64_t K
   if (ldy < K) return fail(FP8_ERR_INVALID_ARG, "%s: ldy (%lld) < K (%lld)", who, (long long)ldy, (long long)K);
   const bool empty = MN == 0 || K == 0;
   if (!empty && (q == nullptr || sf == nullptr || y == nullptr)) return fail(FP8_ERR_INVALID_ARG, "%s: null codes, scales or output", who);
-  if (MN > kMaxDim || K > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31", who);
+  if (MN > kMaxDim || K > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31 - 1024", who);
   if (!aligned16(q) || !aligned16(sf)) return fail(FP8_ERR_ALIGNMENT, "%s: the codes and scales must be 16-byte aligned", who);
   if (!aligned_to(y, dt == FP8_DT_F32 ? 4 : 2) || !aligned_to(scale_inv, 4))
     return fail(FP8_ERR_ALIGNMENT, "%s: y or scale_inv is not aligned to its elements", who);
@@ -178,7 +178,7 @@ fp8_status_t fp4_scaled_mm(const void* A, const void* sfa, const void* B, const 
   if (!empty && C == nullptr) return fail(FP8_ERR_INVALID_ARG, "%s: null C", who);
   if (!empty && K > 0 && (A == nullptr || B == nullptr || sfa == nullptr || sfb == nullptr))
     return fail(FP8_ERR_INVALID_ARG, "%s: null A, B or scales", who);
-  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31", who);
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(FP8_ERR_UNSUPPORTED, "%s: dimension >= 2^31 - 1024", who);
   if (!aligned16(A) || !aligned16(B) || !aligned16(sfa) || !aligned16(sfb) || !aligned16(C))
     return fail(FP8_ERR_ALIGNMENT, "%s: A, B, their scales and C must be 16-byte aligned", who);
   if (ldc % (dt == FP8_DT_F32 ? 4 : 8) != 0)

@@ -431,7 +431,8 @@ fp8_status_t fp8_linear_bwd_noalloc(const void* dy_bf16, int64_t M, int64_t K, i
  * ((m / 128) * ceil(G / 4) + g / 4) * 512 for G = ceil(K / 16) (ceil(K / 32)) groups, the byte of
  * (m, g) at 16 (m % 32) + 4 ((m / 32) % 4) + g % 4 in it; fp4_scale_bytes(fmt, MN, K) bytes in
  * all. The quantiser writes the atoms whole: scales past the last row or group are 0 (NVFP4) or
- * e = 0 (MXFP4). Any MN and K. Both buffers are caller-owned and 16-byte aligned. */
+ * e = 0 (MXFP4). Any MN and K below 2^31 - 1024 (FP8_ERR_UNSUPPORTED from there on). Both buffers
+ * are caller-owned and 16-byte aligned. */
 typedef enum { FP4_NVFP4 = 0, FP4_MXFP4 = 1 } fp4_format_t;
 
 /* Element types of outputs that come in more than one. */
@@ -540,7 +541,7 @@ typedef struct {
 
 /* Forward. Refused (FP8_ERR_INVALID_ARG): a missing r, no output, gate without gate_rows > 0, norm
  * parameters without a norm, post norm or gate without o, unknown types or kinds, eps < 0 or not
- * finite; FP8_ERR_UNSUPPORTED: tokens or width >= 2^31, hq with width % 32 != 0. */
+ * finite; FP8_ERR_UNSUPPORTED: tokens or width >= 2^31 - 1024, hq with width % 32 != 0. */
 fp8_status_t fp8_block_norm_fwd(const fp8_block_norm_t* f, void* stream);
 
 /* Backward from f's inputs (r is read for dres_scale only), its r_out (as written by the forward),

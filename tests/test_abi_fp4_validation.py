@@ -160,3 +160,12 @@ def test_every_declared_fp4_function_is_exported_and_bound(g):
     names = set(re.findall(r"\b(fp4_[a-z0-9_]+)\s*\(", re.sub(r"/\*.*?\*/", "", header, flags=re.S)))
     assert {"fp4_quantize", "fp4_dequantize", "fp4_scaled_mm", "fp4_row_bytes", "fp4_scale_bytes"} <= names
     assert all(hasattr(g.lib, n) and hasattr(g, n) for n in names)
+
+
+def test_sizes_whose_tiles_end_past_32_bits(g):
+    """A tile that a dimension ends in has to end below 2^31."""
+    un, n = g.FP8_ERR_UNSUPPORTED, (1 << 31) - 1024
+    refused(g, un, "2^31 - 1024", g.fp4_quantize, A, 1, n, n, 0, 0, None, B, C)
+    refused(g, un, "2^31 - 1024", g.fp4_dequantize, A, B, n, 1, 0, None, C, 0, 1)
+    refused(g, un, "2^31 - 1024", g.fp4_scaled_mm, A, S, B, S, 1, n, 16, 0, None, None, C, 0, 1 << 31)
+    refused(g, un, "2^31 - 1024", lambda: g.fp8_block_norm_fwd(g.block_norm(n, 8, 0, 0, r=A, ld_r=8, r_out=B, ld_r_out=8)))
