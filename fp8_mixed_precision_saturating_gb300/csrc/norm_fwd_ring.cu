@@ -47,16 +47,15 @@ __device__ __forceinline__ void normalize(Pair (&x)[E / 2], int kind, float2 st)
   for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], rstd);
 }
 
-// One CTA per SM, of several teams that take rows in turn. Asynchronous bulk copies bring a team's next rows into its
-// ring in shared memory while the present one is worked on, so the loads never wait for the arithmetic; the parameters
-// are in shared memory once for all teams, ones where there are none and the gate's row multiplied in where all tokens
-// share it. 16384 x 4096 bf16: parameters read from L1 beside the rings (some 30 KB of it, half of the reads missed)
-// 110 us; kept in shared memory, 95 in a row of calls (5.7 TB/s, 0.83 of a plain copy), the issue slots half used. A row's
-// chain (wait, two sums over its warps, stores) with 24 warps on an SM is what is left. BIAS: there is a bias.
-template <typename TS, typename TB, int E, bool FULL, int MOST, bool BIAS>
-__global__ void __launch_bounds__(MOST, 1) norm_fwd_ring_kernel(const NormFwd f, uint32_t gate_rows, int stages) {
+// At most one CTA per SM, of several teams of up to WARPS warps that take rows in turn. Asynchronous bulk copies bring a
+// team's next rows into its ring in shared memory while the present one is worked on, so the loads never wait for the
+// arithmetic; the parameters are in shared memory once for all teams, ones where there are none and the gate's row
+// multiplied in where all tokens share it. 16384 x 4096 bf16: parameters read from L1 beside the rings (some 30 KB of it,
+// half of the reads missed) 110 us; kept in shared memory 95; with as many teams as the memory needs (ring_plan) 82.7,
+// 6.5 TB/s. BIAS: there is a bias.
+template <typename TS, typename TB, int E, bool FULL, int WARPS, bool BIAS>
+__global__ void __launch_bounds__(WARPS == 16 ? 512 : 768, 1) norm_fwd_ring_kernel(const NormFwd f, uint32_t gate_rows, int stages) {
   using R = Row<4, E, FULL>;
-  constexpr int WARPS = MOST == 768 ? 8 : 16;  // of a team, at most
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Red reds[kMostTeams];
   __shared__ __align__(8) uint64_t bars[kMostTeams][kMaxStages];
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(MOST, 1) norm_fwd_ring_kernel(const NormFwd f,
     bulk_load(dst, static_cast<const TS*>(f.r) + t * f.ld_r, r_bytes, bar0 + 8 * s);
     bulk_load(dst + r_bytes, static_cast<const TB*>(f.o) + t * f.ld_o, o_bytes, bar0 + 8 * s);
   };
-  const uint32_t T = static_cast<uint32_t>(f.tokens), t0 = blockIdx.x + team * gridDim.x, step = gridDim.x * teams;
+  const uint32_t T = static_cast<uint32_t>(f.tokens), t0 = blockIdx.x * teams + team, step = gridDim.x * teams;
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && t0 + s * static_cast<uint64_t>(step) < T; ++s) fetch(t0 + s * step, s);
   const int tid = team * blockDim.x + threadIdx.x, threads = blockDim.x * teams;
@@ -180,34 +179,51 @@ __global__ void __launch_bounds__(MOST, 1) norm_fwd_ring_kernel(const NormFwd f,
 }
 
 struct RingPlan {
-  int threads, teams, stages, bytes;  // of a team, teams, rows each holds, shared memory
+  int threads, teams, ctas, stages, bytes;  // of a team, teams, CTAs, rows each team holds, shared memory
 };
 
+// As many rows at once as keep the memory busy, and no more: the teams' time for a row, which grows with the warps on an SM,
+// times the memory's rate over the row's bytes. Past that the copies and stores only stand in each other's way:
+// 16384 x 4096 bf16 in 3 teams on each of 152 SMs 95 us, in 2 on 143 of them 82.7 (6.5 TB/s), in 2 on 128 90.6; 32768 x 2048
+// 94 and 82; 16384 x 4096 with an fp32 stream 136 in 3 teams, 129 in 1. The constants are measured times (us) of a row alone: two
+// layer norms 1.7, two root mean squares 0.88, one norm 0.55, with 4-bit codes 1.1 more, above 8 warps 0.2 more.
 RingPlan ring_plan(const NormFwd& f, int64_t row, int columns, bool bias) {
   RingPlan p{};
   p.threads = static_cast<int>((f.width + 32 * columns - 1) / (32 * columns)) * 32;
-  p.teams = p.threads > 256 ? 1 : 768 / p.threads;  // (by registers: 80 a thread of 768, 128 of 512)
-  if (p.teams > kMostTeams) p.teams = kMostTeams;
+  const int sms = num_sms(), warps = p.threads / 32, room_for = p.threads > 384 ? 1 : 768 / p.threads, most = room_for < kMostTeams ? room_for : kMostTeams;
+  const int64_t ss = f.stream_f32 ? 4 : 2, bs = f.block_f32 ? 4 : 2;
+  const float bytes = static_cast<float>(f.width) *
+                      (static_cast<float>(ss + bs + (f.r_out != nullptr ? ss : 0) + (f.h != nullptr ? bs : 0)) + (f.hq != nullptr ? 0.5625f : 0.0f));
+  float chain = f.post == kLayer || f.pre == kLayer ? 1.7f : f.post == kNone || f.pre == kNone ? 0.55f : 0.88f;
+  if (warps > 8) chain += 0.2f;
+  if (f.hq != nullptr) chain += 1.1f;
+  float rows = 0.0f;
+  for (p.teams = 1;; ++p.teams) {
+    rows = (chain + 0.034f * static_cast<float>(p.teams * warps)) * 6.6e6f / bytes;
+    if (p.teams == most || static_cast<float>(p.teams * sms) >= 0.98f * rows) break;
+  }
+  const int ctas = static_cast<int>(rows / static_cast<float>(p.teams)) + 1;
+  p.ctas = ctas < sms ? ctas : sms;
   const int64_t params = (bias ? 16 : 8) * f.width, room = (kRingBytes - params) / (row * p.teams);
   p.stages = static_cast<int>(room < 0 ? 0 : room < kMaxStages ? room : kMaxStages);
   p.bytes = static_cast<int>(params + p.stages * p.teams * row);
   return p;
 }
 
-template <typename TS, typename TB, int E, bool FULL, int MOST, bool BIAS>
+template <typename TS, typename TB, int E, bool FULL, int WARPS, bool BIAS>
 cudaError_t launch_kernel(const NormFwd& f, const RingPlan& p, cudaStream_t stream) {
   static bool done[64] = {};  // the limit is per device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
-    e = cudaFuncSetAttribute(norm_fwd_ring_kernel<TS, TB, E, FULL, MOST, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    e = cudaFuncSetAttribute(norm_fwd_ring_kernel<TS, TB, E, FULL, WARPS, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (e == cudaSuccess && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return e;
   NormFwd g = f;
   g.w = wait_ctl();
   if (g.w.err == nullptr) return cudaErrorInvalidDevice;
-  return launch_pdl(norm_fwd_ring_kernel<TS, TB, E, FULL, MOST, BIAS>, dim3(num_sms()), dim3(p.threads, p.teams), p.bytes, stream, g, gate_rows_of(f), p.stages);
+  return launch_pdl(norm_fwd_ring_kernel<TS, TB, E, FULL, WARPS, BIAS>, dim3(p.ctas), dim3(p.threads, p.teams), p.bytes, stream, g, gate_rows_of(f), p.stages);
 }
 
 template <typename TS, typename TB>
@@ -221,12 +237,14 @@ cudaError_t ring_as(const NormFwd& f, cudaStream_t stream, bool* taken) {
   const RingPlan p = ring_plan(f, f.width * (ss + bs), 16, bias);
   if (p.stages == 0) return cudaSuccess;
   *taken = true;
+  // (8 warps are sums of two reads: with 12 for all of them two layer norms took 117 us instead of 106)
   if (p.threads <= 256) {
-    if (full) return bias ? launch_kernel<TS, TB, 16, true, 768, true>(f, p, stream) : launch_kernel<TS, TB, 16, true, 768, false>(f, p, stream);
-    return bias ? launch_kernel<TS, TB, 16, false, 768, true>(f, p, stream) : launch_kernel<TS, TB, 16, false, 768, false>(f, p, stream);
+    if (full) return bias ? launch_kernel<TS, TB, 16, true, 8, true>(f, p, stream) : launch_kernel<TS, TB, 16, true, 8, false>(f, p, stream);
+    return bias ? launch_kernel<TS, TB, 16, false, 8, true>(f, p, stream) : launch_kernel<TS, TB, 16, false, 8, false>(f, p, stream);
   }
-  if (full) return bias ? launch_kernel<TS, TB, 16, true, 512, true>(f, p, stream) : launch_kernel<TS, TB, 16, true, 512, false>(f, p, stream);
-  return bias ? launch_kernel<TS, TB, 16, false, 512, true>(f, p, stream) : launch_kernel<TS, TB, 16, false, 512, false>(f, p, stream);
+  if (p.threads <= 384) return bias ? launch_kernel<TS, TB, 16, false, 12, true>(f, p, stream) : launch_kernel<TS, TB, 16, false, 12, false>(f, p, stream);
+  if (full) return bias ? launch_kernel<TS, TB, 16, true, 16, true>(f, p, stream) : launch_kernel<TS, TB, 16, true, 16, false>(f, p, stream);
+  return bias ? launch_kernel<TS, TB, 16, false, 16, true>(f, p, stream) : launch_kernel<TS, TB, 16, false, 16, false>(f, p, stream);
 }
 
 }  // namespace

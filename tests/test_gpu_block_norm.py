@@ -228,6 +228,43 @@ def test_4_bits_with_a_tensor_scale_and_without_h(g):
     assert np.array_equal(outs[0], outs[1])
 
 
+# many rows: the kernel with rows ahead in shared memory (more than two rows per SM, 1024 to 8192 columns, rows of whole 16 bytes)
+@pytest.mark.parametrize("D", [1024, 1032, 1536, 2048, 3000, 4096, 4104, 5120, 6144, 6152, 8192, 8184])
+@pytest.mark.parametrize("stream", ["bf16", "f32"])
+def test_forward_many_rows(g, D, stream):
+    for T, post, pre, rows, wb, pad in ((305, 1, 1, 0, True, 0), (701, 2, 2, 100, True, 8), (1001, 1, 1, 1 << 40, False, 0), (457, 0, 2, 1, True, 0), (913, 2, 0, 0, False, 8)):
+        c = Case(g, T, D, stream, "bf16", post, pre, rows, wb=wb, pad=pad)
+        c.forward()
+        check_forward(c)
+
+
+@pytest.mark.parametrize("D", [1024, 5120, 8192])
+def test_forward_many_rows_f32(g, D):
+    for post, pre, rows in ((1, 1, 0), (2, 2, 7)):
+        c = Case(g, 500, D, "f32", "f32", post, pre, rows)
+        c.forward()
+        check_forward(c)
+
+
+@pytest.mark.parametrize("fmt", [fp4.NV, fp4.MX])
+@pytest.mark.parametrize("T,D", [(400, 1024), (333, 4096), (310, 5120), (321, 8192), (500, 1056)])
+def test_many_rows_into_4_bits(g, fmt, T, D):
+    test_forward_into_4_bits(g, fmt, T, D, "bf16", "bf16")
+
+
+def test_forward_many_rows_in_place(g):
+    c = Case(g, 2000, 2048, "bf16", "bf16", 1, 1, 300)
+    plan = c.plan(r_out=c.out("bf16"), h=c.out("bf16"))
+    g.fp8_block_norm_fwd(plan)
+    r, h = c.r.clone(), c.out("bf16")
+    f = g.block_norm(c.T, c.D, g.FP8_DT_BF16, g.FP8_DT_BF16, post=1, pre=1, eps=c.eps, r=r, ld_r=c.D, o=c.o, ld_o=c.D, gate=c.gate, ld_gate=c.D, gate_rows=300,
+                     res_scale=c.alpha, r_out=r, ld_r_out=c.D, h=h, ld_h=c.D, **c.par)
+    g.fp8_block_norm_fwd(f)
+    out = c.out("bf16"), c.out("bf16")
+    g.fp8_block_norm_fwd(c.plan(r_out=out[0], h=out[1]))
+    assert torch.equal(r, out[0]) and torch.equal(h, out[1])
+
+
 # ------------------------------------------------------------------------------------------------
 # backward
 # ------------------------------------------------------------------------------------------------
@@ -313,6 +350,14 @@ def test_backward_sizes_and_types(g, T, D, stream, block):
 def test_backward_kinds_and_gates(g, post, pre, rows):
     for T, D, pad in ((41, 256, 0), (700, 64, 8), (10, 131, 5)):
         c = Case(g, T, D, "f32", "bf16", post, pre, rows, pad=pad)
+        check_backward(c, run_backward(c))
+
+
+@pytest.mark.parametrize("T,D", [(913, 40), (2500, 64), (800, 520), (701, 2048), (650, 2056), (500, 4096), (333, 8192), (640, 1025), (320, 8200)])
+@pytest.mark.parametrize("stream", ["bf16", "f32"])
+def test_backward_many_rows(g, T, D, stream):
+    for post, pre, rows, pad in ((1, 1, 1 << 40, 0), (2, 2, 100, 8)):
+        c = Case(g, T, D, stream, "bf16", post, pre, rows, pad=pad)
         check_backward(c, run_backward(c))
 
 
