@@ -157,6 +157,7 @@ template <typename TS, typename TB, int VEC, int E, bool FULL>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_ctas, uint32_t gate_rows) {
   using R = Row<VEC, E, FULL>;
   __shared__ Red red;
+  __shared__ float table[4][8];
   if (blockDim.x > 32) red.clear();
   pdl_wait();
   pdl_trigger();
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_
   R::template load<true>(static_cast<const TS*>(f.r) + t * f.ld_r + c, left, x);
   if (f.o != nullptr) R::template load<true>(static_cast<const TB*>(f.o) + t * f.ld_o + c, left, n);
   const float alpha = f.res_scale != nullptr ? __ldg(f.res_scale) : 1.0f;
+  fill_table(f, table[threadIdx.y], threadIdx.x);
   const int D = static_cast<int>(f.width);
   if (f.o != nullptr) {
     const float2 post = held_stat<VEC, E, FULL>(f.post, D, f.eps, n, left, red, turn);
@@ -202,10 +204,14 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwd f, int row_
   held_affine<VEC, E, FULL>(x, f.pre, pre, f.w_pre, f.b_pre, c, left);
   if (f.h != nullptr) R::store(static_cast<TB*>(f.h) + t * f.ld_h + c, left, x);
   if (f.hq != nullptr) {
-    if (f.h_fmt == 0)
-      emit_row<0, VEC, E>(f, x, t, c, left);
+    if (blockDim.x > 32)
+      __syncthreads();
     else
-      emit_row<1, VEC, E>(f, x, t, c, left);
+      __syncwarp();
+    if (f.h_fmt == 0)
+      emit_row<0, VEC, E>(f, x, t, c, left, table[threadIdx.y]);
+    else
+      emit_row<1, VEC, E>(f, x, t, c, left, nullptr);
   }
 }
 

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : 768, 1) norm_fwd_ring_kern
   using R = Row<4, E, FULL>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Red reds[kMostTeams];
+  __shared__ float table[8];
   __shared__ __align__(8) uint64_t bars[kMostTeams][kMaxStages];
   __shared__ volatile int fail[kMostTeams][2];  // rows in turn, so that no wait of the next row is taken for this one's
   const int team = threadIdx.y, teams = blockDim.y;
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : 768, 1) norm_fwd_ring_kern
       keep_product(par + 3 * D, f.b_pre, 0.0f, static_cast<const TB*>(nullptr), D, tid, threads);
     }
   }
+  fill_table(f, table, tid);
   if (f.hq != nullptr) fill_scales(f, blockIdx.x * static_cast<int64_t>(threads) + tid, static_cast<int64_t>(gridDim.x) * threads);
   __syncthreads();
   const uint32_t w_post = smem_u32(par + c), w_pre = w_post + 4 * D, b_post = w_pre + 4 * D, b_pre = b_post + 4 * D;
@@ -166,9 +168,9 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : 768, 1) norm_fwd_ring_kern
     if (f.h != nullptr) R::store(static_cast<TB*>(f.h) + t * f.ld_h + c, left, x);
     if (f.hq != nullptr) {
       if (f.h_fmt == 0)
-        emit_row<0, 4, E>(f, x, t, c, left);
+        emit_row<0, 4, E>(f, x, t, c, left, table);
       else
-        emit_row<1, 4, E>(f, x, t, c, left);
+        emit_row<1, 4, E>(f, x, t, c, left, table);
     }
   }
   if (stop && threadIdx.x == 0) {  // copies in flight land (microseconds) before the CTA can exit
