@@ -107,6 +107,18 @@ __device__ __forceinline__ uint32_t cvt8_e2m1(const float (&v)[8]) {
   return r;
 }
 
+// 4 values -> 4 codes in the low 16 bits (and again in the high ones).
+__device__ __forceinline__ uint32_t cvt4_e2m1(float v0, float v1, float v2, float v3) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "mov.b32 %0, {b0, b1, b0, b1};\n\t}"
+      : "=r"(r)
+      : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+  return r;
+}
+
 // 8 codes -> 8 fp32 values.
 __device__ __forceinline__ void e2m1_values(uint32_t codes, float (&v)[8]) {
   uint32_t h[4];
