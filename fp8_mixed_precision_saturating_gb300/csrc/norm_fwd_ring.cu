@@ -188,7 +188,7 @@ struct RingPlan {
 // times the memory's rate over the row's bytes. Past that the copies and stores only stand in each other's way:
 // 16384 x 4096 bf16 in 3 teams on each of 152 SMs 95 us, in 2 on 143 of them 82.7 (6.5 TB/s), in 2 on 128 90.6; 32768 x 2048
 // 94 and 82; 16384 x 4096 with an fp32 stream 136 in 3 teams, 129 in 1. The constants are measured times (us) of a row alone: two
-// layer norms 1.7, two root mean squares 0.88, one norm 0.55, with 4-bit codes 1.1 more, above 8 warps 0.2 more.
+// layer norms 1.7, two root mean squares 0.88, one norm 0.55, with 4-bit codes 0.5 more, above 8 warps 0.2 more.
 RingPlan ring_plan(const NormFwd& f, int64_t row, int columns, bool bias) {
   RingPlan p{};
   p.threads = static_cast<int>((f.width + 32 * columns - 1) / (32 * columns)) * 32;
@@ -198,7 +198,7 @@ RingPlan ring_plan(const NormFwd& f, int64_t row, int columns, bool bias) {
                       (static_cast<float>(ss + bs + (f.r_out != nullptr ? ss : 0) + (f.h != nullptr ? bs : 0)) + (f.hq != nullptr ? 0.5625f : 0.0f));
   float chain = f.post == kLayer || f.pre == kLayer ? 1.7f : f.post == kNone || f.pre == kNone ? 0.55f : 0.88f;
   if (warps > 8) chain += 0.2f;
-  if (f.hq != nullptr) chain += 1.1f;
+  if (f.hq != nullptr) chain += 0.5f;
   float rows = 0.0f;
   for (p.teams = 1;; ++p.teams) {
     rows = (chain + 0.034f * static_cast<float>(p.teams * warps)) * 6.6e6f / bytes;
