@@ -242,11 +242,9 @@ cudaError_t fwd_as(const NormFwd& f, cudaStream_t stream) {
     if (!vec) return launch_rows<TS, TB, 1, 8, false>(f, stream);
     return f.width % 256 == 0 ? launch_rows<TS, TB, 4, 8, true>(f, stream) : launch_rows<TS, TB, 4, 8, false>(f, stream);
   }
-  if (!few) {
-    bool taken = false;
-    const cudaError_t e = launch_norm_fwd_ring(f, stream, &taken);
-    if (e != cudaSuccess || taken) return e;
-  }
+  bool taken = false;
+  const cudaError_t e = launch_norm_fwd_ring(f, stream, &taken);
+  if (e != cudaSuccess || taken) return e;
   if (f.width <= 8192) {
     // single elements: 8 a lane keep 48 registers and twice the warps on an SM (4099 x 1537, fp32 stream: 26.5 -> 19.0 us);
     // a row of more than 16 warps takes 16 a lane

@@ -252,6 +252,36 @@ def test_many_rows_into_4_bits(g, fmt, T, D):
     test_forward_into_4_bits(g, fmt, T, D, "bf16", "bf16")
 
 
+# more than 8 rows per SM (narrow rows: 32), where the rows ahead begin to pay
+@pytest.mark.parametrize("T,D", [(1217, 1024), (1301, 1032), (1400, 2048), (1217, 3000), (1300, 4096), (1217, 4104), (1250, 5120), (1217, 6152), (1300, 8192), (4865, 768), (5000, 520)])
+@pytest.mark.parametrize("stream", ["bf16", "f32"])
+def test_forward_rows_ahead(g, T, D, stream):
+    for post, pre, rows, wb, pad in ((1, 1, 1 << 40, False, 0), (2, 2, 100, True, 8)):
+        c = Case(g, T, D, stream, "bf16", post, pre, rows, wb=wb, pad=pad)
+        c.forward()
+        check_forward(c)
+
+
+@pytest.mark.parametrize("post,pre,rows,wb", [(0, 2, 1, True), (2, 0, 0, False), (1, 2, 0, True), (0, 1, 0, False), (1, 0, 300, True)])
+def test_kinds_with_rows_ahead(g, post, pre, rows, wb):
+    c = Case(g, 1500, 1536, "bf16", "bf16", post, pre, rows, wb=wb, alpha=False)
+    c.forward()
+    check_forward(c)
+
+
+@pytest.mark.parametrize("T,D", [(1217, 1024), (1250, 5120), (1300, 8192)])
+def test_f32_rows_ahead(g, T, D):
+    c = Case(g, T, D, "f32", "f32", 2, 1, 7)
+    c.forward()
+    check_forward(c)
+
+
+@pytest.mark.parametrize("fmt", [fp4.NV, fp4.MX])
+@pytest.mark.parametrize("T,D", [(1300, 1056), (1217, 4096), (1217, 5120), (4870, 768)])
+def test_rows_ahead_into_4_bits(g, fmt, T, D):
+    test_forward_into_4_bits(g, fmt, T, D, "bf16", "bf16")
+
+
 def test_forward_many_rows_in_place(g):
     c = Case(g, 2000, 2048, "bf16", "bf16", 1, 1, 300)
     plan = c.plan(r_out=c.out("bf16"), h=c.out("bf16"))
