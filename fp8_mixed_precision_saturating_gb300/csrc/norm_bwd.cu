@@ -401,10 +401,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
 }
 
 // Column sums over the parts' rows: 8 V columns per CTA (V = 4 where rows are whole 16 bytes). Its 16 warps take
-// consecutive ranges of the parts, the four quarters of a warp every fourth one, so that some 1200 parts are three rounds of
-// loads for a lane; the sums are added in this order whatever runs first. Bound by the latency of those rounds: 6 us for 456
-// parts of 1536 columns with 9 gate groups, behind 28 us for the parts (a warp a range, its lanes over columns: 10). blockIdx.y 0 .. 3: the parameters (and alpha); from 4
-// on: the gate groups that several parts share.
+// consecutive ranges of the parts, the four quarters of a warp every fourth one, so that some 1200 parts are three rounds
+// of loads for a lane; the sums are added in this order whatever runs first. Bound by the latency of those rounds: 6 us
+// for 456 parts of 1536 columns with 9 gate groups, behind 28 us for the parts (a warp a range, its lanes over columns:
+// 10). blockIdx.y 0 .. 3: the parameters (and alpha); from 4 on: the gate groups that several parts share.
 constexpr int kReduceWarps = 16, kBatch = 8;
 
 template <int V>

@@ -11,10 +11,10 @@ using namespace norms;
 // One CTA per SM, of several teams, each with its part of the tokens. Asynchronous bulk copies bring a team's next rows
 // into its ring in shared memory while the present one is worked on; w_pre and w_post (times the gate's row where all
 // tokens share it) are in shared memory once for all teams. There are dh, dr_out, o, dr and do here, and a norm before
-// the next block. SUM: sum dh and sum g are wanted.
-// 16384 x 4096 bf16 with the residual scale's gradient (939 MB): 146 us and 6 for the sums, 0.9 of a
-// plain copy's rate (two CTAs per SM with the parameters from L1: 165 in all); 4100 x 1536, fp32 stream, layer norms with biases: 28 and 6, where a part's 9 rows are a chain
-// of latencies. Room for 768 threads instead of 640 (80 registers) spilled: 42 us for both.
+// the next block. SUM: sum dh and sum g are wanted. 16384 x 4096 bf16 with the residual scale's gradient (939 MB): 146 us
+// and 6 for the sums, 0.9 of a plain copy's rate (two CTAs per SM with the parameters from L1: 165 in all); 4100 x 1536,
+// fp32 stream, layer norms with biases: 28 and 6, where a part's 9 rows are a chain of latencies. Room for 768 threads
+// instead of 640 (80 registers) spilled: 42 us for both.
 template <typename TS, typename TB, int E, bool FULL, bool SUM>
 __global__ void __launch_bounds__(E == 8 ? 640 : 512, 1)
     norm_bwd_ring_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per, int parts, int stages) {

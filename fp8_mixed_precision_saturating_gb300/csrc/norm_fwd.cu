@@ -235,16 +235,16 @@ cudaError_t fwd_as(const NormFwd& f, cudaStream_t stream) {
   const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.ld_r_out, ss, 4 * ss) &&
                    rows_aligned(f.o, f.ld_o, bs, 4 * bs) && rows_aligned(f.h, f.ld_h, bs, 4 * bs) && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) &&
                    rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16) && rows_aligned(f.b_pre, 0, 4, 16);
-  // 16 elements per lane keep enough loads in flight for the memory's rate; with no more rows than a few per SM the
-  // latency counts instead, and a row is spread over twice the lanes
-  const bool few = f.tokens <= 2ll * num_sms();
-  if (f.width <= 256 || (few && f.width <= 4096)) {
-    if (!vec) return launch_rows<TS, TB, 1, 8, false>(f, stream);
-    return f.width % 256 == 0 ? launch_rows<TS, TB, 4, 8, true>(f, stream) : launch_rows<TS, TB, 4, 8, false>(f, stream);
-  }
   bool taken = false;
   const cudaError_t e = launch_norm_fwd_ring(f, stream, &taken);
   if (e != cudaSuccess || taken) return e;
+  // 16 elements a lane keep the loads of a wide row in flight (304 x 4096 3.5 us, with 8 4.3) and make a row of up to 512 columns
+  // one warp's, without a barrier (60000 x 512 44 us, with 8 63). With 8 a row in between has shorter chains (1 x 768 2.4 us,
+  // with 16 2.8; 1000 x 768 3.1, 3.4), and one of 256 columns is a warp's as well
+  if (f.width <= 256 || (f.width > 512 && f.width < 1024)) {
+    if (!vec) return launch_rows<TS, TB, 1, 8, false>(f, stream);
+    return f.width % 256 == 0 ? launch_rows<TS, TB, 4, 8, true>(f, stream) : launch_rows<TS, TB, 4, 8, false>(f, stream);
+  }
   if (f.width <= 8192) {
     // single elements: 8 a lane keep 48 registers and twice the warps on an SM (4099 x 1537, fp32 stream: 26.5 -> 19.0 us);
     // a row of more than 16 warps takes 16 a lane
