@@ -64,7 +64,7 @@ fp8_status_t check_norm(const fp8_block_norm_t* f, const char* who) {
   if (f->tokens > 0 && f->width > 0 && f->o == nullptr && (f->post != FP8_NORM_NONE || f->gate != nullptr))
     return fail(FP8_ERR_INVALID_ARG, "%s: a norm after the block or a gate without o", who);
   const int64_t ss = f->stream_dt == FP8_DT_F32 ? 4 : 2, bs = f->block_dt == FP8_DT_F32 ? 4 : 2;
-  const int64_t groups = f->gate != nullptr ? (f->tokens + f->gate_rows - 1) / f->gate_rows : 0;
+  const int64_t groups = f->gate != nullptr && f->tokens > 0 ? (f->tokens - 1) / f->gate_rows + 1 : 0;
   FP8GB_TRY(check_matrix(f->r, f->ld_r, f->tokens, f->width, ss, who, "r"));
   FP8GB_TRY(check_matrix(f->o, f->ld_o, f->tokens, f->width, bs, who, "o"));
   FP8GB_TRY(check_matrix(f->gate, f->ld_gate, groups, f->width, bs, who, "gate"));
@@ -91,7 +91,8 @@ NormFwd to_fwd(const fp8_block_norm_t* f) {
   n.ld_r = f->ld_r;
   n.ld_o = f->ld_o;
   n.ld_gate = f->ld_gate;
-  n.gate_rows = f->gate_rows;
+  // a gate of more rows than there are tokens is one for all of them; past here its ends and counts fit 64 bits
+  n.gate_rows = f->gate != nullptr && f->gate_rows < f->tokens ? f->gate_rows : f->tokens;
   n.res_scale = f->res_scale;
   n.w_post = f->w_post;
   n.b_post = f->b_post;

@@ -11,7 +11,7 @@ cudaError_t launch_norm_fwd_ring(const NormFwd& f, cudaStream_t stream, bool* ta
 
 namespace norms {
 
-inline uint32_t gate_rows_of(const NormFwd& f) { return static_cast<uint32_t>(f.gate == nullptr || f.gate_rows > f.tokens ? f.tokens : f.gate_rows); }
+inline uint32_t gate_rows_of(const NormFwd& f) { return static_cast<uint32_t>(f.gate_rows); }
 
 // The quotients that NVFP4's group factors are made of (fp4::quotient), by 8 threads; the caller puts a barrier before emit_row.
 __device__ __forceinline__ float h_scale_of(const NormFwd& f) { return f.h_scale != nullptr ? __ldg(f.h_scale) : 1.0f; }

@@ -500,7 +500,7 @@ typedef struct {
   int64_t ld_o;
   const void* gate;            /* [ceil(tokens / gate_rows), width]; row t takes row t / gate_rows. NULL: 1 */
   int64_t ld_gate;
-  int64_t gate_rows;
+  int64_t gate_rows;           /* > 0 with a gate; any number from tokens on is one gate for all */
   const float* res_scale;      /* alpha, one fp32; NULL: 1 */
   const float* w_post;         /* [width]; NULL: ones */
   const float* b_post;         /* [width]; NULL: zeros */
