@@ -50,18 +50,28 @@ __device__ __forceinline__ float sixth(float a) {
   return __fmaf_rn(__fmaf_rn(-6.0f, q, a), r, q);
 }
 
+// The smallest E4M3 code whose value c makes fl32(s / c) finite, for a tensor scale s: the next value above s / 2^128, 1 (2^-9)
+// for any s up to 2^118. Under larger ones a group's scale above 0 is raised to it: an infinite factor would make its
+// zeros no numbers, where this way its codes still stand for its elements, in larger steps.
+__device__ __forceinline__ uint32_t least_scale(float s) {
+  const float u = s * 0x1p-64f * 0x1p-64f;
+  const uint32_t c = u >= 0x1p-6f ? (__float_as_uint(u) >> 20) - (120u << 3) : static_cast<uint32_t>(u * 512.0f);
+  return min(c + 1u, 0x7Eu);
+}
+
 // NVFP4's scale byte and factor as group_scale gives them, with the quotients s / 1, s / 1.125, ..., s / 1.875 in
-// `table` (filled by quotient): an E4M3 value is one of those eight times a power of two, so fl32(s / c) is an entry
-// times an exact power. A division per group of 16 would be a third of a quantiser's instructions.
+// `table` (filled by quotient) and least_scale(s) in `least`: an E4M3 value is one of those eight times a power of two, so
+// fl32(s / c) is an entry times an exact power. A division per group of 16 would be a third of a quantiser's instructions.
 __device__ __forceinline__ float quotient(float s, int i) { return __fdiv_rn(s, 1.0f + 0.125f * static_cast<float>(i)); }
-__device__ __forceinline__ uint32_t group_scale_nv(uint32_t abits, float s, const float* table, float& mul) {
+__device__ __forceinline__ uint32_t group_scale_nv(uint32_t abits, float s, uint32_t least, const float* table, float& mul) {
   mul = 0.0f;
   if (abits > 0x7F800000u) return 0x7Fu;
   const float t = sixth(fminf(__fmul_rn(__uint_as_float(abits), s), 3.402823466e38f));
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(t));
-  const uint32_t v = __float_as_uint(e4m3_value(c));
-  if (v != 0u) mul = __fmul_rn(table[(v >> 20) & 7u], __uint_as_float((254u << 23) - (v & 0x7F800000u)));
+  uint16_t e4m3;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e4m3) : "f"(0.0f), "f"(t));
+  if (e4m3 == 0) return 0u;
+  const uint32_t c = max(static_cast<uint32_t>(e4m3), least), v = __float_as_uint(e4m3_value(c));
+  mul = __fmul_rn(table[(v >> 20) & 7u], __uint_as_float((254u << 23) - (v & 0x7F800000u)));
   return c;
 }
 
@@ -74,9 +84,11 @@ __device__ __forceinline__ uint32_t group_scale(uint32_t abits, float s, float& 
   if (abits > 0x7F800000u) return F4<FMT>::kScaleNaN;
   if constexpr (FMT == 0) {
     const float t = __fdiv_rn(__fmul_rn(__uint_as_float(abits), s), 6.0f);
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(t));
-    if (c != 0) mul = __fdiv_rn(s, e4m3_value(c));
+    uint16_t e4m3;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e4m3) : "f"(0.0f), "f"(t));
+    if (e4m3 == 0) return 0u;
+    const uint32_t c = max(static_cast<uint32_t>(e4m3), least_scale(s));
+    mul = __fdiv_rn(s, e4m3_value(c));
     return c;
   } else {
     abits = min(abits, 0x7F7F0000u);  // an infinity counts as the largest finite bf16

@@ -24,7 +24,7 @@ __device__ __forceinline__ void fill_table(const NormFwd& f, float* table, int t
 template <int FMT>
 __device__ __forceinline__ uint32_t h_group_scale(uint32_t a, float s, bool tabled, const float* table, float& mul) {
   if constexpr (FMT == 0) {
-    if (tabled) return fp4::group_scale_nv(a, s, table, mul);
+    if (tabled) return fp4::group_scale_nv(a, s, 1u, table, mul);
   }
   return fp4::group_scale<FMT>(a, s, mul);
 }

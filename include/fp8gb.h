@@ -414,8 +414,9 @@ fp8_status_t fp8_linear_bwd_noalloc(const void* dy_bf16, int64_t M, int64_t K, i
  * rounded to nearest, ties to even, saturating; the groups run along the contraction:
  *   FP4_NVFP4  one E4M3 scale per 16 elements and, optionally, one fp32 scale for the tensor.
  *              With s the tensor's scale and d its inverse (1, 1 without one) and a the group's
- *              max |x|: c = e4m3(fl32(fl32(a s) / 6)), r = fl32(s / c) (0 if c = 0),
- *              code = e2m1(fl32(x r)); it stands for code * c * d. The tensor's scale follows
+ *              max |x|: c = e4m3(fl32(fl32(a s) / 6)), r = fl32(s / c) (0 if c = 0; a c above 0
+ *              under which r overflows, s being above 2^118, is raised to the smallest one that
+ *              gives a finite r), code = e2m1(fl32(x r)); it stands for code * c * d. The tensor's scale follows
  *              the library's rule with the format's largest value 6 * 448: s = fl32(2688 / amax),
  *              d = fl32(amax / 2688), and 1, 1 where amax is zero, not finite or makes s overflow.
  *   FP4_MXFP4  one power of two per 32 elements (UE8M0 byte e + 127), e the smallest integer with
@@ -513,7 +514,7 @@ typedef struct {
   void* hq;                    /* h as a 4-bit operand (MN = tokens, K = width), from the fp32 values; */
   void* hsf;                   /* both NULL: not written. width % 32 == 0 */
   int32_t h_fmt;               /* fp4_format_t of hq */
-  const float* h_scale;        /* NVFP4: h's tensor scale s (device fp32); NULL: 1 */
+  const float* h_scale;        /* NVFP4: h's tensor scale s (device fp32, finite, above 0); NULL: 1 */
   float* stat_post;            /* [tokens, 2]: mean (0 for RMS) and 1 / root; NULL: not written */
   float* stat_pre;
 } fp8_block_norm_t;

@@ -2,7 +2,8 @@
 byte layout of codes and scales, and the product, in numpy.
 
 E2M1: sign, 2 exponent bits (bias 1), 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
-NVFP4: c = e4m3(fl32(fl32(a s) / 6)) per 16 elements (a: the group's amax, s the tensor's scale),
+NVFP4: c = e4m3(fl32(fl32(a s) / 6)) per 16 elements (a: the group's amax, s the tensor's scale), a c that is
+       not 0 raised to the smallest one whose fl32(s / c) is finite,
        code = e2m1(fl32(x fl32(s / c))); the fp32 roundings are part of the definition.
 MXFP4: 2^e per 32 elements, e the smallest integer with 6 2^e >= a (0 for a = 0, at least -127).
 A NaN in a group: scale NaN, zero codes. An infinity counts as the largest finite bf16 in a.
@@ -52,6 +53,13 @@ def mx_exponent(a: float) -> int:
     return max(-127, e - 3 if m <= 0.75 else e - 2)
 
 
+def least_scale(s) -> int:
+    """The smallest E4M3 code above 0 under which the tensor scale s (finite, above 0) gives a finite factor."""
+    with np.errstate(over="ignore"):
+        finite = np.isfinite(np.float32(s) / fp8.decode_array(np.arange(1, 127, dtype=np.uint8), fp8.E4M3).astype(np.float32))
+    return 1 + int(np.argmax(finite))
+
+
 def scale_value(byte, fmt) -> np.ndarray:
     byte = np.asarray(byte, dtype=np.uint8)
     if fmt == NV:
@@ -74,6 +82,7 @@ def quantize(x, fmt, s=np.float32(1.0)):
         if fmt == NV:
             t = (a * np.float32(s)).astype(np.float32) / np.float32(6.0)
             byte = fp8.cast(t, fp8.E4M3)
+            byte = np.where(byte > 0, np.maximum(byte, least_scale(s)), 0).astype(np.uint8)
             c = fp8.decode_array(byte, fp8.E4M3).astype(np.float32)
             mul = np.where(c > 0, np.float32(s) / np.where(c > 0, c, np.float32(1)), np.float32(0)).astype(np.float32)
         else:
