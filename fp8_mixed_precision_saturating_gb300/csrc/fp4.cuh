@@ -61,7 +61,8 @@ __device__ __forceinline__ uint32_t least_scale(float s) {
 
 // NVFP4's scale byte and factor as group_scale gives them, with the quotients s / 1, s / 1.125, ..., s / 1.875 in
 // `table` (filled by quotient) and least_scale(s) in `least`: an E4M3 value is one of those eight times a power of two, so
-// fl32(s / c) is an entry times an exact power. A division per group of 16 would be a third of a quantiser's instructions.
+// fl32(s / c) is an entry times an exact power. (An infinity needs no clamp: the scales that come here are
+// at least 2688 / the largest finite bf16, and that has the largest c then too.) A division per group of 16 would be a third of a quantiser's instructions.
 __device__ __forceinline__ float quotient(float s, int i) { return __fdiv_rn(s, 1.0f + 0.125f * static_cast<float>(i)); }
 __device__ __forceinline__ uint32_t group_scale_nv(uint32_t abits, float s, uint32_t least, const float* table, float& mul) {
   mul = 0.0f;
@@ -83,6 +84,7 @@ __device__ __forceinline__ uint32_t group_scale(uint32_t abits, float s, float& 
   mul = 0.0f;
   if (abits > 0x7F800000u) return F4<FMT>::kScaleNaN;
   if constexpr (FMT == 0) {
+    if (abits == 0x7F800000u) abits = 0x7F7F0000u;  // an infinity counts as the largest finite bf16
     const float t = __fdiv_rn(__fmul_rn(__uint_as_float(abits), s), 6.0f);
     uint16_t e4m3;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e4m3) : "f"(0.0f), "f"(t));

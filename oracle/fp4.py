@@ -80,6 +80,7 @@ def quantize(x, fmt, s=np.float32(1.0)):
     with np.errstate(all="ignore"):
         a = np.abs(np.where(np.isnan(z), 0, z)).max(axis=2).astype(np.float32)
         if fmt == NV:
+            a = np.where(np.isinf(a), np.float32(BF16_MAX), a)
             t = (a * np.float32(s)).astype(np.float32) / np.float32(6.0)
             byte = fp8.cast(t, fp8.E4M3)
             byte = np.where(byte > 0, np.maximum(byte, least_scale(s)), 0).astype(np.uint8)
