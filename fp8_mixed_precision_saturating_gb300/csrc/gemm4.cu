@@ -561,6 +561,7 @@ __global__ void __launch_bounds__(192)
         uint32_t r[16];
         tmem_ld16(acc + c, r);
         tmem_ld_wait();
+        reg_fence(r);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (c + j < live && n < p.N) put(out + (mb * BN + c + j) * p.ldc + n, __fmul_rn(__uint_as_float(r[j]), d));
@@ -577,6 +578,7 @@ __global__ void __launch_bounds__(192)
         uint32_t r[16];
         tmem_ld16(acc + c, r);
         tmem_ld_wait();
+        reg_fence(r);
 #pragma unroll
         for (int j = 0; j < 16; ++j) tile[(c + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
       }
