@@ -497,6 +497,7 @@ except ImportError:
     pass
 if _fastcall is not None:
     _NAMES = ("fp4_quantize", "fp4_dequantize", "fp4_scaled_mm", "fp8_block_norm_fwd", "fp8_block_norm_bwd")
-    _fastcall.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NAMES), _check, _stream)
+    _fastcall.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NAMES), _check, _stream,
+                   (fp8_tensor_state_t, fp8_block_norm_t, fp8_block_norm_grad_t))
     _by_ctypes = {n: globals()[n] for n in _NAMES}  # (what a host without Python.h calls)
     globals().update({n: getattr(_fastcall, n) for n in _NAMES})

@@ -2,8 +2,9 @@
  *
  * A product of one token takes some 6 us on the GPU. A call of it through ctypes and its Python wrapper takes 4.9 us of
  * the host's time, 2.3 of them inside the library (Grace); through this module 3.1. Same functions, names, argument
- * order, defaults and errors as the ctypes wrappers of __init__.py, which stay and are used where this module could not
- * be built. The library's functions come in as addresses (init), so nothing is linked. */
+ * order, defaults and refusals as the ctypes wrappers of __init__.py, which stay and are used where this module could not
+ * be built; an argument of a wrong type is a TypeError here and a ctypes.ArgumentError there. The library's functions come
+ * in as addresses (init), so nothing is linked. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -14,6 +15,7 @@
 enum { QUANTIZE, DEQUANTIZE, SCALED_MM, NORM_FWD, NORM_BWD, COUNT };
 static void* g_fn[COUNT];
 static PyObject *g_error, *g_stream, *g_raw, *g_device; /* callables: of a status; of None; of a device; of nothing */
+static PyObject *g_state, *g_norm, *g_grad; /* the classes of the ctypes structures */
 static PyObject *s_data_ptr, *s_cuda_stream, *s_c;
 
 /* Arguments by position, then by name, into out[n]; what is left out stays NULL and must not be required. */
@@ -56,20 +58,34 @@ static int pointer(PyObject* o, void** p) {
   return !PyErr_Occurred();
 }
 
-/* The address of a ctypes structure, or of the one in a Python object's attribute c; the caller keeps o alive. */
-static int structure(PyObject* o, void** p) {
+/* The address of an instance of a ctypes structure. Nothing else is taken: the library reads the whole of it. */
+static int structure(PyObject* o, PyObject* type, void** p) {
   *p = NULL;
   if (o == NULL || o == Py_None) return 1;
-  PyObject* c = PyObject_CheckBuffer(o) ? Py_NewRef(o) : PyObject_GetAttr(o, s_c);
-  if (c == NULL) return 0;
-  Py_buffer b;
-  const int ok = PyObject_GetBuffer(c, &b, PyBUF_SIMPLE) == 0;
-  if (ok) {
-    *p = b.buf;
-    PyBuffer_Release(&b);
+  const int is = PyObject_IsInstance(o, type);
+  if (is < 0) return 0;
+  if (!is) {
+    PyErr_Format(PyExc_TypeError, "expected %s, not %s", ((PyTypeObject*)type)->tp_name, Py_TYPE(o)->tp_name);
+    return 0;
   }
-  Py_DECREF(c);
-  return ok;
+  Py_buffer b;
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) return 0;
+  *p = b.buf;
+  PyBuffer_Release(&b);
+  return 1;
+}
+
+/* A tensor's state, or an object that has one in its attribute c; *keep holds it over the call. */
+static int state(PyObject* o, void** p, PyObject** keep) {
+  *keep = NULL;
+  if (o != NULL && o != Py_None && !Py_IS_TYPE(o, (PyTypeObject*)g_state)) {
+    const int is = PyObject_IsInstance(o, g_state);
+    if (is < 0) return 0;
+    if (!is && (o = *keep = PyObject_GetAttr(o, s_c)) == NULL) return 0;
+  }
+  if (structure(o, g_state, p)) return 1;
+  Py_CLEAR(*keep);
+  return 0;
 }
 
 static int integer(PyObject* o, int64_t* v) {
@@ -127,14 +143,16 @@ static PyObject* quantize(PyObject* self, PyObject* const* args, Py_ssize_t narg
   void *x, *st, *q, *sf, *qT, *sfT, *s;
   int64_t rows, cols, ld;
   int fmt, mode;
+  PyObject* keep;
   (void)self;
   if (!take("fp4_quantize", names, 12, 9, args, nargs, kw, a) || !pointer(a[0], &x) || !integer(a[1], &rows) || !integer(a[2], &cols) ||
-      !integer(a[3], &ld) || !integer32(a[4], &fmt) || !integer32(a[5], &mode) || !structure(a[6], &st) || !pointer(a[7], &q) || !pointer(a[8], &sf) ||
-      !pointer(a[9], &qT) || !pointer(a[10], &sfT) || !stream(a[11], &s))
+      !integer(a[3], &ld) || !integer32(a[4], &fmt) || !integer32(a[5], &mode) || !pointer(a[7], &q) || !pointer(a[8], &sf) || !pointer(a[9], &qT) ||
+      !pointer(a[10], &sfT) || !stream(a[11], &s) || !state(a[6], &st, &keep))
     return NULL;
   fp8_status_t r;
   CALL(r, ((fp8_status_t(*)(const void*, int64_t, int64_t, int64_t, fp4_format_t, fp8_scaling_t, const fp8_tensor_state_t*, void*, void*, void*, void*,
                             void*))g_fn[QUANTIZE])(x, rows, cols, ld, (fp4_format_t)fmt, (fp8_scaling_t)mode, st, q, sf, qT, sfT, s));
+  Py_XDECREF(keep);
   return status(r);
 }
 
@@ -176,7 +194,7 @@ static PyObject* norm_fwd(PyObject* self, PyObject* const* args, Py_ssize_t narg
   PyObject* a[2];
   void *f, *s;
   (void)self;
-  if (!take("fp8_block_norm_fwd", names, 2, 1, args, nargs, kw, a) || !structure(a[0], &f) || !stream(a[1], &s)) return NULL;
+  if (!take("fp8_block_norm_fwd", names, 2, 1, args, nargs, kw, a) || !structure(a[0], g_norm, &f) || !stream(a[1], &s)) return NULL;
   fp8_status_t r;
   CALL(r, ((fp8_status_t(*)(const fp8_block_norm_t*, void*))g_fn[NORM_FWD])(f, s));
   return status(r);
@@ -188,7 +206,7 @@ static PyObject* norm_bwd(PyObject* self, PyObject* const* args, Py_ssize_t narg
   void *f, *b, *w, *s;
   int64_t n;
   (void)self;
-  if (!take("fp8_block_norm_bwd", names, 5, 4, args, nargs, kw, a) || !structure(a[0], &f) || !structure(a[1], &b) || !pointer(a[2], &w) ||
+  if (!take("fp8_block_norm_bwd", names, 5, 4, args, nargs, kw, a) || !structure(a[0], g_norm, &f) || !structure(a[1], g_grad, &b) || !pointer(a[2], &w) ||
       !integer(a[3], &n) || !stream(a[4], &s))
     return NULL;
   fp8_status_t r;
@@ -196,11 +214,13 @@ static PyObject* norm_bwd(PyObject* self, PyObject* const* args, Py_ssize_t narg
   return status(r);
 }
 
-/* init((addresses in the order above), error callable, stream callable) */
+/* init((addresses in the order above), error callable, stream callable, (classes of the state, the norm, its gradients)) */
 static PyObject* init(PyObject* self, PyObject* args) {
   PyObject *addresses, *error, *current;
+  PyTypeObject *state, *norm, *grad;
   (void)self;
-  if (!PyArg_ParseTuple(args, "O!OO", &PyTuple_Type, &addresses, &error, &current)) return NULL;
+  if (!PyArg_ParseTuple(args, "O!OO(O!O!O!)", &PyTuple_Type, &addresses, &error, &current, &PyType_Type, &state, &PyType_Type, &norm, &PyType_Type, &grad))
+    return NULL;
   if (PyTuple_GET_SIZE(addresses) != COUNT) {
     PyErr_SetString(PyExc_ValueError, "one address per function");
     return NULL;
@@ -211,6 +231,9 @@ static PyObject* init(PyObject* self, PyObject* args) {
   }
   Py_XSETREF(g_error, Py_NewRef(error));
   Py_XSETREF(g_stream, Py_NewRef(current));
+  Py_XSETREF(g_state, Py_NewRef((PyObject*)state));
+  Py_XSETREF(g_norm, Py_NewRef((PyObject*)norm));
+  Py_XSETREF(g_grad, Py_NewRef((PyObject*)grad));
   Py_RETURN_NONE;
 }
 
