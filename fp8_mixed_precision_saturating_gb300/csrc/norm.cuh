@@ -338,10 +338,11 @@ __device__ __forceinline__ float affine(float z, const float* w, const float* b,
   return b != nullptr ? z + b[c] : z;
 }
 
-// Whether a matrix can be read in pieces of `bytes` bytes: its start and its rows.
-inline bool rows_aligned(const void* p, int64_t ld, int64_t size, int bytes) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * size) % bytes == 0);
+// Whether a matrix can be read in pieces of `bytes` bytes: its start and, if there are several, its rows.
+inline bool rows_aligned(const void* p, int64_t rows, int64_t ld, int64_t size, int bytes) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (rows <= 1 || (ld * size) % bytes == 0));
 }
+__host__ __device__ inline int64_t gate_groups(const NormFwd& f) { return (f.tokens + f.gate_rows - 1) / f.gate_rows; }  // rows of a gate
 
 }  // namespace norms
 }  // namespace fp8gb

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(32 * kReduceWarps) norm_bwd_reduce_kernel(cons
     return;
   }
   // by groups where they are fewer than the parts, else by the parts' borders
-  const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
+  const int64_t groups = gate_groups(f);
   const bool by_group = groups < parts;
   for (int64_t i = blockIdx.y - 4; i < (by_group ? groups : parts - 1); i += gridDim.y - 4) {
     const int64_t grp = by_group ? i : (i + 1) * rows_per / f.gate_rows, ga = grp * f.gate_rows, ge = min(ga + f.gate_rows, f.tokens);
@@ -507,10 +507,10 @@ cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t st
   } else if (f.width > 8192) {
     e = launch_pdl(norm_bwd_any_kernel<TS, TB>, dim3(pl.parts), dim3(kThreads), 0, stream, f, b, part, part_alpha, pl.rows_per);
   } else {
-    const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.ld_r_out, ss, 4 * ss) &&
-                     rows_aligned(f.o, f.ld_o, bs, 4 * bs) && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) && rows_aligned(b.dh, b.ld_dh, bs, 4 * bs) &&
-                     rows_aligned(b.dr_out, b.ld_dr_out, ss, 4 * ss) && rows_aligned(b.dr, b.ld_dr, ss, 4 * ss) && rows_aligned(b.dO, b.ld_do, bs, 4 * bs) &&
-                     rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16);
+    const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.tokens, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.tokens, f.ld_r_out, ss, 4 * ss) &&
+                     rows_aligned(f.o, f.tokens, f.ld_o, bs, 4 * bs) && rows_aligned(f.gate, gate_groups(f), f.ld_gate, bs, 4 * bs) && rows_aligned(b.dh, f.tokens, b.ld_dh, bs, 4 * bs) &&
+                     rows_aligned(b.dr_out, f.tokens, b.ld_dr_out, ss, 4 * ss) && rows_aligned(b.dr, f.tokens, b.ld_dr, ss, 4 * ss) && rows_aligned(b.dO, f.tokens, b.ld_do, bs, 4 * bs) &&
+                     rows_aligned(f.w_post, 1, 0, 4, 16) && rows_aligned(f.b_post, 1, 0, 4, 16) && rows_aligned(f.w_pre, 1, 0, 4, 16);
     if (columns_of(f.width) == 8)
       e = vec ? launch_rows<TS, TB, 4, 8>(f, b, pl, part, part_alpha, stream) : launch_rows<TS, TB, 1, 8>(f, b, pl, part, part_alpha, stream);
     else
@@ -519,7 +519,7 @@ cudaError_t bwd_as(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t st
   if (e != cudaSuccess) return e;
   int64_t shared = 0;  // gate groups that may be shared
   if (b.dgate != nullptr && pl.parts > 1) {
-    const int64_t groups = (f.tokens + f.gate_rows - 1) / f.gate_rows;
+    const int64_t groups = gate_groups(f);
     shared = groups < pl.parts ? groups : pl.parts - 1;
   }
   const int cols = f.width % 4 == 0 ? 32 : 8;

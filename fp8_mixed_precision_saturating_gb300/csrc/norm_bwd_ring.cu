@@ -302,11 +302,11 @@ template <typename TS, typename TB>
 cudaError_t ring_as(const NormFwd& f, const NormBwd& b, const BwdPlan& pl, float* part, double* part_alpha, cudaStream_t stream, bool* taken) {
   const int64_t ss = sizeof(TS), bs = sizeof(TB);
   if (b.dh == nullptr || b.dr_out == nullptr || b.dr == nullptr || b.dO == nullptr || f.o == nullptr || f.pre == kNone ||
-      f.width > 8192 || f.width * bs % 16 != 0 || f.width * ss % 16 != 0 || !rows_aligned(b.dh, b.ld_dh, bs, 16) || !rows_aligned(f.r_out, f.ld_r_out, ss, 16) ||
-      !rows_aligned(b.dr_out, b.ld_dr_out, ss, 16) || !rows_aligned(f.o, f.ld_o, bs, 16) ||
-      (b.dres_scale != nullptr && !rows_aligned(f.r, f.ld_r, ss, 16)) || !rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) ||
-      !rows_aligned(b.dr, b.ld_dr, ss, 4 * ss) || !rows_aligned(b.dO, b.ld_do, bs, 4 * bs) || !rows_aligned(f.w_post, 0, 4, 16) ||
-      !rows_aligned(f.b_post, 0, 4, 16))
+      f.width > 8192 || f.width * bs % 16 != 0 || f.width * ss % 16 != 0 || !rows_aligned(b.dh, f.tokens, b.ld_dh, bs, 16) || !rows_aligned(f.r_out, f.tokens, f.ld_r_out, ss, 16) ||
+      !rows_aligned(b.dr_out, f.tokens, b.ld_dr_out, ss, 16) || !rows_aligned(f.o, f.tokens, f.ld_o, bs, 16) ||
+      (b.dres_scale != nullptr && !rows_aligned(f.r, f.tokens, f.ld_r, ss, 16)) || !rows_aligned(f.gate, gate_groups(f), f.ld_gate, bs, 4 * bs) ||
+      !rows_aligned(b.dr, f.tokens, b.ld_dr, ss, 4 * ss) || !rows_aligned(b.dO, f.tokens, b.ld_do, bs, 4 * bs) || !rows_aligned(f.w_post, 1, 0, 4, 16) ||
+      !rows_aligned(f.b_post, 1, 0, 4, 16))
     return cudaSuccess;
   const int teams = pl.per_sm;
   const int64_t row = f.width * (2 * bs + (b.dres_scale != nullptr ? 3 : 2) * ss), params = 8 * f.width, room = (kRingBytes - params) / (row * teams);

@@ -232,9 +232,9 @@ cudaError_t launch_rows(const NormFwd& f, cudaStream_t stream) {
 template <typename TS, typename TB>
 cudaError_t fwd_as(const NormFwd& f, cudaStream_t stream) {
   const int64_t ss = sizeof(TS), bs = sizeof(TB);
-  const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.ld_r_out, ss, 4 * ss) &&
-                   rows_aligned(f.o, f.ld_o, bs, 4 * bs) && rows_aligned(f.h, f.ld_h, bs, 4 * bs) && rows_aligned(f.gate, f.ld_gate, bs, 4 * bs) &&
-                   rows_aligned(f.w_post, 0, 4, 16) && rows_aligned(f.b_post, 0, 4, 16) && rows_aligned(f.w_pre, 0, 4, 16) && rows_aligned(f.b_pre, 0, 4, 16);
+  const bool vec = f.width % 4 == 0 && rows_aligned(f.r, f.tokens, f.ld_r, ss, 4 * ss) && rows_aligned(f.r_out, f.tokens, f.ld_r_out, ss, 4 * ss) &&
+                   rows_aligned(f.o, f.tokens, f.ld_o, bs, 4 * bs) && rows_aligned(f.h, f.tokens, f.ld_h, bs, 4 * bs) && rows_aligned(f.gate, gate_groups(f), f.ld_gate, bs, 4 * bs) &&
+                   rows_aligned(f.w_post, 1, 0, 4, 16) && rows_aligned(f.b_post, 1, 0, 4, 16) && rows_aligned(f.w_pre, 1, 0, 4, 16) && rows_aligned(f.b_pre, 1, 0, 4, 16);
   bool taken = false;
   const cudaError_t e = launch_norm_fwd_ring(f, stream, &taken);
   if (e != cudaSuccess || taken) return e;

@@ -235,9 +235,9 @@ cudaError_t ring_as(const NormFwd& f, cudaStream_t stream, bool* taken) {
   // per CTA from registers: 1000 x 4096 8.6, 7.7; 2000 x 4096 15.3, 17.1; 1000 x 8192 17.5, 18.8; 400 x 768 4.0, 3.4; 16384 x 768
   // 22.4, 27.9; 60000 x 512 44, 44)
   const int64_t rows = f.width > 4096 ? 4 : f.width >= 1024 ? 8 : 32;
-  if (f.o == nullptr || f.tokens < rows * num_sms() || f.width <= 512 || f.width > 8192 || f.width * ss % 16 != 0 || f.width * bs % 16 != 0 || !rows_aligned(f.r, f.ld_r, ss, 16) ||
-      !rows_aligned(f.o, f.ld_o, bs, 16) || !rows_aligned(f.r_out, f.ld_r_out, ss, 4 * ss) || !rows_aligned(f.h, f.ld_h, bs, 4 * bs) ||
-      !rows_aligned(f.gate, f.ld_gate, bs, 4 * bs))
+  if (f.o == nullptr || f.tokens < rows * num_sms() || f.width <= 512 || f.width > 8192 || f.width * ss % 16 != 0 || f.width * bs % 16 != 0 || !rows_aligned(f.r, f.tokens, f.ld_r, ss, 16) ||
+      !rows_aligned(f.o, f.tokens, f.ld_o, bs, 16) || !rows_aligned(f.r_out, f.tokens, f.ld_r_out, ss, 4 * ss) || !rows_aligned(f.h, f.tokens, f.ld_h, bs, 4 * bs) ||
+      !rows_aligned(f.gate, gate_groups(f), f.ld_gate, bs, 4 * bs))
     return cudaSuccess;
   const bool bias = f.b_post != nullptr || f.b_pre != nullptr, full = f.width % 512 == 0;
   const RingPlan p = ring_plan(f, f.width * (ss + bs), 16, bias);
