@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : 768, 1) norm_fwd_ring_kern
     keep_product(par, f.w_post, 1.0f, one, D, tid, threads);
     keep_product(par + D, f.w_pre, 1.0f, static_cast<const TB*>(nullptr), D, tid, threads);
     if constexpr (BIAS) {
-      keep_product(par + 2 * D, f.b_post, 0.0f, one, D, tid, threads);
+      keep_product(par + 2 * D, f.b_post, 0.0f, f.b_post != nullptr ? one : nullptr, D, tid, threads);  // (no bias: 0, not 0 times the gate)
       keep_product(par + 3 * D, f.b_pre, 0.0f, static_cast<const TB*>(nullptr), D, tid, threads);
     }
   }
