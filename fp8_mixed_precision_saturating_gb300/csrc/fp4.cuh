@@ -78,9 +78,9 @@ __device__ __forceinline__ uint32_t group_scale_nv(uint32_t abits, float s, uint
 
 // The scale byte of a group whose largest magnitude is `a` (fp32 bits `abits`, NaN if the group
 // holds one), and the fp32 factor its elements are multiplied by before the cast (0 when they
-// are all coded as zero: a zero scale).
+// are all coded as zero: a zero scale). least: least_scale(s) (NVFP4).
 template <int FMT>
-__device__ __forceinline__ uint32_t group_scale(uint32_t abits, float s, float& mul) {
+__device__ __forceinline__ uint32_t group_scale(uint32_t abits, float s, uint32_t least, float& mul) {
   mul = 0.0f;
   if (abits > 0x7F800000u) return F4<FMT>::kScaleNaN;
   if constexpr (FMT == 0) {
@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t group_scale(uint32_t abits, float s, float& 
     uint16_t e4m3;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e4m3) : "f"(0.0f), "f"(t));
     if (e4m3 == 0) return 0u;
-    const uint32_t c = max(static_cast<uint32_t>(e4m3), least_scale(s));
+    const uint32_t c = max(static_cast<uint32_t>(e4m3), least);
     mul = __fdiv_rn(s, e4m3_value(c));
     return c;
   } else {

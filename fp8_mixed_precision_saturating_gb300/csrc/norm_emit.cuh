@@ -22,11 +22,11 @@ __device__ __forceinline__ void fill_table(const NormFwd& f, float* table, int t
 // The group's scale byte and the factor of its elements. The caller's tensor scale may be any number: outside
 // [2^-100, 2^100] the table's quotients could round where the division does not, so it is divided then (tabled: not).
 template <int FMT>
-__device__ __forceinline__ uint32_t h_group_scale(uint32_t a, float s, bool tabled, const float* table, float& mul) {
+__device__ __forceinline__ uint32_t h_group_scale(uint32_t a, float s, uint32_t least, bool tabled, const float* table, float& mul) {
   if constexpr (FMT == 0) {
     if (tabled) return fp4::group_scale_nv(a, s, 1u, table, mul);
   }
-  return fp4::group_scale<FMT>(a, s, mul);
+  return fp4::group_scale<FMT>(a, s, least, mul);
 }
 
 // |a| and |b|'s larger one, NaN if either is
@@ -39,14 +39,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // One element of h a lane as a 4-bit code, its group held by neighbouring lanes. q, sf: the row's codes, and its byte of
 // group 0 in the scale atoms.
 template <int FMT>
-__device__ __forceinline__ void emit_single(float h, int c, int width, float s, bool tabled, const float* table, uint8_t* q, uint8_t* sf) {
+__device__ __forceinline__ void emit_single(float h, int c, int width, float s, uint32_t least, bool tabled, const float* table, uint8_t* q, uint8_t* sf) {
   constexpr int G = fp4::F4<FMT>::kGroup;
   uint32_t a = __float_as_uint(h) & 0x7FFFFFFFu;
   const uint32_t mask = G == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);  // the group's lanes
 #pragma unroll
   for (int o = 1; o < G; o <<= 1) a = max(a, __shfl_xor_sync(mask, a, o));
   float mul;
-  const uint32_t b = h_group_scale<FMT>(a, s, tabled, table, mul);
+  const uint32_t b = h_group_scale<FMT>(a, s, least, tabled, table, mul);
   float w[8] = {};
   w[0] = __fmul_rn(h, mul);
   uint32_t code = fp4::cvt8_e2m1(w) & 15u;
@@ -62,7 +62,7 @@ __device__ __forceinline__ void emit_single(float h, int c, int width, float s, 
 // columns in the row from the lane's first one on. Bound by the instructions around it: 16384 x 4096 into NVFP4 in 87 us
 // (every lane making its groups' scales and storing 16 bits an item: 115; without codes and with h in bf16: 83).
 template <int FMT, int N>
-__device__ __forceinline__ void emit_items(const Pair* h, int c, int left, float s, bool tabled, const float* table, uint8_t* q, uint8_t* sf) {
+__device__ __forceinline__ void emit_items(const Pair* h, int c, int left, float s, uint32_t least, bool tabled, const float* table, uint8_t* q, uint8_t* sf) {
   static_assert(N == 2 || N == 4, "items");
   constexpr uint32_t ALL = 0xFFFFFFFFu;
   constexpr int G = fp4::F4<FMT>::kGroup;
@@ -85,7 +85,7 @@ __device__ __forceinline__ void emit_items(const Pair* h, int c, int left, float
   }
   if constexpr (FMT == 1) m = max(m, __shfl_xor_sync(ALL, m, 4));
   float mul;
-  const uint32_t b = h_group_scale<FMT>(m, s, tabled, table, mul);
+  const uint32_t b = h_group_scale<FMT>(m, s, least, tabled, table, mul);
   if (b == fp4::F4<FMT>::kScaleNaN) mul = __uint_as_float(0x7FC00000u);
   const bool mine = 128 * j < left;
   const int g = (c + 128 * j) / G;
@@ -119,17 +119,18 @@ template <int FMT, int VEC, int E>
 __device__ __forceinline__ void emit_row(const NormFwd& f, const Pair (&h)[E / 2], int64_t t, int c, int left, const float* table) {
   const float s = h_scale_of(f);
   const bool tabled = s >= 7.888609e-31f && s <= 1.2676506e30f;
+  const uint32_t least = fp4::least_scale(s);
   const int width = static_cast<int>(f.width);
   uint8_t *q = f.hq + t * fp4::row_bytes(width), *sf = f.hsf + fp4::scale_offset(t, 0, fp4::atoms_along(FMT, width));
   if constexpr (VEC == 4) {
     constexpr int N = E == 8 ? 2 : 4;
 #pragma unroll
-    for (int i = 0; i < E / 4; i += N) emit_items<FMT, N>(h + 2 * i, c + 128 * i, left - 128 * i, s, tabled, table, q, sf);
+    for (int i = 0; i < E / 4; i += N) emit_items<FMT, N>(h + 2 * i, c + 128 * i, left - 128 * i, s, least, tabled, table, q, sf);
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float2 a = split(h[i / 2]);
-      if (32 * i < left) emit_single<FMT>(i & 1 ? a.y : a.x, c + 32 * i, width, s, tabled, table, q, sf);
+      if (32 * i < left) emit_single<FMT>(i & 1 ? a.y : a.x, c + 32 * i, width, s, least, tabled, table, q, sf);
     }
   }
   // the last atom's groups past the row

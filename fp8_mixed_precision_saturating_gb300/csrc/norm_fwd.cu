@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f)
     }
     if (f.hq != nullptr) {
       const float s = f.h_scale != nullptr ? *f.h_scale : 1.0f;
+      const uint32_t least = fp4::least_scale(s);
       const int64_t atoms = fp4::atoms_along(f.h_fmt, f.width), pitch = fp4::row_bytes(f.width);
       const int group = f.h_fmt == 0 ? 16 : 32;
       for (int64_t g = threadIdx.x; g < f.width / group; g += kThreads) {
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f)
         auto hv = [&](int64_t c) { return affine((mid(c) - pre.x) * pre.y, f.w_pre, f.b_pre, c); };
         for (int i = 0; i < group; ++i) a = max(a, __float_as_uint(hv(g * group + i)) & 0x7FFFFFFFu);
         float mul;
-        const uint32_t b = f.h_fmt == 0 ? fp4::group_scale<0>(a, s, mul) : fp4::group_scale<1>(a, s, mul);
+        const uint32_t b = f.h_fmt == 0 ? fp4::group_scale<0>(a, s, least, mul) : fp4::group_scale<1>(a, s, least, mul);
         f.hsf[fp4::scale_offset(t, g, atoms)] = static_cast<uint8_t>(b);
         for (int i = 0; i < group; i += 8) {
           float w[8];

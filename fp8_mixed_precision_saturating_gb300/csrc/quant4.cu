@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256) quant4_kernel(const uint16_t* x, int rows
   const uint32_t least = fp4::least_scale(s);
   if (FMT == 0 && tid < 8) table[tid] = fp4::quotient(s, tid);
   auto group = [&](uint32_t bf16_bits, float& mul) {
-    return FMT == 0 ? fp4::group_scale_nv(bf16_bits << 16, s, least, table, mul) : fp4::group_scale<FMT>(bf16_bits << 16, s, mul);
+    return FMT == 0 ? fp4::group_scale_nv(bf16_bits << 16, s, least, table, mul) : fp4::group_scale<FMT>(bf16_bits << 16, s, least, mul);
   };
   __syncthreads();
   uint32_t am = 0;  // largest magnitude of the tile (NaN included; delayed scaling records it)
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(256) quant4_rows_kernel(const uint16_t* x, int
     if constexpr (FMT == 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     am = max(am, m);
     float mul;
-    const uint32_t c = FMT == 0 ? fp4::group_scale_nv(m << 16, s, least, table, mul) : fp4::group_scale<FMT>(m << 16, s, mul);
+    const uint32_t c = FMT == 0 ? fp4::group_scale_nv(m << 16, s, least, table, mul) : fp4::group_scale<FMT>(m << 16, s, least, mul);
     uint2 o = cast16(w, mul);
     if (c == fp4::F4<FMT>::kScaleNaN) o = make_uint2(0u, 0u);
     if (m0 + 32 * j < rows && c0 / 2 < pitch) *reinterpret_cast<uint2*>(q + (m0 + 32 * j) * pitch + c0 / 2) = o;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(256) quant4_cols_kernel(const uint16_t* x, int
       const uint32_t a = e ? m >> 16 : m & 0xFFFFu;
       am = max(am, a);
       float mul;
-      const uint32_t c = FMT == 0 ? fp4::group_scale_nv(a << 16, s, least, table, mul) : fp4::group_scale<FMT>(a << 16, s, mul);
+      const uint32_t c = FMT == 0 ? fp4::group_scale_nv(a << 16, s, least, table, mul) : fp4::group_scale<FMT>(a << 16, s, least, mul);
       const int col = col0 + 2 * h + e, grp = k0 / G;
       s_sfT[(grp >> 2) * 512 + 16 * (col & 31) + 4 * (col >> 5) + (grp & 3)] = static_cast<uint8_t>(c);
 #pragma unroll
