@@ -417,37 +417,103 @@ def fp4_scaled_mm(A, sfa, B, sfb, M, N, K, fmt, scale_inv_a, scale_inv_b, C, dt,
 
 
 # ---- the norms around a block ----------------------------------------------------------
-def _fill(c, names, given):
-    """Set the pointers and leading dimensions of an argument block; a matrix given as a tensor brings its own
-    row stride unless ld_<name> is given too."""
+_TYPES = {FP8_DT_BF16: "torch.bfloat16", FP8_DT_F32: "torch.float32"}
+
+
+def _types_of(dt):
+    return [_TYPES[dt]] if dt in _TYPES else []  # (an unknown one is refused by the call)
+
+
+def _of_type(name, t, types):
+    """A tensor's elements are what the library reads there (``types``: names of torch types, empty: not known here)."""
+    if types and str(t.dtype) not in types:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(types)}")
+
+
+def _matrix(name, t, rows, cols):
+    """The leading dimension of a matrix given as a tensor, a vector being one row: rows of consecutive elements, at least
+    ``rows`` x ``cols``."""
+    if t.dim() not in (1, 2):
+        raise ValueError(f"{name} has {t.dim()} dimensions: give it as a matrix, or its leading dimension too")
+    n, m = (1, t.shape[0]) if t.dim() == 1 else t.shape
+    if m > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row are {t.stride(-1)} apart, not next to each other")
+    if n < rows or m < cols:
+        raise ValueError(f"{name} is {tuple(t.shape)}, smaller than [{rows}, {cols}]")
+    return t.stride(0) if n > 1 else max(m, 1)
+
+
+def _vector(name, t, n):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, fewer than {n}")
+
+
+def _fill(c, names, given, checks):
+    """Set the fields of an argument block. A matrix given as a tensor brings its own row pitch unless ld_<name> is given too.
+    Tensors are looked at first: checks[name] = (types, rows or None for a vector, columns or elements)."""
     unknown = set(given) - set(names)
     if unknown:
         raise TypeError(f"{type(c).__name__} has no {', '.join(sorted(unknown))}")
-    fields = {n for n, _ in c._fields_}
+    pointers = {n for n, t in c._fields_ if t is ctypes.c_void_p}
     for name, v in given.items():
-        if name in fields and dict(c._fields_)[name] is ctypes.c_void_p:
-            setattr(c, name, _ptr(v))
-            ld = "ld_" + name.rstrip("_")
-            if ld in fields and ld not in given and v is not None and not isinstance(v, int):
-                setattr(c, ld, v.stride(0))
-        else:
+        if name not in pointers:
             setattr(c, name, v)
+            continue
+        if hasattr(v, "data_ptr"):
+            types, rows, cols = checks[name]
+            ld = "ld_" + name.rstrip("_")
+            _of_type(name, v, types)
+            if rows is None:
+                _vector(name, v, cols)
+            elif ld not in given:
+                setattr(c, ld, _matrix(name, v, rows, cols))
+        setattr(c, name, _ptr(v))
     c._keep = given  # the tensors stay alive with the block
     return c
 
 
 def block_norm(tokens, width, stream_dt, block_dt, post=FP8_NORM_NONE, pre=FP8_NORM_RMS, eps=1e-5, **tensors):
     """An fp8_block_norm_t: what a program keeps for the norms around one block. Keywords are the fields of
-    the C struct (r, o, gate, gate_rows, res_scale, w_post, ..., stat_pre; include/fp8gb.h)."""
+    the C struct (r, o, gate, gate_rows, res_scale, w_post, ..., stat_pre; include/fp8gb.h). A tensor's type, size and
+    strides are checked here (a leading dimension that is given by hand is taken as it is)."""
     c = fp8_block_norm_t(tokens=tokens, width=width, stream_dt=stream_dt, block_dt=block_dt, post=post, pre=pre, eps=eps)
-    return _fill(c, [n for n, _ in fp8_block_norm_t._fields_[7:]], tensors)
+    stream, block, f32, u8 = _types_of(stream_dt), _types_of(block_dt), ["torch.float32"], ["torch.uint8"]
+    fmt, gate_rows = tensors.get("h_fmt", FP4_NVFP4), tensors.get("gate_rows", 0)
+    groups = -(-tokens // gate_rows) if gate_rows > 0 else 0
+    checks = {"r": (stream, tokens, width), "r_out": (stream, tokens, width), "o": (block, tokens, width), "h": (block, tokens, width),
+              "gate": (block, groups, width), "res_scale": (f32, None, 1), "h_scale": (f32, None, 1), "stat_post": (f32, None, 2 * tokens),
+              "stat_pre": (f32, None, 2 * tokens), "hq": (u8, None, tokens * lib.fp4_row_bytes(width)), "hsf": (u8, None, lib.fp4_scale_bytes(fmt, tokens, width)),
+              **{k: (f32, None, width) for k in ("w_post", "b_post", "w_pre", "b_pre")}}
+    return _fill(c, [n for n, _ in fp8_block_norm_t._fields_[7:]], tensors, checks)
+
+
+_GRADS = ("dh", "dr_out", "dr", "do_")
 
 
 def block_norm_grad(**tensors):
     """An fp8_block_norm_grad_t; keywords are its fields, with ``do`` for ``do_``."""
     if "do" in tensors:
         tensors["do_"] = tensors.pop("do")
-    return _fill(fp8_block_norm_grad_t(), [n for n, _ in fp8_block_norm_grad_t._fields_], tensors)
+    checks = {n: (["torch.float32"], None, 1) for n, t in fp8_block_norm_grad_t._fields_ if t is ctypes.c_void_p}
+    checks.update({n: (list(_TYPES.values()), 0, 0) for n in _GRADS})  # (which type and how large: fp8_block_norm_bwd_workspace_bytes)
+    return _fill(fp8_block_norm_grad_t(), [n for n, _ in fp8_block_norm_grad_t._fields_], tensors, checks)
+
+
+def _check_grads(f, b):
+    """The tensors of a gradient block against the norm's sizes and types."""
+    given, groups = getattr(b, "_keep", {}), -(-f.tokens // f.gate_rows) if f.gate_rows > 0 else 0
+    for name, v in given.items():
+        if not hasattr(v, "data_ptr"):
+            continue
+        if name in _GRADS:
+            dt = f.block_dt if name in ("dh", "do_") else f.stream_dt
+            _of_type(name, v, _types_of(dt))
+            if "ld_" + name.rstrip("_") not in given:
+                _matrix(name, v, f.tokens, f.width)
+        else:
+            _vector(name, v, groups * f.width if name == "dgate" else 1 if name == "dres_scale" else f.width)
 
 
 def fp8_block_norm_fwd(f, stream=None):
@@ -459,6 +525,9 @@ def fp8_block_norm_bwd(f, b, workspace, workspace_bytes, stream=None):
 
 
 def fp8_block_norm_bwd_workspace_bytes(f, b) -> int:
+    """Bytes of workspace; b's tensors are checked against f's sizes and types on the way."""
+    if isinstance(f, fp8_block_norm_t) and isinstance(b, fp8_block_norm_grad_t):
+        _check_grads(f, b)
     n = lib.fp8_block_norm_bwd_workspace_bytes(f, b)
     if n < 0:
         raise Fp8Error(FP8_ERR_INVALID_ARG, fp8_get_last_error_detail())
