@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8gb.so")
-FASTCALL = os.path.join(PKG, "_fastcall.so")
+# (named for this interpreter: another one does not import it)
+FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "api4.cu", "quant4.cu", "gemm4.cu", "norm_fwd.cu", "norm_fwd_ring.cu", "norm_bwd.cu", "norm_bwd_ring.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
@@ -40,7 +41,10 @@ def python_header() -> str | None:
 
 
 def build_fastcall():
-    """_fastcall.so: the binding's calls in C (csrc/fastcall.c); without Python.h the ctypes wrappers are used alone."""
+    """_fastcall: the binding's calls in C (csrc/fastcall.c); without Python.h the ctypes wrappers are used alone."""
+    untagged = os.path.join(PKG, "_fastcall.so")  # an older build's, which any interpreter would import
+    if untagged != FASTCALL and os.path.exists(untagged):
+        os.remove(untagged)
     include = python_header()
     if include is None:
         return
