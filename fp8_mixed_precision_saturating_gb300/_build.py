@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +16,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8gb.so")
 # (named for this interpreter: another one does not import it)
 FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+FASTCALL_SOURCE = os.path.join(CSRC, "fastcall.c")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "api4.cu", "quant4.cu", "gemm4.cu", "norm_fwd.cu", "norm_fwd_ring.cu", "norm_bwd.cu", "norm_bwd_ring.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
@@ -28,7 +30,7 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "fastcall.c"]
     files.append(os.path.join(INCLUDE, "fp8gb.h"))
     files.append(os.path.abspath(__file__))
     return files
@@ -40,32 +42,40 @@ def python_header() -> str | None:
     return d if os.path.exists(os.path.join(d, "Python.h")) and shutil.which("gcc") else None
 
 
-def build_fastcall():
-    """_fastcall: the binding's calls in C (csrc/fastcall.c); without Python.h the ctypes wrappers are used alone."""
+def build_fastcall(force: bool = False) -> bool:
+    """_fastcall: the binding's calls in C. Without Python.h, or where it does not compile (it needs Python 3.10), the ctypes
+    wrappers are used alone."""
     untagged = os.path.join(PKG, "_fastcall.so")  # an older build's, which any interpreter would import
     if untagged != FASTCALL and os.path.exists(untagged):
         os.remove(untagged)
     include = python_header()
     if include is None:
-        return
+        return False
+    if not force and _newer(FASTCALL, [FASTCALL_SOURCE, os.path.join(INCLUDE, "fp8gb.h"), os.path.abspath(__file__)]):
+        return True
     tmp = FASTCALL + ".tmp"
-    r = subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE, os.path.join(CSRC, "fastcall.c"), "-o", tmp],
-                       capture_output=True, text=True)
+    r = subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE, FASTCALL_SOURCE, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on fastcall.c:\n{r.stdout}\n{r.stderr}")
+        if os.path.exists(FASTCALL):  # made from another source
+            os.remove(FASTCALL)
+        warnings.warn(f"fastcall.c did not compile; calls go through ctypes:\n{r.stdout}\n{r.stderr}", RuntimeWarning, stacklevel=2)
+        return False
     os.replace(tmp, FASTCALL)
+    return True
+
+
+def _newer(path, sources) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in sources)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or (python_header() and not os.path.exists(FASTCALL)):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIB, _inputs())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source for sm_103a and link libfp8gb.so. Returns its path."""
     if not force and up_to_date():
+        build_fastcall()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -89,7 +99,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    build_fastcall()
+    build_fastcall(force=True)
     os.replace(tmp, LIB)
     return LIB
 
