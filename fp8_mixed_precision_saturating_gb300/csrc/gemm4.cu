@@ -18,12 +18,13 @@
 
 #include "fp4.cuh"
 #include "kernels.h"
+#include "mm4_plan.h"
 #include "ptx.cuh"
 
 namespace fp8gb {
 namespace {
 
-constexpr int kStageK = 256;            // contraction elements per stage: rows of 128 bytes
+constexpr int kStageK = kMm4StageK;     // contraction elements per stage: rows of 128 bytes
 constexpr int kOpBytes = 128 * 128;     // 128 rows of an operand
 constexpr int kStg = 32 * 128;          // an epilogue warp's staging buffer: 32 rows of 128 bytes
 
@@ -166,7 +167,7 @@ struct Pair {
   // SPLIT: the partial tile lies where the operands were
   static constexpr int TILE_PITCH = 260 * 4;  // bytes of a row: lanes' 16 bytes in different banks
   static_assert(128 * TILE_PITCH <= OFF_SF, "partial tile");
-  static constexpr int MOST_SPLITS = 4;
+  static constexpr int MOST_SPLITS = kMm4PairSplits;
   static constexpr int NBAR = 2 * STAGES + 4;  // full, empty, tile done [2], shared columns read, final
   static constexpr int OFF_SLOT = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM = OFF_SLOT + 16 + 1024;
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(192)
     __syncwarp();
     cluster_sync_all();
     const int c0 = live * rank / splits, c1 = live * (rank + 1) / splits;
-    cluster_sum<8, 2>(c0 * 32 + static_cast<int>(threadIdx.x), c1 * 32, C::THREADS, 0, 1, splits, rank, [&](int i) { return base + 16 * i; },
+    cluster_sum<kMm4Splits, 2>(c0 * 32 + static_cast<int>(threadIdx.x), c1 * 32, C::THREADS, 0, 1, splits, rank, [&](int i) { return base + 16 * i; },
                       [&](int i, float4 s) {
                         const int n = nb * 128 + 4 * (i & 31);
                         put4(out + (mb * BN + (i >> 5)) * p.ldc + n, s, d, p.N - n);
@@ -619,10 +620,10 @@ bool scales_map(CUtensorMap* m, const void* sf, int fmt, int64_t mn, int64_t k, 
 }
 
 // Once per device and kernel: the shared-memory limit; and per cluster size (up to 8), how many clusters are resident
-// at once.
+// at once (0: none fits, which is no error here).
 template <auto Kernel>
 cudaError_t prepare(int smem, int threads, int cluster, int* resident) {
-  static bool done[64] = {};
+  static bool done[64] = {}, asked[64][9] = {};
   static int count[64][9] = {};
   static std::mutex mu;
   int dev = 0;
@@ -635,7 +636,7 @@ cudaError_t prepare(int smem, int threads, int cluster, int* resident) {
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
-  if (count[dev][cluster] == 0) {
+  if (!asked[dev][cluster]) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(threads);
@@ -647,9 +648,14 @@ cudaError_t prepare(int smem, int threads, int cluster, int* resident) {
     cfg.numAttrs = 1;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(Kernel), &cfg);
-    if (e != cudaSuccess) return e;
-    if (n <= 0) return cudaErrorInvalidConfiguration;
+    if (e == cudaErrorInvalidClusterSize) {
+      cudaGetLastError();
+      n = 0;
+    } else if (e != cudaSuccess) {
+      return e;
+    }
     count[dev][cluster] = n;
+    asked[dev][cluster] = true;
   }
   *resident = count[dev][cluster];
   return cudaSuccess;
@@ -678,6 +684,7 @@ cudaError_t launch_pair(const Mm4Args& g, int splits, cudaStream_t stream, const
   int clusters = 0;
   const cudaError_t e = prepare<mm4_pair_kernel<FMT, F32, SPLIT>>(C::SMEM, C::THREADS, 2 * splits, &clusters);
   if (e != cudaSuccess) return e;
+  if (clusters <= 0) return cudaErrorInvalidConfiguration;
   CUtensorMap a, b, sa, sb, c;
   if (!codes_map(&a, g.A, g.M, g.K, 128) || !codes_map(&b, g.B, g.N, g.K, 128) || !scales_map(&sa, g.sfa, FMT, g.M, g.K, 1) ||
       !scales_map(&sb, g.sfb, FMT, g.N, g.K, 2) ||
@@ -711,9 +718,12 @@ cudaError_t launch_pair(const Mm4Args& g, int splits, cudaStream_t stream, const
 template <int FMT, int BN, typename T>
 cudaError_t launch_split(const Mm4Args& g, int splits, cudaStream_t stream, const char** why) {
   using C = Split<FMT, BN>;
-  int n = 0;
-  const cudaError_t e = prepare<mm4_split_kernel<FMT, BN, T>>(C::SMEM, C::THREADS, splits, &n);
-  if (e != cudaSuccess) return e;
+  for (int n = 0;; --splits) {  // clusters that the device holds
+    const cudaError_t e = prepare<mm4_split_kernel<FMT, BN, T>>(C::SMEM, C::THREADS, splits, &n);
+    if (e != cudaSuccess) return e;
+    if (n > 0) break;
+    if (splits == 1) return cudaErrorInvalidConfiguration;
+  }
   CUtensorMap w, x, sw, sx;
   if (!codes_map(&w, g.B, g.N, g.K, 128) || !codes_map(&x, g.A, g.M, g.K, BN) || !scales_map(&sw, g.sfb, FMT, g.N, g.K, 1) ||
       !scales_map(&sx, g.sfa, FMT, g.M, g.K, 1)) {
@@ -734,78 +744,46 @@ cudaError_t launch_split(const Mm4Args& g, int splits, cudaStream_t stream, cons
   return launch_cluster(mm4_split_kernel<FMT, BN, T>, grid, C::THREADS, C::SMEM, splits, stream, w, x, sw, sx, p);
 }
 
-// How a product is run: CTA pairs (bn == 0), or clusters of `splits` with tiles of 128 x bn.
-struct Plan {
-  int bn, splits;
-};
-
 // How many clusters of each number of splits the current device holds at once, asked once.
 template <int FMT, typename T>
-struct Clusters {
-  int pair[Pair<FMT>::MOST_SPLITS + 1], one[9];  // CTA pairs; single CTAs with 128-wide tiles
-  static cudaError_t of(const Clusters** out) {
-    static Clusters all[64];
-    static bool done[64] = {};
-    static std::mutex mu;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lk(mu);
-    if (!done[dev]) {
-      using P = Pair<FMT>;
-      using S = Split<FMT, 128>;
-      for (int s = 1; s <= P::MOST_SPLITS && e == cudaSuccess; ++s)
-        e = s == 1 ? prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, false>>(P::SMEM, P::THREADS, 2, &all[dev].pair[s])
-                   : prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, true>>(P::SMEM, P::THREADS, 2 * s, &all[dev].pair[s]);
-      for (int s = 1; s <= 8 && e == cudaSuccess; ++s) e = prepare<mm4_split_kernel<FMT, 128, T>>(S::SMEM, S::THREADS, s, &all[dev].one[s]);
-      if (e != cudaSuccess) return e;
-      done[dev] = true;
-    }
-    *out = &all[dev];
-    return cudaSuccess;
-  }
-};
-
-// The cheapest plan. Up to 64 rows of A the weights' bytes and the latency decide: one CTA per SM (more of them measured
-// slower: 1 x 4096 x 4096 took 3.9 us in 128 CTAs, 4.4 in 256), at least two stages each. Above, the measured times of
-// a stage and of what comes before and after the stages (us, GB300): a pair does 256 x 256 x 256 in 0.27, a CTA
-// 128 x 128 x 256 in 0.31; summing the parts of a split tile takes 3.6 on pairs (128 KB per CTA), 1.2 otherwise, where
-// the single CTA's unsplit epilogue takes 2.
-template <int FMT, typename T>
-cudaError_t choose(int64_t M, int64_t N, int64_t K, Plan* plan) {
-  const int64_t stages = (K + kStageK - 1) / kStageK, sms = num_sms();
-  const int64_t cols = (N + 127) / 128;
-  if (M <= 64) {
-    plan->bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    int64_t s = sms / cols;
-    s = s < stages / 2 ? s : stages / 2;
-    plan->splits = static_cast<int>(s < 1 ? 1 : s > 8 ? 8 : s);
-    return cudaSuccess;
-  }
-  const Clusters<FMT, T>* fit = nullptr;
-  const cudaError_t e = Clusters<FMT, T>::of(&fit);
+cudaError_t clusters_held(const Mm4Clusters** out) {
+  static Mm4Clusters all[64];
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  float best = 0.0f;
-  auto offer = [&](int bn, int splits, float us) {
-    if (plan->splits != 0 && us >= best) return;
-    best = us;
-    *plan = {bn, splits};
-  };
-  *plan = {0, 0};
-  const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), small = (M + 127) / 128 * cols;
-  for (int s = 1; s <= Pair<FMT>::MOST_SPLITS && s <= stages && (s == 1 || tiles <= fit->pair[s]); ++s)
-    offer(0, s, 4.3f + 0.27f * static_cast<float>((stages + s - 1) / s * ((tiles + fit->pair[s] - 1) / fit->pair[s])) + (s > 1 ? 3.6f : 0.0f));
-  for (int s = 1; s <= 8 && s <= stages && small <= (s == 1 ? sms : fit->one[s]); ++s)
-    offer(128, s, 4.0f + 0.31f * static_cast<float>((stages + s - 1) / s) + (s > 1 ? 1.2f : 2.0f));
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!done[dev]) {
+    using P = Pair<FMT>;
+    using S = Split<FMT, 128>;
+    for (int s = 1; s <= kMm4PairSplits && e == cudaSuccess; ++s)
+      e = s == 1 ? prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, false>>(P::SMEM, P::THREADS, 2, &all[dev].pair[s])
+                 : prepare<mm4_pair_kernel<FMT, sizeof(T) == 4, true>>(P::SMEM, P::THREADS, 2 * s, &all[dev].pair[s]);
+    for (int s = 1; s <= kMm4Splits && e == cudaSuccess; ++s) e = prepare<mm4_split_kernel<FMT, 128, T>>(S::SMEM, S::THREADS, s, &all[dev].one[s]);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  *out = &all[dev];
   return cudaSuccess;
 }
 
 template <int FMT, typename T>
 cudaError_t launch_as(const Mm4Args& g, cudaStream_t stream, const char** why) {
-  Plan p{0, 0};
-  const cudaError_t e = choose<FMT, T>(g.M, g.N, g.K, &p);
-  if (e != cudaSuccess) return e;
+  Mm4Plan p{0, 0};
+  if (g.M <= 64) {
+    p = mm4_plan_few_rows(g.M, g.N, g.K, num_sms());
+  } else {
+    const Mm4Clusters* fit = nullptr;
+    const cudaError_t e = clusters_held<FMT, T>(&fit);
+    if (e != cudaSuccess) return e;
+    p = mm4_plan(g.M, g.N, g.K, num_sms(), *fit);
+    if (p.splits == 0) {
+      *why = "the device holds no cluster of two CTAs";
+      return cudaErrorInvalidConfiguration;
+    }
+  }
   switch (p.bn) {
     case 0:
       return p.splits > 1 ? launch_pair<FMT, sizeof(T) == 4, true>(g, p.splits, stream, why) : launch_pair<FMT, sizeof(T) == 4, false>(g, 1, stream, why);
