@@ -180,28 +180,24 @@ struct Row {
 constexpr int kMaxStages = 4;            // rows that a ring in shared memory holds
 constexpr int kRingBytes = 216 * 1024;   // of an SM's shared memory for its CTAs' rings
 
-// A row's columns from the ring's copy, or from global memory.
-template <bool RING, int VEC, int E, bool FULL, typename T>
-__device__ __forceinline__ void row_of(const uint8_t* held, int at, const void* base, int64_t ld, int64_t t, int c, int left, Pair (&x)[E / 2]) {
-  if constexpr (RING) {
-    const T* p = reinterpret_cast<const T*>(held + at) + c;
+// A row's columns from its copy in shared memory, items of 4 as Row<4, E, FULL> has them.
+template <int E, bool FULL, typename T>
+__device__ __forceinline__ void held_row(const uint8_t* row, int c, int left, Pair (&x)[E / 2]) {
+  const T* p = reinterpret_cast<const T*>(row) + c;
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const bool in = FULL || 128 * i < left;
-      if constexpr (sizeof(T) == 4) {
-        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in) q = *reinterpret_cast<const float4*>(p + 128 * i);
-        x[2 * i] = pair(q.x, q.y);
-        x[2 * i + 1] = pair(q.z, q.w);
-      } else {
-        uint2 q = make_uint2(0u, 0u);
-        if (in) q = *reinterpret_cast<const uint2*>(p + 128 * i);
-        x[2 * i] = pair_of(q.x);
-        x[2 * i + 1] = pair_of(q.y);
-      }
+  for (int i = 0; i < E / 4; ++i) {
+    const bool in = FULL || 128 * i < left;
+    if constexpr (sizeof(T) == 4) {
+      float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (in) q = *reinterpret_cast<const float4*>(p + 128 * i);
+      x[2 * i] = pair(q.x, q.y);
+      x[2 * i + 1] = pair(q.z, q.w);
+    } else {
+      uint2 q = make_uint2(0u, 0u);
+      if (in) q = *reinterpret_cast<const uint2*>(p + 128 * i);
+      x[2 * i] = pair_of(q.x);
+      x[2 * i + 1] = pair_of(q.y);
     }
-  } else {
-    Row<VEC, E, FULL>::template load<true>(static_cast<const T*>(base) + t * ld + c, left, x);
   }
 }
 

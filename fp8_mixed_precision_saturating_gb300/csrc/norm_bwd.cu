@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
   // EARLY: all of a row's loads at once, an input that is not there as a row of no columns, so that no branch parts
   // them (16384 x 52 bf16: 26.3 -> 17.1 us; 4099 x 1537 in 8 columns a lane, fp32 stream: 50.9 -> 45.5). With 16 columns a lane the registers
   // are short, and single 16-bit elements take one each (4099 x 1537 bf16: 54.3 -> 62.8).
-  constexpr bool FULL = false, EARLY = E == 8 && (VEC == 4 || sizeof(TS) == 4);
-  using R = Row<VEC, E, FULL>;
+  constexpr bool EARLY = E == 8 && (VEC == 4 || sizeof(TS) == 4);
+  using R = Row<VEC, E, false>;
   constexpr int H = E / 2;
   __shared__ Red red;
   __shared__ double red_alpha[16];
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
             for (int i = 0; i < H; ++i) v[i] = fma2(p[i], ag[i], v[i]);
           }
         }
-        leave<VEC, E, FULL, false>((whole ? b.dgate + grp * D : mine + (grp == grp0 ? 4 : 5) * static_cast<int64_t>(D)) + c, left, v);
+        leave<VEC, E, false, false>((whole ? b.dgate + grp * D : mine + (grp == grp0 ? 4 : 5) * static_cast<int64_t>(D)) + c, left, v);
       }
       auto spend = [&](int k, Pair(&a)[H]) {  // gate times the sum, onto what earlier gates left
         Pair v[H];
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
 #pragma unroll
           for (int i = 0; i < H; ++i) a[i] = add2(a[i], v[i]);
         }
-        leave<VEC, E, FULL, true>(p, left, a);
+        leave<VEC, E, false, true>(p, left, a);
 #pragma unroll
         for (int i = 0; i < H; ++i) a[i] = zero;
       };
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormFwd f, const No
       }
     }
   }
-  if (b.dw_pre != nullptr) leave<VEC, E, FULL, true>(mine + c, left, aw_pre);
-  if constexpr (SUM) leave<VEC, E, FULL, true>(mine + D + c, left, ab_pre);
+  if (b.dw_pre != nullptr) leave<VEC, E, false, true>(mine + c, left, aw_pre);
+  if constexpr (SUM) leave<VEC, E, false, true>(mine + D + c, left, ab_pre);
   if (b.dres_scale != nullptr) {
     double a = static_cast<double>(al_hi) + static_cast<double>(al_lo);
 #pragma unroll

@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(E == 8 ? 640 : 512, 1)
       grp_end += f.gate_rows;
     }
     Pair dz[H], z[H], w[H];
-    row_of<true, 4, E, FULL, TB>(held, 0, nullptr, 0, t, c, left, dz);
-    row_of<true, 4, E, FULL, TS>(held, at_r_out, nullptr, 0, t, c, left, z);
+    held_row<E, FULL, TB>(held, c, left, dz);
+    held_row<E, FULL, TS>(held + at_r_out, c, left, z);
     if constexpr (SUM) {
 #pragma unroll
       for (int i = 0; i < H; ++i) ab_pre[i] = add2(ab_pre[i], dz[i]);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(E == 8 ? 640 : 512, 1)
         q1 = team_sum<WARPS>(sum2(sq), red, turn) * inv;
       }
       const Pair q = both(-q1);
-      row_of<true, 4, E, FULL, TS>(held, at_dr, nullptr, 0, t, c, left, w);
+      held_row<E, FULL, TS>(held + at_dr, c, left, w);
 #pragma unroll
       for (int i = 0; i < H; ++i) dz[i] = fma2(z[i], q, dz[i]);
       if (f.pre == kLayer) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(E == 8 ? 640 : 512, 1)
     // dz: g, the gradient at r'
     R::clear(dz, left);
     if (b.dres_scale != nullptr) {
-      row_of<true, 4, E, FULL, TS>(held, at_r, nullptr, 0, t, c, left, z);
+      held_row<E, FULL, TS>(held + at_r, c, left, z);
       Pair s = zero;
 #pragma unroll
       for (int i = 0; i < H; ++i) s = fma2(dz[i], z[i], s);
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(E == 8 ? 640 : 512, 1)
 #pragma unroll
     for (int i = 0; i < H; ++i) w[i] = mul2(dz[i], alpha);
     R::store(static_cast<TS*>(b.dr) + t * b.ld_dr + c, left, w);
-    row_of<true, 4, E, FULL, TB>(held, at_o, nullptr, 0, t, c, left, z);
+    held_row<E, FULL, TB>(held + at_o, c, left, z);
     if (f.post != kNone) {
       if (f.post == kLayer) {
         const Pair m = both(-post.x);

@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : 768, 1) norm_fwd_ring_kern
     if (!mbar_wait(bar0 + 8 * stage, phase, f.w, DEV_ERR_WAIT_PRODUCER)) failed[odd] = 1;
     const uint8_t* held = smem + ring0 + stage * bytes;
     Pair x[E / 2], n[E / 2];
-    row_of<true, 4, E, FULL, TS>(held, 0, nullptr, 0, t, c, left, x);
-    row_of<true, 4, E, FULL, TB>(held, r_bytes, nullptr, 0, t, c, left, n);
+    held_row<E, FULL, TS>(held, c, left, x);
+    held_row<E, FULL, TB>(held + r_bytes, c, left, n);
     const float2 post = team_stat<WARPS, E, FULL>(f.post, inv, f.eps, n, left, red, turn);
     if (f.post == kNone) team_sync();
     // a barrier of the team is behind its reads of the row: a later one may land there
