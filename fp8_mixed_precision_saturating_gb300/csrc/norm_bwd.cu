@@ -13,7 +13,8 @@ namespace {
 using namespace norms;
 
 // Any width and alignment: the row read again for every pass over it, the column sums in the
-// workspace (which its CTA alone touches).
+// workspace (which its CTA alone touches). Bound by those sums' way through global memory, row by row:
+// 8192 x 12288 bf16 4.4 ms, where the rows' bytes take 0.18.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kThreads) norm_bwd_any_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha,
                                                            int64_t rows_per) {

@@ -14,7 +14,8 @@ using namespace norms;
 // the next block. SUM: sum dh and sum g are wanted. 16384 x 4096 bf16 with the residual scale's gradient (939 MB): 146 us
 // and 6 for the sums, 0.9 of a plain copy's rate (two CTAs per SM with the parameters from L1: 165 in all); 4100 x 1536,
 // fp32 stream, layer norms with biases: 28 and 6, where a part's 9 rows are a chain of latencies. Room for 768 threads
-// instead of 640 (80 registers) spilled: 42 us for both.
+// instead of 640 (80 registers) spilled: 42 us for both. SUM with 16 columns a thread spills too (122 to 270 bytes: four
+// sums beside three rows): 16384 x 4096 bf16, layer norms, biases, a gate per 512 rows: 211 us, where the rows' bytes take 119.
 template <typename TS, typename TB, int E, bool FULL, bool SUM>
 __global__ void __launch_bounds__(E == 8 ? 640 : 512, 1)
     norm_bwd_ring_kernel(const NormFwd f, const NormBwd b, float* part, double* part_alpha, int64_t rows_per, int parts, int stages) {

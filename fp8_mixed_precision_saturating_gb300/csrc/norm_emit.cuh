@@ -71,7 +71,7 @@ __device__ __forceinline__ void emit_single(float h, int c, int width, float s, 
 // Four (N = 4) or two items of 4 neighbouring elements, 128 columns apart, of every lane. A group of an item is held by 4
 // (NVFP4) or 8 lanes. Their maxima are reduced so that every one of four (two) neighbouring lanes ends with another item's,
 // makes its scale once for all of them and stores it; likewise each stores the 8 (4) bytes of codes of one item. left:
-// columns in the row from the lane's first one on. Bound by the instructions around it: 16384 x 4096 into NVFP4 in 87 us
+// columns in the row from the lane's first one on. Bound by the instructions around it: 16384 x 4096 into NVFP4 in 86 us
 // (every lane making its groups' scales and storing 16 bits an item: 115; without codes and with h in bf16: 83).
 template <int FMT, int N>
 __device__ __forceinline__ void emit_items(const Pair* h, int c, int left, float s, uint32_t least, bool tabled, const float* table, uint8_t* q, uint8_t* sf) {

@@ -26,7 +26,8 @@ __device__ __forceinline__ float2 row_stat(int kind, int64_t width, float eps, R
   return st;
 }
 
-// Any width and alignment: one CTA per token, the row read again for every pass over it.
+// Any width and alignment: one CTA per token, the row read again for every pass over it. 2048 x 20480 bf16 252 us, where
+// the rows' bytes take 49.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kThreads) norm_fwd_any_kernel(const NormFwd f) {
   __shared__ Red red;

@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(256) quant4_rows_kernel(const uint16_t* x, int
 
 // Down the columns alone, from 16-byte aligned rows: 128 rows by 128 columns per CTA, read straight into registers (a
 // warp takes 16 rows, a lane 4 columns; MXFP4: 32 rows of half the columns, a lane 2); only codes and scales pass
-// through shared memory, to leave in 64- and 512-byte pieces. 4096 x 14336: 30.2 us, 5.0 TB/s (through the tile 31.9;
-// 256 rows per CTA 32.9).
+// through shared memory, to leave in 64- and 512-byte pieces. 4096 x 14336: 28.1 us, 5.4 TB/s (when it was 30.2: through
+// the tile 31.9, 256 rows per CTA 32.9).
 template <int FMT>
 __global__ void __launch_bounds__(256) quant4_cols_kernel(const uint16_t* x, int rows, int cols, int64_t ld, QuantState st, int delayed, uint8_t* qT,
                                                           uint8_t* sfT, int tiles_x, int backwards) {

@@ -464,7 +464,7 @@ fp8_status_t fp4_dequantize(const void* q, const void* sf, int64_t MN, int64_t K
 
 /* C [M, N] = A B^T of two 4-bit operands of one format, A with MN = M, B with MN = N, both along K:
  *   C_ij = round( d_a d_b sum_g c_a[i,g] c_b[j,g] sum_{k in g} a_ik b_jk ),  fp32 accumulation,
- * d_a and d_b the operands' inverse tensor scales (device fp32 each; NULL: 1), C bf16 or fp32 with
+ * d_a and d_b the operands' inverse tensor scales (device fp32 each, multiplied in fp32; NULL: 1), C bf16 or fp32 with
  * leading dimension ldc >= N, 16-byte aligned, ldc a multiple of 8 (bf16) or 4 (fp32); elements of
  * C's rows past N are not written. With operands quantised along the contraction this is the
  * forward (x, W^T), the data gradient (dy, W) and the weight gradient (x^T, dy^T); a few rows of A
