@@ -175,10 +175,9 @@ def _check(status: int) -> int:
 
 
 def _ptr(t):
-    try:
-        return t.data_ptr()
-    except AttributeError:  # None or a raw device address
+    if t is None or isinstance(t, int):
         return t
+    return t.data_ptr()  # (anything else, a host buffer above all, has none)
 
 
 def _no_torch_stream():
