@@ -32,6 +32,9 @@ FP8_SCALE_CURRENT, FP8_SCALE_DELAYED = 0, 1
 FP4_NVFP4, FP4_MXFP4 = 0, 1
 FP8_DT_BF16, FP8_DT_F32 = 0, 1
 FP8_NORM_NONE, FP8_NORM_RMS, FP8_NORM_LAYER = 0, 1, 2
+FP8_ROPE_HALF, FP8_ROPE_INTERLEAVED = 0, 1
+FP8_ROPE_PLAIN, FP8_ROPE_LINEAR, FP8_ROPE_BASE, FP8_ROPE_PARTS, FP8_ROPE_PARTS_BY_INDEX = range(5)
+FP8_KV_BF16, FP8_KV_MX_E4M3 = 0, 1
 
 
 class fp8_tensor_state_t(ctypes.Structure):
@@ -62,6 +65,37 @@ class fp8_block_norm_grad_t(ctypes.Structure):
     _fields_ = [("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64), ("dr_out", ctypes.c_void_p), ("ld_dr_out", ctypes.c_int64)]
     _fields_ += [("dr", ctypes.c_void_p), ("ld_dr", ctypes.c_int64), ("do_", ctypes.c_void_p), ("ld_do", ctypes.c_int64)]
     _fields_ += [(n, ctypes.c_void_p) for n in ("dgate", "dres_scale", "dw_post", "db_post", "dw_pre", "db_pre")]
+
+
+def _heads(*names):
+    """Fields of head tensors: address, elements between tokens, elements between heads."""
+    return [f for n in names for f in ((n, ctypes.c_void_p), ("ld_" + n, ctypes.c_int64), ("hs_" + n, ctypes.c_int64))]
+
+
+class fp8_qk_rope_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64)]
+    _fields_ += [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "rot_dims", "dt", "layout", "norm")]
+    _fields_ += [("eps", ctypes.c_float), ("amplitude", ctypes.c_float), ("turns", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+    _fields_ += _heads("q", "k", "v") + [("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p)] + _heads("q_out", "k_out")
+
+
+class fp8_qk_rope_grad_t(ctypes.Structure):
+    _fields_ = _heads("dq_out", "dk_out", "dq", "dk") + [("dw_q", ctypes.c_void_p), ("dw_k", ctypes.c_void_p)]
+
+
+class fp8_kv_cache_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("format", "pages", "page_size", "heads", "head_dim")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")]
+
+
+class fp8_kv_batch_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int32), ("table_width", ctypes.c_int32), ("ld_table", ctypes.c_int64)]
+    _fields_ += [(n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table")]
+
+
+class fp8_paged_attention_t(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)] + _heads("q", "out") + [("lse", ctypes.c_void_p)]
 
 
 class fp8_mm_problem_t(ctypes.Structure):
@@ -104,6 +138,8 @@ _SP = ctypes.POINTER(fp8_tensor_state_t)
 _MP = ctypes.POINTER(fp8_mm_problem_t)
 
 _NP, _GP = ctypes.POINTER(fp8_block_norm_t), ctypes.POINTER(fp8_block_norm_grad_t)
+_RP, _RGP = ctypes.POINTER(fp8_qk_rope_t), ctypes.POINTER(fp8_qk_rope_grad_t)
+_CP, _BP, _AP = ctypes.POINTER(fp8_kv_cache_t), ctypes.POINTER(fp8_kv_batch_t), ctypes.POINTER(fp8_paged_attention_t)
 _SIGS = {
     "fp8_quantize": [_P, _I64, _I64, _I64, _I, _I, _I, _SP, _P, _P, _P, _P],
     "fp8_scaled_mm": [_P, _I, _P, _I, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I64, _P],
@@ -124,6 +160,11 @@ _SIGS = {
     "fp4_scaled_mm": [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _I, _I64, _P],
     "fp8_block_norm_fwd": [_NP, _P],
     "fp8_block_norm_bwd": [_NP, _GP, _P, _I64, _P],
+    "fp8_rope_turns": [ctypes.c_int32, ctypes.c_double, _I] + [ctypes.c_double] * 4 + [_P],
+    "fp8_qk_rope_fwd": [_RP, _P],
+    "fp8_qk_rope_bwd": [_RP, _RGP, _P, _I64, _P],
+    "fp8_kv_append": [_RP, _CP, _BP, _P],
+    "fp8_paged_attention": [_AP, _CP, _BP, _P, _I64, _P],
     "fp8_history_commit": [_SP, _P],
     "fp8_history_commit_many": [_SP, ctypes.c_int32, _P],
     "fp8_poll_device_error": [],
@@ -147,6 +188,10 @@ lib.fp4_scale_bytes.argtypes = [_I, _I64, _I64]
 lib.fp4_scale_bytes.restype = ctypes.c_int64
 lib.fp8_block_norm_bwd_workspace_bytes.argtypes = [_NP, _GP]
 lib.fp8_block_norm_bwd_workspace_bytes.restype = ctypes.c_int64
+lib.fp8_qk_rope_bwd_workspace_bytes.argtypes = [_RP, _RGP]
+lib.fp8_qk_rope_bwd_workspace_bytes.restype = ctypes.c_int64
+lib.fp8_paged_attention_workspace_bytes.argtypes = [_AP, _CP, _BP]
+lib.fp8_paged_attention_workspace_bytes.restype = ctypes.c_int64
 lib.fp8_status_string.argtypes = [ctypes.c_int]
 lib.fp8_status_string.restype = ctypes.c_char_p
 
@@ -533,6 +578,183 @@ def fp8_block_norm_bwd_workspace_bytes(f, b) -> int:
     return n
 
 
+# ---- heads turned by their position, a paged cache, attention over it -------------------------
+def fp8_rope_turns(rot_dims, base, kind, factor, original, low, high, turns):
+    """turns: the address of rot_dims / 2 unsigned 64-bit numbers in host memory (rope_turns makes a tensor)."""
+    return _check(lib.fp8_rope_turns(rot_dims, base, kind, factor, original, low, high, turns))
+
+
+def rope_turns(rot_dims, base, kind=FP8_ROPE_PLAIN, factor=1.0, original=0.0, low=1.0, high=4.0, device="cuda"):
+    """The frequencies of a rotation as fractions of a turn per position, an int64 tensor [rot_dims / 2] that holds the
+    unsigned numbers of include/fp8gb.h; what a program keeps for all its layers."""
+    import torch
+    host = (ctypes.c_uint64 * max(rot_dims // 2, 1))()
+    fp8_rope_turns(rot_dims, base, kind, factor, original, low, high, host)
+    return torch.tensor(list((ctypes.c_int64 * len(host)).from_buffer(host))[: rot_dims // 2], dtype=torch.int64, device=device)
+
+
+def _head_tensor(name, t, tokens, heads, dim):
+    """Elements between two tokens and between two heads of a tensor [tokens, heads, dim]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} has {t.dim()} dimensions: give it as [tokens, heads, head_dim], or its ld and hs too")
+    if t.shape[0] < tokens or t.shape[1] < heads or t.shape[2] < dim:
+        raise ValueError(f"{name} is {tuple(t.shape)}, smaller than [{tokens}, {heads}, {dim}]")
+    if dim > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head are {t.stride(2)} apart, not next to each other")
+    return t.stride(0), t.stride(1)
+
+
+def _fill_heads(c, names, given, checks):
+    """Set the fields of an argument block with head tensors. A tensor brings its strides unless ld_<name> and hs_<name> are
+    given too. checks[name] = (types, (tokens, heads, dim)) or (types, elements of a vector)."""
+    unknown = set(given) - set(names)
+    if unknown:
+        raise TypeError(f"{type(c).__name__} has no {', '.join(sorted(unknown))}")
+    for name, v in given.items():
+        if name not in checks:
+            setattr(c, name, v)
+            continue
+        types, size = checks[name]
+        if hasattr(v, "data_ptr"):
+            _of_type(name, v, types)
+            if not isinstance(size, tuple):
+                _vector(name, v, size)
+            elif "ld_" + name in given or "hs_" + name in given:
+                if "ld_" + name not in given or "hs_" + name not in given:
+                    raise TypeError(f"{name}: ld_{name} and hs_{name} go together")
+            else:
+                ld, hs = _head_tensor(name, v, *size)
+                setattr(c, "ld_" + name, ld)
+                setattr(c, "hs_" + name, hs)
+        setattr(c, name, _ptr(v))
+    c._keep = given
+    return c
+
+
+def qk_rope(tokens, q_heads, k_heads, head_dim, rot_dims, dt, layout=FP8_ROPE_HALF, norm=FP8_NORM_NONE, eps=1e-6, amplitude=1.0, **tensors):
+    """An fp8_qk_rope_t: what a program keeps for the heads of one layer. Keywords are the fields of the C struct (turns, pos, q, k, v, w_q,
+    w_k, q_out, k_out; include/fp8gb.h); head tensors are [tokens, heads, head_dim] views with any strides but the last."""
+    c = fp8_qk_rope_t(tokens=tokens, q_heads=q_heads, k_heads=k_heads, head_dim=head_dim, rot_dims=rot_dims, dt=dt, layout=layout, norm=norm, eps=eps,
+                      amplitude=amplitude)
+    types, f32, q, k = _types_of(dt), ["torch.float32"], (tokens, q_heads, head_dim), (tokens, k_heads, head_dim)
+    checks = {"turns": (["torch.int64", "torch.uint64"], rot_dims // 2), "pos": (["torch.int32"], tokens), "w_q": (f32, head_dim), "w_k": (f32, head_dim),
+              "q": (types, q), "q_out": (types, q), "k": (types, k), "k_out": (types, k), "v": (types, k)}
+    return _fill_heads(c, [n for n, _ in fp8_qk_rope_t._fields_[10:]], tensors, checks)
+
+
+def qk_rope_grad(**tensors):
+    """An fp8_qk_rope_grad_t; keywords are its fields."""
+    types = list(_TYPES.values())
+    checks = {n: (types, (0, 0, 0)) for n in ("dq_out", "dk_out", "dq", "dk")}
+    checks.update({n: (["torch.float32"], 1) for n in ("dw_q", "dw_k")})  # (which type and how large: fp8_qk_rope_bwd_workspace_bytes)
+    return _fill_heads(fp8_qk_rope_grad_t(), [n for n, _ in fp8_qk_rope_grad_t._fields_], tensors, checks)
+
+
+def _check_rope_grads(f, b):
+    """The tensors of a gradient block against the heads' sizes and types."""
+    given = getattr(b, "_keep", {})
+    for name, v in given.items():
+        if not hasattr(v, "data_ptr"):
+            continue
+        if name in ("dw_q", "dw_k"):
+            _vector(name, v, f.head_dim)
+        else:
+            _of_type(name, v, _types_of(f.dt))
+            if "ld_" + name not in given:
+                _head_tensor(name, v, f.tokens, f.q_heads if name.startswith("dq") else f.k_heads, f.head_dim)
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None):
+    """An fp8_kv_cache_t of tensors [pages, heads, page_size, head_dim] (any strides but the last: keys and values alike): bf16, or
+    uint8 codes with uint8 scales [pages, heads, page_size, head_dim / 32], contiguous."""
+    if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k and v: [pages, heads, page_size, head_dim], of the same shape and strides")
+    if k.shape[3] > 1 and k.stride(3) != 1:
+        raise ValueError("k: the elements of a head are not next to each other")
+    mx = k_scale is not None or v_scale is not None
+    for name, t in (("k", k), ("v", v)):
+        _of_type(name, t, ["torch.uint8"] if mx else ["torch.bfloat16"])
+    pages, heads, page, dim = k.shape
+    if mx:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or tuple(t.shape) != (pages, heads, page, dim // 32) or not t.is_contiguous():
+                raise ValueError(f"{name}: [pages, heads, page_size, head_dim / 32], contiguous")
+            _of_type(name, t, ["torch.uint8"])
+    c = fp8_kv_cache_t(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), FP8_KV_MX_E4M3 if mx else FP8_KV_BF16, pages, page, heads, dim, *k.stride()[:3])
+    c._keep = (k, v, k_scale, v_scale)
+    return c
+
+
+def kv_batch(tokens, q_start, kv_len, page_table):
+    """An fp8_kv_batch_t of int32 tensors q_start [seqs + 1], kv_len [seqs] and page_table [seqs, table_width]."""
+    seqs = kv_len.numel()
+    for name, t in (("q_start", q_start), ("kv_len", kv_len), ("page_table", page_table)):
+        _of_type(name, t, ["torch.int32"])
+    _vector("q_start", q_start, seqs + 1)
+    _vector("kv_len", kv_len, seqs)
+    if page_table.dim() != 2 or page_table.shape[0] != seqs:
+        raise ValueError(f"page_table is {tuple(page_table.shape)}, not [{seqs}, table_width]")
+    c = fp8_kv_batch_t(tokens, seqs, page_table.shape[1], _matrix("page_table", page_table, seqs, 0), q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr())
+    c._keep = (q_start, kv_len, page_table)
+    return c
+
+
+def paged_attention(q_heads, scale, window=0, q=None, out=None, lse=None, **strides):
+    """An fp8_paged_attention_t: bf16 head tensors q and out [tokens, q_heads, head_dim], lse [tokens, q_heads] fp32 or None. Sizes are
+    checked against a cache and a batch by fp8_paged_attention_workspace_bytes."""
+    bf = ["torch.bfloat16"]
+    given = {n: v for n, v in (("q", q), ("out", out), ("lse", lse)) if v is not None}
+    return _fill_heads(fp8_paged_attention_t(q_heads=q_heads, window=window, scale=scale), [n for n, _ in fp8_paged_attention_t._fields_[3:]], {**given, **strides},
+                       {"q": (bf, (0, q_heads, 0)), "out": (bf, (0, q_heads, 0)), "lse": (["torch.float32"], 0)})
+
+
+def _check_attention(a, c, b):
+    given = getattr(a, "_keep", {})
+    for name, v in given.items():
+        if not hasattr(v, "data_ptr"):
+            continue
+        if name == "lse":
+            _vector(name, v, b.tokens * a.q_heads)
+        elif "ld_" + name not in given:
+            _head_tensor(name, v, b.tokens, a.q_heads, c.head_dim)
+
+
+def fp8_qk_rope_fwd(f, stream=None):
+    return _check(lib.fp8_qk_rope_fwd(f, _stream(stream)))
+
+
+def fp8_qk_rope_bwd(f, b, workspace, workspace_bytes, stream=None):
+    return _check(lib.fp8_qk_rope_bwd(f, b, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def fp8_qk_rope_bwd_workspace_bytes(f, b) -> int:
+    """Bytes of workspace; b's tensors are checked against f's sizes and types on the way."""
+    if isinstance(f, fp8_qk_rope_t) and isinstance(b, fp8_qk_rope_grad_t):
+        _check_rope_grads(f, b)
+    n = lib.fp8_qk_rope_bwd_workspace_bytes(f, b)
+    if n < 0:
+        raise Fp8Error(FP8_ERR_INVALID_ARG, fp8_get_last_error_detail())
+    return n
+
+
+def fp8_kv_append(f, cache, batch, stream=None):
+    return _check(lib.fp8_kv_append(f, cache, batch, _stream(stream)))
+
+
+def fp8_paged_attention(a, cache, batch, workspace, workspace_bytes, stream=None):
+    return _check(lib.fp8_paged_attention(a, cache, batch, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def fp8_paged_attention_workspace_bytes(a, cache, batch) -> int:
+    """Bytes of workspace; a's tensors are checked against the cache's and the batch's sizes on the way."""
+    if isinstance(a, fp8_paged_attention_t) and isinstance(cache, fp8_kv_cache_t) and isinstance(batch, fp8_kv_batch_t):
+        _check_attention(a, cache, batch)
+    n = lib.fp8_paged_attention_workspace_bytes(a, cache, batch)
+    if n < 0:
+        raise Fp8Error(FP8_ERR_INVALID_ARG, fp8_get_last_error_detail())
+    return n
+
+
 def fp8_history_commit(st, stream=None):
     return _check(lib.fp8_history_commit(_state(st), _stream(stream)))
 
@@ -564,8 +786,10 @@ try:
 except ImportError:
     pass
 if _fastcall is not None:
-    _NAMES = ("fp4_quantize", "fp4_dequantize", "fp4_scaled_mm", "fp8_block_norm_fwd", "fp8_block_norm_bwd")
+    _NAMES = ("fp4_quantize", "fp4_dequantize", "fp4_scaled_mm", "fp8_block_norm_fwd", "fp8_block_norm_bwd", "fp8_qk_rope_fwd", "fp8_qk_rope_bwd",
+              "fp8_kv_append", "fp8_paged_attention")
     _fastcall.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NAMES), _check, _stream,
-                   (fp8_tensor_state_t, fp8_block_norm_t, fp8_block_norm_grad_t))
+                   (fp8_tensor_state_t, fp8_block_norm_t, fp8_block_norm_grad_t, fp8_qk_rope_t, fp8_qk_rope_grad_t, fp8_kv_cache_t, fp8_kv_batch_t,
+                    fp8_paged_attention_t))
     _by_ctypes = {n: globals()[n] for n in _NAMES}  # (what a host without Python.h calls)
     globals().update({n: getattr(_fastcall, n) for n in _NAMES})

@@ -1,4 +1,4 @@
-/* fastcall.c -- the 4-bit and block-norm entry points called from Python without ctypes.
+/* fastcall.c -- the 4-bit, block-norm and attention entry points called from Python without ctypes.
  *
  * A product of one token takes some 6 us on the GPU. A call of it through ctypes and its Python wrapper takes 4.9 us of
  * the host's time, 2.3 of them inside the library (Grace); through this module 3.1. Same functions, names, argument
@@ -12,10 +12,10 @@
 
 #include "fp8gb.h"
 
-enum { QUANTIZE, DEQUANTIZE, SCALED_MM, NORM_FWD, NORM_BWD, COUNT };
+enum { QUANTIZE, DEQUANTIZE, SCALED_MM, NORM_FWD, NORM_BWD, ROPE_FWD, ROPE_BWD, APPEND, ATTENTION, COUNT };
 static void* g_fn[COUNT];
 static PyObject *g_error, *g_stream, *g_raw, *g_device; /* callables: of a status; of None; of a device; of nothing */
-static PyObject *g_state, *g_norm, *g_grad; /* the classes of the ctypes structures */
+static PyObject *g_state, *g_norm, *g_grad, *g_rope, *g_rope_grad, *g_cache, *g_batch, *g_attention; /* the classes of the ctypes structures */
 static PyObject *s_data_ptr, *s_cuda_stream, *s_c;
 
 /* Arguments by position, then by name, into out[n]; what is left out stays NULL and must not be required. */
@@ -214,12 +214,68 @@ static PyObject* norm_bwd(PyObject* self, PyObject* const* args, Py_ssize_t narg
   return status(r);
 }
 
-/* init((addresses in the order above), error callable, stream callable, (classes of the state, the norm, its gradients)) */
+static PyObject* rope_fwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+  static const char* const names[] = {"f", "stream"};
+  PyObject* a[2];
+  void *f, *s;
+  (void)self;
+  if (!take("fp8_qk_rope_fwd", names, 2, 1, args, nargs, kw, a) || !structure(a[0], g_rope, &f) || !stream(a[1], &s)) return NULL;
+  fp8_status_t r;
+  CALL(r, ((fp8_status_t(*)(const fp8_qk_rope_t*, void*))g_fn[ROPE_FWD])(f, s));
+  return status(r);
+}
+
+static PyObject* rope_bwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+  static const char* const names[] = {"f", "b", "workspace", "workspace_bytes", "stream"};
+  PyObject* a[5];
+  void *f, *b, *w, *s;
+  int64_t n;
+  (void)self;
+  if (!take("fp8_qk_rope_bwd", names, 5, 4, args, nargs, kw, a) || !structure(a[0], g_rope, &f) || !structure(a[1], g_rope_grad, &b) || !pointer(a[2], &w) ||
+      !integer(a[3], &n) || !stream(a[4], &s))
+    return NULL;
+  fp8_status_t r;
+  CALL(r, ((fp8_status_t(*)(const fp8_qk_rope_t*, const fp8_qk_rope_grad_t*, void*, int64_t, void*))g_fn[ROPE_BWD])(f, b, w, n, s));
+  return status(r);
+}
+
+static PyObject* append(PyObject* self, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+  static const char* const names[] = {"f", "cache", "batch", "stream"};
+  PyObject* a[4];
+  void *f, *c, *b, *s;
+  (void)self;
+  if (!take("fp8_kv_append", names, 4, 3, args, nargs, kw, a) || !structure(a[0], g_rope, &f) || !structure(a[1], g_cache, &c) || !structure(a[2], g_batch, &b) ||
+      !stream(a[3], &s))
+    return NULL;
+  fp8_status_t r;
+  CALL(r, ((fp8_status_t(*)(const fp8_qk_rope_t*, const fp8_kv_cache_t*, const fp8_kv_batch_t*, void*))g_fn[APPEND])(f, c, b, s));
+  return status(r);
+}
+
+static PyObject* attention(PyObject* self, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+  static const char* const names[] = {"a", "cache", "batch", "workspace", "workspace_bytes", "stream"};
+  PyObject* a[6];
+  void *f, *c, *b, *w, *s;
+  int64_t n;
+  (void)self;
+  if (!take("fp8_paged_attention", names, 6, 5, args, nargs, kw, a) || !structure(a[0], g_attention, &f) || !structure(a[1], g_cache, &c) ||
+      !structure(a[2], g_batch, &b) || !pointer(a[3], &w) || !integer(a[4], &n) || !stream(a[5], &s))
+    return NULL;
+  fp8_status_t r;
+  CALL(r, ((fp8_status_t(*)(const fp8_paged_attention_t*, const fp8_kv_cache_t*, const fp8_kv_batch_t*, void*, int64_t, void*))g_fn[ATTENTION])(f, c, b, w, n, s));
+  return status(r);
+}
+
+/* init((addresses in the order above), error callable, stream callable, (classes of the state, the norm, its gradients, the heads, their
+ * gradients, the cache, the batch, the attention)) */
 static PyObject* init(PyObject* self, PyObject* args) {
   PyObject *addresses, *error, *current;
-  PyTypeObject *state, *norm, *grad;
+  PyTypeObject* classes[8];
+  PyObject** const held[8] = {&g_state, &g_norm, &g_grad, &g_rope, &g_rope_grad, &g_cache, &g_batch, &g_attention};
   (void)self;
-  if (!PyArg_ParseTuple(args, "O!OO(O!O!O!)", &PyTuple_Type, &addresses, &error, &current, &PyType_Type, &state, &PyType_Type, &norm, &PyType_Type, &grad))
+  if (!PyArg_ParseTuple(args, "O!OO(O!O!O!O!O!O!O!O!)", &PyTuple_Type, &addresses, &error, &current, &PyType_Type, &classes[0], &PyType_Type, &classes[1],
+                        &PyType_Type, &classes[2], &PyType_Type, &classes[3], &PyType_Type, &classes[4], &PyType_Type, &classes[5], &PyType_Type, &classes[6],
+                        &PyType_Type, &classes[7]))
     return NULL;
   if (PyTuple_GET_SIZE(addresses) != COUNT) {
     PyErr_SetString(PyExc_ValueError, "one address per function");
@@ -231,9 +287,7 @@ static PyObject* init(PyObject* self, PyObject* args) {
   }
   Py_XSETREF(g_error, Py_NewRef(error));
   Py_XSETREF(g_stream, Py_NewRef(current));
-  Py_XSETREF(g_state, Py_NewRef((PyObject*)state));
-  Py_XSETREF(g_norm, Py_NewRef((PyObject*)norm));
-  Py_XSETREF(g_grad, Py_NewRef((PyObject*)grad));
+  for (int i = 0; i < 8; ++i) Py_XSETREF(*held[i], Py_NewRef((PyObject*)classes[i]));
   Py_RETURN_NONE;
 }
 
@@ -255,6 +309,10 @@ static PyMethodDef methods[] = {
     {"fp4_scaled_mm", (PyCFunction)(void (*)(void))scaled_mm, METH_FASTCALL | METH_KEYWORDS, NULL},
     {"fp8_block_norm_fwd", (PyCFunction)(void (*)(void))norm_fwd, METH_FASTCALL | METH_KEYWORDS, NULL},
     {"fp8_block_norm_bwd", (PyCFunction)(void (*)(void))norm_bwd, METH_FASTCALL | METH_KEYWORDS, NULL},
+    {"fp8_qk_rope_fwd", (PyCFunction)(void (*)(void))rope_fwd, METH_FASTCALL | METH_KEYWORDS, NULL},
+    {"fp8_qk_rope_bwd", (PyCFunction)(void (*)(void))rope_bwd, METH_FASTCALL | METH_KEYWORDS, NULL},
+    {"fp8_kv_append", (PyCFunction)(void (*)(void))append, METH_FASTCALL | METH_KEYWORDS, NULL},
+    {"fp8_paged_attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL | METH_KEYWORDS, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -213,4 +213,63 @@ cudaError_t launch_norm_fwd(const NormFwd& f, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormFwd& f, const NormBwd& b, void* ws, cudaStream_t stream);
 int64_t norm_bwd_workspace_bytes(const NormFwd& f);
 
+// Heads between the projections: the fields of fp8_qk_rope_t and fp8_qk_rope_grad_t, checked.
+struct Heads {
+  const void* in;
+  void* out;
+  int64_t ld_in, hs_in, ld_out, hs_out;
+  const float* w;
+  int n;  // heads of this part; 0: not in this call
+};
+struct Turn {
+  int64_t tokens;
+  int head_dim, rot_dims;
+  bool f32, interleaved, norm;
+  float eps, amplitude;
+  const uint64_t* turns;
+  const int32_t* pos;
+};
+struct TurnGrad {
+  const void* dy;
+  void* dx;
+  int64_t ld_dy, hs_dy, ld_dx, hs_dx;
+  float* dw;
+};
+// part 0 queries, 1 keys; tokens > 0
+cudaError_t launch_qk_rope_fwd(const Turn& f, const Heads (&part)[2], cudaStream_t stream);
+cudaError_t launch_qk_rope_bwd(const Turn& f, const Heads (&part)[2], const TurnGrad (&grad)[2], void* ws, cudaStream_t stream);
+int64_t qk_rope_bwd_workspace_bytes(const Turn& f);
+
+// A paged cache and a batch over it: the fields of fp8_kv_cache_t and fp8_kv_batch_t, checked.
+struct Cache {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  bool mx;
+  int pages, page_size, page_bits, heads, head_dim;
+  int64_t page_stride, head_stride, token_stride;
+};
+struct Batch {
+  int64_t tokens, ld_table;
+  int seqs, table_width;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+};
+// part 0 queries, 1 keys, 2 values; tokens > 0
+cudaError_t launch_kv_append(const Turn& f, const Heads (&part)[3], const Cache& c, const Batch& b, cudaStream_t stream);
+
+struct Attention {
+  int q_heads, window;
+  float scale;
+  const void* q;
+  void* out;
+  int64_t ld_q, hs_q, ld_out, hs_out;
+  float* lse;
+};
+// tokens, seqs > 0
+cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Batch& b, void* ws, cudaStream_t stream, const char** why);
+int64_t paged_attention_workspace_bytes(const Attention& a, const Cache& c, const Batch& b);
+
 }  // namespace fp8gb

@@ -1,0 +1,424 @@
+// qk_rope.cu -- heads of queries and keys: norm over each head and rotation by the token's position, forward and
+// backward (mathematics and layout: heads.cuh).
+//
+// What bounds it: memory. Forward reads and writes each element once; backward reads the gradient and, with a norm, the
+// input, and writes one gradient. A token's angles are worked out once per item (a token and a run of its heads)
+// and serve all its rows; a lane's norm weight, angle and amplitude are one factor per member of a pair
+//   y_u = r (u uc - v vs),  y_v = r (u us + v vc),   uc = w_u cos a, us = w_u sin a, vs = w_v sin a, vc = w_v cos a.
+// Backward: with (du, dv) the incoming pair turned back, z = x r, dz = w d:
+//   dx = r (dz - z mean(dz z)),   dw = sum over tokens and heads of d z.
+#include "heads.cuh"
+
+namespace fp8gb {
+namespace {
+
+using namespace heads;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+struct Args {
+  Turn t;
+  Heads part[2];
+  TurnGrad grad[2];
+  int per;            // heads of one item
+  int items0, items;  // items of a token: of the queries, in all
+  int64_t total;
+  float* sums;        // [CTAs, 2, head_dim]
+};
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const void* p, int64_t ld, int64_t hs, int64_t t, int h) {
+  return static_cast<const T*>(p) + t * ld + h * hs;
+}
+
+// Item i: a token, a part, and heads h0 .. h1 - 1 of it.
+struct Item {
+  int64_t token;
+  int part, h0, h1;
+};
+__device__ __forceinline__ Item item_of(int64_t i, const Args& g) {
+  Item m;
+  m.token = i / g.items;
+  int j = static_cast<int>(i - m.token * g.items);
+  m.part = j >= g.items0;
+  if (m.part) j -= g.items0;
+  m.h0 = j * g.per;
+  m.h1 = min(m.h0 + g.per, g.part[m.part].n);
+  return m;
+}
+
+template <typename T, bool INTER, int LPR>
+__global__ void __launch_bounds__(kThreads) qk_rope_fwd_kernel(const __grid_constant__ Args g) {
+  constexpr int RPW = 32 / LPR, U = 4;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
+  const Lane a = lane_of<INTER>(lane % LPR, g.t.head_dim, g.t.rot_dims);
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (i >= g.total) return;
+  const Item m = item_of(i, g);
+  const Heads& p = g.part[m.part];
+  const T* in = row_of<T>(p.in, p.ld_in, p.hs_in, m.token, 0);
+  T* out = static_cast<T*>(p.out) + m.token * p.ld_out;
+  Raw<T, INTER> raw[U];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int h = h0 + j * RPW + sub;
+      if (a.in && h < m.h1) raw[j].load(in + h * p.hs_in, a.o0, a.o1);
+    }
+  };
+  load(m.h0);
+  float c[4], s[4], wu[4], wv[4];
+  angles(a, g.t.turns, g.t.rot_dims, g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token), g.t.amplitude, c, s);
+  weights<INTER>(a, p.w, wu, wv);
+  float uc[4], us[4], vc[4], vs[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) uc[k] = wu[k] * c[k], us[k] = wu[k] * s[k], vc[k] = wv[k] * c[k], vs[k] = wv[k] * s[k];
+  const float inv_dim = 1.0f / static_cast<float>(g.t.head_dim);
+#pragma unroll 1
+  for (int h0 = m.h0; h0 < m.h1; h0 += U * RPW) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float u[4] = {}, v[4] = {}, yu[4], yv[4];
+      const int h = h0 + j * RPW + sub;
+      const bool live = a.in && h < m.h1;
+      if (live) raw[j].get(u, v);
+      float r = 1.0f;
+      if (g.t.norm) {
+        float q = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
+        r = rsqrtf(fmaf(row_sum<LPR>(q), inv_dim, g.t.eps));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        yu[k] = r * fmaf(u[k], uc[k], -(v[k] * vs[k]));
+        yv[k] = r * fmaf(u[k], us[k], v[k] * vc[k]);
+      }
+      if (live) Raw<T, INTER>::put(out + h * p.hs_out, a.o0, a.o1, yu, yv);
+    }
+    if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
+  }
+}
+
+// Sum a lane's 8 columns over the rows that a warp holds at once, and over the CTA's warps, into the CTA's part of the sums.
+template <bool INTER, int LPR>
+__device__ __forceinline__ void store_sums(const Args& g, const Lane& a, float (&du)[2][4], float (&dv)[2][4]) {
+  __shared__ float share[kWarps][2][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int m = LPR; m < 32; m <<= 1) {
+        du[p][k] += __shfl_xor_sync(0xFFFFFFFFu, du[p][k], m);
+        dv[p][k] += __shfl_xor_sync(0xFFFFFFFFu, dv[p][k], m);
+      }
+      if (lane < LPR && a.in) {
+        share[warp][p][INTER ? a.o0 + 2 * k : a.o0 + k] = du[p][k];
+        share[warp][p][INTER ? a.o0 + 2 * k + 1 : a.o1 + k] = dv[p][k];
+      }
+    }
+  __syncthreads();
+  for (int x = threadIdx.x; x < 2 * g.t.head_dim; x += kThreads) {
+    const int p = x / g.t.head_dim, d = x - p * g.t.head_dim;
+    float q = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) q += share[w][p][d];
+    g.sums[static_cast<int64_t>(blockIdx.x) * 2 * g.t.head_dim + x] = q;
+  }
+}
+
+template <typename T, bool INTER, int LPR, bool NORM, bool DW>
+__global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_constant__ Args g) {
+  constexpr int RPW = 32 / LPR, U = NORM ? 2 : 4;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
+  const Lane a = lane_of<INTER>(lane % LPR, g.t.head_dim, g.t.rot_dims);
+  const float inv_dim = 1.0f / static_cast<float>(g.t.head_dim);
+  float su[2][4] = {}, sv[2][4] = {};
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < g.total; i += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const Item m = item_of(i, g);
+    const Heads& p = g.part[m.part];
+    const TurnGrad& b = g.grad[m.part];
+    const T* dy = row_of<T>(b.dy, b.ld_dy, b.hs_dy, m.token, 0);
+    const T* in = NORM ? row_of<T>(p.in, p.ld_in, p.hs_in, m.token, 0) : nullptr;
+    T* dx = static_cast<T*>(b.dx) + m.token * b.ld_dx;
+    Raw<T, INTER> rd[U], rx[U];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int h = h0 + j * RPW + sub;
+        if (a.in && h < m.h1) {
+          rd[j].load(dy + h * b.hs_dy, a.o0, a.o1);
+          if constexpr (NORM) rx[j].load(in + h * p.hs_in, a.o0, a.o1);
+        }
+      }
+    };
+    load(m.h0);
+    float c[4], s[4], wu[4], wv[4];
+    angles(a, g.t.turns, g.t.rot_dims, g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token), g.t.amplitude, c, s);
+    if constexpr (NORM) weights<INTER>(a, p.w, wu, wv);
+    float au[4] = {}, av[4] = {};
+#pragma unroll 1
+    for (int h0 = m.h0; h0 < m.h1; h0 += U * RPW) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float du[4] = {}, dv[4] = {}, yu[4], yv[4];
+        const int h = h0 + j * RPW + sub;
+        const bool live = a.in && h < m.h1;
+        if (live) rd[j].get(du, dv);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          yu[k] = fmaf(du[k], c[k], dv[k] * s[k]);
+          yv[k] = fmaf(dv[k], c[k], -(du[k] * s[k]));
+        }
+        if constexpr (NORM) {
+          float u[4] = {}, v[4] = {};
+          if (live) rx[j].get(u, v);
+          float q = 0.0f, e = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
+            e = fmaf(yu[k] * wu[k], u[k], fmaf(yv[k] * wv[k], v[k], e));
+          }
+#pragma unroll
+          for (int x = LPR / 2; x > 0; x >>= 1) {
+            q += __shfl_xor_sync(0xFFFFFFFFu, q, x);
+            e += __shfl_xor_sync(0xFFFFFFFFu, e, x);
+          }
+          const float r = rsqrtf(fmaf(q, inv_dim, g.t.eps)), f = r * r * e * inv_dim;  // z mean(dz z) = x r (r e / dim)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (DW) {
+              au[k] = fmaf(yu[k], u[k] * r, au[k]);
+              av[k] = fmaf(yv[k], v[k] * r, av[k]);
+            }
+            yu[k] = r * fmaf(-u[k], f, yu[k] * wu[k]);
+            yv[k] = r * fmaf(-v[k], f, yv[k] * wv[k]);
+          }
+        }
+        if (live && b.dx != nullptr) Raw<T, INTER>::put(dx + h * b.hs_dx, a.o0, a.o1, yu, yv);
+      }
+      if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
+    }
+    if constexpr (DW) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (m.part == 0) {
+          su[0][k] += au[k], sv[0][k] += av[k];
+        } else {
+          su[1][k] += au[k], sv[1][k] += av[k];
+        }
+      }
+    }
+  }
+  if constexpr (DW) store_sums<INTER, LPR>(g, a, su, sv);
+}
+
+// Rows of single elements, a warp each; forward (BWD false) or backward.
+template <typename T, bool BWD>
+__global__ void __launch_bounds__(kThreads) qk_rope_any_kernel(const __grid_constant__ Args g) {
+  __shared__ float share[kWarps][256];
+  __shared__ float sums[kWarps][2][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = g.t.head_dim, R = g.t.rot_dims;
+  const float inv_dim = 1.0f / static_cast<float>(D);
+  float acc[2][8] = {};
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < g.total; i += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const Item m = item_of(i, g);
+    const Heads& p = g.part[m.part];
+    const TurnGrad& b = g.grad[m.part];
+    const int32_t pos = g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token);
+    // of element d: its partner, and cos, +-sin with which y_d = x_d c + x_partner s (backward: the other sign)
+    float c[8], s[8], w[8];
+    int mate[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int d = lane + 32 * k;
+      c[k] = 1.0f, s[k] = 0.0f, w[k] = 1.0f, mate[k] = d & 255;
+      if (d < R) {
+        const bool second = g.t.interleaved ? d & 1 : d >= R / 2;
+        const int pair = g.t.interleaved ? d >> 1 : second ? d - R / 2 : d;
+        const float2 t = cos_sin(__ldg(g.t.turns + pair), pos);
+        c[k] = t.x * g.t.amplitude;
+        s[k] = t.y * g.t.amplitude * (second != BWD ? 1.0f : -1.0f);
+        mate[k] = g.t.interleaved ? d ^ 1 : second ? d - R / 2 : d + R / 2;
+      }
+      if (d < D && p.w != nullptr) w[k] = __ldg(p.w + d);
+    }
+    for (int h = m.h0; h < m.h1; ++h) {
+      float x[8], r = 1.0f;
+      const T* in = row_of<T>(p.in, p.ld_in, p.hs_in, m.token, h);
+      const T* dy = row_of<T>(b.dy, b.ld_dy, b.hs_dy, m.token, h);
+      const bool reads_x = !BWD || g.t.norm;
+      float q = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = lane + 32 * k;
+        x[k] = reads_x && d < D ? element(in + d) : 0.0f;
+        q = fmaf(x[k], x[k], q);
+      }
+      if (g.t.norm) r = rsqrtf(fmaf(row_sum<32>(q), inv_dim, g.t.eps));
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = lane + 32 * k;
+        y[k] = BWD ? (d < D ? element(dy + d) : 0.0f) : x[k] * r * w[k];
+        share[warp][d] = y[k];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = fmaf(y[k], c[k], share[warp][mate[k]] * s[k]);
+      __syncwarp();
+      if constexpr (BWD) {
+        if (g.t.norm) {
+          float e = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float z = x[k] * r;
+            if (m.part == 0)
+              acc[0][k] = fmaf(y[k], z, acc[0][k]);
+            else
+              acc[1][k] = fmaf(y[k], z, acc[1][k]);
+            e = fmaf(y[k] * w[k], z, e);
+          }
+          e = row_sum<32>(e) * inv_dim;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = r * (y[k] * w[k] - x[k] * r * e);
+        }
+      }
+      T* out = BWD ? static_cast<T*>(b.dx) : static_cast<T*>(p.out);
+      const int64_t at = BWD ? m.token * b.ld_dx + h * b.hs_dx : m.token * p.ld_out + h * p.hs_out;
+      if (out != nullptr)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (lane + 32 * k < D) set_element(out + at + lane + 32 * k, y[k]);
+    }
+  }
+  if (BWD && g.sums != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[warp][0][lane + 32 * k] = acc[0][k], sums[warp][1][lane + 32 * k] = acc[1][k];
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+      const int part = x / D, d = x - part * D;
+      float q = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) q += sums[j][part][d];
+      g.sums[static_cast<int64_t>(blockIdx.x) * 2 * D + x] = q;
+    }
+  }
+}
+
+// dw of both parts from the CTAs' sums: a warp per column, 32 partial sums of every 32nd CTA, in order.
+__global__ void __launch_bounds__(kThreads) qk_rope_dw_kernel(const float* sums, int ctas, int dim, float* dw_q, float* dw_k) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, x = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (x >= 2 * dim) return;
+  float* out = x < dim ? dw_q : dw_k;
+  if (out == nullptr) return;
+  float q = 0.0f;
+#pragma unroll 4
+  for (int c = lane; c < ctas; c += 32) q += sums[static_cast<int64_t>(c) * 2 * dim + x];
+  q = row_sum<32>(q);
+  if (lane == 0) out[x < dim ? x : x - dim] = q;
+}
+
+int bwd_ctas() { return 3 * num_sms(); }
+
+bool chunks_of(const void* p, int64_t ld, int64_t hs, int64_t bytes, int64_t elem) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * elem % bytes == 0 && hs * elem % bytes == 0);
+}
+
+template <typename F>
+cudaError_t by_kind(const Turn& t, F&& f) {
+  const int lpr = t.head_dim <= 64 ? 8 : t.head_dim <= 128 ? 16 : 32;
+#define FP8GB_LPR(T, I) (lpr == 8 ? f.template operator()<T, I, 8>() : lpr == 16 ? f.template operator()<T, I, 16>() : f.template operator()<T, I, 32>())
+  if (t.f32) return t.interleaved ? FP8GB_LPR(float, true) : FP8GB_LPR(float, false);
+  return t.interleaved ? FP8GB_LPR(bf16, true) : FP8GB_LPR(bf16, false);
+#undef FP8GB_LPR
+}
+
+// Items: a token's heads in runs of `per`, so that there are at least `want` of them where that leaves a run at least `least` heads.
+void set_items(Args& g, int64_t want, int least) {
+  const int heads = max(g.part[0].n, g.part[1].n);
+  const int64_t runs = min(static_cast<int64_t>((heads + least - 1) / least), max(int64_t{1}, (want + g.t.tokens - 1) / g.t.tokens));
+  g.per = static_cast<int>((heads + runs - 1) / runs);
+  g.items0 = (g.part[0].n + g.per - 1) / g.per;
+  g.items = g.items0 + (g.part[1].n + g.per - 1) / g.per;
+  g.total = g.t.tokens * g.items;
+}
+
+struct FwdLaunch {
+  const Args& g;
+  cudaStream_t s;
+  template <typename T, bool I, int L>
+  cudaError_t operator()() const {
+    return launch_pdl(qk_rope_fwd_kernel<T, I, L>, dim3(static_cast<unsigned>((g.total + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, g);
+  }
+};
+
+struct BwdLaunch {
+  const Args& g;
+  cudaStream_t s;
+  int ctas;
+  template <typename T, bool I, int L>
+  cudaError_t operator()() const {
+    auto* k = g.t.norm ? (g.sums != nullptr ? qk_rope_bwd_kernel<T, I, L, true, true> : qk_rope_bwd_kernel<T, I, L, true, false>) : qk_rope_bwd_kernel<T, I, L, false, false>;
+    return launch_pdl(k, dim3(ctas), dim3(kThreads), 0, s, g);
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_qk_rope_fwd(const Turn& f, const Heads (&part)[2], cudaStream_t stream) {
+  Args g{};
+  g.t = f;
+  g.part[0] = part[0];
+  g.part[1] = part[1];
+  const int64_t elem = f.f32 ? 4 : 2, bytes = f.f32 || f.interleaved ? 16 : 8;
+  bool vec = f.head_dim % 8 == 0 && (f.interleaved || f.rot_dims % 8 == 0);
+  for (const Heads& p : part)
+    if (p.n > 0) vec = vec && chunks_of(p.in, p.ld_in, p.hs_in, bytes, elem) && chunks_of(p.out, p.ld_out, p.hs_out, bytes, elem);
+  set_items(g, int64_t{64} * num_sms(), 8);
+  if (vec) return by_kind(f, FwdLaunch{g, stream});
+  const unsigned ctas = static_cast<unsigned>(min((g.total + kWarps - 1) / kWarps, int64_t{8} * num_sms()));
+  return f.f32 ? launch_pdl(qk_rope_any_kernel<float, false>, dim3(ctas), dim3(kThreads), 0, stream, g)
+               : launch_pdl(qk_rope_any_kernel<bf16, false>, dim3(ctas), dim3(kThreads), 0, stream, g);
+}
+
+int64_t qk_rope_bwd_workspace_bytes(const Turn& f) { return static_cast<int64_t>(bwd_ctas()) * 2 * f.head_dim * 4; }
+
+cudaError_t launch_qk_rope_bwd(const Turn& f, const Heads (&part)[2], const TurnGrad (&grad)[2], void* ws, cudaStream_t stream) {
+  Args g{};
+  g.t = f;
+  bool vec = f.head_dim % 8 == 0 && (f.interleaved || f.rot_dims % 8 == 0);
+  const int64_t elem = f.f32 ? 4 : 2, bytes = f.f32 || f.interleaved ? 16 : 8;
+  for (int p = 0; p < 2; ++p) {
+    g.part[p] = part[p];
+    g.grad[p] = grad[p];
+    if (part[p].n == 0) continue;
+    vec = vec && chunks_of(grad[p].dy, grad[p].ld_dy, grad[p].hs_dy, bytes, elem) && chunks_of(grad[p].dx, grad[p].ld_dx, grad[p].hs_dx, bytes, elem) &&
+          (!f.norm || chunks_of(part[p].in, part[p].ld_in, part[p].hs_in, bytes, elem));
+  }
+  const bool dw = grad[0].dw != nullptr || grad[1].dw != nullptr;
+  if (dw) g.sums = static_cast<float*>(ws);
+  set_items(g, int64_t{8} * bwd_ctas() * kWarps, 8);
+  const int ctas = static_cast<int>(min((g.total + kWarps - 1) / kWarps, static_cast<int64_t>(bwd_ctas())));
+  cudaError_t e;
+  if (vec)
+    e = by_kind(f, BwdLaunch{g, stream, ctas});
+  else
+    e = f.f32 ? launch_pdl(qk_rope_any_kernel<float, true>, dim3(ctas), dim3(kThreads), 0, stream, g)
+              : launch_pdl(qk_rope_any_kernel<bf16, true>, dim3(ctas), dim3(kThreads), 0, stream, g);
+  if (e != cudaSuccess || !dw) return e;
+  const float* sums = g.sums;
+  return launch_pdl(qk_rope_dw_kernel, dim3((2 * f.head_dim + kWarps - 1) / kWarps), dim3(kThreads), 0, stream, sums, ctas, f.head_dim, grad[0].dw, grad[1].dw);
+}
+
+}  // namespace fp8gb

@@ -556,6 +556,160 @@ fp8_status_t fp8_block_norm_bwd(const fp8_block_norm_t* f, const fp8_block_norm_
 /* Bytes of workspace the backward needs on the current device; negative on an error. */
 int64_t fp8_block_norm_bwd_workspace_bytes(const fp8_block_norm_t* f, const fp8_block_norm_grad_t* b);
 
+/* ------------------------------------------------------------------------------------------
+ * Between a block's projections: heads turned by their position, a paged cache, attention over it
+ * ------------------------------------------------------------------------------------------
+ * What stands between the QKV projection and the output projection ([GUARD] "Real products...": norms and softmax
+ * stay in high precision; [SPEED] "Explanation": the projections on either side). The pages have no such entry points.
+ *
+ * Head tensors hold [tokens, heads, head_dim] elements at x + token * ld_x + head * hs_x, the elements of a head next to
+ * each other: a part of the projection's output rows as it stands, or heads apart. The rows of a tensor must not overlap,
+ * and either each token's heads lie between two tokens' beginnings or each head's tokens between two heads'.
+ *
+ * Rotation: pair i of a head (of rot_dims / 2) of the token at position p turns by the angle
+ *   theta = 2 pi p turns[i] / 2^64:   (a, b) -> amplitude (a cos theta - b sin theta, a sin theta + b cos theta),
+ * HALF pairs elements i and i + rot_dims / 2, INTERLEAVED 2 i and 2 i + 1; elements from rot_dims on stay. turns[i] is a
+ * frequency as a fraction of a turn per position in 64 bits, so that p * turns[i] modulo 2^64 is the angle exactly, at
+ * any position. fp8_rope_turns makes them on the host:
+ *   PLAIN    f_i = base^(-2 i / rot_dims) radians per position
+ *   LINEAR   f_i / factor
+ *   BASE     PLAIN with base * factor^(rot_dims / (rot_dims - 2))
+ *   PARTS    with r = original f_i / 2 pi, the turns over the original length: f_i / factor for r <= low, f_i for r >= high,
+ *            (1 - s) f_i / factor + s f_i with s = (r - low) / (high - low) between
+ *   PARTS_BY_INDEX  the same with s linear in i between the (real) indices where r is low and high */
+typedef enum { FP8_ROPE_HALF = 0, FP8_ROPE_INTERLEAVED = 1 } fp8_rope_layout_t;
+typedef enum {
+  FP8_ROPE_PLAIN = 0,
+  FP8_ROPE_LINEAR = 1,
+  FP8_ROPE_BASE = 2,
+  FP8_ROPE_PARTS = 3,
+  FP8_ROPE_PARTS_BY_INDEX = 4
+} fp8_rope_scaling_t;
+
+/* turns: HOST memory, rot_dims / 2 numbers. base > 1; rot_dims even, 0 .. 256 (BASE: from 4 on); factor > 0 (all but PLAIN), original > 0
+ * and 0 < low < high (the PARTS forms); all finite. No GPU is needed. */
+fp8_status_t fp8_rope_turns(int32_t rot_dims, double base, fp8_rope_scaling_t kind, double factor, double original,
+                            double low, double high, uint64_t* turns);
+
+/* Arguments of fp8_qk_rope_fwd, of what its backward reads, and of fp8_kv_append. Device pointers, caller-owned; tensors aligned to
+ * their elements (rows of 8 bytes (bf16) or 16 (fp32) are faster). */
+typedef struct {
+  int64_t tokens;
+  int32_t q_heads, k_heads, head_dim, rot_dims;
+  int32_t dt;              /* fp8_dtype_t of the head tensors */
+  int32_t layout;          /* fp8_rope_layout_t */
+  int32_t norm;            /* FP8_NORM_NONE, or FP8_NORM_RMS: x / sqrt(mean(x^2) + eps) w over each head before it turns */
+  float eps;
+  float amplitude;         /* 1, or what a stretched context asks for; not 0 */
+  const uint64_t* turns;   /* [rot_dims / 2] */
+  const int32_t* pos;      /* [tokens]; NULL: token t is at position t (fp8_kv_append: at its place in its sequence) */
+  const void* q;           /* NULL with q_out NULL: no queries in this call; the same for k */
+  int64_t ld_q, hs_q;
+  const void* k;
+  int64_t ld_k, hs_k;
+  const void* v;           /* fp8_kv_append alone */
+  int64_t ld_v, hs_v;
+  const float* w_q;        /* [head_dim] each; NULL: ones */
+  const float* w_k;
+  void* q_out;             /* may be q itself with the same strides; the same for k */
+  int64_t ld_q_out, hs_q_out;
+  void* k_out;
+  int64_t ld_k_out, hs_k_out;
+} fp8_qk_rope_t;
+
+/* Gradients of the same: in dq_out and dk_out, at q_out and k_out; out dq and dk (may be the incoming ones themselves with the
+ * same strides), dw_q and dw_k [head_dim] (overwritten, fp32; summed over all tokens and heads). A part with its
+ * incoming gradient NULL is left out. */
+typedef struct {
+  const void* dq_out;
+  int64_t ld_dq_out, hs_dq_out;
+  const void* dk_out;
+  int64_t ld_dk_out, hs_dk_out;
+  void* dq;
+  int64_t ld_dq, hs_dq;
+  void* dk;
+  int64_t ld_dk, hs_dk;
+  float* dw_q;
+  float* dw_k;
+} fp8_qk_rope_grad_t;
+
+/* q_out = turned(norm(q)), k_out likewise, arithmetic in fp32, rounded once. head_dim 1 .. 256, at most 32767 heads each. */
+fp8_status_t fp8_qk_rope_fwd(const fp8_qk_rope_t* f, void* stream);
+
+/* Backward from f's q and k as they were before the forward (read with a norm only). workspace: device, 16-byte aligned, at least
+ * fp8_qk_rope_bwd_workspace_bytes(f, b) bytes (0 without dw), contents irrelevant before and after; calls that may overlap need
+ * their own. Sums over the tokens are taken in a fixed order. */
+fp8_status_t fp8_qk_rope_bwd(const fp8_qk_rope_t* f, const fp8_qk_rope_grad_t* b, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+int64_t fp8_qk_rope_bwd_workspace_bytes(const fp8_qk_rope_t* f, const fp8_qk_rope_grad_t* b);
+
+/* A cache of keys and values in pages of page_size tokens: element d of token s of head h in page p at
+ * p * page_stride + h * head_stride + s * token_stride + d of k and of v (elements; the innermost of heads and tokens either way).
+ *   FP8_KV_BF16     bf16
+ *   FP8_KV_MX_E4M3  E4M3 codes with MX units along a head: per 32 elements one power of two 2^e, e the smallest integer with
+ *                   448 * 2^e >= the group's amax (0 for a zero amax, at least -127), in k_scale and v_scale as the byte e + 127,
+ *                   [pages, heads, page_size, head_dim / 32] contiguous. An infinity saturates (it counts as the
+ *                   largest finite bf16); a group that holds a NaN has the scale 0xFF and stands for NaNs.
+ * page_size: a power of two, 8 .. 4096. All buffers 16-byte aligned, strides of whole 16 bytes. */
+typedef enum { FP8_KV_BF16 = 0, FP8_KV_MX_E4M3 = 1 } fp8_kv_format_t;
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int32_t format;
+  int32_t pages, page_size, heads, head_dim;
+  int64_t page_stride, head_stride, token_stride;
+} fp8_kv_cache_t;
+
+/* A batch of sequences, their lengths on the device (so that a captured call serves other lengths): the new tokens of
+ * sequence s are rows q_start[s] .. q_start[s + 1] - 1 of the head tensors; its cache holds kv_len[s] tokens with the new ones,
+ * which come last: row i of them is at position kv_len[s] - (q_start[s + 1] - q_start[s]) + i. Position p lies in page
+ * page_table[s * ld_table + p / page_size]. Rows from q_start[seqs] on belong to nobody: they are neither read nor written.
+ * Values out of range stay harmless: q_start is taken within 0 .. tokens (and as no new tokens where it falls), a negative
+ * kv_len as 0; positions below 0 or from table_width * page_size on are neither stored nor seen; a page outside
+ * the cache holds zeros and takes nothing. */
+typedef struct {
+  int64_t tokens;            /* rows of the head tensors */
+  int32_t seqs;
+  int32_t table_width;       /* pages per sequence at most */
+  int64_t ld_table;
+  const int32_t* q_start;    /* [seqs + 1] */
+  const int32_t* kv_len;     /* [seqs] */
+  const int32_t* page_table; /* [seqs, table_width] */
+} fp8_kv_batch_t;
+
+/* q_out = turned(norm(q)); turned(norm(k)) and v into the cache at the new tokens' positions, from the fp32 values, rounded once. f: dt
+ * FP8_DT_BF16, k_heads and head_dim the cache's, k_out NULL, tokens the batch's. Tokens of two sequences that name the
+ * same page and place overwrite each other. */
+fp8_status_t fp8_kv_append(const fp8_qk_rope_t* f, const fp8_kv_cache_t* c, const fp8_kv_batch_t* b, void* stream);
+
+/* Attention of the new tokens over the cache (which holds them already): for row i of sequence s at position p, query head h and
+ * its cache head h / (q_heads / heads):
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q . k_j),   p - window < j <= p  (window 0: no lower end),  j < kv_len,
+ *   lse = log sum_j w_j (NULL: not written).
+ * A row that sees nothing, or only keys of weight 0, gets out = 0 and lse = -infinity. Keys and values in masked places do not
+ * touch a row, whatever they are. Products with fp32 accumulation, statistics in fp32; the weights are rounded to bf16 for the second
+ * product (their sum is not). q, out: bf16 head tensors [tokens, q_heads, head_dim], 16-byte aligned, strides multiples of 8;
+ * lse [tokens, q_heads] fp32. head_dim 64 or 128; q_heads a multiple of the cache's heads, at most 128 times as many. */
+typedef struct {
+  int32_t q_heads;
+  int32_t window;
+  float scale;
+  const void* q;
+  int64_t ld_q, hs_q;
+  void* out;
+  int64_t ld_out, hs_out;
+  float* lse;
+} fp8_paged_attention_t;
+
+/* workspace: device, 16-byte aligned, fp8_paged_attention_workspace_bytes(a, c, b) bytes (which does not depend on the lengths), zero-filled before
+ * its first use and left reusable by every successful call; calls that may overlap need their own. The result
+ * depends on nothing but the inputs. */
+fp8_status_t fp8_paged_attention(const fp8_paged_attention_t* a, const fp8_kv_cache_t* c, const fp8_kv_batch_t* b, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+int64_t fp8_paged_attention_workspace_bytes(const fp8_paged_attention_t* a, const fp8_kv_cache_t* c, const fp8_kv_batch_t* b);
+
 /* Push st->amax_cur into the history: amax_history[hist_count % hist_len] = amax_cur;
  * hist_count += 1; amax_cur = 0 (the next step's delayed casts start a new running maximum).
  * [GUARD] "Real products...": amax history tracking. */
