@@ -147,6 +147,7 @@ fp8_status_t check_attention(const fp8_paged_attention_t* a, const fp8_kv_cache_
   if (a->q_heads % c->heads != 0) return fail(FP8_ERR_INVALID_ARG, "%s: q_heads (%d) is no multiple of the cache's heads (%d)", who, (int)a->q_heads, (int)c->heads);
   if (c->head_dim != 64 && c->head_dim != 128) return fail(FP8_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", who);
   if (a->q_heads / c->heads > 128) return fail(FP8_ERR_UNSUPPORTED, "%s: more than 128 query heads for one of the cache's", who);
+  if (b->seqs > kAttendMaxSeqs) return fail(FP8_ERR_UNSUPPORTED, "%s: more than %d sequences", who, kAttendMaxSeqs);
   if (a->q_heads > kMaxHeads) return fail(FP8_ERR_UNSUPPORTED, "%s: 32768 heads or more", who);
   if (b->tokens > 0 && (a->q == nullptr || a->out == nullptr)) return fail(FP8_ERR_INVALID_ARG, "%s: null q or out", who);
   FP8GB_TRY(check_heads(a->q, a->ld_q, a->hs_q, b->tokens, a->q_heads, c->head_dim, 2, who, "q"));

@@ -1662,6 +1662,20 @@ bool encode_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, ui
          CUDA_SUCCESS;
 }
 
+bool encode_tmap_nd(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, int swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr || rank < 2 || rank > 4) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int64_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   const TileChoice c = choose_tile(M, N, K, num_sms(), pair_capacity(), 2);

@@ -55,6 +55,10 @@ bool encode_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, ui
 bool encode_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t d0, uint64_t d1, uint64_t d2,
                     uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2);
 
+// Tiled tensor map of `rank` (3 or 4) dimensions, element type dt, strides of dimensions 1 .. in bytes; swizzle 128 or 0.
+bool encode_tmap_nd(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, int swizzle);
+
 // Streaming multiprocessors of the current device (cached per device).
 int num_sms();
 
@@ -268,6 +272,7 @@ struct Attention {
   int64_t ld_q, hs_q, ld_out, hs_out;
   float* lse;
 };
+constexpr int kAttendMaxSeqs = 16384;  // sequences of one call (their costs are held in shared memory)
 // tokens, seqs > 0
 cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Batch& b, void* ws, cudaStream_t stream, const char** why);
 int64_t paged_attention_workspace_bytes(const Attention& a, const Cache& c, const Batch& b);

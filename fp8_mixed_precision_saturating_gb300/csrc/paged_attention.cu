@@ -1,92 +1,918 @@
-// paged_attention.cu -- attention of new tokens over a paged cache.
+// paged_attention.cu -- attention of new tokens over a paged cache on the tensor cores.
 //
-// The simplest form: a warp per token and query head, one key after the other.
+//   out_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale q_i . k_j - m_i)
+//
+// in one pass over the keys with a running reference m: per tile of 128 keys S = Q K^T (tcgen05, bf16, fp32 in tensor memory), the
+// weights in registers, P = bf16(weights) back to tensor memory over S, O += P V with P read from there. A CTA stays on its
+// SM and works through a run of tiles (attend_walk.cuh); its warps divide the work:
+//   0-3 (and 4-7)  weights, one thread per row: 128 rows of a tile each
+//   4-11 or 8-11   keys and values on their way: 8-bit codes into bf16 (exactly: a code times a power of two), and what must not be
+//                  multiplied by a weight of zero out of the last tiles (below)
+//   12, 13         copies (TMA, one box per page), tensor-core instructions
+// Two forms (NQ): 2 tiles of rows over the same keys, one's weights worked out while the other is on the tensor cores, where units
+// have more than 128 rows; 1 tile of rows with two S in turn where they have fewer (single tokens), twice the warps for the 8-bit conversion.
+//
+// The reference moves only where a row's maximum passes it by more than 8 (in log2 of the weights; below, exp cannot overflow
+// and fp32 sums lose nothing): then O in tensor memory and the sum are scaled, otherwise O is never touched.
+//
+// Masked places. Weights are set, not added to, so keys may be anything. A value that is not finite would make 0 * inf of a
+// weight of zero: in tiles with keys that some row does not see (the last ones, and the first ones of a window) values
+// behind the end become zero, and others that are not finite become zero as well and are added at the end to the rows that see them.
+//
+// A unit cut by the end of a CTA's run leaves sum, reference and O of each part in the workspace; the CTA that finds itself the last
+// of them (a counter) adds them up in the order of the parts, so the result does not depend on who that is.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "attend_walk.cuh"
 #include "heads.cuh"
+#include "kernels.h"
 
 namespace fp8gb {
 namespace {
 
-using namespace heads;
+using namespace attend;
+using heads::bf16;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512;
+constexpr int kPanel = 16384;        // 128 rows of 128 bytes
+constexpr int kCounterBytes = 4096;  // of the workspace: two counters per CTA
+constexpr int kMaxCtas = kCounterBytes / 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;
 
-struct Args {
+template <int D, bool MX, int NQ>
+struct Form {
+  static constexpr int PANELS = D / 64;
+  static constexpr int TILE = PANELS * kPanel;  // 128 rows of bf16
+  static constexpr int STAGES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  // tiles from one tile of values in a stage to the next one in it: with an odd number of stages keys come between
+  static constexpr int VALUES_EVERY = STAGES % 2 != 0 ? 2 * STAGES : STAGES;
+  static constexpr int RAW = 128 * D + 4 * D;   // 128 rows of codes and their units
+  static constexpr int RAWS = MX ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int PREP_WARP = MX && NQ == 1 ? 4 : 8;  // the first of them
+  static constexpr int PREP_WARPS = 12 - PREP_WARP;
+  static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
+  static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
+  static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
+  static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 6 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+  static constexpr int SMEM = OFF_MISC + 256 + 1024;
+  static_assert(RAW % 128 == 0 && OFF_RAW % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
+  static_assert(OFF_RAW >= 4 * kAttendMaxSeqs, "room for the sequences' costs");
+};
+
+struct Params {
   Attention a;
   Cache c;
   Batch b;
+  int group, tokens_per_tile, capacity;
+  float c2;   // |scale| log2 e
+  bool flip;  // scale < 0
+  char* parts;
+  unsigned* counters;
+  WaitCtl w;
 };
 
-template <int D, bool MX>
-__global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_constant__ Args g) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+// What is not in rings, at OFF_MISC.
+struct Misc {
+  Place start;
+  int64_t total;
+  int runs;
+  uint32_t tmem;
+  int last[2];
+  uint32_t bad[8];  // of each raw tile, the boxes whose page is outside the cache
+  int dirty[16];  // the last segment with tiles, of those with this number modulo 16, that holds values that are not finite in edge tiles
+};
+static_assert(sizeof(Misc) <= 256, "misc");
+
+struct Sequences {
+  const Batch& b;
+  int capacity, seqs;
+  __device__ __forceinline__ Seq seq(int s) const {
+    return seq_of(__ldg(b.q_start + s), __ldg(b.q_start + s + 1), __ldg(b.kv_len + s), static_cast<int>(b.tokens), capacity);
+  }
+};
+
+// ---- where this CTA's run begins -------------------------------------------------------------------------------------
+__device__ void find_start(const Params& p, const Sequences& src, int per, uint32_t* cost, Misc* misc, int64_t* share) {
+  constexpr uint32_t kLong = 0xFFFFFFFFu;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seqs = src.seqs;
+  bool some_long = false;
+  for (int s = tid; s < seqs; s += kThreads) {
+    const Seq q = src.seq(s);
+    uint32_t n = 0;
+    if (q.n > 4 * per) {
+      n = kLong;
+      some_long = true;
+    } else {
+      for (int b = 0; b * per < q.n; ++b) n += items_of(q, b, per, p.a.window);
+    }
+    cost[s] = n;
+  }
+  if (__syncthreads_or(some_long)) {
+    for (int s = warp; s < seqs; s += kThreads / 32) {
+      if (cost[s] != kLong) continue;
+      const Seq q = src.seq(s);
+      uint32_t n = 0;
+      for (int b = lane; static_cast<int64_t>(b) * per < q.n; b += 32) n += items_of(q, b, per, p.a.window);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+      __syncwarp();
+      if (lane == 0) cost[s] = n;
+    }
+    __syncthreads();
+  }
+  const int chunk = (seqs + kThreads - 1) / kThreads, s0 = min(tid * chunk, seqs), s1 = min(s0 + chunk, seqs);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += static_cast<int64_t>(cost[s]) * p.c.heads;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) share[warp] = upto;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += share[w];
+    total += share[w];
+  }
+  const int runs = static_cast<int>(min(total, static_cast<int64_t>(gridDim.x)));  // none of them empty
+  const bool works = static_cast<int>(blockIdx.x) < runs;
+  const int64_t begin = works ? begin_of(total, blockIdx.x, runs) : 0, end = works ? begin_of(total, blockIdx.x + 1, runs) : 0;
+  if (tid == 0) {
+    misc->total = total;
+    misc->runs = runs;
+    misc->start.item = begin;
+    misc->start.end = end;
+  }
+  int64_t at = before + upto - mine;
+  if (begin < end && at <= begin && begin < at + mine) {
+    int s = s0;
+    for (; s < s1 - 1 && at + static_cast<int64_t>(cost[s]) * p.c.heads <= begin; ++s) at += static_cast<int64_t>(cost[s]) * p.c.heads;
+    misc->start.seq = s;
+    misc->start.head = static_cast<int>((begin - at) / cost[s]);
+    misc->start.off = static_cast<int>((begin - at) % cost[s]);
+  }
+  __syncthreads();
+  if (warp == 0 && begin < end) {
+    const Seq q = src.seq(misc->start.seq);
+    uint32_t rest = static_cast<uint32_t>(misc->start.off);
+    int block = 0;
+    for (int b0 = 0; static_cast<int64_t>(b0) * per < q.n; b0 += 32) {
+      const int64_t b = b0 + lane;
+      const uint32_t n = b * per < q.n ? items_of(q, static_cast<int>(b), per, p.a.window) : 0u;
+      uint32_t upto_b = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto_b, o);
+        if (lane >= o) upto_b += x;
+      }
+      const uint32_t all = __shfl_sync(0xFFFFFFFFu, upto_b, 31);
+      if (rest < all) {
+        const int l = __ffs(__ballot_sync(0xFFFFFFFFu, upto_b > rest)) - 1;
+        rest -= __shfl_sync(0xFFFFFFFFu, upto_b - n, l);
+        block = b0 + l;
+        break;
+      }
+      rest -= all;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      misc->start.block = block;
+      misc->start.off = static_cast<int>(rest);
+    }
+  }
+}
+
+// ---- small pieces ----------------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t both(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float exp2_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// Whether either half of a word is a bf16 that is not finite.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  const uint32_t bad = not_finite(w);
+  return w & ~((bad & 0x8000u ? 0xFFFFu : 0u) | (bad & 0x80000000u ? 0xFFFF0000u : 0u));
+}
+
+// Two E4M3 codes (bytes 0 and 1, or 2 and 3, of w) as two bf16, times f. A code's exponent and mantissa in bf16's places are the value
+// times 2^-120 (subnormals included), exactly.
+__device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t which, __nv_bfloat162 f) {
+  const uint32_t x = __byte_perm(w, 0u, which);  // the codes in the high bytes of the halves
+  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+  __nv_bfloat162 v;
+  memcpy(&v, &y, 4);
+  v = __hmul2(v, f);
+  uint32_t r;
+  memcpy(&r, &v, 4);
+  return r;
+}
+__device__ __forceinline__ __nv_bfloat162 bf16_pair(uint32_t bits) {
+  const uint32_t w = bits | (bits << 16);
+  __nv_bfloat162 v;
+  memcpy(&v, &w, 4);
+  return v;
+}
+
+// A value of the cache that is not finite, or 0.
+template <bool MX, int D>
+__device__ float unusual(const Params& p, int64_t row, int64_t unit, int d) {
+  float v;
+  if constexpr (MX) {
+    const uint32_t u = p.c.v_scale[unit + d / 32], b = static_cast<const uint8_t*>(p.c.v)[row + d];
+    if (u == 0xFFu) return __int_as_float(0x7FFFFFFF);
+    v = __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7Fu) << 20)) * 0x1p120f * (u == 0u ? 0x1p-127f : __uint_as_float(u << 23));
+  } else {
+    v = __bfloat162float(static_cast<const bf16*>(p.c.v)[row + d]);
+  }
+  return isfinite(v) ? 0.0f : v;
+}
+
+template <int D, bool MX, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ Params p) {
+  using F = Form<D, MX, NQ>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Misc* misc = reinterpret_cast<Misc*>(smem + F::OFF_MISC);
+  const uint32_t q_full = base + F::OFF_BAR, q_empty = q_full + 16, kv_full = q_empty + 16, kv_empty = kv_full + 8 * F::STAGES;
+  const uint32_t raw_full = kv_empty + 8 * F::STAGES, raw_empty = raw_full + 8 * F::RAWS, s_full = raw_empty + 8 * F::RAWS;
+  const uint32_t p_ready = s_full + 16, o_done = p_ready + 16, v_fixed = o_done + 16, bar_final = v_fixed + 8 * F::STAGES;
+  const int per = NQ * p.tokens_per_tile;
+  const Sequences src{p.b, p.capacity, p.b.seqs};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_ready + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    for (int i = 0; i < F::STAGES; ++i) {
+      mbar_init(kv_full + 8 * i, MX ? F::PREP_WARPS : 1);
+      mbar_init(kv_empty + 8 * i, 1);
+      mbar_init(v_fixed + 8 * i, 4);
+    }
+    for (int i = 0; i < F::RAWS; ++i) {
+      mbar_init(raw_full + 8 * i, 1);
+      mbar_init(raw_empty + 8 * i, F::PREP_WARPS);
+    }
+    mbar_init(bar_final, 1);
+    fence_mbar_init();
+    for (int i = 0; i < 16; ++i) misc->dirty[i] = -1;
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_u32(&misc->tmem), 512);
+    tmem_relinquish();
+  }
   pdl_wait();
   pdl_trigger();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t t = i / g.a.q_heads;
-  const int h = static_cast<int>(i - t * g.a.q_heads), hk = h / (g.a.q_heads / g.c.heads);
-  if (t >= g.b.tokens) return;
-  const Place at = place_of(t, g.b, lane);
-  if (at.seq < 0) return;
-  const bf16* q = static_cast<const bf16*>(g.a.q) + t * g.a.ld_q + h * g.a.hs_q;
-  float x[E], o[E] = {}, m = -INFINITY, l = 0.0f;
+  // (the costs lie where the tiles will: written before the barrier, fenced against the copies)
+  find_start(p, src, per, reinterpret_cast<uint32_t*>(smem), misc, reinterpret_cast<int64_t*>(smem + F::OFF_MISC - 8 * F::NBAR - 8 * (kThreads / 32)));
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  const int64_t total = misc->total;
+  const int runs = misc->runs;
+  Walk<Sequences> k(src, misc->start, p.c.heads, per, p.a.window);
+
+  if (warp == 12) {
+    // ---- copies ------------------------------------------------------------------------------------------------------
+    const int rows = min(p.c.page_size, kTile);  // of a box
+    bool ok = true;
+    int n = 0;  // items so far
+    for (; ok && k.live(); k.next()) {
+      if (k.a >= k.b) continue;
+      const int buf = NQ == 1 ? k.filled & 1 : 0, use = NQ == 1 ? k.filled >> 1 : k.filled;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty + 8 * buf, (use & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
+      if (!ok) break;
+      const int t0 = k.at.block * per, tiles = NQ == 2 && t0 + p.tokens_per_tile < k.s.n ? 2 : 1;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(q_full + 8 * buf, static_cast<uint32_t>(tiles * p.tokens_per_tile * p.group * D * 2));
+        for (int i = 0; i < tiles; ++i)
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = element(q + lane * E + e);
-  const int64_t capacity = static_cast<int64_t>(g.b.table_width) << g.c.page_bits;
-  const int64_t end = min(min(at.pos + 1, capacity), static_cast<int64_t>(max(0, __ldg(g.b.kv_len + at.seq))));
-  int64_t j = g.a.window > 0 ? max(int64_t{0}, at.pos + 1 - g.a.window) : 0;
-  for (; j < end; ++j) {
-    const int page = __ldg(g.b.page_table + at.seq * g.b.ld_table + (j >> g.c.page_bits));
-    float k[E] = {}, v[E] = {};
-    if (page >= 0 && page < g.c.pages) {
-      const int slot = static_cast<int>(j & (g.c.page_size - 1));
-      const int64_t row = page * g.c.page_stride + hk * g.c.head_stride + slot * g.c.token_stride + lane * E;
-      if constexpr (MX) {
-        const int64_t unit = ((static_cast<int64_t>(page) * g.c.heads + hk) * g.c.page_size + slot) * (D / 32) + lane * E / 32;
-        auto get = [&](const void* codes, const uint8_t* units, float (&y)[E]) {
-          const uint32_t u = units[unit];
-          const float f = u == 0xFFu ? __int_as_float(0x7FFFFFFF) : exp2f(static_cast<float>(static_cast<int>(u) - 127));
+          for (int j = 0; j < F::PANELS; ++j)
+            tma_load_3d(base + (NQ == 1 ? buf : i) * F::TILE + j * kPanel, &tm_q, q_full + 8 * buf, 64 * j, k.at.head * p.group, k.s.first + t0 + i * p.tokens_per_tile);
+      }
+      __syncwarp();
+      const int32_t* table = p.b.page_table + k.at.seq * p.b.ld_table;
+      auto page_of = [&](int t) {  // lane l: the tile's page l, -1 outside the cache or past the end
+        const int key = t * kTile + lane * rows;
+        int page = -1;
+        if (t < k.b && lane * rows < kTile && key < k.s.seen) page = __ldg(table + (key >> p.c.page_bits));
+        return page;
+      };
+      int next = page_of(k.a);
+      for (int t = k.a; t < k.b; ++t, ++n) {
+        const int page = next, boxes = min(kTile / rows, (min(k.s.seen - t * kTile, kTile) + rows - 1) / rows);
+        next = page_of(t + 1);
+        const int within = (t * kTile) & (p.c.page_size - 1);
+        const bool good = page >= 0 && page < p.c.pages;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const uint32_t b = static_cast<const uint8_t*>(codes)[row + e];
-            const float w = __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7Fu) << 20)) * 0x1p120f;
-            y[e] = w * f;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int u = 2 * n + kv;
+          const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
+          if constexpr (!MX) {
+            const int slot = u % F::STAGES;
+            const uint32_t bar = kv_full + 8 * slot, dst = base + F::OFF_KV + slot * F::TILE;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
+            if (!ok) break;
+            if (elect_one()) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * D * 2));
+            __syncwarp();
+            if (lane < boxes)
+#pragma unroll
+              for (int j = 0; j < F::PANELS; ++j) tma_load_4d(dst + j * kPanel + lane * rows * 128, map, bar, 64 * j, within, k.at.head, good ? page : -1);
+          } else {
+            const int slot = u % F::RAWS;
+            const uint32_t bar = raw_full + 8 * slot, dst = base + F::OFF_RAW + slot * F::RAW;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_empty + 8 * slot, ((u / F::RAWS) & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
+            if (!ok) break;
+            // the codes of a page outside the cache are zeros (the copy's fill); its units are not copied
+            const uint32_t found = __ballot_sync(0xFFFFFFFFu, lane < boxes && good);
+            if (elect_one()) {
+              misc->bad[slot] = ~found & ((1u << boxes) - 1u);
+              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * D + __popc(found) * rows * (D / 32)));
+            }
+            __syncwarp();
+            if (lane < boxes) {
+              tma_load_4d(dst + lane * rows * D, map, bar, 0, within, k.at.head, good ? page : -1);
+              if (good) {
+                const uint8_t* units = (kv == 0 ? p.c.k_scale : p.c.v_scale) + ((static_cast<int64_t>(page) * p.c.heads + k.at.head) * p.c.page_size + within) * (D / 32);
+                bulk_load(dst + 128 * D + lane * rows * (D / 32), units, rows * (D / 32), bar);
+              }
+            }
           }
-        };
-        get(g.c.k, g.c.k_scale, k);
-        get(g.c.v, g.c.v_scale, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) k[e] = element(static_cast<const bf16*>(g.c.k) + row + e), v[e] = element(static_cast<const bf16*>(g.c.v) + row + e);
+          __syncwarp();
+        }
+        if (!ok) break;
       }
     }
-    float d = 0.0f;
+    if (!ok) {  // let the copies in flight land (microseconds) before the CTA can exit
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {
+      }
+    }
+  } else if (warp == 13) {
+    // ---- tensor-core instructions --------------------------------------------------------------------------------------
+    constexpr uint32_t kScores = idesc_bf16(128, 128, false), kValues = idesc_bf16(128, D, true);
+    Walk<Sequences> ahead = k;  // the scores' place: one item before the values'
+    bool ok = true, more;
+    int n_s = 0, n_v = 0, t_s = 0, seen_p[2] = {0, 0};
+    auto settle = [&](Walk<Sequences>& w) {
+      while (w.live() && w.a >= w.b) w.next();
+      return w.live();
+    };
+    auto part = [&](const Walk<Sequences>& w, int q) { return w.part_of(q * p.tokens_per_tile, p.tokens_per_tile); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, p.w, DEV_ERR_WAIT_MMA)); };
+    more = settle(ahead);
+    t_s = ahead.a;
+    auto await_keys = [&]() {
+      const int u = 2 * n_s;
+      if (t_s == ahead.a) wait(q_full + 8 * (NQ == 1 ? ahead.filled & 1 : 0), (NQ == 1 ? ahead.filled >> 1 : ahead.filled) & 1);
+      wait(kv_full + 8 * (u % F::STAGES), (u / F::STAGES) & 1);
+      tc_fence_after();
+    };
+    auto scores = [&](int q) {  // S = Q K^T
+      if (ok && elect_one()) {
+        const int slot = NQ == 2 ? q : n_s & 1;
+        const uint32_t qa = base + (NQ == 2 ? q : ahead.filled & 1) * F::TILE, ka = base + F::OFF_KV + ((2 * n_s) % F::STAGES) * F::TILE;
 #pragma unroll
-    for (int e = 0; e < E; ++e) d = fmaf(x[e], k[e], d);
-    d = row_sum<32>(d) * g.a.scale;
-    const float n = fmaxf(m, d), base = n == -INFINITY ? 0.0f : n;
-    const float old = __expf(m - base), w = __expf(d - base);
-    l = l * old + w;
-    m = n;
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t o = (i >> 2) * kPanel + (i & 3) * 32;
+          mma_bf16(tmem + 128 * slot, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), kScores, i > 0);
+        }
+        mma_commit(s_full + 8 * slot);
+      }
+      __syncwarp();
+    };
+    auto scores_done = [&]() {
+      if (ok && elect_one()) {
+        mma_commit(kv_empty + 8 * ((2 * n_s) % F::STAGES));
+        if (t_s + 1 == ahead.b) mma_commit(q_empty + 8 * (NQ == 1 ? ahead.filled & 1 : 0));
+      }
+      __syncwarp();
+      ++n_s;
+      if (++t_s == ahead.b) {
+        ahead.next();
+        more = settle(ahead);
+        t_s = ahead.a;
+      }
+    };
+    auto values = [&](int q, bool first) {  // O += P V
+      if (ok && elect_one()) {
+        const int slot = NQ == 2 ? q : n_v & 1;
+        const uint32_t va = base + F::OFF_KV + ((2 * n_v + 1) % F::STAGES) * F::TILE, o = tmem + 256 + 128 * q;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e] * old);
+        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, tmem + 128 * slot + 64 + 8 * i, smem_desc_sw128_mn(va + i * 2048), kValues, !first || i > 0);
+        mma_commit(o_done + 8 * q);
+      }
+      __syncwarp();
+    };
+    auto await_values = [&]() {
+      const int u = 2 * n_v + 1;
+      if (!MX) wait(v_fixed + 8 * (u % F::STAGES), (u / F::VALUES_EVERY) & 1);
+      wait(kv_full + 8 * (u % F::STAGES), (u / F::STAGES) & 1);
+      tc_fence_after();
+    };
+    if (more) {
+      await_keys();
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const Keys t = part(ahead, q);
+        if (t.lo <= t_s && t_s < t.hi) scores(q);
+      }
+      scores_done();
+    }
+    for (; ok && settle(k); k.next()) {
+      Keys mine[NQ];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) mine[q] = part(k, q);
+      for (int t = k.a; ok && t < k.b; ++t) {
+        bool have_values = false, have_keys = false;
+        const bool next = more;
+        if constexpr (NQ == 1) {
+          if (next) {
+            await_keys();
+            scores(0);
+            scores_done();
+          }
+          wait(p_ready + 8 * (n_v & 1), (n_v >> 1) & 1);
+          await_values();
+          values(0, t == mine[0].lo);
+        } else {
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (mine[q].lo <= t && t < mine[q].hi) {
+              wait(p_ready + 8 * q, seen_p[q]++ & 1);
+              if (!have_values) {
+                await_values();
+                have_values = true;
+              } else {
+                tc_fence_after();
+              }
+              values(q, t == mine[q].lo);
+            }
+            if (next) {
+              const Keys s = part(ahead, q);
+              if (s.lo <= t_s && t_s < s.hi) {
+                if (!have_keys) {
+                  await_keys();
+                  have_keys = true;
+                }
+                scores(q);
+              }
+            }
+          }
+        }
+        if (NQ == 2 && !have_values) await_values();
+        if (ok && elect_one()) mma_commit(kv_empty + 8 * ((2 * n_v + 1) % F::STAGES));
+        __syncwarp();
+        if (NQ == 2 && next) {
+          if (!have_keys) await_keys();
+          scores_done();
+        }
+        ++n_v;
+      }
+    }
+    if (elect_one()) mma_commit(bar_final);
+    __syncwarp();
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar_final, 0))
+      if (globaltimer_ns() - t0 > 1000000000ull) {
+        atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
+        break;
+      }
+  } else if (warp >= F::PREP_WARP && warp < 12) {
+    // ---- keys and values on their way ----------------------------------------------------------------------------------
+    const int tid = threadIdx.x - 32 * F::PREP_WARP, rows = min(p.c.page_size, kTile);
+    bool ok = true;
+    int n = 0;
+    for (; ok && k.live(); k.next()) {
+      for (int t = k.a; ok && t < k.b; ++t, ++n) {
+        const bool edge = k.edge(t);
+        const int live = k.s.seen - t * kTile;  // rows that hold keys
+        if constexpr (!MX) {
+          const int u = 2 * n + 1;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(kv_full + 8 * (u % F::STAGES), (u / F::STAGES) & 1, p.w, DEV_ERR_WAIT_EPILOGUE));
+          if (!ok) break;
+          uint8_t* v = smem + F::OFF_KV + (u % F::STAGES) * F::TILE;
+          bool bad = false;
+#pragma unroll 4
+          for (int i = tid; edge && i < F::PANELS * 1024; i += 128) {
+            uint4* at = reinterpret_cast<uint4*>(v) + i;
+            const uint4 x = *at;
+            if (((i & 1023) >> 3) >= live) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else if ((not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) != 0u) {
+              *at = make_uint4(finite_part(x.x), finite_part(x.y), finite_part(x.z), finite_part(x.w));
+              bad = true;
+            }
+          }
+          if (bad) misc->dirty[k.filled & 15] = k.filled;
+          if (edge) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_fixed + 8 * (u % F::STAGES));
+        } else {
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const int u = 2 * n + kv, raw = u % F::RAWS, slot = u % F::STAGES;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_full + 8 * raw, (u / F::RAWS) & 1, p.w, DEV_ERR_WAIT_EPILOGUE) &&
+                                             mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
+            if (!ok) break;
+            const uint8_t* codes = smem + F::OFF_RAW + raw * F::RAW;
+            const uint8_t* units = codes + 128 * D;
+            uint8_t* out = smem + F::OFF_KV + slot * F::TILE;
+            const uint32_t lost = misc->bad[raw];
+            bool bad = false;
+#pragma unroll 2
+            for (int i = tid; i < 8 * D; i += 32 * F::PREP_WARPS) {  // 16 codes each
+              const int row = i / (D / 16), c = i % (D / 16);
+              const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * i);
+              const uint32_t unit = units[row * (D / 32) + c / 2];
+              // 2^(unit - 127) 2^120 in one factor where that is a bf16, otherwise in two
+              const bool large = unit >= 135u;
+              const __nv_bfloat162 f = bf16_pair(large ? 0x7B80u : (unit + 120u) << 7);
+              uint32_t y[8];
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[2 * e] = decode2(w[e], 0x1404u, f);
+                y[2 * e + 1] = decode2(w[e], 0x3424u, f);
+              }
+              if (large) {
+                const __nv_bfloat162 g = bf16_pair(unit == 255u ? 0x7FC0u : unit << 7);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  __nv_bfloat162 z;
+                  memcpy(&z, &y[e], 4);
+                  z = __hmul2(z, g);
+                  memcpy(&y[e], &z, 4);
+                }
+              }
+              if (lost != 0u && (lost >> (row / rows) & 1u)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = 0u;
+              }
+              if (kv == 1 && edge) {
+                if (row >= live) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] = 0u;
+                } else {
+                  uint32_t any = 0u;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) any |= not_finite(y[e]);
+                  if (any != 0u) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = finite_part(y[e]);
+                    bad = true;
+                  }
+                }
+              }
+              uint8_t* panel = out + (c >> 2) * kPanel + row * 128;
+              const int c0 = 2 * (c & 3), flip = (c >> 2) & 1;  // (the panels' lanes take their two stores in opposite order: other banks)
+              const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+              *reinterpret_cast<uint4*>(panel + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
+              *reinterpret_cast<uint4*>(panel + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
+            }
+            if (bad) misc->dirty[k.filled & 15] = k.filled;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(kv_full + 8 * slot);
+              mbar_arrive(raw_empty + 8 * raw);
+            }
+          }
+        }
+      }
+    }
+  } else if (warp < 4 * NQ) {
+    // ---- weights: a thread per row -------------------------------------------------------------------------------------
+    const int q = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t o_at = tmem + lanes + 256 + 128 * q;
+    const int token = row / p.group, head = row - token * p.group;
+    const float c2 = p.c2, slack = fminf(kSlack / c2, 3.0e38f);
+    bool ok = true;
+    int n = 0;  // tiles of this warpgroup so far
+    for (; k.live(); k.next()) {
+      const int i0 = k.at.block * per + q * p.tokens_per_tile, i = i0 + token;
+      if (i0 >= k.s.n) continue;
+      const bool valid = token < p.tokens_per_tile && i < k.s.n;
+      Keys mine{0, 0};
+      if (valid) mine = keys_of(k.s, i, p.a.window);
+      const Keys part = k.part_of(q * p.tokens_per_tile, p.tokens_per_tile);
+      const bool any = __any_sync(0xFFFFFFFFu, valid);
+      float m = -INFINITY, limit = -INFINITY, l = 0.0f;
+      for (int t = part.lo; t < part.hi; ++t, ++n) {
+        const int slot = NQ == 2 ? q : n & 1;
+        const uint32_t s_at = tmem + lanes + 128 * slot;
+        ok = ok && mbar_wait(s_full + 8 * slot, (NQ == 2 ? n : n >> 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
+        __syncwarp();
+        tc_fence_after();
+        if (any) {
+          const int c_lo = mine.lo - t * kTile, c_hi = mine.hi - t * kTile;
+          const bool whole = __all_sync(0xFFFFFFFFu, !valid || (c_lo <= 0 && c_hi >= kTile));
+          uint32_t r[64];
+          auto load = [&](int half) {
+            tmem_ld64(s_at + 64 * half, r);
+            tmem_ld_wait();
+            reg_fence(r);
+            if (p.flip)
+#pragma unroll
+              for (int e = 0; e < 64; ++e) r[e] ^= 0x80000000u;
+            if (!whole) {
+              const int lo = c_lo - 64 * half;
+              const uint32_t width = static_cast<uint32_t>(most(c_hi - c_lo, 0));
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (static_cast<uint32_t>(e - lo) >= width) r[e] = 0xFF800000u;
+            }
+          };
+          auto highest = [&](float x) {
+            float y = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              x = fmaxf(x, __uint_as_float(r[e]));
+              y = fmaxf(y, __uint_as_float(r[e + 1]));
+            }
+            return fmaxf(x, y);
+          };
+          load(0);
+          float top = highest(-INFINITY);
+          load(1);
+          top = highest(top);
+          const bool move = valid && top > limit;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            const float to = move ? top : m;
+            if (t > part.lo) {
+              const float f = move ? exp2_of((m - to) * c2) : 1.0f;
+              l *= f;
+              ok = ok && mbar_wait(o_done + 8 * q, (n - 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                uint32_t x[32];
+                tmem_ld32(o_at + d, x);
+                tmem_ld_wait();
+                reg_fence(x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tmem_st32(o_at + d, x);
+              }
+            }
+            m = to;
+            if (move) limit = top + slack;
+          }
+          const uint64_t c = both(c2), shift = both(m == -INFINITY ? 0.0f : -(m * c2));
+          uint64_t sum0 = 0, sum1 = 0;
+          auto weigh = [&](int half) {
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 x = split(fma2(pair(r[2 * e], r[2 * e + 1]), c, shift));
+              const float a = exp2_of(x.x), b = exp2_of(x.y);
+              const uint64_t ab = pair(__float_as_uint(a), __float_as_uint(b));
+              if (e & 1)
+                sum1 = add2(sum1, ab);
+              else
+                sum0 = add2(sum0, ab);
+              w[e] = heads::pack(a, b);
+            }
+            tmem_st32(s_at + 64 + 32 * half, w);
+          };
+          weigh(1);  // (both halves' weights lie over the second half's scores, which are in registers)
+          load(0);
+          weigh(0);
+          const float2 s = split(add2(sum0, sum1));
+          l += s.x + s.y;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + 8 * slot);
+      }
+      // ---- the unit's end, or this CTA's part's ------------------------------------------------------------------------
+      const bool some = part.lo < part.hi, alone = k.first() && k.last();
+      const int64_t out_row = (static_cast<int64_t>(k.s.first) + i) * p.a.ld_out + (static_cast<int64_t>(k.at.head) * p.group + head) * p.a.hs_out;
+      const int64_t lse_row = (static_cast<int64_t>(k.s.first) + i) * p.a.q_heads + k.at.head * p.group + head;
+      const int64_t unit0 = k.at.item - k.at.off;
+      const int c0 = alone ? 0 : cta_of(total, unit0, runs), c1 = alone ? 0 : cta_of(total, unit0 + k.items - 1, runs);
+      constexpr int64_t kPart = 128 * (D + 2) * 4;  // bytes of one tile's part: (reference, sum) of each row, then O
+      auto part_at = [&](int cta) { return p.parts + (static_cast<int64_t>(2 * cta + (cta == c0 ? 1 : 0)) * NQ + q) * kPart; };
+      if (any) {
+        if (some) {
+          ok = ok && mbar_wait(o_done + 8 * q, (n - 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
+          __syncwarp();
+          tc_fence_after();
+        }
+        const bool dirty = some && *reinterpret_cast<volatile int*>(&misc->dirty[k.filled & 15]) == k.filled;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        char* to = alone ? nullptr : part_at(blockIdx.x);
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t x[32];
+          if (some) {
+            tmem_ld32(o_at + d, x);
+            tmem_ld_wait();
+            reg_fence(x);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = 0u;
+          }
+          if (dirty && valid) {
+            for (int t = part.lo; t < part.hi; ++t) {
+              if (!k.edge(t)) continue;
+              for (int j = most(mine.lo, t * kTile); j < least(mine.hi, t * kTile + kTile); ++j) {
+                const int page = __ldg(p.b.page_table + k.at.seq * p.b.ld_table + (j >> p.c.page_bits));
+                if (page < 0 || page >= p.c.pages) continue;
+                const int at = j & (p.c.page_size - 1);
+                const int64_t v_row = page * p.c.page_stride + k.at.head * p.c.head_stride + at * p.c.token_stride;
+                const int64_t unit = ((static_cast<int64_t>(page) * p.c.heads + k.at.head) * p.c.page_size + at) * (D / 32);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + unusual<MX, D>(p, v_row, unit, d + e));
+              }
+            }
+          }
+          if (!valid) continue;
+          if (alone) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<bf16*>(p.a.out) + out_row + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float a = __uint_as_float(x[8 * e + 2 * j]), b = __uint_as_float(x[8 * e + 2 * j + 1]);
+                w[j] = l == 0.0f ? 0u : heads::pack(a * inv, b * inv);
+              }
+              out[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4* o = reinterpret_cast<float4*>(to + 1024 + (static_cast<int64_t>(row) * D + d) * 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg(o + e, make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+          }
+        }
+        if (valid && alone && p.a.lse != nullptr) p.a.lse[lse_row] = l == 0.0f ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+        if (valid && !alone) __stcg(reinterpret_cast<float2*>(to) + row, make_float2(m * c2, l));
+      }
+      tc_fence_before();
+      if (!alone) {
+        __threadfence();
+        bar_sync(1 + q, 128);
+        if (row == 0) {
+          const unsigned before = atomicAdd(p.counters + 2 * c0 + q, 1u);
+          misc->last[q] = before == static_cast<unsigned>(c1 - c0);
+          if (misc->last[q]) p.counters[2 * c0 + q] = 0u;
+        }
+        bar_sync(1 + q, 128);
+        if (misc->last[q]) {
+          __threadfence();
+          const int rows = least(k.s.n - i0, p.tokens_per_tile) * p.group;
+          for (int x = row; x < rows * (D / 4); x += 128) {
+            const int r = x / (D / 4), d = 4 * (x - r * (D / 4));
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(part_at(c)) + r).x);
+            if (top == -INFINITY) top = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const char* at = part_at(c);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(at) + r);
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(at + 1024 + (static_cast<int64_t>(r) * D + d) * 4));
+              const float w = exp2_of(ml.x - top);
+              if (ml.y != 0.0f) {  // (a part that saw nothing)
+                sum = fmaf(w, ml.y, sum);
+                o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
+              }
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int tk = r / p.group, hd = r - tk * p.group;
+            const int64_t tok = static_cast<int64_t>(k.s.first) + i0 + tk;
+            bf16* out = static_cast<bf16*>(p.a.out) + tok * p.a.ld_out + (static_cast<int64_t>(k.at.head) * p.group + hd) * p.a.hs_out + d;
+            *reinterpret_cast<uint2*>(out) = sum == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
+            if (d == 0 && p.a.lse != nullptr) p.a.lse[tok * p.a.q_heads + k.at.head * p.group + hd] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+          }
+        }
+      }
+    }
   }
-  bf16* out = static_cast<bf16*>(g.a.out) + t * g.a.ld_out + h * g.a.hs_out;
-#pragma unroll
-  for (int e = 0; e < E; ++e) set_element(out + lane * E + e, l == 0.0f ? 0.0f : o[e] / l);
-  if (g.a.lse != nullptr && lane == 0) g.a.lse[t * g.a.q_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int ctas() { return min(num_sms(), kMaxCtas); }
+
+// Two tiles of rows where units have more than one tile's on average.
+bool two_tiles(const Attention& a, const Cache& c, const Batch& b) { return b.tokens * (a.q_heads / c.heads) > static_cast<int64_t>(b.seqs) * kTile; }
+
+template <int D, bool MX, int NQ>
+cudaError_t launch_form(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Params& p, cudaStream_t stream) {
+  using F = Form<D, MX, NQ>;
+  auto* kernel = paged_attention_kernel<D, MX, NQ>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(ctas()), dim3(kThreads), F::SMEM, stream, q, k, v, p);
 }
 
 }  // namespace
 
-int64_t paged_attention_workspace_bytes(const Attention&, const Cache&, const Batch&) { return 0; }
+int64_t paged_attention_workspace_bytes(const Attention& a, const Cache& c, const Batch& b) {
+  return kCounterBytes + static_cast<int64_t>(ctas()) * 2 * (two_tiles(a, c, b) ? 2 : 1) * 128 * (c.head_dim + 2) * 4;
+}
 
-cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Batch& b, void*, cudaStream_t stream, const char**) {
-  const Args g{a, c, b};
-  const dim3 grid(static_cast<unsigned>((b.tokens * a.q_heads + kWarps - 1) / kWarps));
-  if (c.head_dim == 64)
-    return c.mx ? launch_pdl(paged_attention_kernel<64, true>, grid, dim3(kThreads), 0, stream, g) : launch_pdl(paged_attention_kernel<64, false>, grid, dim3(kThreads), 0, stream, g);
-  return c.mx ? launch_pdl(paged_attention_kernel<128, true>, grid, dim3(kThreads), 0, stream, g) : launch_pdl(paged_attention_kernel<128, false>, grid, dim3(kThreads), 0, stream, g);
+cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Batch& b, void* ws, cudaStream_t stream, const char** why) {
+  Params p{};
+  p.a = a;
+  p.c = c;
+  p.b = b;
+  p.group = a.q_heads / c.heads;
+  p.tokens_per_tile = kTile / p.group;
+  // (a cache without pages holds nothing, and the tensor maps need an address)
+  const int64_t reach = c.pages > 0 ? static_cast<int64_t>(b.table_width) << c.page_bits : 0;
+  p.capacity = static_cast<int>(min(reach, int64_t{0x7FFFFF00}));
+  // scale 0: every weight is 1, and -infinity times it stays -infinity
+  p.c2 = max(std::fabs(a.scale) * kLog2e, 1.0e-44f);
+  p.flip = a.scale < 0.0f;
+  p.counters = static_cast<unsigned*>(ws);
+  p.parts = static_cast<char*>(ws) + kCounterBytes;
+  p.w = wait_ctl();
+  if (p.w.err == nullptr) {
+    *why = "device error word unavailable";
+    return cudaErrorInvalidDevice;
+  }
+  const uint64_t D = static_cast<uint64_t>(c.head_dim), row = 2 * D;
+  CUtensorMap mq, mk, mv;
+  auto or_row = [](int64_t n, int64_t stride_bytes, uint64_t otherwise) { return n > 1 ? static_cast<uint64_t>(stride_bytes) : otherwise; };
+  const uint64_t q_dims[3] = {D, static_cast<uint64_t>(a.q_heads), static_cast<uint64_t>(b.tokens)};
+  const uint64_t q_strides[2] = {or_row(a.q_heads, 2 * a.hs_q, row), or_row(b.tokens, 2 * a.ld_q, row)};
+  const uint32_t q_box[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(p.tokens_per_tile)};
+  const int64_t size = c.mx ? 1 : 2;
+  const uint64_t one = size * D, pages = static_cast<uint64_t>(max(c.pages, 1));
+  const uint64_t kv_dims[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads), pages};
+  const uint64_t kv_strides[3] = {static_cast<uint64_t>(size * c.token_stride), or_row(c.heads, size * c.head_stride, one), or_row(c.pages, size * c.page_stride, one)};
+  const uint32_t kv_box[4] = {c.mx ? static_cast<uint32_t>(D) : 64u, static_cast<uint32_t>(min(c.page_size, kTile)), 1, 1};
+  const CUtensorMapDataType dt = c.mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const void* k = c.pages > 0 ? c.k : a.q;
+  const void* v = c.pages > 0 ? c.v : a.q;
+  if (!encode_tmap_nd(&mq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_dims, q_strides, q_box, 128) || !encode_tmap_nd(&mk, k, dt, 4, kv_dims, kv_strides, kv_box, c.mx ? 0 : 128) ||
+      !encode_tmap_nd(&mv, v, dt, 4, kv_dims, kv_strides, kv_box, c.mx ? 0 : 128)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  const bool two = two_tiles(a, c, b);
+#define FP8GB_FORM(D, MX) (two ? launch_form<D, MX, 2>(mq, mk, mv, p, stream) : launch_form<D, MX, 1>(mq, mk, mv, p, stream))
+  if (c.head_dim == 64) return c.mx ? FP8GB_FORM(64, true) : FP8GB_FORM(64, false);
+  return c.mx ? FP8GB_FORM(128, true) : FP8GB_FORM(128, false);
+#undef FP8GB_FORM
 }
 
 }  // namespace fp8gb

@@ -691,7 +691,8 @@ fp8_status_t fp8_kv_append(const fp8_qk_rope_t* f, const fp8_kv_cache_t* c, cons
  * A row that sees nothing, or only keys of weight 0, gets out = 0 and lse = -infinity. Keys and values in masked places do not
  * touch a row, whatever they are. Products with fp32 accumulation, statistics in fp32; the weights are rounded to bf16 for the second
  * product (their sum is not). q, out: bf16 head tensors [tokens, q_heads, head_dim], 16-byte aligned, strides multiples of 8;
- * lse [tokens, q_heads] fp32. head_dim 64 or 128; q_heads a multiple of the cache's heads, at most 128 times as many. */
+ * lse [tokens, q_heads] fp32. head_dim 64 or 128; q_heads a multiple of the cache's heads, at most 128 times as many; at most 16384
+ * sequences. */
 typedef struct {
   int32_t q_heads;
   int32_t window;

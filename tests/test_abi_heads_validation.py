@@ -163,6 +163,7 @@ def test_attention(g):
     refused(g, inv, "multiple", name, attn(q_heads=5, ld_q=320, ld_out=320), cache(g, heads=2, page_stride=2048), batch(g), *ws)
     refused(g, un, "64 or 128", name, attn(), cache(g, head_dim=32), batch(g), *ws)
     refused(g, un, "128 query heads", name, attn(q_heads=129, ld_q=1 << 20, ld_out=1 << 20), cache(g), batch(g), *ws)
+    refused(g, un, "sequences", name, attn(), cache(g), batch(g, seqs=16385), *ws)
     refused(g, un, "2^40", name, attn(ld_q=1 << 41), cache(g), batch(g), *ws)
     for kw in (dict(q=A + 8), dict(out=B + 2), dict(ld_q=260), dict(hs_out=68, ld_out=512)):
         refused(g, al, "16-byte", name, attn(**kw), cache(g), batch(g), *ws)
