@@ -37,12 +37,18 @@ using heads::bf16;
 
 constexpr int kThreads = 512;
 constexpr int kPanel = 16384;        // 128 rows of 128 bytes
+constexpr int kBoxRows = 16;         // of a copy, at most
 constexpr int kCounterBytes = 4096;  // of the workspace: two counters per CTA
 constexpr int kMaxCtas = kCounterBytes / 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
+// Registers of the warpgroups where a thread holds a row's 128 scores; 512 threads are launched with 128 each.
+constexpr int kWeightRegs = 184, kCopyRegs = 64;
+template <int NQ>
+constexpr int kPrepRegs = NQ == 2 ? 80 : 128;
+static_assert(2 * kWeightRegs + kPrepRegs<2> + kCopyRegs <= 512 && kWeightRegs + 2 * kPrepRegs<1> + kCopyRegs <= 512, "registers");
 
-template <int D, bool MX, int NQ>
+template <int D, bool MX, int NQ, bool SPREAD>
 struct Form {
   static constexpr int PANELS = D / 64;
   static constexpr int TILE = PANELS * kPanel;  // 128 rows of bf16
@@ -51,14 +57,17 @@ struct Form {
   static constexpr int VALUES_EVERY = STAGES % 2 != 0 ? 2 * STAGES : STAGES;
   static constexpr int RAW = 128 * D + 4 * D;   // 128 rows of codes and their units
   static constexpr int RAWS = MX ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int PREP_WARP = MX && NQ == 1 ? 4 : 8;  // the first of them
+  static constexpr int PREP_WARP = NQ == 1 ? 4 : 8;  // the first of them
   static constexpr int PREP_WARPS = 12 - PREP_WARP;
+  static_assert(NQ == 2 || NQ == 1, "tiles");
+  static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
   static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
   static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
   static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
   static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 6 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int SMEM = OFF_MISC + 256 + 1024;
+  static constexpr int OFF_STATS = OFF_MISC + 256;  // SPREAD: (reference, sum) of each warp's rows
+  static constexpr int SMEM = OFF_STATS + (SPREAD ? 1024 : 0) + 1024;
   static_assert(RAW % 128 == 0 && OFF_RAW % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
   static_assert(OFF_RAW >= 4 * kAttendMaxSeqs, "room for the sequences' costs");
 };
@@ -214,6 +223,11 @@ __device__ __forceinline__ float2 split(uint64_t a) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float exp2_of(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -261,11 +275,11 @@ __device__ float unusual(const Params& p, int64_t row, int64_t unit, int d) {
   return isfinite(v) ? 0.0f : v;
 }
 
-template <int D, bool MX, int NQ>
+template <int D, bool MX, int NQ, bool SPREAD>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ Params p) {
-  using F = Form<D, MX, NQ>;
+  using F = Form<D, MX, NQ, SPREAD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(smem);
@@ -280,19 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
-      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, SPREAD ? 2 : 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
     }
     for (int i = 0; i < F::STAGES; ++i) {
-      mbar_init(kv_full + 8 * i, MX ? F::PREP_WARPS : 1);
+      mbar_init(kv_full + 8 * i, MX ? 4 : 1);
       mbar_init(kv_empty + 8 * i, 1);
-      mbar_init(v_fixed + 8 * i, 4);
+      mbar_init(v_fixed + 8 * i, F::PREP_WARPS);
     }
     for (int i = 0; i < F::RAWS; ++i) {
       mbar_init(raw_full + 8 * i, 1);
-      mbar_init(raw_empty + 8 * i, F::PREP_WARPS);
+      mbar_init(raw_empty + 8 * i, 4);
     }
     mbar_init(bar_final, 1);
     fence_mbar_init();
@@ -317,10 +331,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t total = misc->total;
   const int runs = misc->runs;
   Walk<Sequences> k(src, misc->start, p.c.heads, per, p.a.window);
+  auto weights_at = [&](int slot) { return tmem + (SPREAD ? 384 + 64 * slot : 128 * slot + 64); };
 
+  if constexpr (!SPREAD) {
+    if (warp >= 12) {
+      fewer_registers<kCopyRegs>();
+    } else if (warp >= 4 * NQ) {
+      fewer_registers<kPrepRegs<NQ>>();
+    }
+  }
   if (warp == 12) {
     // ---- copies ------------------------------------------------------------------------------------------------------
-    const int rows = min(p.c.page_size, kTile);  // of a box
+    const int rows = min(p.c.page_size, kBoxRows);  // of a box
     bool ok = true;
     int n = 0;  // items so far
     for (; ok && k.live(); k.next()) {
@@ -330,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const int t0 = k.at.block * per, tiles = NQ == 2 && t0 + p.tokens_per_tile < k.s.n ? 2 : 1;
       if (elect_one()) {
-        mbar_arrive_expect_tx(q_full + 8 * buf, static_cast<uint32_t>(tiles * p.tokens_per_tile * p.group * D * 2));
-        for (int i = 0; i < tiles; ++i)
+        mbar_arrive_expect_tx(q_full + 8 * buf, static_cast<uint32_t>((SPREAD ? 4 : tiles) * p.tokens_per_tile * p.group * D * 2));
+        for (int i = 0; i < (SPREAD ? 4 : tiles); ++i)
 #pragma unroll
           for (int j = 0; j < F::PANELS; ++j)
-            tma_load_3d(base + (NQ == 1 ? buf : i) * F::TILE + j * kPanel, &tm_q, q_full + 8 * buf, 64 * j, k.at.head * p.group, k.s.first + t0 + i * p.tokens_per_tile);
+            tma_load_3d(base + (NQ == 1 ? buf : i) * F::TILE + j * kPanel + (SPREAD ? i * 4096 : 0), &tm_q, q_full + 8 * buf, 64 * j, k.at.head * p.group,
+                        k.s.first + t0 + (SPREAD ? 0 : i * p.tokens_per_tile));
       }
       __syncwarp();
       const int32_t* table = p.b.page_table + k.at.seq * p.b.ld_table;
@@ -348,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = k.a; t < k.b; ++t, ++n) {
         const int page = next, boxes = min(kTile / rows, (min(k.s.seen - t * kTile, kTile) + rows - 1) / rows);
         next = page_of(t + 1);
-        const int within = (t * kTile) & (p.c.page_size - 1);
+        const int within = (t * kTile + lane * rows) & (p.c.page_size - 1);
         const bool good = page >= 0 && page < p.c.pages;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -445,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = NQ == 2 ? q : n_v & 1;
         const uint32_t va = base + F::OFF_KV + ((2 * n_v + 1) % F::STAGES) * F::TILE, o = tmem + 256 + 128 * q;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, tmem + 128 * slot + 64 + 8 * i, smem_desc_sw128_mn(va + i * 2048), kValues, !first || i > 0);
-        mma_commit(o_done + 8 * q);
+        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights_at(slot) + 8 * i, smem_desc_sw128_mn(va + i * 2048), kValues, !first || i > 0);
+        mma_commit(o_done + 8 * (NQ == 2 ? q : slot));
       }
       __syncwarp();
     };
@@ -526,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else if (warp >= F::PREP_WARP && warp < 12) {
     // ---- keys and values on their way ----------------------------------------------------------------------------------
-    const int tid = threadIdx.x - 32 * F::PREP_WARP, rows = min(p.c.page_size, kTile);
+    // (one tile of rows: 8-bit keys in the first four warps, values in the others)
+    const int mine = MX && NQ == 1 ? (warp - F::PREP_WARP) >> 2 : -1, tid = (threadIdx.x - 32 * F::PREP_WARP) % (MX ? 128 : 32 * F::PREP_WARPS), rows = min(p.c.page_size, kBoxRows);
     bool ok = true;
     int n = 0;
     for (; ok && k.live(); k.next()) {
@@ -540,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* v = smem + F::OFF_KV + (u % F::STAGES) * F::TILE;
           bool bad = false;
 #pragma unroll 4
-          for (int i = tid; edge && i < F::PANELS * 1024; i += 128) {
+          for (int i = tid; (SPREAD || edge) && i < F::PANELS * 1024; i += 32 * F::PREP_WARPS) {
             uint4* at = reinterpret_cast<uint4*>(v) + i;
             const uint4 x = *at;
             if (((i & 1023) >> 3) >= live) {
@@ -551,12 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (bad) misc->dirty[k.filled & 15] = k.filled;
-          if (edge) fence_proxy_async_smem();
+          if (SPREAD || edge) fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(v_fixed + 8 * (u % F::STAGES));
         } else {
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
+          for (int kv = mine < 0 ? 0 : mine; kv <= (mine < 0 ? 1 : mine); ++kv) {
             const int u = 2 * n + kv, raw = u % F::RAWS, slot = u % F::STAGES;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_full + 8 * raw, (u / F::RAWS) & 1, p.w, DEV_ERR_WAIT_EPILOGUE) &&
                                              mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
@@ -567,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lost = misc->bad[raw];
             bool bad = false;
 #pragma unroll 2
-            for (int i = tid; i < 8 * D; i += 32 * F::PREP_WARPS) {  // 16 codes each
+            for (int i = tid; i < 8 * D; i += 128) {  // 16 codes each
               const int row = i / (D / 16), c = i % (D / 16);
               const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * i);
               const uint32_t unit = units[row * (D / 32) + c / 2];
@@ -595,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = 0u;
               }
-              if (kv == 1 && edge) {
+              if (kv == 1 && (edge || (SPREAD && unit >= 247u))) {  // (448 times a smaller one is finite)
                 if (row >= live) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e) y[e] = 0u;
@@ -628,14 +652,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 4 * NQ) {
-    // ---- weights: a thread per row -------------------------------------------------------------------------------------
-    const int q = warp >> 2, row = threadIdx.x & 127;
+    // ---- weights: a thread per row; SPREAD: a thread per row and quarter of a tile's keys ------------------------------
+    if constexpr (!SPREAD) more_registers<kWeightRegs>();
+    const int q = warp >> 2, row = SPREAD ? lane : threadIdx.x & 127, key0 = SPREAD ? 32 * warp : 0;
+    constexpr int KEYS = SPREAD ? 32 : kTile;  // of a tile, a thread's
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_at = tmem + lanes + 256 + 128 * q;
-    const int token = row / p.group, head = row - token * p.group;
+    const int token = row / p.group;
     const float c2 = p.c2, slack = fminf(kSlack / c2, 3.0e38f);
     bool ok = true;
     int n = 0;  // tiles of this warpgroup so far
+    // The last product with the values that this warpgroup has given weights to. One tile: two may be on their way when the last
+    // weights are written, so they report in turn to two barriers (of which neither can be a phase ahead of what is asked).
+    auto values_done = [&]() { return mbar_wait(o_done + 8 * (NQ == 2 ? q : (n - 1) & 1), (NQ == 2 ? n - 1 : (n - 1) >> 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE); };
+    if constexpr (SPREAD) {  // the weights that this warp's copy of the rows gives to the other warps' keys
+      uint32_t none[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) none[e] = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmem_st32(tmem + lanes + 384 + 32 * e, none);
+      tmem_st_wait();
+    }
     for (; k.live(); k.next()) {
       const int i0 = k.at.block * per + q * p.tokens_per_tile, i = i0 + token;
       if (i0 >= k.s.n) continue;
@@ -647,71 +684,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, limit = -INFINITY, l = 0.0f;
       for (int t = part.lo; t < part.hi; ++t, ++n) {
         const int slot = NQ == 2 ? q : n & 1;
-        const uint32_t s_at = tmem + lanes + 128 * slot;
+        const uint32_t s_at = tmem + lanes + 128 * slot + key0, w_at = weights_at(slot) + lanes + key0 / 2;
         ok = ok && mbar_wait(s_full + 8 * slot, (NQ == 2 ? n : n >> 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
         __syncwarp();
         tc_fence_after();
         if (any) {
-          const int c_lo = mine.lo - t * kTile, c_hi = mine.hi - t * kTile;
-          const bool whole = __all_sync(0xFFFFFFFFu, !valid || (c_lo <= 0 && c_hi >= kTile));
-          uint32_t r[64];
-          auto load = [&](int half) {
-            tmem_ld64(s_at + 64 * half, r);
-            tmem_ld_wait();
-            reg_fence(r);
+          const int c_lo = mine.lo - t * kTile - key0, c_hi = mine.hi - t * kTile - key0;
+          const bool whole = __all_sync(0xFFFFFFFFu, !valid || (c_lo <= 0 && c_hi >= KEYS));
+          const uint32_t width = static_cast<uint32_t>(most(c_hi - c_lo, 0));
+          float top = -INFINITY;
+          auto look = [&](uint32_t (&r)[32], int from) {  // what a thread does with 32 scores before it knows the tile's highest
             if (p.flip)
 #pragma unroll
-              for (int e = 0; e < 64; ++e) r[e] ^= 0x80000000u;
+              for (int e = 0; e < 32; ++e) r[e] ^= 0x80000000u;
             if (!whole) {
-              const int lo = c_lo - 64 * half;
-              const uint32_t width = static_cast<uint32_t>(most(c_hi - c_lo, 0));
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (static_cast<uint32_t>(e - lo) >= width) r[e] = 0xFF800000u;
+              for (int e = 0; e < 32; ++e)
+                if (static_cast<uint32_t>(e + from - c_lo) >= width) r[e] = 0xFF800000u;
             }
-          };
-          auto highest = [&](float x) {
-            float y = -INFINITY;
+            float x = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              x = fmaxf(x, __uint_as_float(r[e]));
-              y = fmaxf(y, __uint_as_float(r[e + 1]));
+            for (int e = 0; e < 32; e += 4) {
+              x = max3(x, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+              top = max3(top, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
             }
-            return fmaxf(x, y);
+            top = fmaxf(top, x);
           };
-          load(0);
-          float top = highest(-INFINITY);
-          load(1);
-          top = highest(top);
-          const bool move = valid && top > limit;
-          if (__any_sync(0xFFFFFFFFu, move)) {
+          auto move_to = [&]() {  // the reference, where it has to
+            const bool move = valid && top > limit;
+            if (!__any_sync(0xFFFFFFFFu, move)) return;
             const float to = move ? top : m;
             if (t > part.lo) {
               const float f = move ? exp2_of((m - to) * c2) : 1.0f;
               l *= f;
-              ok = ok && mbar_wait(o_done + 8 * q, (n - 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
+              ok = ok && values_done();
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
-                uint32_t x[32];
-                tmem_ld32(o_at + d, x);
+              for (int d = 0; d < D; d += 16) {
+                uint32_t x[16];
+                tmem_ld16(o_at + d, x);
                 tmem_ld_wait();
                 reg_fence(x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                tmem_st32(o_at + d, x);
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tmem_st16(o_at + d, x);
               }
             }
             m = to;
             if (move) limit = top + slack;
-          }
-          const uint64_t c = both(c2), shift = both(m == -INFINITY ? 0.0f : -(m * c2));
-          uint64_t sum0 = 0, sum1 = 0;
-          auto weigh = [&](int half) {
-            uint32_t w[32];
+          };
+          const uint64_t c = both(c2);
+          uint64_t shift = 0, sum0 = 0, sum1 = 0;
+          auto weigh = [&](uint32_t (&r)[32], int from) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               const float2 x = split(fma2(pair(r[2 * e], r[2 * e + 1]), c, shift));
               const float a = exp2_of(x.x), b = exp2_of(x.y);
               const uint64_t ab = pair(__float_as_uint(a), __float_as_uint(b));
@@ -721,11 +749,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum0 = add2(sum0, ab);
               w[e] = heads::pack(a, b);
             }
-            tmem_st32(s_at + 64 + 32 * half, w);
+            tmem_st16(w_at + from / 2, w);
           };
-          weigh(1);  // (both halves' weights lie over the second half's scores, which are in registers)
-          load(0);
-          weigh(0);
+          uint32_t r0[32];
+          tmem_ld32(s_at, r0);
+          tmem_ld_wait();
+          reg_fence(r0);
+          if constexpr (SPREAD) {
+            look(r0, 0);
+            move_to();
+            shift = both(m == -INFINITY ? 0.0f : -(m * c2));
+            weigh(r0, 0);
+          } else {
+            uint32_t r1[32], r2[32], r3[32];
+            tmem_ld32(s_at + 32, r1);
+            look(r0, 0);
+            tmem_ld_wait();
+            reg_fence(r1);
+            tmem_ld32(s_at + 64, r2);
+            look(r1, 32);
+            tmem_ld_wait();
+            reg_fence(r2);
+            tmem_ld32(s_at + 96, r3);
+            look(r2, 64);
+            tmem_ld_wait();
+            reg_fence(r3);
+            look(r3, 96);
+            move_to();
+            shift = both(m == -INFINITY ? 0.0f : -(m * c2));
+            weigh(r0, 0);
+            weigh(r1, 32);
+            weigh(r2, 64);
+            weigh(r3, 96);
+          }
           const float2 s = split(add2(sum0, sum1));
           l += s.x + s.y;
           tmem_st_wait();
@@ -736,21 +792,116 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the unit's end, or this CTA's part's ------------------------------------------------------------------------
       const bool some = part.lo < part.hi, alone = k.first() && k.last();
-      const int64_t out_row = (static_cast<int64_t>(k.s.first) + i) * p.a.ld_out + (static_cast<int64_t>(k.at.head) * p.group + head) * p.a.hs_out;
-      const int64_t lse_row = (static_cast<int64_t>(k.s.first) + i) * p.a.q_heads + k.at.head * p.group + head;
       const int64_t unit0 = k.at.item - k.at.off;
       const int c0 = alone ? 0 : cta_of(total, unit0, runs), c1 = alone ? 0 : cta_of(total, unit0 + k.items - 1, runs);
       constexpr int64_t kPart = 128 * (D + 2) * 4;  // bytes of one tile's part: (reference, sum) of each row, then O
       auto part_at = [&](int cta) { return p.parts + (static_cast<int64_t>(2 * cta + (cta == c0 ? 1 : 0)) * NQ + q) * kPart; };
-      if (any) {
-        if (some) {
-          ok = ok && mbar_wait(o_done + 8 * q, (n - 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
-          __syncwarp();
-          tc_fence_after();
+      char* to = alone ? nullptr : part_at(blockIdx.x);
+      const int rows = least(k.s.n - i0, p.tokens_per_tile) * p.group;  // of this tile
+      auto out_at = [&](int r) {
+        const int tk = r / p.group, hd = r - tk * p.group;
+        return static_cast<bf16*>(p.a.out) + (static_cast<int64_t>(k.s.first) + i0 + tk) * p.a.ld_out + (static_cast<int64_t>(k.at.head) * p.group + hd) * p.a.hs_out;
+      };
+      auto set_lse = [&](int r, float reference, float sum) {
+        if (p.a.lse == nullptr) return;
+        const int tk = r / p.group, hd = r - tk * p.group;
+        p.a.lse[(static_cast<int64_t>(k.s.first) + i0 + tk) * p.a.q_heads + k.at.head * p.group + hd] = sum == 0.0f ? -INFINITY : (reference + log2f(sum)) * kLn2;
+      };
+      auto put8 = [&](int r, int d, const float (&y)[8], float sum, float inv) {  // 8 elements of a row, done or as they are
+        if (alone) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = sum == 0.0f ? 0u : heads::pack(y[2 * j] * inv, y[2 * j + 1] * inv);
+          *reinterpret_cast<uint4*>(out_at(r) + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          float4* o = reinterpret_cast<float4*>(to + 1024 + (static_cast<int64_t>(r) * D + d) * 4);
+          __stcg(o, make_float4(y[0], y[1], y[2], y[3]));
+          __stcg(o + 1, make_float4(y[4], y[5], y[6], y[7]));
         }
-        const bool dirty = some && *reinterpret_cast<volatile int*>(&misc->dirty[k.filled & 15]) == k.filled;
+      };
+      auto add_unusual = [&](int d, float (&x)[8]) {  // what was taken out of the values that this thread's row sees
+        for (int t = part.lo; t < part.hi; ++t) {
+          if (!SPREAD && !k.edge(t)) continue;
+          for (int j = most(mine.lo, t * kTile + key0); j < least(mine.hi, t * kTile + key0 + KEYS); ++j) {
+            const int page = __ldg(p.b.page_table + k.at.seq * p.b.ld_table + (j >> p.c.page_bits));
+            if (page < 0 || page >= p.c.pages) continue;
+            const int at = j & (p.c.page_size - 1);
+            const int64_t v_row = page * p.c.page_stride + k.at.head * p.c.head_stride + at * p.c.token_stride;
+            const int64_t unit = ((static_cast<int64_t>(page) * p.c.heads + k.at.head) * p.c.page_size + at) * (D / 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += unusual<MX, D>(p, v_row, unit, d + e);
+          }
+        }
+      };
+      if (some && any) {
+        ok = ok && values_done();
+        __syncwarp();
+        tc_fence_after();
+      }
+      const bool dirty = some && *reinterpret_cast<volatile int*>(&misc->dirty[k.filled & 15]) == k.filled;
+      if constexpr (SPREAD) {
+        // the four warps' copies of a row, each over its own keys, are brought to one reference and added
+        float2* stats = reinterpret_cast<float2*>(smem + F::OFF_STATS);
+        float4* share = reinterpret_cast<float4*>(smem + (k.filled & 1) * F::TILE);  // (the unit's queries, which nothing reads any more)
+        stats[threadIdx.x] = make_float2(m * c2, l);
+        bar_sync(1, 128);
+        auto joined = [&](int r) {
+          float2 s = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) s.x = fmaxf(s.x, stats[32 * w + r].x);
+          if (s.x == -INFINITY) s.x = 0.0f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) s.y = fmaf(exp2_of(stats[32 * w + r].x - s.x), stats[32 * w + r].y, s.y);
+          return s;
+        };
+        const float f = exp2_of(m * c2 - joined(lane).x);
+        const int r = threadIdx.x >> 2, e0 = threadIdx.x & 3;  // a row and 8 of 32 columns
+        const float2 s = joined(r);
+        const float inv = s.y == 0.0f ? 0.0f : 1.0f / s.y;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          if (some) {
+            uint32_t x[32];
+            tmem_ld32(o_at + d, x);
+            tmem_ld_wait();
+            reg_fence(x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float y[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(x[8 * e + j]) * f;
+              if (dirty && valid) add_unusual(d + 8 * e, y);
+              share[threadIdx.x * 8 + ((2 * e) ^ (lane & 7))] = make_float4(y[0], y[1], y[2], y[3]);
+              share[threadIdx.x * 8 + ((2 * e + 1) ^ (lane & 7))] = make_float4(y[4], y[5], y[6], y[7]);
+            }
+          }
+          bar_sync(1, 128);
+          if (r < rows) {
+            float y[8] = {};
+            if (some) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const float4 a = share[(32 * w + r) * 8 + ((2 * e0) ^ (r & 7))], b = share[(32 * w + r) * 8 + ((2 * e0 + 1) ^ (r & 7))];
+                y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w, y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
+              }
+            }
+            put8(r, d + 8 * e0, y, s.y, inv);
+          }
+          bar_sync(1, 128);
+        }
+        if (e0 == 0 && r < rows) {
+          if (alone)
+            set_lse(r, s.x, s.y);
+          else
+            __stcg(reinterpret_cast<float2*>(to) + r, make_float2(s.y == 0.0f ? -INFINITY : s.x, s.y));
+        }
+        if (some) {
+          fence_proxy_async_smem();
+          bar_sync(1, 128);
+          if (threadIdx.x == 0) mbar_arrive(q_empty + 8 * (k.filled & 1));
+        }
+      } else if (any) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        char* to = alone ? nullptr : part_at(blockIdx.x);
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
@@ -762,48 +913,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = 0u;
           }
-          if (dirty && valid) {
-            for (int t = part.lo; t < part.hi; ++t) {
-              if (!k.edge(t)) continue;
-              for (int j = most(mine.lo, t * kTile); j < least(mine.hi, t * kTile + kTile); ++j) {
-                const int page = __ldg(p.b.page_table + k.at.seq * p.b.ld_table + (j >> p.c.page_bits));
-                if (page < 0 || page >= p.c.pages) continue;
-                const int at = j & (p.c.page_size - 1);
-                const int64_t v_row = page * p.c.page_stride + k.at.head * p.c.head_stride + at * p.c.token_stride;
-                const int64_t unit = ((static_cast<int64_t>(page) * p.c.heads + k.at.head) * p.c.page_size + at) * (D / 32);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + unusual<MX, D>(p, v_row, unit, d + e));
-              }
-            }
-          }
           if (!valid) continue;
-          if (alone) {
-            uint4* out = reinterpret_cast<uint4*>(static_cast<bf16*>(p.a.out) + out_row + d);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
+          for (int e = 0; e < 4; ++e) {
+            float y[8];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float a = __uint_as_float(x[8 * e + 2 * j]), b = __uint_as_float(x[8 * e + 2 * j + 1]);
-                w[j] = l == 0.0f ? 0u : heads::pack(a * inv, b * inv);
-              }
-              out[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            float4* o = reinterpret_cast<float4*>(to + 1024 + (static_cast<int64_t>(row) * D + d) * 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              __stcg(o + e, make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+            for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(x[8 * e + j]);
+            if (dirty) add_unusual(d + 8 * e, y);
+            put8(row, d + 8 * e, y, l, inv);
           }
         }
-        if (valid && alone && p.a.lse != nullptr) p.a.lse[lse_row] = l == 0.0f ? -INFINITY : (m * c2 + log2f(l)) * kLn2;
+        if (valid && alone) set_lse(row, m * c2, l);
         if (valid && !alone) __stcg(reinterpret_cast<float2*>(to) + row, make_float2(m * c2, l));
       }
       tc_fence_before();
       if (!alone) {
         __threadfence();
         bar_sync(1 + q, 128);
-        if (row == 0) {
+        if ((threadIdx.x & 127) == 0) {
           const unsigned before = atomicAdd(p.counters + 2 * c0 + q, 1u);
           misc->last[q] = before == static_cast<unsigned>(c1 - c0);
           if (misc->last[q]) p.counters[2 * c0 + q] = 0u;
@@ -811,8 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_sync(1 + q, 128);
         if (misc->last[q]) {
           __threadfence();
-          const int rows = least(k.s.n - i0, p.tokens_per_tile) * p.group;
-          for (int x = row; x < rows * (D / 4); x += 128) {
+          for (int x = threadIdx.x & 127; x < rows * (D / 4); x += 128) {
             const int r = x / (D / 4), d = 4 * (x - r * (D / 4));
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
@@ -831,11 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int tk = r / p.group, hd = r - tk * p.group;
-            const int64_t tok = static_cast<int64_t>(k.s.first) + i0 + tk;
-            bf16* out = static_cast<bf16*>(p.a.out) + tok * p.a.ld_out + (static_cast<int64_t>(k.at.head) * p.group + hd) * p.a.hs_out + d;
-            *reinterpret_cast<uint2*>(out) = sum == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
-            if (d == 0 && p.a.lse != nullptr) p.a.lse[tok * p.a.q_heads + k.at.head * p.group + hd] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            *reinterpret_cast<uint2*>(out_at(r) + d) = sum == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
+            if (d == 0) set_lse(r, top, sum);
           }
         }
       }
@@ -854,10 +977,16 @@ int ctas() { return min(num_sms(), kMaxCtas); }
 // Two tiles of rows where units have more than one tile's on average.
 bool two_tiles(const Attention& a, const Cache& c, const Batch& b) { return b.tokens * (a.q_heads / c.heads) > static_cast<int64_t>(b.seqs) * kTile; }
 
-template <int D, bool MX, int NQ>
+// And one tile of 32 rows, four times over, where they have fewer still.
+bool spread(const Attention& a, const Cache& c, const Batch& b) {
+  const int64_t group = a.q_heads / c.heads;
+  return group <= 32 && b.tokens * group <= static_cast<int64_t>(b.seqs) * 32;
+}
+
+template <int D, bool MX, int NQ, bool SPREAD>
 cudaError_t launch_form(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Params& p, cudaStream_t stream) {
-  using F = Form<D, MX, NQ>;
-  auto* kernel = paged_attention_kernel<D, MX, NQ>;
+  using F = Form<D, MX, NQ, SPREAD>;
+  auto* kernel = paged_attention_kernel<D, MX, NQ, SPREAD>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(ctas()), dim3(kThreads), F::SMEM, stream, q, k, v, p);
@@ -875,7 +1004,8 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
   p.c = c;
   p.b = b;
   p.group = a.q_heads / c.heads;
-  p.tokens_per_tile = kTile / p.group;
+  const bool two = two_tiles(a, c, b), four = spread(a, c, b);
+  p.tokens_per_tile = (four ? 32 : kTile) / p.group;
   // (a cache without pages holds nothing, and the tensor maps need an address)
   const int64_t reach = c.pages > 0 ? static_cast<int64_t>(b.table_width) << c.page_bits : 0;
   p.capacity = static_cast<int>(min(reach, int64_t{0x7FFFFF00}));
@@ -899,7 +1029,7 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
   const uint64_t one = size * D, pages = static_cast<uint64_t>(max(c.pages, 1));
   const uint64_t kv_dims[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads), pages};
   const uint64_t kv_strides[3] = {static_cast<uint64_t>(size * c.token_stride), or_row(c.heads, size * c.head_stride, one), or_row(c.pages, size * c.page_stride, one)};
-  const uint32_t kv_box[4] = {c.mx ? static_cast<uint32_t>(D) : 64u, static_cast<uint32_t>(min(c.page_size, kTile)), 1, 1};
+  const uint32_t kv_box[4] = {c.mx ? static_cast<uint32_t>(D) : 64u, static_cast<uint32_t>(min(c.page_size, kBoxRows)), 1, 1};
   const CUtensorMapDataType dt = c.mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const void* k = c.pages > 0 ? c.k : a.q;
   const void* v = c.pages > 0 ? c.v : a.q;
@@ -908,8 +1038,10 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  const bool two = two_tiles(a, c, b);
-#define FP8GB_FORM(D, MX) (two ? launch_form<D, MX, 2>(mq, mk, mv, p, stream) : launch_form<D, MX, 1>(mq, mk, mv, p, stream))
+#define FP8GB_FORM(D, MX)                                          \
+  (two    ? launch_form<D, MX, 2, false>(mq, mk, mv, p, stream)      \
+   : four ? launch_form<D, MX, 1, true>(mq, mk, mv, p, stream)       \
+          : launch_form<D, MX, 1, false>(mq, mk, mv, p, stream))
   if (c.head_dim == 64) return c.mx ? FP8GB_FORM(64, true) : FP8GB_FORM(64, false);
   return c.mx ? FP8GB_FORM(128, true) : FP8GB_FORM(128, false);
 #undef FP8GB_FORM
