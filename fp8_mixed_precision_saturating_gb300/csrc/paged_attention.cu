@@ -52,11 +52,11 @@ template <int D, bool MX, int NQ, bool SPREAD>
 struct Form {
   static constexpr int PANELS = D / 64;
   static constexpr int TILE = PANELS * kPanel;  // 128 rows of bf16
-  static constexpr int STAGES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 5 : 8);
   // tiles from one tile of values in a stage to the next one in it: with an odd number of stages keys come between
   static constexpr int VALUES_EVERY = STAGES % 2 != 0 ? 2 * STAGES : STAGES;
   static constexpr int RAW = 128 * D + 4 * D;   // 128 rows of codes and their units
-  static constexpr int RAWS = MX ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 5 : 3) : (NQ == 1 ? 8 : 6)) : 0;
   static constexpr int PREP_WARP = NQ == 1 ? 4 : 8;  // the first of them
   static constexpr int PREP_WARPS = 12 - PREP_WARP;
   static_assert(NQ == 2 || NQ == 1, "tiles");
@@ -242,17 +242,29 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
   return w & ~((bad & 0x8000u ? 0xFFFFu : 0u) | (bad & 0x80000000u ? 0xFFFF0000u : 0u));
 }
 
-// Two E4M3 codes (bytes 0 and 1, or 2 and 3, of w) as two bf16, times f. A code's exponent and mantissa in bf16's places are the value
-// times 2^-120 (subnormals included), exactly.
-__device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t which, __nv_bfloat162 f) {
-  const uint32_t x = __byte_perm(w, 0u, which);  // the codes in the high bytes of the halves
-  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+// 16 E4M3 codes as bf16, times f. A code's exponent and mantissa in bf16's places are the value times 2^-120 (subnormals
+// included), exactly: each half takes a code and its sign's eight copies, moved up by four.
+__device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t w) {
   __nv_bfloat162 v;
-  memcpy(&v, &y, 4);
-  v = __hmul2(v, f);
+  memcpy(&v, &w, 4);
+  return v;
+}
+__device__ __forceinline__ uint32_t times(uint32_t w, __nv_bfloat162 f) {
+  const __nv_bfloat162 v = __hmul2(as_pair(w), f);
   uint32_t r;
   memcpy(&r, &v, 4);
   return r;
+}
+__device__ __forceinline__ void decode16(const uint4& x, __nv_bfloat162 f, uint32_t (&y)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t a, b;
+    asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w[e]));
+    asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(w[e]));
+    y[2 * e] = times((a << 4) & 0x87F087F0u, f);
+    y[2 * e + 1] = times((b << 4) & 0x87F087F0u, f);
+  }
 }
 __device__ __forceinline__ __nv_bfloat162 bf16_pair(uint32_t bits) {
   const uint32_t w = bits | (bits << 16);
@@ -590,55 +602,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* out = smem + F::OFF_KV + slot * F::TILE;
             const uint32_t lost = misc->bad[raw];
             bool bad = false;
-#pragma unroll 2
-            for (int i = tid; i < 8 * D; i += 128) {  // 16 codes each
-              const int row = i / (D / 16), c = i % (D / 16);
-              const uint4 x = *reinterpret_cast<const uint4*>(codes + 16 * i);
-              const uint32_t unit = units[row * (D / 32) + c / 2];
-              // 2^(unit - 127) 2^120 in one factor where that is a bf16, otherwise in two
-              const bool large = unit >= 135u;
-              const __nv_bfloat162 f = bf16_pair(large ? 0x7B80u : (unit + 120u) << 7);
-              uint32_t y[8];
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            // a thread's 16 columns of every kStep-th row; the swizzle's place is the same in all of them
+            constexpr int kLanes = D / 16, kStep = 128 / kLanes, kRows = 128 / kStep;
+            const int row0 = tid / kLanes, c = tid % kLanes;
+            uint8_t* panel = out + (c >> 2) * kPanel + row0 * 128;
+            const int flip = (c >> 2) & 1;  // (the panels' lanes take their two stores in opposite order: other banks)
+            uint4* first = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + flip) ^ (row0 & 7)) << 4));
+            uint4* second = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + 1 - flip) ^ (row0 & 7)) << 4));
+            auto store = [&](int j, const uint32_t (&y)[8]) {
+              const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+              first[j * kStep * 8] = flip ? hi : lo;
+              second[j * kStep * 8] = flip ? lo : hi;
+            };
+            uint4 x[kRows];
+            uint32_t unit[kRows], largest = 0u;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[2 * e] = decode2(w[e], 0x1404u, f);
-                y[2 * e + 1] = decode2(w[e], 0x3424u, f);
+            for (int j = 0; j < kRows; ++j) {
+              x[j] = reinterpret_cast<const uint4*>(codes)[tid + 128 * j];
+              unit[j] = units[(row0 + j * kStep) * (D / 32) + c / 2];
+            }
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) largest = max(largest, unit[j]);
+            if (largest < 135u && lost == 0u && (kv == 0 || !edge)) {  // 2^(unit - 127) 2^120 is a bf16
+#pragma unroll
+              for (int j = 0; j < kRows; ++j) {
+                uint32_t y[8];
+                decode16(x[j], bf16_pair((unit[j] + 120u) << 7), y);
+                store(j, y);
               }
-              if (large) {
-                const __nv_bfloat162 g = bf16_pair(unit == 255u ? 0x7FC0u : unit << 7);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kRows; ++j) {
+                const int row = row0 + j * kStep;
+                uint32_t y[8], any = 0u;
+                decode16(x[j], bf16_pair(0x7B80u), y);  // in two factors
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  __nv_bfloat162 z;
-                  memcpy(&z, &y[e], 4);
-                  z = __hmul2(z, g);
-                  memcpy(&y[e], &z, 4);
+                  y[e] = times(y[e], bf16_pair(unit[j] == 255u ? 0x7FC0u : unit[j] == 0u ? 0x0040u : unit[j] << 7));
+                  if ((lost >> (row / rows) & 1u) || (kv == 1 && row >= live)) y[e] = 0u;
+                  any |= not_finite(y[e]);
                 }
-              }
-              if (lost != 0u && (lost >> (row / rows) & 1u)) {
+                if (kv == 1 && (edge || SPREAD) && any != 0u) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = 0u;
-              }
-              if (kv == 1 && (edge || (SPREAD && unit >= 247u))) {  // (448 times a smaller one is finite)
-                if (row >= live) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = 0u;
-                } else {
-                  uint32_t any = 0u;
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) any |= not_finite(y[e]);
-                  if (any != 0u) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = finite_part(y[e]);
-                    bad = true;
-                  }
+                  for (int e = 0; e < 8; ++e) y[e] = finite_part(y[e]);
+                  bad = true;
                 }
+                store(j, y);
               }
-              uint8_t* panel = out + (c >> 2) * kPanel + row * 128;
-              const int c0 = 2 * (c & 3), flip = (c >> 2) & 1;  // (the panels' lanes take their two stores in opposite order: other banks)
-              const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-              *reinterpret_cast<uint4*>(panel + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
-              *reinterpret_cast<uint4*>(panel + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
             }
             if (bad) misc->dirty[k.filled & 15] = k.filled;
             fence_proxy_async_smem();
