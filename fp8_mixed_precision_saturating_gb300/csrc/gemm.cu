@@ -1665,10 +1665,10 @@ bool encode_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, ui
 bool encode_tmap_nd(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const uint64_t* dims, const uint64_t* strides,
                     const uint32_t* box, int swizzle) {
   EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr || rank < 2 || rank > 4) return false;
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4];
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  if (fn == nullptr || rank < 2 || rank > 5) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5];
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
   return fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -55,7 +55,7 @@ bool encode_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, ui
 bool encode_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t d0, uint64_t d1, uint64_t d2,
                     uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2);
 
-// Tiled tensor map of `rank` (3 or 4) dimensions, element type dt, strides of dimensions 1 .. in bytes; swizzle 128 or 0.
+// Tiled tensor map of `rank` (2 to 5) dimensions, element type dt, strides of dimensions 1 .. in bytes; swizzle 128 or 0.
 bool encode_tmap_nd(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const uint64_t* dims, const uint64_t* strides,
                     const uint32_t* box, int swizzle);
 

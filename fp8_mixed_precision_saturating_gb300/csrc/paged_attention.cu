@@ -23,7 +23,9 @@
 // of them (a counter) adds them up in the order of the parts, so the result does not depend on who that is.
 #include <cuda_bf16.h>
 
+#include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "attend_walk.cuh"
 #include "heads.cuh"
@@ -37,7 +39,6 @@ using heads::bf16;
 
 constexpr int kThreads = 512;
 constexpr int kPanel = 16384;        // 128 rows of 128 bytes
-constexpr int kBoxRows = 16;         // of a copy, at most
 constexpr int kCounterBytes = 4096;  // of the workspace: two counters per CTA
 constexpr int kMaxCtas = kCounterBytes / 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -52,6 +53,8 @@ template <int D, bool MX, int NQ, bool SPREAD>
 struct Form {
   static constexpr int PANELS = D / 64;
   static constexpr int TILE = PANELS * kPanel;  // 128 rows of bf16
+  // keys and values: groups of 8 rows, each panel's 8 x 128 bytes after the other (queries: a panel's 128 rows together)
+  static constexpr int GROUP = PANELS * 1024;
   static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 5 : 8);
   // tiles from one tile of values in a stage to the next one in it: with an odd number of stages keys come between
   static constexpr int VALUES_EVERY = STAGES % 2 != 0 ? 2 * STAGES : STAGES;
@@ -79,6 +82,7 @@ struct Params {
   int group, tokens_per_tile, capacity;
   float c2;   // |scale| log2 e
   bool flip;  // scale < 0
+  int page_steps, head_steps;  // of a bf16 cache's pages and heads in its tensor maps' last dimension
   char* parts;
   unsigned* counters;
   WaitCtl w;
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 12) {
     // ---- copies ------------------------------------------------------------------------------------------------------
-    const int rows = min(p.c.page_size, kBoxRows);  // of a box
+    const int rows = min(p.c.page_size, kTile);  // of a box
     bool ok = true;
     int n = 0;  // items so far
     for (; ok && k.live(); k.next()) {
@@ -396,9 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (elect_one()) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * D * 2));
             __syncwarp();
-            if (lane < boxes)
-#pragma unroll
-              for (int j = 0; j < F::PANELS; ++j) tma_load_4d(dst + j * kPanel + lane * rows * 128, map, bar, 64 * j, within, k.at.head, good ? page : -1);
+            if (lane < boxes) tma_load_5d(dst + lane * rows * D * 2, map, bar, 0, 0, 0, within >> 3, good ? page * p.page_steps + k.at.head * p.head_steps : -1);
           } else {
             const int slot = u % F::RAWS;
             const uint32_t bar = raw_full + 8 * slot, dst = base + F::OFF_RAW + slot * F::RAW;
@@ -455,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t qa = base + (NQ == 2 ? q : ahead.filled & 1) * F::TILE, ka = base + F::OFF_KV + ((2 * n_s) % F::STAGES) * F::TILE;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t o = (i >> 2) * kPanel + (i & 3) * 32;
-          mma_bf16(tmem + 128 * slot, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), kScores, i > 0);
+          mma_bf16(tmem + 128 * slot, smem_desc_sw128(qa + (i >> 2) * kPanel + (i & 3) * 32), smem_desc_sw128(ka + (i >> 2) * 1024 + (i & 3) * 32, F::GROUP, 16), kScores,
+                   i > 0);
         }
         mma_commit(s_full + 8 * slot);
       }
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = NQ == 2 ? q : n_v & 1;
         const uint32_t va = base + F::OFF_KV + ((2 * n_v + 1) % F::STAGES) * F::TILE, o = tmem + 256 + 128 * q;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights_at(slot) + 8 * i, smem_desc_sw128_mn(va + i * 2048), kValues, !first || i > 0);
+        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights_at(slot) + 8 * i, smem_desc_sw128(va + 2 * i * F::GROUP, F::GROUP, 1024), kValues, !first || i > 0);
         mma_commit(o_done + 8 * (NQ == 2 ? q : slot));
       }
       __syncwarp();
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= F::PREP_WARP && warp < 12) {
     // ---- keys and values on their way ----------------------------------------------------------------------------------
     // (one tile of rows: 8-bit keys in the first four warps, values in the others)
-    const int mine = MX && NQ == 1 ? (warp - F::PREP_WARP) >> 2 : -1, tid = (threadIdx.x - 32 * F::PREP_WARP) % (MX ? 128 : 32 * F::PREP_WARPS), rows = min(p.c.page_size, kBoxRows);
+    const int mine = MX && NQ == 1 ? (warp - F::PREP_WARP) >> 2 : -1, tid = (threadIdx.x - 32 * F::PREP_WARP) % (MX ? 128 : 32 * F::PREP_WARPS), rows = min(p.c.page_size, kTile);
     bool ok = true;
     int n = 0;
     for (; ok && k.live(); k.next()) {
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = tid; (SPREAD || edge) && i < F::PANELS * 1024; i += 32 * F::PREP_WARPS) {
             uint4* at = reinterpret_cast<uint4*>(v) + i;
             const uint4 x = *at;
-            if (((i & 1023) >> 3) >= live) {
+            if ((i / (F::GROUP / 16)) * 8 + ((i >> 3) & 7) >= live) {
               *at = make_uint4(0u, 0u, 0u, 0u);
             } else if ((not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) != 0u) {
               *at = make_uint4(finite_part(x.x), finite_part(x.y), finite_part(x.z), finite_part(x.w));
@@ -605,14 +607,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a thread's 16 columns of every kStep-th row; the swizzle's place is the same in all of them
             constexpr int kLanes = D / 16, kStep = 128 / kLanes, kRows = 128 / kStep;
             const int row0 = tid / kLanes, c = tid % kLanes;
-            uint8_t* panel = out + (c >> 2) * kPanel + row0 * 128;
+            uint8_t* panel = out + (row0 >> 3) * F::GROUP + (c >> 2) * 1024 + (row0 & 7) * 128;
             const int flip = (c >> 2) & 1;  // (the panels' lanes take their two stores in opposite order: other banks)
             uint4* first = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + flip) ^ (row0 & 7)) << 4));
             uint4* second = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + 1 - flip) ^ (row0 & 7)) << 4));
             auto store = [&](int j, const uint32_t (&y)[8]) {
               const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-              first[j * kStep * 8] = flip ? hi : lo;
-              second[j * kStep * 8] = flip ? lo : hi;
+              first[j * (kStep / 8) * (F::GROUP / 16)] = flip ? hi : lo;
+              second[j * (kStep / 8) * (F::GROUP / 16)] = flip ? lo : hi;
             };
             uint4 x[kRows];
             uint32_t unit[kRows], largest = 0u;
@@ -1035,16 +1037,33 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
   const uint64_t q_dims[3] = {D, static_cast<uint64_t>(a.q_heads), static_cast<uint64_t>(b.tokens)};
   const uint64_t q_strides[2] = {or_row(a.q_heads, 2 * a.hs_q, row), or_row(b.tokens, 2 * a.ld_q, row)};
   const uint32_t q_box[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(p.tokens_per_tile)};
-  const int64_t size = c.mx ? 1 : 2;
-  const uint64_t one = size * D, pages = static_cast<uint64_t>(max(c.pages, 1));
-  const uint64_t kv_dims[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads), pages};
-  const uint64_t kv_strides[3] = {static_cast<uint64_t>(size * c.token_stride), or_row(c.heads, size * c.head_stride, one), or_row(c.pages, size * c.page_stride, one)};
-  const uint32_t kv_box[4] = {c.mx ? static_cast<uint32_t>(D) : 64u, static_cast<uint32_t>(min(c.page_size, kBoxRows)), 1, 1};
-  const CUtensorMapDataType dt = c.mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t pages = static_cast<uint64_t>(max(c.pages, 1));
   const void* k = c.pages > 0 ? c.k : a.q;
   const void* v = c.pages > 0 ? c.v : a.q;
-  if (!encode_tmap_nd(&mq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_dims, q_strides, q_box, 128) || !encode_tmap_nd(&mk, k, dt, 4, kv_dims, kv_strides, kv_box, c.mx ? 0 : 128) ||
-      !encode_tmap_nd(&mv, v, dt, 4, kv_dims, kv_strides, kv_box, c.mx ? 0 : 128)) {
+  bool made = encode_tmap_nd(&mq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_dims, q_strides, q_box, 128);
+  const uint32_t rows = static_cast<uint32_t>(min(c.page_size, kTile));
+  if (c.mx) {
+    const uint64_t dims[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads), pages};
+    const uint64_t strides[3] = {static_cast<uint64_t>(c.token_stride), or_row(c.heads, c.head_stride, D), or_row(c.pages, c.page_stride, D)};
+    const uint32_t box[4] = {static_cast<uint32_t>(D), rows, 1, 1};
+    made = made && encode_tmap_nd(&mk, k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box, 0) && encode_tmap_nd(&mv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box, 0);
+  } else {
+    // a tile's rows by groups of 8, both panels of a group one after the other: with a box for each panel the two halves of
+    // a row's 256 bytes were fetched far apart (64 tokens over 4096: 1.0 TB/s with 128 rows a box, 5.8 with 16, 6.1 so)
+    const int64_t ps = c.pages > 1 ? c.page_stride : 0, hs = c.heads > 1 ? c.head_stride : 0, both = std::gcd(ps, hs), unit = both != 0 ? both : c.token_stride;
+    const int64_t steps = (static_cast<int64_t>(pages) - 1) * (ps / unit) + (c.heads - 1) * (hs / unit) + 1;
+    if (steps > 0x7FFFFFFF) {
+      *why = "pages and heads of the cache lie at strides whose common part is too small";
+      return cudaErrorInvalidValue;
+    }
+    p.page_steps = static_cast<int>(ps / unit);
+    p.head_steps = static_cast<int>(hs / unit);
+    const uint64_t dims[5] = {64, 8, D / 64, static_cast<uint64_t>(c.page_size / 8), static_cast<uint64_t>(steps)};
+    const uint64_t strides[4] = {static_cast<uint64_t>(2 * c.token_stride), 128, static_cast<uint64_t>(16 * c.token_stride), static_cast<uint64_t>(2 * unit)};
+    const uint32_t box[5] = {64, 8, static_cast<uint32_t>(D / 64), rows / 8, 1};
+    made = made && encode_tmap_nd(&mk, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, dims, strides, box, 128) && encode_tmap_nd(&mv, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, dims, strides, box, 128);
+  }
+  if (!made) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }

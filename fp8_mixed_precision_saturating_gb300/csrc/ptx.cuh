@@ -205,6 +205,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
+// 5-D tiled load of one box into shared memory (single CTA).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1, int32_t c2, int32_t c3, int32_t c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 // 2-D tiled load into this CTA's shared memory whose transaction bytes are signalled on an
 // mbarrier of either CTA of the pair (shared::cluster address `bar_cluster`).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int32_t c0,
@@ -517,6 +525,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   d |= static_cast<uint64_t>(1u) << 46;                           // version
   d |= static_cast<uint64_t>(2u) << 61;                           // 128-byte swizzle
   return d;
+}
+
+// The same with the strides given: bytes between 8-row groups, and (MN-major) between 128-byte MN chunks.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t group_stride, uint32_t chunk_stride) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(chunk_stride >> 4) << 16) | (static_cast<uint64_t>(group_stride >> 4) << 32) |
+         (static_cast<uint64_t>(1u) << 46) | (static_cast<uint64_t>(2u) << 61);
 }
 
 // The same for an MN-major tile written by TMA as boxes of 128 MN bytes x K rows with the
