@@ -44,9 +44,9 @@ constexpr int kMaxCtas = kCounterBytes / 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
 // Registers of the warpgroups where a thread holds a row's 128 scores; 512 threads are launched with 128 each.
-constexpr int kWeightRegs = 184, kCopyRegs = 64;
+constexpr int kWeightRegs = 168, kCopyRegs = 96;
 template <int NQ>
-constexpr int kPrepRegs = NQ == 2 ? 80 : 128;
+constexpr int kPrepRegs = NQ == 2 ? 80 : 120;
 static_assert(2 * kWeightRegs + kPrepRegs<2> + kCopyRegs <= 512 && kWeightRegs + 2 * kPrepRegs<1> + kCopyRegs <= 512, "registers");
 
 template <int D, bool MX, int NQ, bool SPREAD>
@@ -55,11 +55,9 @@ struct Form {
   static constexpr int TILE = PANELS * kPanel;  // 128 rows of bf16
   // keys and values: groups of 8 rows, each panel's 8 x 128 bytes after the other (queries: a panel's 128 rows together)
   static constexpr int GROUP = PANELS * 1024;
-  static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 5 : 8);
-  // tiles from one tile of values in a stage to the next one in it: with an odd number of stages keys come between
-  static constexpr int VALUES_EVERY = STAGES % 2 != 0 ? 2 * STAGES : STAGES;
+  static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 4 : 8);
   static constexpr int RAW = 128 * D + 4 * D;   // 128 rows of codes and their units
-  static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 5 : 3) : (NQ == 1 ? 8 : 6)) : 0;
+  static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 8 : 6)) : 0;
   static constexpr int PREP_WARP = NQ == 1 ? 4 : 8;  // the first of them
   static constexpr int PREP_WARPS = 12 - PREP_WARP;
   static_assert(NQ == 2 || NQ == 1, "tiles");
@@ -71,6 +69,10 @@ struct Form {
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int OFF_STATS = OFF_MISC + 256;  // SPREAD: (reference, sum) of each warp's rows
   static constexpr int SMEM = OFF_STATS + (SPREAD ? 1024 : 0) + 1024;
+  // A wait names a phase by its parity, so whoever waits on a barrier has to see all of its phases. Where keys and values have
+  // different waiters (the warps that look at bf16 values, the two groups that convert 8-bit tiles) a stage is always
+  // one or the other's.
+  static_assert(MX ? NQ == 2 || (STAGES % 2 == 0 && RAWS % 2 == 0) : STAGES % 2 == 0, "stages");
   static_assert(RAW % 128 == 0 && OFF_RAW % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
   static_assert(OFF_RAW >= 4 * kAttendMaxSeqs, "room for the sequences' costs");
 };
@@ -433,134 +435,162 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 13) {
     // ---- tensor-core instructions --------------------------------------------------------------------------------------
-    constexpr uint32_t kScores = idesc_bf16(128, 128, false), kValues = idesc_bf16(128, D, true);
-    Walk<Sequences> ahead = k;  // the scores' place: one item before the values'
-    bool ok = true, more;
-    int n_s = 0, n_v = 0, t_s = 0, seen_p[2] = {0, 0};
-    auto settle = [&](Walk<Sequences>& w) {
-      while (w.live() && w.a >= w.b) w.next();
-      return w.live();
-    };
-    auto part = [&](const Walk<Sequences>& w, int q) { return w.part_of(q * p.tokens_per_tile, p.tokens_per_tile); };
-    auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, p.w, DEV_ERR_WAIT_MMA)); };
-    more = settle(ahead);
-    t_s = ahead.a;
-    auto await_keys = [&]() {
-      const int u = 2 * n_s;
-      if (t_s == ahead.a) wait(q_full + 8 * (NQ == 1 ? ahead.filled & 1 : 0), (NQ == 1 ? ahead.filled >> 1 : ahead.filled) & 1);
-      wait(kv_full + 8 * (u % F::STAGES), (u / F::STAGES) & 1);
-      tc_fence_after();
-    };
-    auto scores = [&](int q) {  // S = Q K^T
-      if (ok && elect_one()) {
-        const int slot = NQ == 2 ? q : n_s & 1;
-        const uint32_t qa = base + (NQ == 2 ? q : ahead.filled & 1) * F::TILE, ka = base + F::OFF_KV + ((2 * n_s) % F::STAGES) * F::TILE;
+    // One thread for all of it: with the whole warp walking along and electing a thread for each group of instructions, votes and
+    // convergence took some 1700 clocks of an item's 5000 (two tiles of 128 wide heads; 4380 so).
+    if (elect_one()) {
+      constexpr uint32_t kScores = idesc_bf16(128, 128, false), kValues = idesc_bf16(128, D, true);
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) { ok = mbar_wait(bar, parity, p.w, DEV_ERR_WAIT_MMA) && ok; };
+      // What the loop below needs of a segment, so that it touches the walks at a segment's end only.
+      struct Part {
+        int t, end, lo[NQ], hi[NQ], filled;
+        bool live;
+      };
+      auto part_of = [&](Walk<Sequences>& w, Part& x) {
+        while (w.live() && w.a >= w.b) w.next();
+        x.live = w.live();
+        if (!x.live) return;
+        x.t = w.a;
+        x.end = w.b;
+        x.filled = w.filled;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          mma_bf16(tmem + 128 * slot, smem_desc_sw128(qa + (i >> 2) * kPanel + (i & 3) * 32), smem_desc_sw128(ka + (i >> 2) * 1024 + (i & 3) * 32, F::GROUP, 16), kScores,
-                   i > 0);
+        for (int q = 0; q < NQ; ++q) {
+          const Keys r = w.part_of(q * p.tokens_per_tile, p.tokens_per_tile);
+          x.lo[q] = r.lo;
+          x.hi[q] = r.hi;
         }
+      };
+      Walk<Sequences> ahead = k;
+      Part s, v;  // the scores' place, one item ahead, and the values'
+      part_of(ahead, s);
+      part_of(k, v);
+      int k_stage = 0, v_stage = 1, s_slot = 0, v_slot = 0;
+      uint32_t k_phase = 0, v_phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      auto await_keys = [&]() {
+        if (s.t == ahead.a) {
+          const int buf = NQ == 1 ? s.filled & 1 : 0;
+          wait(q_full + 8 * buf, buf == 0 ? q_phase[0] : q_phase[1]);
+          if (buf == 0)
+            q_phase[0] ^= 1;
+          else
+            q_phase[1] ^= 1;
+        }
+        wait(kv_full + 8 * k_stage, k_phase);
+        tc_fence_after();
+      };
+      auto await_values = [&]() {
+        if (!MX) wait(v_fixed + 8 * v_stage, v_phase);
+        wait(kv_full + 8 * v_stage, v_phase);
+        tc_fence_after();
+      };
+      auto scores = [&](int q) {  // S = Q K^T
+        const int slot = NQ == 2 ? q : s_slot;
+        const uint64_t qd = smem_desc_sw128(base + (NQ == 2 ? q : s.filled & 1) * F::TILE);
+        const uint64_t kd = smem_desc_sw128(base + F::OFF_KV + k_stage * F::TILE, F::GROUP, 16);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) mma_bf16(tmem + 128 * slot, qd + (((i >> 2) * kPanel + (i & 3) * 32) >> 4), kd + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), kScores, i > 0);
         mma_commit(s_full + 8 * slot);
-      }
-      __syncwarp();
-    };
-    auto scores_done = [&]() {
-      if (ok && elect_one()) {
-        mma_commit(kv_empty + 8 * ((2 * n_s) % F::STAGES));
-        if (t_s + 1 == ahead.b) mma_commit(q_empty + 8 * (NQ == 1 ? ahead.filled & 1 : 0));
-      }
-      __syncwarp();
-      ++n_s;
-      if (++t_s == ahead.b) {
-        ahead.next();
-        more = settle(ahead);
-        t_s = ahead.a;
-      }
-    };
-    auto values = [&](int q, bool first) {  // O += P V
-      if (ok && elect_one()) {
-        const int slot = NQ == 2 ? q : n_v & 1;
-        const uint32_t va = base + F::OFF_KV + ((2 * n_v + 1) % F::STAGES) * F::TILE, o = tmem + 256 + 128 * q;
+      };
+      auto scores_done = [&]() {
+        const bool last = s.t + 1 == s.end;
+        mma_commit(kv_empty + 8 * k_stage);
+        k_stage += 2;
+        if (k_stage >= F::STAGES) {
+          k_stage -= F::STAGES;
+          k_phase ^= 1;
+        }
+        s_slot ^= 1;
+        ++s.t;
+        if (last) {
+          mma_commit(q_empty + 8 * (NQ == 1 ? s.filled & 1 : 0));
+          ahead.next();
+          part_of(ahead, s);
+        }
+      };
+      auto values = [&](int q, bool first) {  // O += P V
+        const int slot = NQ == 2 ? q : v_slot;
+        const uint64_t vd = smem_desc_sw128(base + F::OFF_KV + v_stage * F::TILE, F::GROUP, 1024);
+        const uint32_t weights = weights_at(slot), o = tmem + 256 + 128 * q, later = first ? 0u : 1u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights_at(slot) + 8 * i, smem_desc_sw128(va + 2 * i * F::GROUP, F::GROUP, 1024), kValues, !first || i > 0);
+        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights + 8 * i, vd + ((2 * i * F::GROUP) >> 4), kValues, i > 0 ? 1u : later);
         mma_commit(o_done + 8 * (NQ == 2 ? q : slot));
-      }
-      __syncwarp();
-    };
-    auto await_values = [&]() {
-      const int u = 2 * n_v + 1;
-      if (!MX) wait(v_fixed + 8 * (u % F::STAGES), (u / F::VALUES_EVERY) & 1);
-      wait(kv_full + 8 * (u % F::STAGES), (u / F::STAGES) & 1);
-      tc_fence_after();
-    };
-    if (more) {
-      await_keys();
+      };
+      auto values_done = [&]() {
+        mma_commit(kv_empty + 8 * v_stage);
+        v_stage += 2;
+        if (v_stage >= F::STAGES) {
+          v_stage -= F::STAGES;
+          v_phase ^= 1;
+        }
+        v_slot ^= 1;
+        if (++v.t == v.end) {
+          k.next();
+          part_of(k, v);
+        }
+      };
+      if (s.live) {
+        await_keys();
+        if (ok) {
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const Keys t = part(ahead, q);
-        if (t.lo <= t_s && t_s < t.hi) scores(q);
+          for (int q = 0; q < NQ; ++q)
+            if (s.lo[q] <= s.t && s.t < s.hi[q]) scores(q);
+          scores_done();
+        }
       }
-      scores_done();
-    }
-    for (; ok && settle(k); k.next()) {
-      Keys mine[NQ];
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) mine[q] = part(k, q);
-      for (int t = k.a; ok && t < k.b; ++t) {
-        bool have_values = false, have_keys = false;
-        const bool next = more;
+      while (ok && v.live) {
+        const bool next = s.live;
         if constexpr (NQ == 1) {
           if (next) {
             await_keys();
+            if (!ok) break;
             scores(0);
             scores_done();
           }
-          wait(p_ready + 8 * (n_v & 1), (n_v >> 1) & 1);
+          wait(p_ready + 8 * v_slot, v_slot == 0 ? p_phase[0] : p_phase[1]);
+          if (v_slot == 0)
+            p_phase[0] ^= 1;
+          else
+            p_phase[1] ^= 1;
           await_values();
-          values(0, t == mine[0].lo);
+          if (!ok) break;
+          values(0, v.t == v.lo[0]);
+          values_done();
         } else {
+          bool have_values = false, have_keys = false;
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            if (mine[q].lo <= t && t < mine[q].hi) {
-              wait(p_ready + 8 * q, seen_p[q]++ & 1);
-              if (!have_values) {
-                await_values();
-                have_values = true;
-              } else {
-                tc_fence_after();
-              }
-              values(q, t == mine[q].lo);
+            if (v.lo[q] <= v.t && v.t < v.hi[q]) {
+              if (!have_values) await_values();
+              have_values = true;
+              wait(p_ready + 8 * q, p_phase[q]);
+              p_phase[q] ^= 1;
+              tc_fence_after();
+              if (!ok) break;
+              values(q, v.t == v.lo[q]);
             }
-            if (next) {
-              const Keys s = part(ahead, q);
-              if (s.lo <= t_s && t_s < s.hi) {
-                if (!have_keys) {
-                  await_keys();
-                  have_keys = true;
-                }
-                scores(q);
-              }
+            if (next && s.lo[q] <= s.t && s.t < s.hi[q]) {
+              if (!have_keys) await_keys();
+              have_keys = true;
+              if (!ok) break;
+              scores(q);
             }
           }
+          if (ok && !have_values) await_values();
+          if (ok && next && !have_keys) await_keys();
+          if (!ok) break;
+          values_done();
+          if (next) scores_done();
         }
-        if (NQ == 2 && !have_values) await_values();
-        if (ok && elect_one()) mma_commit(kv_empty + 8 * ((2 * n_v + 1) % F::STAGES));
-        __syncwarp();
-        if (NQ == 2 && next) {
-          if (!have_keys) await_keys();
-          scores_done();
-        }
-        ++n_v;
       }
+      mma_commit(bar_final);
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar_final, 0))
+        if (globaltimer_ns() - t0 > 1000000000ull) {
+          atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
+          break;
+        }
     }
-    if (elect_one()) mma_commit(bar_final);
     __syncwarp();
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar_final, 0))
-      if (globaltimer_ns() - t0 > 1000000000ull) {
-        atomicOr(p.w.err, DEV_ERR_WAIT_TEARDOWN);
-        break;
-      }
   } else if (warp >= F::PREP_WARP && warp < 12) {
     // ---- keys and values on their way ----------------------------------------------------------------------------------
     // (one tile of rows: 8-bit keys in the first four warps, values in the others)
