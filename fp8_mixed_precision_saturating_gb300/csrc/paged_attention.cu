@@ -67,8 +67,8 @@ struct Form {
   static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
   static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 6 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int OFF_STATS = OFF_MISC + 256;  // SPREAD: (reference, sum) of each warp's rows
-  static constexpr int SMEM = OFF_STATS + (SPREAD ? 1024 : 0) + 1024;
+  static constexpr int OFF_STATS = OFF_MISC + 256;  // (reference, sum) of each row, SPREAD: of each warp's rows
+  static constexpr int SMEM = OFF_STATS + 1024 * NQ + 1024;
   // A wait names a phase by its parity, so whoever waits on a barrier has to see all of its phases. Where keys and values have
   // different waiters (the warps that look at bf16 values, the two groups that convert 8-bit tiles) a stage is always
   // one or the other's.
@@ -511,6 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = NQ == 2 ? q : v_slot;
         const uint64_t vd = smem_desc_sw128(base + F::OFF_KV + v_stage * F::TILE, F::GROUP, 1024);
         const uint32_t weights = weights_at(slot), o = tmem + 256 + 128 * q, later = first ? 0u : 1u;
+        wait(p_ready + 8 * slot, slot == 0 ? p_phase[0] : p_phase[1]);
+        if (slot == 0)
+          p_phase[0] ^= 1;
+        else
+          p_phase[1] ^= 1;
+        tc_fence_after();
+        if (!ok) return;
 #pragma unroll
         for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights + 8 * i, vd + ((2 * i * F::GROUP) >> 4), kValues, i > 0 ? 1u : later);
         mma_commit(o_done + 8 * (NQ == 2 ? q : slot));
@@ -546,14 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             scores(0);
             scores_done();
           }
-          wait(p_ready + 8 * v_slot, v_slot == 0 ? p_phase[0] : p_phase[1]);
-          if (v_slot == 0)
-            p_phase[0] ^= 1;
-          else
-            p_phase[1] ^= 1;
           await_values();
           if (!ok) break;
           values(0, v.t == v.lo[0]);
+          if (!ok) break;
           values_done();
         } else {
           bool have_values = false, have_keys = false;
@@ -562,11 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (v.lo[q] <= v.t && v.t < v.hi[q]) {
               if (!have_values) await_values();
               have_values = true;
-              wait(p_ready + 8 * q, p_phase[q]);
-              p_phase[q] ^= 1;
-              tc_fence_after();
               if (!ok) break;
               values(q, v.t == v.lo[q]);
+              if (!ok) break;
             }
             if (next && s.lo[q] <= s.t && s.t < s.hi[q]) {
               if (!have_keys) await_keys();
@@ -794,28 +795,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(w_at + from / 2, w);
           };
           uint32_t r0[32];
-          tmem_ld32(s_at, r0);
-          tmem_ld_wait();
-          reg_fence(r0);
           if constexpr (SPREAD) {
+            tmem_ld32(s_at, r0);
+            tmem_ld_wait();
+            reg_fence(r0);
             look(r0, 0);
             move_to();
             shift = both(m == -INFINITY ? 0.0f : -(m * c2));
             weigh(r0, 0);
           } else {
             uint32_t r1[32], r2[32], r3[32];
+            tmem_ld32(s_at, r0);
             tmem_ld32(s_at + 32, r1);
-            look(r0, 0);
             tmem_ld_wait();
+            reg_fence(r0);
             reg_fence(r1);
             tmem_ld32(s_at + 64, r2);
+            tmem_ld32(s_at + 96, r3);
+            look(r0, 0);
             look(r1, 32);
             tmem_ld_wait();
             reg_fence(r2);
-            tmem_ld32(s_at + 96, r3);
-            look(r2, 64);
-            tmem_ld_wait();
             reg_fence(r3);
+            look(r2, 64);
             look(r3, 96);
             move_to();
             shift = both(m == -INFINITY ? 0.0f : -(m * c2));
@@ -980,27 +982,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_sync(1 + q, 128);
         if (misc->last[q]) {
           __threadfence();
-          for (int x = threadIdx.x & 127; x < rows * (D / 4); x += 128) {
-            const int r = x / (D / 4), d = 4 * (x - r * (D / 4));
+          // first each row's reference and sum over the parts, then the rows' elements, 16 bytes a thread: several parts' loads at
+          // once where there are few rows and many parts, several rows' otherwise (one after the other an end took 50 us
+          // of two tiles' 256 rows)
+          float2* stats = reinterpret_cast<float2*>(smem + F::OFF_STATS) + 128 * q;
+          const int t = threadIdx.x & 127;
+          if (t < rows) {
             float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(part_at(c)) + r).x);
+#pragma unroll 8
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(part_at(c)) + t).x);
             if (top == -INFINITY) top = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
             for (int c = c0; c <= c1; ++c) {
-              const char* at = part_at(c);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(at) + r);
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(at + 1024 + (static_cast<int64_t>(r) * D + d) * 4));
-              const float w = exp2_of(ml.x - top);
-              if (ml.y != 0.0f) {  // (a part that saw nothing)
-                sum = fmaf(w, ml.y, sum);
-                o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
-              }
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_at(c)) + t);
+              sum = fmaf(exp2_of(ml.x - top), ml.y, sum);
             }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            *reinterpret_cast<uint2*>(out_at(r) + d) = sum == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
-            if (d == 0) set_lse(r, top, sum);
+            set_lse(t, top, sum);
+            stats[t] = make_float2(top, sum == 0.0f ? 0.0f : 1.0f / sum);
+          }
+          bar_sync(1 + q, 128);
+          const int all = rows * (D / 4);
+          auto add = [&](float4& o, const float2& ml, const float4& y, float top) {
+            const float w = exp2_of(ml.x - top);
+            if (ml.y != 0.0f) o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);  // (0: a part that saw nothing)
+          };
+          auto ml_at = [&](int c, int x) { return __ldcg(reinterpret_cast<const float2*>(part_at(c)) + x / (D / 4)); };
+          auto o_at_part = [&](int c, int x) { return __ldcg(reinterpret_cast<const float4*>(part_at(c) + 1024) + x); };
+          auto finish = [&](int x, const float4& o) {
+            const int r = x / (D / 4);
+            const float inv = stats[r].y;
+            *reinterpret_cast<uint2*>(out_at(r) + 4 * (x - r * (D / 4))) =
+                inv == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
+          };
+          if (all <= 512) {
+#pragma unroll 1
+            for (int x = t; x < all; x += 128) {
+              const float top = stats[x / (D / 4)].x;
+              float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+              for (int c = c0; c <= c1; ++c) add(o, ml_at(c, x), o_at_part(c, x), top);
+              finish(x, o);
+            }
+          } else {
+            constexpr int kBatch = 8;
+#pragma unroll 1
+            for (int x0 = t; x0 < all; x0 += 128 * kBatch) {
+              float4 o[kBatch] = {};
+#pragma unroll 1
+              for (int c = c0; c <= c1; ++c) {
+                float4 y[kBatch];
+                float2 ml[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                  ml[b] = ml_at(c, least(x0 + 128 * b, all - 1));
+                  y[b] = o_at_part(c, least(x0 + 128 * b, all - 1));
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) add(o[b], ml[b], y[b], stats[least(x0 + 128 * b, all - 1) / (D / 4)].x);
+              }
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b)
+                if (x0 + 128 * b < all) finish(x0 + 128 * b, o[b]);
+            }
           }
         }
       }
