@@ -43,12 +43,6 @@ constexpr int kCounterBytes = 4096;  // of the workspace: two counters per CTA
 constexpr int kMaxCtas = kCounterBytes / 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
-// Registers of the warpgroups where a thread holds a row's 128 scores; 512 threads are launched with 128 each.
-constexpr int kWeightRegs = 168, kCopyRegs = 96;
-template <int NQ>
-constexpr int kPrepRegs = NQ == 2 ? 80 : 120;
-static_assert(2 * kWeightRegs + kPrepRegs<2> + kCopyRegs <= 512 && kWeightRegs + 2 * kPrepRegs<1> + kCopyRegs <= 512, "registers");
-
 template <int D, bool MX, int NQ, bool SPREAD>
 struct Form {
   static constexpr int PANELS = D / 64;
@@ -65,7 +59,7 @@ struct Form {
   static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
   static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
   static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
-  static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 6 + 1;
+  static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 12 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int OFF_STATS = OFF_MISC + 256;  // (reference, sum) of each row, SPREAD: of each warp's rows
   static constexpr int SMEM = OFF_STATS + 1024 * NQ + 1024;
@@ -305,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Misc* misc = reinterpret_cast<Misc*>(smem + F::OFF_MISC);
   const uint32_t q_full = base + F::OFF_BAR, q_empty = q_full + 16, kv_full = q_empty + 16, kv_empty = kv_full + 8 * F::STAGES;
   const uint32_t raw_full = kv_empty + 8 * F::STAGES, raw_empty = raw_full + 8 * F::RAWS, s_full = raw_empty + 8 * F::RAWS;
-  const uint32_t p_ready = s_full + 16, o_done = p_ready + 16, v_fixed = o_done + 16, bar_final = v_fixed + 8 * F::STAGES;
+  const uint32_t p_ready = s_full + 32, o_done = p_ready + 32, v_fixed = o_done + 32, bar_final = v_fixed + 8 * F::STAGES;
   const int per = NQ * p.tokens_per_tile;
   const Sequences src{p.b, p.capacity, p.b.seqs};
 
@@ -313,6 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, SPREAD ? 2 : 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
@@ -349,15 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t total = misc->total;
   const int runs = misc->runs;
   Walk<Sequences> k(src, misc->start, p.c.heads, per, p.a.window);
-  auto weights_at = [&](int slot) { return tmem + (SPREAD ? 384 + 64 * slot : 128 * slot + 64); };
+  // Scores and weights in tensor memory. SPREAD: two tiles' scores in turn, their weights beside them. Otherwise a tile's scores in two
+  // halves of 64 keys (slot 2 q + half), each followed over itself by its weights: one half is on the tensor cores while the
+  // other's weights are worked out (with a tile's scores in one piece the tensor cores waited for half of the time).
+  auto scores_at = [&](int slot) { return tmem + (SPREAD ? 128 : 64) * slot; };
+  auto weights_at = [&](int slot) { return SPREAD ? tmem + 384 + 64 * slot : scores_at(slot) + 32; };
 
-  if constexpr (!SPREAD) {
-    if (warp >= 12) {
-      fewer_registers<kCopyRegs>();
-    } else if (warp >= 4 * NQ) {
-      fewer_registers<kPrepRegs<NQ>>();
-    }
-  }
   if (warp == 12) {
     // ---- copies ------------------------------------------------------------------------------------------------------
     const int rows = min(p.c.page_size, kTile);  // of a box
@@ -438,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One thread for all of it: with the whole warp walking along and electing a thread for each group of instructions, votes and
     // convergence took some 1700 clocks of an item's 5000 (two tiles of 128 wide heads; 4380 so).
     if (elect_one()) {
-      constexpr uint32_t kScores = idesc_bf16(128, 128, false), kValues = idesc_bf16(128, D, true);
+      constexpr uint32_t kScores = idesc_bf16(128, SPREAD ? 128 : 64, false), kValues = idesc_bf16(128, D, true);
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) { ok = mbar_wait(bar, parity, p.w, DEV_ERR_WAIT_MMA) && ok; };
       // What the loop below needs of a segment, so that it touches the walks at a segment's end only.
@@ -483,12 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(kv_full + 8 * v_stage, v_phase);
         tc_fence_after();
       };
-      auto scores = [&](int q) {  // S = Q K^T
-        const int slot = NQ == 2 ? q : s_slot;
+      auto scores = [&](int q, int half) {  // S = Q K^T
+        const int slot = SPREAD ? s_slot : 2 * q + half;
         const uint64_t qd = smem_desc_sw128(base + (NQ == 2 ? q : s.filled & 1) * F::TILE);
-        const uint64_t kd = smem_desc_sw128(base + F::OFF_KV + k_stage * F::TILE, F::GROUP, 16);
+        const uint64_t kd = smem_desc_sw128(base + F::OFF_KV + k_stage * F::TILE + half * 8 * F::GROUP, F::GROUP, 16);
+        const uint32_t to = scores_at(slot);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) mma_bf16(tmem + 128 * slot, qd + (((i >> 2) * kPanel + (i & 3) * 32) >> 4), kd + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), kScores, i > 0);
+        for (int i = 0; i < D / 16; ++i) mma_bf16(to, qd + (((i >> 2) * kPanel + (i & 3) * 32) >> 4), kd + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), kScores, i > 0);
         mma_commit(s_full + 8 * slot);
       };
       auto scores_done = [&]() {
@@ -507,20 +501,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           part_of(ahead, s);
         }
       };
-      auto values = [&](int q, bool first) {  // O += P V
-        const int slot = NQ == 2 ? q : v_slot;
-        const uint64_t vd = smem_desc_sw128(base + F::OFF_KV + v_stage * F::TILE, F::GROUP, 1024);
+      auto values = [&](int q, int half, uint32_t phase, bool first) {  // O += P V
+        constexpr int STEPS = SPREAD ? 8 : 4;  // of 16 keys
+        const int slot = SPREAD ? v_slot : 2 * q + half;
+        const uint64_t vd = smem_desc_sw128(base + F::OFF_KV + v_stage * F::TILE + half * 8 * F::GROUP, F::GROUP, 1024);
         const uint32_t weights = weights_at(slot), o = tmem + 256 + 128 * q, later = first ? 0u : 1u;
-        wait(p_ready + 8 * slot, slot == 0 ? p_phase[0] : p_phase[1]);
-        if (slot == 0)
-          p_phase[0] ^= 1;
-        else
-          p_phase[1] ^= 1;
+        wait(p_ready + 8 * slot, phase);
         tc_fence_after();
         if (!ok) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16_ts(o, weights + 8 * i, vd + ((2 * i * F::GROUP) >> 4), kValues, i > 0 ? 1u : later);
-        mma_commit(o_done + 8 * (NQ == 2 ? q : slot));
+        for (int i = 0; i < STEPS; ++i) mma_bf16_ts(o, weights + 8 * i, vd + ((2 * i * F::GROUP) >> 4), kValues, i > 0 ? 1u : later);
+        mma_commit(o_done + 8 * slot);
       };
       auto values_done = [&]() {
         mma_commit(kv_empty + 8 * v_stage);
@@ -539,46 +530,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         await_keys();
         if (ok) {
 #pragma unroll
-          for (int q = 0; q < NQ; ++q)
-            if (s.lo[q] <= s.t && s.t < s.hi[q]) scores(q);
+          for (int h = 0; h < (SPREAD ? 1 : 2); ++h)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+              if (s.lo[q] <= s.t && s.t < s.hi[q]) scores(q, h);
           scores_done();
         }
       }
       while (ok && v.live) {
         const bool next = s.live;
-        if constexpr (NQ == 1) {
+        if constexpr (SPREAD) {
           if (next) {
             await_keys();
             if (!ok) break;
-            scores(0);
+            scores(0, 0);
             scores_done();
           }
           await_values();
+          values(0, 0, v_slot == 0 ? p_phase[0] : p_phase[1], v.t == v.lo[0]);
           if (!ok) break;
-          values(0, v.t == v.lo[0]);
-          if (!ok) break;
+          if (v_slot == 0)
+            p_phase[0] ^= 1;
+          else
+            p_phase[1] ^= 1;
           values_done();
         } else {
-          bool have_values = false, have_keys = false;
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (v.lo[q] <= v.t && v.t < v.hi[q]) {
-              if (!have_values) await_values();
-              have_values = true;
-              if (!ok) break;
-              values(q, v.t == v.lo[q]);
-              if (!ok) break;
-            }
-            if (next && s.lo[q] <= s.t && s.t < s.hi[q]) {
-              if (!have_keys) await_keys();
-              have_keys = true;
-              if (!ok) break;
-              scores(q);
-            }
-          }
-          if (ok && !have_values) await_values();
-          if (ok && next && !have_keys) await_keys();
+          // a half's product with the values, then the next tile's scores over its weights: both in order on the tensor cores
+          await_values();
           if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              if (v.lo[q] <= v.t && v.t < v.hi[q]) values(q, h, p_phase[q], h == 0 && v.t == v.lo[q]);
+              if (h == 0 && q == 0 && ok && next) await_keys();
+              if (ok && next && s.lo[q] <= s.t && s.t < s.hi[q]) scores(q, h);
+            }
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+            if (v.lo[q] <= v.t && v.t < v.hi[q]) p_phase[q] ^= 1;
           values_done();
           if (next) scores_done();
         }
@@ -696,18 +687,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 4 * NQ) {
     // ---- weights: a thread per row; SPREAD: a thread per row and quarter of a tile's keys ------------------------------
-    if constexpr (!SPREAD) more_registers<kWeightRegs>();
     const int q = warp >> 2, row = SPREAD ? lane : threadIdx.x & 127, key0 = SPREAD ? 32 * warp : 0;
-    constexpr int KEYS = SPREAD ? 32 : kTile;  // of a tile, a thread's
+    constexpr int HALVES = SPREAD ? 1 : 2, KEYS = SPREAD ? 32 : 64;  // steps of a tile, a thread's keys of a step
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_at = tmem + lanes + 256 + 128 * q;
     const int token = row / p.group;
     const float c2 = p.c2, slack = fminf(kSlack / c2, 3.0e38f);
     bool ok = true;
     int n = 0;  // tiles of this warpgroup so far
-    // The last product with the values that this warpgroup has given weights to. One tile: two may be on their way when the last
-    // weights are written, so they report in turn to two barriers (of which neither can be a phase ahead of what is asked).
-    auto values_done = [&]() { return mbar_wait(o_done + 8 * (NQ == 2 ? q : (n - 1) & 1), (NQ == 2 ? n - 1 : (n - 1) >> 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE); };
+    // A step's slot, and its barriers' phase. When the scores of a step are there, the product with the values of the last step but one is
+    // done; of the last step's the barrier tells (the other of two, so that neither can be a phase ahead of what is asked).
+    auto slot_of = [&](int tile, int half) { return SPREAD ? tile & 1 : 2 * q + half; };
+    auto phase_of = [&](int tile) { return static_cast<uint32_t>(SPREAD ? tile >> 1 : tile) & 1u; };
+    auto values_done = [&](int tile, int half) { return mbar_wait(o_done + 8 * slot_of(tile, half), phase_of(tile), p.w, DEV_ERR_WAIT_EPILOGUE); };
     if constexpr (SPREAD) {  // the weights that this warp's copy of the rows gives to the other warps' keys
       uint32_t none[32];
 #pragma unroll
@@ -726,113 +718,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = __any_sync(0xFFFFFFFFu, valid);
       float m = -INFINITY, limit = -INFINITY, l = 0.0f;
       for (int t = part.lo; t < part.hi; ++t, ++n) {
-        const int slot = NQ == 2 ? q : n & 1;
-        const uint32_t s_at = tmem + lanes + 128 * slot + key0, w_at = weights_at(slot) + lanes + key0 / 2;
-        ok = ok && mbar_wait(s_full + 8 * slot, (NQ == 2 ? n : n >> 1) & 1, p.w, DEV_ERR_WAIT_EPILOGUE);
-        __syncwarp();
-        tc_fence_after();
-        if (any) {
-          const int c_lo = mine.lo - t * kTile - key0, c_hi = mine.hi - t * kTile - key0;
-          const bool whole = __all_sync(0xFFFFFFFFu, !valid || (c_lo <= 0 && c_hi >= KEYS));
-          const uint32_t width = static_cast<uint32_t>(most(c_hi - c_lo, 0));
-          float top = -INFINITY;
-          auto look = [&](uint32_t (&r)[32], int from) {  // what a thread does with 32 scores before it knows the tile's highest
-            if (p.flip)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] ^= 0x80000000u;
-            if (!whole) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (static_cast<uint32_t>(e + from - c_lo) >= width) r[e] = 0xFF800000u;
-            }
-            float x = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              x = max3(x, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-              top = max3(top, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
-            }
-            top = fmaxf(top, x);
-          };
-          auto move_to = [&]() {  // the reference, where it has to
-            const bool move = valid && top > limit;
-            if (!__any_sync(0xFFFFFFFFu, move)) return;
-            const float to = move ? top : m;
-            if (t > part.lo) {
-              const float f = move ? exp2_of((m - to) * c2) : 1.0f;
-              l *= f;
-              ok = ok && values_done();
-              __syncwarp();
-              tc_fence_after();
 #pragma unroll 1
-              for (int d = 0; d < D; d += 16) {
-                uint32_t x[16];
-                tmem_ld16(o_at + d, x);
-                tmem_ld_wait();
-                reg_fence(x);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                tmem_st16(o_at + d, x);
-              }
-            }
-            m = to;
-            if (move) limit = top + slack;
-          };
-          const uint64_t c = both(c2);
-          uint64_t shift = 0, sum0 = 0, sum1 = 0;
-          auto weigh = [&](uint32_t (&r)[32], int from) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = split(fma2(pair(r[2 * e], r[2 * e + 1]), c, shift));
-              const float a = exp2_of(x.x), b = exp2_of(x.y);
-              const uint64_t ab = pair(__float_as_uint(a), __float_as_uint(b));
-              if (e & 1)
-                sum1 = add2(sum1, ab);
-              else
-                sum0 = add2(sum0, ab);
-              w[e] = heads::pack(a, b);
-            }
-            tmem_st16(w_at + from / 2, w);
-          };
-          uint32_t r0[32];
-          if constexpr (SPREAD) {
+        for (int half = 0; half < HALVES; ++half) {
+          const int slot = slot_of(n, half);
+          const uint32_t s_at = scores_at(slot) + lanes + key0, w_at = weights_at(slot) + lanes + key0 / 2;
+          ok = ok && mbar_wait(s_full + 8 * slot, phase_of(n), p.w, DEV_ERR_WAIT_EPILOGUE);
+          __syncwarp();
+          tc_fence_after();
+          if (any) {
+            uint32_t r0[32], r1[32];
             tmem_ld32(s_at, r0);
-            tmem_ld_wait();
-            reg_fence(r0);
-            look(r0, 0);
-            move_to();
-            shift = both(m == -INFINITY ? 0.0f : -(m * c2));
-            weigh(r0, 0);
-          } else {
-            uint32_t r1[32], r2[32], r3[32];
-            tmem_ld32(s_at, r0);
-            tmem_ld32(s_at + 32, r1);
+            if constexpr (!SPREAD) tmem_ld32(s_at + 32, r1);
             tmem_ld_wait();
             reg_fence(r0);
             reg_fence(r1);
-            tmem_ld32(s_at + 64, r2);
-            tmem_ld32(s_at + 96, r3);
-            look(r0, 0);
-            look(r1, 32);
-            tmem_ld_wait();
-            reg_fence(r2);
-            reg_fence(r3);
-            look(r2, 64);
-            look(r3, 96);
-            move_to();
-            shift = both(m == -INFINITY ? 0.0f : -(m * c2));
-            weigh(r0, 0);
-            weigh(r1, 32);
-            weigh(r2, 64);
-            weigh(r3, 96);
+            const int key = t * kTile + 64 * half + key0;
+            if (p.flip || !__all_sync(0xFFFFFFFFu, !valid || (mine.lo <= key && key + KEYS <= mine.hi))) {
+              const int lo = mine.lo - key;
+              const uint32_t width = static_cast<uint32_t>(most(mine.hi - mine.lo, 0)), sign = p.flip ? 0x80000000u : 0u;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                r0[e] = static_cast<uint32_t>(e - lo) < width ? r0[e] ^ sign : 0xFF800000u;
+                if constexpr (!SPREAD) r1[e] = static_cast<uint32_t>(e + 32 - lo) < width ? r1[e] ^ sign : 0xFF800000u;
+              }
+            }
+            float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              top = max3(top, __uint_as_float(r0[e]), __uint_as_float(r0[e + 1]));
+              top1 = max3(top1, __uint_as_float(r0[e + 2]), __uint_as_float(r0[e + 3]));
+            }
+            if constexpr (!SPREAD) {
+              float top2 = -INFINITY, top3 = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                top2 = max3(top2, __uint_as_float(r1[e]), __uint_as_float(r1[e + 1]));
+                top3 = max3(top3, __uint_as_float(r1[e + 2]), __uint_as_float(r1[e + 3]));
+              }
+              top = max3(top, top2, top3);
+            }
+            top = fmaxf(top, top1);
+            const bool move = valid && top > limit;
+            if (__any_sync(0xFFFFFFFFu, move)) {  // the reference moves
+              const float to = move ? top : m;
+              if (t > part.lo || half > 0) {
+                const float f = move ? exp2_of((m - to) * c2) : 1.0f;
+                l *= f;
+                ok = ok && (half > 0 ? values_done(n, 0) : values_done(n - 1, HALVES - 1));
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll 1
+                for (int d = 0; d < D; d += 16) {
+                  uint32_t x[16];
+                  tmem_ld16(o_at + d, x);
+                  tmem_ld_wait();
+                  reg_fence(x);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                  tmem_st16(o_at + d, x);
+                }
+              }
+              m = to;
+              if (move) limit = top + slack;
+            }
+            const uint64_t c = both(c2), shift = both(m == -INFINITY ? 0.0f : -(m * c2));
+            uint64_t sum0 = 0, sum1 = 0;
+            auto weigh = [&](uint32_t (&r)[32], uint32_t at) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 x = split(fma2(pair(r[2 * e], r[2 * e + 1]), c, shift));
+                const float a = exp2_of(x.x), b = exp2_of(x.y);
+                const uint64_t ab = pair(__float_as_uint(a), __float_as_uint(b));
+                if (e & 1)
+                  sum1 = add2(sum1, ab);
+                else
+                  sum0 = add2(sum0, ab);
+                w[e] = heads::pack(a, b);
+              }
+              tmem_st16(at, w);
+            };
+            weigh(r0, w_at);
+            if constexpr (!SPREAD) weigh(r1, w_at + 16);
+            const float2 s = split(add2(sum0, sum1));
+            l += s.x + s.y;
+            tmem_st_wait();
           }
-          const float2 s = split(add2(sum0, sum1));
-          l += s.x + s.y;
-          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready + 8 * slot);
+          __syncwarp();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready + 8 * slot);
       }
       // ---- the unit's end, or this CTA's part's ------------------------------------------------------------------------
       const bool some = part.lo < part.hi, alone = k.first() && k.last();
@@ -866,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto add_unusual = [&](int d, float (&x)[8]) {  // what was taken out of the values that this thread's row sees
         for (int t = part.lo; t < part.hi; ++t) {
           if (!SPREAD && !k.edge(t)) continue;
-          for (int j = most(mine.lo, t * kTile + key0); j < least(mine.hi, t * kTile + key0 + KEYS); ++j) {
+          for (int j = most(mine.lo, t * kTile + key0); j < least(mine.hi, t * kTile + (SPREAD ? key0 + 32 : kTile)); ++j) {
             const int page = __ldg(p.b.page_table + k.at.seq * p.b.ld_table + (j >> p.c.page_bits));
             if (page < 0 || page >= p.c.pages) continue;
             const int at = j & (p.c.page_size - 1);
@@ -878,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (some && any) {
-        ok = ok && values_done();
+        ok = ok && values_done(n - 1, HALVES - 1);
         __syncwarp();
         tc_fence_after();
       }
