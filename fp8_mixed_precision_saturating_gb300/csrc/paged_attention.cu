@@ -433,11 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       constexpr uint32_t kScores = idesc_bf16(128, SPREAD ? 128 : 64, false), kValues = idesc_bf16(128, D, true);
       bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) { ok = mbar_wait(bar, parity, p.w, DEV_ERR_WAIT_MMA) && ok; };
-      // What the loop below needs of a segment, so that it touches the walks at a segment's end only.
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!mbar_try_wait(bar, parity)) ok = mbar_wait_on(bar, parity, p.w, DEV_ERR_WAIT_MMA) && ok;
+      };
+      // What the loop below needs of a segment, so that it touches the walks at a segment's end only. It is kept short: each of its
+      // instructions comes once per item, from wherever the other warps' code has left it.
       struct Part {
         int t, end, lo[NQ], hi[NQ], filled;
-        bool live;
+        bool live, fresh;
       };
       auto part_of = [&](Walk<Sequences>& w, Part& x) {
         while (w.live() && w.a >= w.b) w.next();
@@ -446,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.t = w.a;
         x.end = w.b;
         x.filled = w.filled;
+        x.fresh = true;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           const Keys r = w.part_of(q * p.tokens_per_tile, p.tokens_per_tile);
@@ -453,20 +457,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.hi[q] = r.hi;
         }
       };
+      // tiles of rows that need the item: a bit each
+      auto needs = [&](const Part& x) {
+        uint32_t r = x.lo[0] <= x.t && x.t < x.hi[0] ? 1u : 0u;
+        if (NQ == 2 && x.lo[NQ - 1] <= x.t && x.t < x.hi[NQ - 1]) r |= 2u;
+        return x.live ? r : 0u;
+      };
+      auto begins = [&](const Part& x) { return (x.t == x.lo[0] ? 1u : 0u) | (NQ == 2 && x.t == x.lo[NQ - 1] ? 2u : 0u); };
       Walk<Sequences> ahead = k;
       Part s, v;  // the scores' place, one item ahead, and the values'
       part_of(ahead, s);
       part_of(k, v);
-      int k_stage = 0, v_stage = 1, s_slot = 0, v_slot = 0;
-      uint32_t k_phase = 0, v_phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      int k_stage = 0, v_stage = 1;
+      uint32_t k_phase = 0, v_phase = 0, q_phase = 0, p_phase = 0, s_slot = 0, v_slot = 0;  // q_phase, p_phase: a bit per buffer, tile or slot
       auto await_keys = [&]() {
-        if (s.t == ahead.a) {
-          const int buf = NQ == 1 ? s.filled & 1 : 0;
-          wait(q_full + 8 * buf, buf == 0 ? q_phase[0] : q_phase[1]);
-          if (buf == 0)
-            q_phase[0] ^= 1;
-          else
-            q_phase[1] ^= 1;
+        if (s.fresh) {
+          const uint32_t buf = NQ == 1 ? s.filled & 1 : 0;
+          wait(q_full + 8 * buf, (q_phase >> buf) & 1u);
+          q_phase ^= 1u << buf;
+          s.fresh = false;
         }
         wait(kv_full + 8 * k_stage, k_phase);
         tc_fence_after();
@@ -476,35 +485,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(kv_full + 8 * v_stage, v_phase);
         tc_fence_after();
       };
+      const uint64_t q_desc = smem_desc_sw128(base), k_desc = smem_desc_sw128(base + F::OFF_KV, F::GROUP, 16), v_desc = smem_desc_sw128(base + F::OFF_KV, F::GROUP, 1024);
       auto scores = [&](int q, int half) {  // S = Q K^T
         const int slot = SPREAD ? s_slot : 2 * q + half;
-        const uint64_t qd = smem_desc_sw128(base + (NQ == 2 ? q : s.filled & 1) * F::TILE);
-        const uint64_t kd = smem_desc_sw128(base + F::OFF_KV + k_stage * F::TILE + half * 8 * F::GROUP, F::GROUP, 16);
+        const uint64_t qd = q_desc + (((NQ == 2 ? q : s.filled & 1) * F::TILE) >> 4), kd = k_desc + ((k_stage * F::TILE + half * 8 * F::GROUP) >> 4);
         const uint32_t to = scores_at(slot);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) mma_bf16(to, qd + (((i >> 2) * kPanel + (i & 3) * 32) >> 4), kd + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), kScores, i > 0);
         mma_commit(s_full + 8 * slot);
       };
-      auto scores_done = [&]() {
-        const bool last = s.t + 1 == s.end;
-        mma_commit(kv_empty + 8 * k_stage);
-        k_stage += 2;
-        if (k_stage >= F::STAGES) {
-          k_stage -= F::STAGES;
-          k_phase ^= 1;
-        }
-        s_slot ^= 1;
-        ++s.t;
-        if (last) {
-          mma_commit(q_empty + 8 * (NQ == 1 ? s.filled & 1 : 0));
-          ahead.next();
-          part_of(ahead, s);
-        }
-      };
       auto values = [&](int q, int half, uint32_t phase, bool first) {  // O += P V
         constexpr int STEPS = SPREAD ? 8 : 4;  // of 16 keys
         const int slot = SPREAD ? v_slot : 2 * q + half;
-        const uint64_t vd = smem_desc_sw128(base + F::OFF_KV + v_stage * F::TILE + half * 8 * F::GROUP, F::GROUP, 1024);
+        const uint64_t vd = v_desc + ((v_stage * F::TILE + half * 8 * F::GROUP) >> 4);
         const uint32_t weights = weights_at(slot), o = tmem + 256 + 128 * q, later = first ? 0u : 1u;
         wait(p_ready + 8 * slot, phase);
         tc_fence_after();
@@ -512,6 +505,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) mma_bf16_ts(o, weights + 8 * i, vd + ((2 * i * F::GROUP) >> 4), kValues, i > 0 ? 1u : later);
         mma_commit(o_done + 8 * slot);
+      };
+      auto scores_done = [&]() {
+        mma_commit(kv_empty + 8 * k_stage);
+        k_stage += 2;
+        if (k_stage >= F::STAGES) {
+          k_stage -= F::STAGES;
+          k_phase ^= 1;
+        }
+        s_slot ^= 1;
+        if (++s.t == s.end) {
+          mma_commit(q_empty + 8 * (NQ == 1 ? s.filled & 1 : 0));
+          ahead.next();
+          part_of(ahead, s);
+        }
       };
       auto values_done = [&]() {
         mma_commit(kv_empty + 8 * v_stage);
@@ -526,53 +533,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           part_of(k, v);
         }
       };
-      if (s.live) {
-        await_keys();
-        if (ok) {
-#pragma unroll
-          for (int h = 0; h < (SPREAD ? 1 : 2); ++h)
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-              if (s.lo[q] <= s.t && s.t < s.hi[q]) scores(q, h);
-          scores_done();
-        }
-      }
-      while (ok && v.live) {
-        const bool next = s.live;
-        if constexpr (SPREAD) {
-          if (next) {
+      // Item by item; the first turn has scores only. Not SPREAD: each half's product with the values, then the next tile's scores
+      // over its weights, both in order on the tensor cores. SPREAD: the next tile's scores first, they have a place of their own.
+      bool started = false;
+      while (ok && (v.live || s.live)) {
+        const uint32_t v_needs = started ? needs(v) : 0u, s_needs = needs(s), v_first = begins(v);
+        const bool v_turn = started, s_turn = s.live;
+        if (SPREAD) {
+          if (s_turn) {
             await_keys();
             if (!ok) break;
             scores(0, 0);
             scores_done();
           }
-          await_values();
-          values(0, 0, v_slot == 0 ? p_phase[0] : p_phase[1], v.t == v.lo[0]);
-          if (!ok) break;
-          if (v_slot == 0)
-            p_phase[0] ^= 1;
-          else
-            p_phase[1] ^= 1;
-          values_done();
+          if (v_turn) {
+            await_values();
+            values(0, 0, (p_phase >> v_slot) & 1u, v_first & 1u);
+            if (!ok) break;
+            p_phase ^= 1u << v_slot;
+            values_done();
+          }
         } else {
-          // a half's product with the values, then the next tile's scores over its weights: both in order on the tensor cores
-          await_values();
+          if (v_turn) await_values();
+#pragma unroll 1
+          for (int x = 0; x < 2 * NQ; ++x) {
+            const int q = NQ == 2 ? x & 1 : 0, half = NQ == 2 ? x >> 1 : x;
+            if (ok && (v_needs >> q) & 1u) values(q, half, (p_phase >> q) & 1u, half == 0 && (v_first >> q) & 1u);
+            if (x == 0 && s_turn && ok) await_keys();
+            if (ok && (s_needs >> q) & 1u) scores(q, half);
+          }
           if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              if (v.lo[q] <= v.t && v.t < v.hi[q]) values(q, h, p_phase[q], h == 0 && v.t == v.lo[q]);
-              if (h == 0 && q == 0 && ok && next) await_keys();
-              if (ok && next && s.lo[q] <= s.t && s.t < s.hi[q]) scores(q, h);
-            }
-          if (!ok) break;
-#pragma unroll
-          for (int q = 0; q < NQ; ++q)
-            if (v.lo[q] <= v.t && v.t < v.hi[q]) p_phase[q] ^= 1;
-          values_done();
-          if (next) scores_done();
+          if (v_turn) {
+            p_phase ^= v_needs;
+            values_done();
+          }
+          if (s_turn) scores_done();
         }
+        started = true;
       }
       mma_commit(bar_final);
       const unsigned long long t0 = globaltimer_ns();

@@ -118,6 +118,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
   }
 }
 
+// The same out of line, for code whose length counts: after a try that found the phase not complete.
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, const WaitCtl w, uint32_t code) {
+  return mbar_wait(bar, parity, w, code);
+}
+
 // ---------------------------------------------------------------------------------------
 // TMA
 // ---------------------------------------------------------------------------------------
