@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
-      mbar_init(q_empty + 8 * i, SPREAD ? 2 : 1);
+      mbar_init(q_empty + 8 * i, SPREAD ? 2 : NQ);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -315,14 +315,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < F::STAGES; ++i) {
       mbar_init(kv_full + 8 * i, MX ? 4 : 1);
-      mbar_init(kv_empty + 8 * i, 1);
+      mbar_init(kv_empty + 8 * i, NQ);
       mbar_init(v_fixed + 8 * i, F::PREP_WARPS);
     }
     for (int i = 0; i < F::RAWS; ++i) {
       mbar_init(raw_full + 8 * i, 1);
       mbar_init(raw_empty + 8 * i, 4);
     }
-    mbar_init(bar_final, 1);
+    mbar_init(bar_final, NQ);
     fence_mbar_init();
     for (int i = 0; i < 16; ++i) misc->dirty[i] = -1;
     tma_prefetch_desc(&tm_q);
@@ -426,10 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (globaltimer_ns() - t0 < 200000ull) {
       }
     }
-  } else if (warp == 13) {
+  } else if (warp >= 13 && warp < 13 + NQ) {
     // ---- tensor-core instructions --------------------------------------------------------------------------------------
-    // One thread for all of it: with the whole warp walking along and electing a thread for each group of instructions, votes and
+    // One thread for each tile of rows: with the whole warp walking along and electing a thread for each group of instructions, votes and
     // convergence took some 1700 clocks of an item's 5000 (two tiles of 128 wide heads; 4380 so).
+    const int q = warp - 13;
     if (elect_one()) {
       constexpr uint32_t kScores = idesc_bf16(128, SPREAD ? 128 : 64, false), kValues = idesc_bf16(128, D, true);
       bool ok = true;
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // What the loop below needs of a segment, so that it touches the walks at a segment's end only. It is kept short: each of its
       // instructions comes once per item, from wherever the other warps' code has left it.
       struct Part {
-        int t, end, lo[NQ], hi[NQ], filled;
+        int t, end, lo, hi, filled;  // lo .. hi - 1: what the tile of rows needs
         bool live, fresh;
       };
       auto part_of = [&](Walk<Sequences>& w, Part& x) {
@@ -450,26 +451,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.end = w.b;
         x.filled = w.filled;
         x.fresh = true;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const Keys r = w.part_of(q * p.tokens_per_tile, p.tokens_per_tile);
-          x.lo[q] = r.lo;
-          x.hi[q] = r.hi;
-        }
+        const Keys r = w.part_of(q * p.tokens_per_tile, p.tokens_per_tile);
+        x.lo = r.lo;
+        x.hi = r.hi;
       };
-      // tiles of rows that need the item: a bit each
-      auto needs = [&](const Part& x) {
-        uint32_t r = x.lo[0] <= x.t && x.t < x.hi[0] ? 1u : 0u;
-        if (NQ == 2 && x.lo[NQ - 1] <= x.t && x.t < x.hi[NQ - 1]) r |= 2u;
-        return x.live ? r : 0u;
-      };
-      auto begins = [&](const Part& x) { return (x.t == x.lo[0] ? 1u : 0u) | (NQ == 2 && x.t == x.lo[NQ - 1] ? 2u : 0u); };
       Walk<Sequences> ahead = k;
       Part s, v;  // the scores' place, one item ahead, and the values'
       part_of(ahead, s);
       part_of(k, v);
       int k_stage = 0, v_stage = 1;
-      uint32_t k_phase = 0, v_phase = 0, q_phase = 0, p_phase = 0, s_slot = 0, v_slot = 0;  // q_phase, p_phase: a bit per buffer, tile or slot
+      uint32_t k_phase = 0, v_phase = 0, q_phase = 0, p_phase = 0, s_slot = 0, v_slot = 0;  // q_phase, p_phase: a bit per buffer or slot
       auto await_keys = [&]() {
         if (s.fresh) {
           const uint32_t buf = NQ == 1 ? s.filled & 1 : 0;
@@ -486,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       };
       const uint64_t q_desc = smem_desc_sw128(base), k_desc = smem_desc_sw128(base + F::OFF_KV, F::GROUP, 16), v_desc = smem_desc_sw128(base + F::OFF_KV, F::GROUP, 1024);
-      auto scores = [&](int q, int half) {  // S = Q K^T
+      auto scores = [&](int half) {  // S = Q K^T
         const int slot = SPREAD ? s_slot : 2 * q + half;
         const uint64_t qd = q_desc + (((NQ == 2 ? q : s.filled & 1) * F::TILE) >> 4), kd = k_desc + ((k_stage * F::TILE + half * 8 * F::GROUP) >> 4);
         const uint32_t to = scores_at(slot);
@@ -494,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < D / 16; ++i) mma_bf16(to, qd + (((i >> 2) * kPanel + (i & 3) * 32) >> 4), kd + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), kScores, i > 0);
         mma_commit(s_full + 8 * slot);
       };
-      auto values = [&](int q, int half, uint32_t phase, bool first) {  // O += P V
+      auto values = [&](int half, uint32_t phase, bool first) {  // O += P V
         constexpr int STEPS = SPREAD ? 8 : 4;  // of 16 keys
         const int slot = SPREAD ? v_slot : 2 * q + half;
         const uint64_t vd = v_desc + ((v_stage * F::TILE + half * 8 * F::GROUP) >> 4);
@@ -537,18 +528,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // over its weights, both in order on the tensor cores. SPREAD: the next tile's scores first, they have a place of their own.
       bool started = false;
       while (ok && (v.live || s.live)) {
-        const uint32_t v_needs = started ? needs(v) : 0u, s_needs = needs(s), v_first = begins(v);
-        const bool v_turn = started, s_turn = s.live;
+        const bool v_turn = started, s_turn = s.live, v_needs = v_turn && v.lo <= v.t && v.t < v.hi, s_needs = s_turn && s.lo <= s.t && s.t < s.hi;
         if (SPREAD) {
           if (s_turn) {
             await_keys();
             if (!ok) break;
-            scores(0, 0);
+            scores(0);
             scores_done();
           }
           if (v_turn) {
             await_values();
-            values(0, 0, (p_phase >> v_slot) & 1u, v_first & 1u);
+            values(0, (p_phase >> v_slot) & 1u, v.t == v.lo);
             if (!ok) break;
             p_phase ^= 1u << v_slot;
             values_done();
@@ -556,15 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           if (v_turn) await_values();
 #pragma unroll 1
-          for (int x = 0; x < 2 * NQ; ++x) {
-            const int q = NQ == 2 ? x & 1 : 0, half = NQ == 2 ? x >> 1 : x;
-            if (ok && (v_needs >> q) & 1u) values(q, half, (p_phase >> q) & 1u, half == 0 && (v_first >> q) & 1u);
-            if (x == 0 && s_turn && ok) await_keys();
-            if (ok && (s_needs >> q) & 1u) scores(q, half);
+          for (int half = 0; half < 2; ++half) {
+            if (ok && v_needs) values(half, p_phase, half == 0 && v.t == v.lo);
+            if (half == 0 && s_turn && ok) await_keys();
+            if (ok && s_needs) scores(half);
           }
           if (!ok) break;
           if (v_turn) {
-            p_phase ^= v_needs;
+            p_phase ^= v_needs ? 1u : 0u;
             values_done();
           }
           if (s_turn) scores_done();
