@@ -11,7 +11,9 @@
 // lane l holding elements l + 32 i, partners read through shared memory.
 //
 // Angles. p * turns[i] modulo 2^64 is the angle as a fraction of a turn with nothing lost; its top 32 bits are split into a quarter
-// turn and a rest within an eighth of a turn either way, whose sine and cosine are taken in fp32 (rest exact to 2^-33 turns).
+// turn and a rest x within an eighth of a turn either way (exact to 2^-33 turns), whose sine and cosine are their Taylor series up to x^9
+// and x^10: what is left out is below 2 10^-9 and 2 10^-10, fp32 rounds at 3 10^-8. The groups of lanes that hold different rows at
+// once share a token's angles: each works out its part of the four and they exchange them.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -19,23 +21,26 @@
 #include <cstdint>
 
 #include "kernels.h"
+#include "norm.cuh"
 
 namespace fp8gb {
 namespace heads {
 
 using bf16 = __nv_bfloat16;
+using norms::add2, norms::both, norms::fma2, norms::mul2, norms::pack2, norms::pair, norms::Pair, norms::pair_of, norms::split, norms::sum2;
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int32_t pos) {
   const uint32_t a = static_cast<uint32_t>((turns * static_cast<uint64_t>(static_cast<int64_t>(pos))) >> 32);
   const uint32_t quarter = (a + (1u << 29)) >> 30;
-  const float r = static_cast<float>(static_cast<int32_t>(a - (quarter << 30))) * 0x1p-31f;  // half turns
-  float s, c;
-  sincospif(r, &s, &c);
+  const float x = static_cast<float>(static_cast<int32_t>(a - (quarter << 30))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float q = x * x;
+  const float s = fmaf(x * q, fmaf(q, fmaf(q, fmaf(q, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  const float c = fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
   const bool odd = quarter & 1u;
-  float x = odd ? s : c, y = odd ? c : s;
-  if ((quarter + 1u) & 2u) x = -x;
-  if (quarter & 2u) y = -y;
-  return make_float2(x, y);
+  float u = odd ? s : c, v = odd ? c : s;
+  if ((quarter + 1u) & 2u) u = -u;
+  if (quarter & 2u) v = -v;
+  return make_float2(u, v);
 }
 
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
@@ -46,7 +51,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return r;
 }
 
-// A lane's 8 elements as they are in memory, and as the members u, v of 4 pairs.
+// A lane's 8 elements as they are in memory, and as the members u, v of 4 pairs, two pairs to a register pair.
 template <typename T, bool INTER>
 struct Raw;
 template <>
@@ -56,25 +61,26 @@ struct Raw<bf16, false> {
     a = __ldcs(reinterpret_cast<const uint2*>(p + o0));
     b = __ldcs(reinterpret_cast<const uint2*>(p + o1));
   }
-  __device__ __forceinline__ void get(float (&u)[4], float (&v)[4]) const {
-    u[0] = lo_of(a.x), u[1] = hi_of(a.x), u[2] = lo_of(a.y), u[3] = hi_of(a.y);
-    v[0] = lo_of(b.x), v[1] = hi_of(b.x), v[2] = lo_of(b.y), v[3] = hi_of(b.y);
+  __device__ __forceinline__ void get(Pair (&u)[2], Pair (&v)[2]) const {
+    u[0] = pair_of(a.x), u[1] = pair_of(a.y);
+    v[0] = pair_of(b.x), v[1] = pair_of(b.y);
   }
-  static __device__ __forceinline__ void put(bf16* p, int o0, int o1, const float (&u)[4], const float (&v)[4]) {
-    __stcs(reinterpret_cast<uint2*>(p + o0), make_uint2(pack(u[0], u[1]), pack(u[2], u[3])));
-    __stcs(reinterpret_cast<uint2*>(p + o1), make_uint2(pack(v[0], v[1]), pack(v[2], v[3])));
+  static __device__ __forceinline__ void put(bf16* p, int o0, int o1, const Pair (&u)[2], const Pair (&v)[2]) {
+    __stcs(reinterpret_cast<uint2*>(p + o0), make_uint2(pack2(u[0]), pack2(u[1])));
+    __stcs(reinterpret_cast<uint2*>(p + o1), make_uint2(pack2(v[0]), pack2(v[1])));
   }
 };
 template <>
 struct Raw<bf16, true> {
   uint4 a;
   __device__ __forceinline__ void load(const bf16* p, int o0, int) { a = __ldcs(reinterpret_cast<const uint4*>(p + o0)); }
-  __device__ __forceinline__ void get(float (&u)[4], float (&v)[4]) const {
-    u[0] = lo_of(a.x), u[1] = lo_of(a.y), u[2] = lo_of(a.z), u[3] = lo_of(a.w);
-    v[0] = hi_of(a.x), v[1] = hi_of(a.y), v[2] = hi_of(a.z), v[3] = hi_of(a.w);
+  __device__ __forceinline__ void get(Pair (&u)[2], Pair (&v)[2]) const {
+    u[0] = pair(lo_of(a.x), lo_of(a.y)), u[1] = pair(lo_of(a.z), lo_of(a.w));
+    v[0] = pair(hi_of(a.x), hi_of(a.y)), v[1] = pair(hi_of(a.z), hi_of(a.w));
   }
-  static __device__ __forceinline__ void put(bf16* p, int o0, int, const float (&u)[4], const float (&v)[4]) {
-    __stcs(reinterpret_cast<uint4*>(p + o0), make_uint4(pack(u[0], v[0]), pack(u[1], v[1]), pack(u[2], v[2]), pack(u[3], v[3])));
+  static __device__ __forceinline__ void put(bf16* p, int o0, int, const Pair (&u)[2], const Pair (&v)[2]) {
+    const float2 u0 = split(u[0]), u1 = split(u[1]), v0 = split(v[0]), v1 = split(v[1]);
+    __stcs(reinterpret_cast<uint4*>(p + o0), make_uint4(pack(u0.x, v0.x), pack(u0.y, v0.y), pack(u1.x, v1.x), pack(u1.y, v1.y)));
   }
 };
 template <bool INTER>
@@ -84,33 +90,35 @@ struct Raw<float, INTER> {
     a = __ldcs(reinterpret_cast<const float4*>(p + o0));
     b = __ldcs(reinterpret_cast<const float4*>(p + o1));
   }
-  __device__ __forceinline__ void get(float (&u)[4], float (&v)[4]) const {
+  __device__ __forceinline__ void get(Pair (&u)[2], Pair (&v)[2]) const {
     if constexpr (INTER) {
-      u[0] = a.x, u[1] = a.z, u[2] = b.x, u[3] = b.z;
-      v[0] = a.y, v[1] = a.w, v[2] = b.y, v[3] = b.w;
+      u[0] = pair(a.x, a.z), u[1] = pair(b.x, b.z);
+      v[0] = pair(a.y, a.w), v[1] = pair(b.y, b.w);
     } else {
-      u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
-      v[0] = b.x, v[1] = b.y, v[2] = b.z, v[3] = b.w;
+      u[0] = pair(a.x, a.y), u[1] = pair(a.z, a.w);
+      v[0] = pair(b.x, b.y), v[1] = pair(b.z, b.w);
     }
   }
-  static __device__ __forceinline__ void put(float* p, int o0, int o1, const float (&u)[4], const float (&v)[4]) {
-    if constexpr (INTER) {
-      __stcs(reinterpret_cast<float4*>(p + o0), make_float4(u[0], v[0], u[1], v[1]));
-      __stcs(reinterpret_cast<float4*>(p + o1), make_float4(u[2], v[2], u[3], v[3]));
-    } else {
-      __stcs(reinterpret_cast<float4*>(p + o0), make_float4(u[0], u[1], u[2], u[3]));
-      __stcs(reinterpret_cast<float4*>(p + o1), make_float4(v[0], v[1], v[2], v[3]));
-    }
+  static __device__ __forceinline__ void arrange(const Pair (&u)[2], const Pair (&v)[2], float4& x, float4& y) {
+    const float2 u0 = split(u[0]), u1 = split(u[1]), v0 = split(v[0]), v1 = split(v[1]);
+    x = INTER ? make_float4(u0.x, v0.x, u0.y, v0.y) : make_float4(u0.x, u0.y, u1.x, u1.y);
+    y = INTER ? make_float4(u1.x, v1.x, u1.y, v1.y) : make_float4(v0.x, v0.y, v1.x, v1.y);
+  }
+  static __device__ __forceinline__ void put(float* p, int o0, int o1, const Pair (&u)[2], const Pair (&v)[2]) {
+    float4 x, y;
+    arrange(u, v, x, y);
+    __stcs(reinterpret_cast<float4*>(p + o0), x);
+    __stcs(reinterpret_cast<float4*>(p + o1), y);
   }
 };
 
 // The same into a row of fp32 in shared memory (put's stores are for global memory alone).
 template <bool INTER>
-__device__ __forceinline__ void put_shared(float* p, int o0, int o1, const float (&u)[4], const float (&v)[4]) {
-  float4* a = reinterpret_cast<float4*>(p + o0);
-  float4* b = reinterpret_cast<float4*>(p + o1);
-  *a = INTER ? make_float4(u[0], v[0], u[1], v[1]) : make_float4(u[0], u[1], u[2], u[3]);
-  *b = INTER ? make_float4(u[2], v[2], u[3], v[3]) : make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void put_shared(float* p, int o0, int o1, const Pair (&u)[2], const Pair (&v)[2]) {
+  float4 x, y;
+  Raw<float, INTER>::arrange(u, v, x, y);
+  *reinterpret_cast<float4*>(p + o0) = x;
+  *reinterpret_cast<float4*>(p + o1) = y;
 }
 
 // Where a lane's chunks begin, and its four angles (cos 1, sin 0 where nothing turns).
@@ -139,16 +147,25 @@ __device__ __forceinline__ Lane lane_of(int l, int dim, int rot) {
   return a;
 }
 
+template <int LPR>
 __device__ __forceinline__ void angles(const Lane& a, const uint64_t* turns, int rot, int32_t pos, float amplitude, float (&c)[4], float (&s)[4]) {
+  constexpr int RPW = 32 / LPR, MINE = 4 / RPW;  // (rows of 8 lanes and more: at most 4 groups)
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  float2 mine[MINE];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (2 * (a.pair + i) < rot) {
-      const float2 t = cos_sin(__ldg(turns + a.pair + i), pos);
-      c[i] = t.x * amplitude;
-      s[i] = t.y * amplitude;
+  for (int j = 0; j < MINE; ++j) {
+    const int pair = a.pair + j * RPW + sub;
+    mine[j] = make_float2(1.0f, 0.0f);
+    if (2 * pair < rot) {
+      mine[j] = cos_sin(__ldg(turns + pair), pos);
+      mine[j].x *= amplitude;
+      mine[j].y *= amplitude;
     }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    c[k] = __shfl_sync(0xFFFFFFFFu, mine[k / RPW].x, (k % RPW) * LPR + l);
+    s[k] = __shfl_sync(0xFFFFFFFFu, mine[k / RPW].y, (k % RPW) * LPR + l);
   }
 }
 
@@ -165,11 +182,43 @@ __device__ __forceinline__ void weights(const Lane& a, const float* w, float (&w
   }
 }
 
+// What the forward multiplies a pair's members with: y_u = r (u uc + v nvs), y_v = r (u us + v vc), r the row's 1 / root.
+struct Factors {
+  Pair uc[2], us[2], vc[2], nvs[2];
+};
+__device__ __forceinline__ Factors factors(const float (&c)[4], const float (&s)[4], const float (&wu)[4], const float (&wv)[4]) {
+  Factors f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Pair pc = pair(c[2 * k], c[2 * k + 1]), ps = pair(s[2 * k], s[2 * k + 1]), pu = pair(wu[2 * k], wu[2 * k + 1]), pv = pair(wv[2 * k], wv[2 * k + 1]);
+    f.uc[k] = mul2(pu, pc);
+    f.us[k] = mul2(pu, ps);
+    f.vc[k] = mul2(pv, pc);
+    f.nvs[k] = mul2(mul2(pv, ps), both(-1.0f));
+  }
+  return f;
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
   for (int m = LPR / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
   return x;
+}
+
+template <int LPR, bool NORM>
+__device__ __forceinline__ void turn(const Factors& f, float inv_dim, float eps, const Pair (&u)[2], const Pair (&v)[2], Pair (&yu)[2], Pair (&yv)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    yu[k] = fma2(u[k], f.uc[k], mul2(v[k], f.nvs[k]));
+    yv[k] = fma2(u[k], f.us[k], mul2(v[k], f.vc[k]));
+  }
+  if constexpr (NORM) {
+    const float q = sum2(fma2(u[0], u[0], fma2(u[1], u[1], fma2(v[0], v[0], mul2(v[1], v[1])))));
+    const Pair r = both(rsqrtf(fmaf(row_sum<LPR>(q), inv_dim, eps)));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) yu[k] = mul2(yu[k], r), yv[k] = mul2(yv[k], r);
+  }
 }
 
 __device__ __forceinline__ float element(const bf16* p) { return __bfloat162float(*p); }

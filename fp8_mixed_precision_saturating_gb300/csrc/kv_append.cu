@@ -79,7 +79,7 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(int64_t i, const Args& g) {
   Item m;
-  m.token = i / g.items;
+  m.token = g.items == 1 ? i : i >> 32 == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(g.items) : i / g.items;
   const int j = static_cast<int>(i - m.token * g.items);
   m.part = j >= g.first[2] ? 2 : j >= g.first[1] ? 1 : 0;
   m.h0 = (j - g.first[m.part]) * g.per;
@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_mx(const float (&x)[8], bool live, int d, 
 }
 
 template <bool INTER, int LPR, bool MX>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_constant__ Args g) {
   constexpr int RPW = 32 / LPR, U = 4;
   // keys on their way into 8 bits: a warp's rows, turned, to be read 8 consecutive elements a lane
   __shared__ __align__(16) float share[MX ? kWarps : 1][MX ? RPW : 1][MX ? LPR * 8 : 4];
@@ -152,13 +152,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     }
     return;
   }
-  Raw<bf16, INTER> raw[U];
+  // (lanes past the head hold zeros; a row past the last one is the last one again, and not stored)
+  Raw<bf16, INTER> raw[U], next[U] = {};
   auto load = [&](int h0) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int h = h0 + j * RPW + sub;
-      if (a.in && h < m.h1) raw[j].load(in + h * p.hs_in, a.o0, a.o1);
-    }
+    for (int j = 0; j < U; ++j)
+      if (a.in) next[j].load(in + min(h0 + j * RPW + sub, m.h1 - 1) * p.hs_in, a.o0, a.o1);
   };
   load(m.h0);
   const Place where = place_of(m.token, g.b, lane);
@@ -166,33 +165,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   if (where.seq < 0 || (m.part == 1 && !at.in)) return;  // a row of nobody; a key without a place
   const int32_t pos = g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(where.pos);
   float c[4], s[4], wu[4], wv[4];
-  angles(a, g.t.turns, g.t.rot_dims, pos, g.t.amplitude, c, s);
+  angles<LPR>(a, g.t.turns, g.t.rot_dims, pos, g.t.amplitude, c, s);
   weights<INTER>(a, p.w, wu, wv);
-  float uc[4], us[4], vc[4], vs[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) uc[k] = wu[k] * c[k], us[k] = wu[k] * s[k], vc[k] = wv[k] * c[k], vs[k] = wv[k] * s[k];
+  const Factors f = factors(c, s, wu, wv);
   const float inv_dim = 1.0f / static_cast<float>(g.t.head_dim);
   bf16* out = m.part == 0 ? static_cast<bf16*>(p.out) + m.token * p.ld_out : nullptr;
 #pragma unroll 1
   for (int h0 = m.h0; h0 < m.h1; h0 += U * RPW) {
 #pragma unroll
+    for (int j = 0; j < U; ++j) raw[j] = next[j];
+    if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
+#pragma unroll
     for (int j = 0; j < U; ++j) {
-      float u[4] = {}, v[4] = {}, yu[4], yv[4];
+      Pair u[2], v[2], yu[2], yv[2];
       const int h = h0 + j * RPW + sub;
       const bool live = a.in && h < m.h1;
-      if (live) raw[j].get(u, v);
-      float r = 1.0f;
-      if (g.t.norm) {
-        float q = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
-        r = rsqrtf(fmaf(row_sum<LPR>(q), inv_dim, g.t.eps));
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        yu[k] = r * fmaf(u[k], uc[k], -(v[k] * vs[k]));
-        yv[k] = r * fmaf(u[k], us[k], v[k] * vc[k]);
-      }
+      raw[j].get(u, v);
+      if (g.t.norm)
+        turn<LPR, true>(f, inv_dim, g.t.eps, u, v, yu, yv);
+      else
+        turn<LPR, false>(f, inv_dim, g.t.eps, u, v, yu, yv);
       if (m.part == 0) {
         if (live) Raw<bf16, INTER>::put(out + h * p.hs_out, a.o0, a.o1, yu, yv);
       } else if constexpr (MX) {
@@ -210,7 +202,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         Raw<bf16, INTER>::put(static_cast<bf16*>(g.c.k) + row_at(at, g.c, h), a.o0, a.o1, yu, yv);
       }
     }
-    if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
   }
 }
 

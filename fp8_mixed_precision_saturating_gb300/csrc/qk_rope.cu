@@ -4,7 +4,8 @@
 // What bounds it: memory. Forward reads and writes each element once; backward reads the gradient and, with a norm, the
 // input, and writes one gradient. A token's angles are worked out once per item (a token and a run of its heads)
 // and serve all its rows; a lane's norm weight, angle and amplitude are one factor per member of a pair
-//   y_u = r (u uc - v vs),  y_v = r (u us + v vc),   uc = w_u cos a, us = w_u sin a, vs = w_v sin a, vc = w_v cos a.
+//   y_u = r (u uc - v vs),  y_v = r (u us + v vc),   uc = w_u cos a, us = w_u sin a, vs = w_v sin a, vc = w_v cos a,
+// and the arithmetic works on two pairs at once (fp32x2).
 // Backward: with (du, dv) the incoming pair turned back, z = x r, dz = w d:
 //   dx = r (dz - z mean(dz z)),   dw = sum over tokens and heads of d z.
 #include "heads.cuh"
@@ -21,35 +22,49 @@ struct Args {
   Heads part[2];
   TurnGrad grad[2];
   int per;            // heads of one item
-  int items0, items;  // items of a token: of the queries, in all
-  int64_t total;
+  int items0, items1; // items of a token: of the queries, of the keys
+  int64_t total0, total;  // items of all queries, in all
   float* sums;        // [CTAs, 2, head_dim]
+  bool fetch_dy[2], fetch_in[2];  // heads next to each other, on 16 bytes: whole items can be fetched ahead
 };
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ const T* row_of(const void* p, int64_t ld, int64_t hs, int64_t t, int h) {
   return static_cast<const T*>(p) + t * ld + h * hs;
 }
 
-// Item i: a token, a part, and heads h0 .. h1 - 1 of it.
+// Item i: a token, a part, and heads h0 .. h1 - 1 of it. All tokens' queries come before the keys: a kernel that steps through the
+// items takes the same share of the long and of the short ones with every warp.
 struct Item {
   int64_t token;
   int part, h0, h1;
 };
 __device__ __forceinline__ Item item_of(int64_t i, const Args& g) {
   Item m;
-  m.token = i / g.items;
-  int j = static_cast<int>(i - m.token * g.items);
-  m.part = j >= g.items0;
-  if (m.part) j -= g.items0;
-  m.h0 = j * g.per;
+  m.part = i >= g.total0;
+  if (m.part) i -= g.total0;
+  const int items = m.part ? g.items1 : g.items0;
+  m.token = items == 1 ? i : i >> 32 == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(items) : i / items;
+  m.h0 = static_cast<int>(i - m.token * items) * g.per;
   m.h1 = min(m.h0 + g.per, g.part[m.part].n);
   return m;
 }
 
-template <typename T, bool INTER, int LPR>
-__global__ void __launch_bounds__(kThreads) qk_rope_fwd_kernel(const __grid_constant__ Args g) {
-  constexpr int RPW = 32 / LPR, U = 4;
+// CTAs of the backward on an SM.
+template <typename T>
+constexpr int kBwdCtas = sizeof(T) == 2 ? 3 : 2;
+
+// Rows of a turn, so that the next turn's loads fit beside them.
+template <typename T>
+constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+
+template <typename T, bool INTER, int LPR, bool NORM>
+__global__ void __launch_bounds__(kThreads, 3) qk_rope_fwd_kernel(const __grid_constant__ Args g) {
+  constexpr int RPW = 32 / LPR, U = kRows<T>;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane a = lane_of<INTER>(lane % LPR, g.t.head_dim, g.t.rot_dims);
   pdl_wait();
@@ -60,163 +75,161 @@ __global__ void __launch_bounds__(kThreads) qk_rope_fwd_kernel(const __grid_cons
   const Heads& p = g.part[m.part];
   const T* in = row_of<T>(p.in, p.ld_in, p.hs_in, m.token, 0);
   T* out = static_cast<T*>(p.out) + m.token * p.ld_out;
-  Raw<T, INTER> raw[U];
+  // (lanes past the head hold zeros; a row past the last one is the last one again, and not stored)
+  Raw<T, INTER> raw[U], next[U] = {};
   auto load = [&](int h0) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int h = h0 + j * RPW + sub;
-      if (a.in && h < m.h1) raw[j].load(in + h * p.hs_in, a.o0, a.o1);
-    }
+    for (int j = 0; j < U; ++j)
+      if (a.in) next[j].load(in + min(h0 + j * RPW + sub, m.h1 - 1) * p.hs_in, a.o0, a.o1);
   };
   load(m.h0);
   float c[4], s[4], wu[4], wv[4];
-  angles(a, g.t.turns, g.t.rot_dims, g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token), g.t.amplitude, c, s);
+  angles<LPR>(a, g.t.turns, g.t.rot_dims, g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token), g.t.amplitude, c, s);
   weights<INTER>(a, p.w, wu, wv);
-  float uc[4], us[4], vc[4], vs[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) uc[k] = wu[k] * c[k], us[k] = wu[k] * s[k], vc[k] = wv[k] * c[k], vs[k] = wv[k] * s[k];
+  const Factors f = factors(c, s, wu, wv);
   const float inv_dim = 1.0f / static_cast<float>(g.t.head_dim);
 #pragma unroll 1
   for (int h0 = m.h0; h0 < m.h1; h0 += U * RPW) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      float u[4] = {}, v[4] = {}, yu[4], yv[4];
-      const int h = h0 + j * RPW + sub;
-      const bool live = a.in && h < m.h1;
-      if (live) raw[j].get(u, v);
-      float r = 1.0f;
-      if (g.t.norm) {
-        float q = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
-        r = rsqrtf(fmaf(row_sum<LPR>(q), inv_dim, g.t.eps));
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        yu[k] = r * fmaf(u[k], uc[k], -(v[k] * vs[k]));
-        yv[k] = r * fmaf(u[k], us[k], v[k] * vc[k]);
-      }
-      if (live) Raw<T, INTER>::put(out + h * p.hs_out, a.o0, a.o1, yu, yv);
-    }
+    for (int j = 0; j < U; ++j) raw[j] = next[j];
     if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
-  }
-}
-
-// Sum a lane's 8 columns over the rows that a warp holds at once, and over the CTA's warps, into the CTA's part of the sums.
-template <bool INTER, int LPR>
-__device__ __forceinline__ void store_sums(const Args& g, const Lane& a, float (&du)[2][4], float (&dv)[2][4]) {
-  __shared__ float share[kWarps][2][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-      for (int m = LPR; m < 32; m <<= 1) {
-        du[p][k] += __shfl_xor_sync(0xFFFFFFFFu, du[p][k], m);
-        dv[p][k] += __shfl_xor_sync(0xFFFFFFFFu, dv[p][k], m);
-      }
-      if (lane < LPR && a.in) {
-        share[warp][p][INTER ? a.o0 + 2 * k : a.o0 + k] = du[p][k];
-        share[warp][p][INTER ? a.o0 + 2 * k + 1 : a.o1 + k] = dv[p][k];
-      }
+    for (int j = 0; j < U; ++j) {
+      Pair u[2], v[2], yu[2], yv[2];
+      raw[j].get(u, v);
+      turn<LPR, NORM>(f, inv_dim, g.t.eps, u, v, yu, yv);
+      const int h = h0 + j * RPW + sub;
+      if (a.in && h < m.h1) Raw<T, INTER>::put(out + h * p.hs_out, a.o0, a.o1, yu, yv);
     }
-  __syncthreads();
-  for (int x = threadIdx.x; x < 2 * g.t.head_dim; x += kThreads) {
-    const int p = x / g.t.head_dim, d = x - p * g.t.head_dim;
-    float q = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) q += share[w][p][d];
-    g.sums[static_cast<int64_t>(blockIdx.x) * 2 * g.t.head_dim + x] = q;
   }
 }
 
 template <typename T, bool INTER, int LPR, bool NORM, bool DW>
-__global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_constant__ Args g) {
-  constexpr int RPW = 32 / LPR, U = NORM ? 2 : 4;
-  const int lane = threadIdx.x & 31, sub = lane / LPR;
+__global__ void __launch_bounds__(kThreads, kBwdCtas<T>) qk_rope_bwd_kernel(const __grid_constant__ Args g) {
+  constexpr int RPW = 32 / LPR, U = NORM ? 1 : kRows<T>;
+  // sums for dw: a warp's columns of both parts, added to after each item
+  __shared__ float share[DW ? kWarps : 1][2][DW ? LPR * 8 : 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   const Lane a = lane_of<INTER>(lane % LPR, g.t.head_dim, g.t.rot_dims);
   const float inv_dim = 1.0f / static_cast<float>(g.t.head_dim);
-  float su[2][4] = {}, sv[2][4] = {};
+  auto column = [&](int k, int member) { return INTER ? a.o0 + 2 * k + member : (member == 0 ? a.o0 : a.o1) + k; };
+  if constexpr (DW) {
+    for (int x = lane; x < 2 * LPR * 8; x += 32) share[warp][x / (LPR * 8)][x % (LPR * 8)] = 0.0f;
+    __syncwarp();
+  }
   pdl_wait();
   pdl_trigger();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < g.total; i += static_cast<int64_t>(gridDim.x) * kWarps) {
+  // An item's rows on their way into L2 while the one before it is worked on: registers hold too few rows to cover the memory's
+  // latency (16384 tokens of 40 heads of 128: 116 us without)
+  auto fetch = [&](int64_t i) {
+    if (i >= g.total) return;
+    const Item m = item_of(i, g);
+    const TurnGrad& b = g.grad[m.part];
+    const Heads& p = g.part[m.part];
+    const uint32_t bytes = static_cast<uint32_t>((m.h1 - m.h0) * g.t.head_dim * static_cast<int>(sizeof(T)));
+    if (lane == 0 && g.fetch_dy[m.part]) prefetch_l2(row_of<T>(b.dy, b.ld_dy, b.hs_dy, m.token, m.h0), bytes);
+    if (NORM && lane == 1 && g.fetch_in[m.part]) prefetch_l2(row_of<T>(p.in, p.ld_in, p.hs_in, m.token, m.h0), bytes);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < g.total; i += step) {
+    fetch(i + step);
     const Item m = item_of(i, g);
     const Heads& p = g.part[m.part];
     const TurnGrad& b = g.grad[m.part];
     const T* dy = row_of<T>(b.dy, b.ld_dy, b.hs_dy, m.token, 0);
     const T* in = NORM ? row_of<T>(p.in, p.ld_in, p.hs_in, m.token, 0) : nullptr;
     T* dx = static_cast<T*>(b.dx) + m.token * b.ld_dx;
-    Raw<T, INTER> rd[U], rx[U];
+    Raw<T, INTER> rd[U], rx[U], next_d[U] = {}, next_x[U] = {};
     auto load = [&](int h0) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int h = h0 + j * RPW + sub;
-        if (a.in && h < m.h1) {
-          rd[j].load(dy + h * b.hs_dy, a.o0, a.o1);
-          if constexpr (NORM) rx[j].load(in + h * p.hs_in, a.o0, a.o1);
+        const int h = min(h0 + j * RPW + sub, m.h1 - 1);
+        if (a.in) {
+          next_d[j].load(dy + h * b.hs_dy, a.o0, a.o1);
+          if constexpr (NORM) next_x[j].load(in + h * p.hs_in, a.o0, a.o1);
         }
       }
     };
     load(m.h0);
     float c[4], s[4], wu[4], wv[4];
-    angles(a, g.t.turns, g.t.rot_dims, g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token), g.t.amplitude, c, s);
+    angles<LPR>(a, g.t.turns, g.t.rot_dims, g.t.pos != nullptr ? __ldg(g.t.pos + m.token) : static_cast<int32_t>(m.token), g.t.amplitude, c, s);
     if constexpr (NORM) weights<INTER>(a, p.w, wu, wv);
-    float au[4] = {}, av[4] = {};
+    Pair au[2] = {}, av[2] = {}, pc[2], ps[2], ns[2], pu[2], pv[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      pc[k] = pair(c[2 * k], c[2 * k + 1]);
+      ps[k] = pair(s[2 * k], s[2 * k + 1]);
+      ns[k] = pair(-s[2 * k], -s[2 * k + 1]);
+      if constexpr (NORM) pu[k] = pair(wu[2 * k], wu[2 * k + 1]), pv[k] = pair(wv[2 * k], wv[2 * k + 1]);
+    }
 #pragma unroll 1
     for (int h0 = m.h0; h0 < m.h1; h0 += U * RPW) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        float du[4] = {}, dv[4] = {}, yu[4], yv[4];
+        rd[j] = next_d[j];
+        if constexpr (NORM) rx[j] = next_x[j];
+      }
+      if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        Pair du[2], dv[2], yu[2], yv[2];
         const int h = h0 + j * RPW + sub;
         const bool live = a.in && h < m.h1;
-        if (live) rd[j].get(du, dv);
+        rd[j].get(du, dv);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          yu[k] = fmaf(du[k], c[k], dv[k] * s[k]);
-          yv[k] = fmaf(dv[k], c[k], -(du[k] * s[k]));
+        for (int k = 0; k < 2; ++k) {
+          yu[k] = fma2(du[k], pc[k], mul2(dv[k], ps[k]));
+          yv[k] = fma2(dv[k], pc[k], mul2(du[k], ns[k]));
         }
         if constexpr (NORM) {
-          float u[4] = {}, v[4] = {};
-          if (live) rx[j].get(u, v);
-          float q = 0.0f, e = 0.0f;
+          Pair u[2], v[2], tu[2], tv[2];
+          rx[j].get(u, v);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
-            e = fmaf(yu[k] * wu[k], u[k], fmaf(yv[k] * wv[k], v[k], e));
-          }
+          for (int k = 0; k < 2; ++k) tu[k] = mul2(yu[k], pu[k]), tv[k] = mul2(yv[k], pv[k]);
+          float q = sum2(fma2(u[0], u[0], fma2(u[1], u[1], fma2(v[0], v[0], mul2(v[1], v[1])))));
+          float e = sum2(fma2(u[0], tu[0], fma2(u[1], tu[1], fma2(v[0], tv[0], mul2(v[1], tv[1])))));
 #pragma unroll
           for (int x = LPR / 2; x > 0; x >>= 1) {
             q += __shfl_xor_sync(0xFFFFFFFFu, q, x);
             e += __shfl_xor_sync(0xFFFFFFFFu, e, x);
           }
-          const float r = rsqrtf(fmaf(q, inv_dim, g.t.eps)), f = r * r * e * inv_dim;  // z mean(dz z) = x r (r e / dim)
+          // dx = r (t - z mean(t z)) = r t - x r^3 mean(t x)
+          const float r = rsqrtf(fmaf(q, inv_dim, g.t.eps));
+          const Pair rr = both(r), rw = both(live ? r : 0.0f), f = both(-r * r * r * e * inv_dim);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             if constexpr (DW) {
-              au[k] = fmaf(yu[k], u[k] * r, au[k]);
-              av[k] = fmaf(yv[k], v[k] * r, av[k]);
+              au[k] = fma2(yu[k], mul2(u[k], rw), au[k]);
+              av[k] = fma2(yv[k], mul2(v[k], rw), av[k]);
             }
-            yu[k] = r * fmaf(-u[k], f, yu[k] * wu[k]);
-            yv[k] = r * fmaf(-v[k], f, yv[k] * wv[k]);
+            yu[k] = fma2(u[k], f, mul2(tu[k], rr));
+            yv[k] = fma2(v[k], f, mul2(tv[k], rr));
           }
         }
         if (live && b.dx != nullptr) Raw<T, INTER>::put(dx + h * b.hs_dx, a.o0, a.o1, yu, yv);
       }
-      if (h0 + U * RPW < m.h1) load(h0 + U * RPW);
     }
     if constexpr (DW) {
+      const float2 pairs[4] = {split(au[0]), split(au[1]), split(av[0]), split(av[1])};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (m.part == 0) {
-          su[0][k] += au[k], sv[0][k] += av[k];
-        } else {
-          su[1][k] += au[k], sv[1][k] += av[k];
-        }
+      for (int k = 0; k < 8; ++k) {
+        float x = k & 1 ? pairs[k >> 1].y : pairs[k >> 1].x;
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        if (sub == 0 && a.in) share[warp][m.part][column(k & 3, k >> 2)] += x;
       }
     }
   }
-  if constexpr (DW) store_sums<INTER, LPR>(g, a, su, sv);
+  if constexpr (DW) {
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * g.t.head_dim; x += kThreads) {
+      const int p = x / g.t.head_dim, d = x - p * g.t.head_dim;
+      float q = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) q += share[w][p][d];
+      g.sums[static_cast<int64_t>(blockIdx.x) * 2 * g.t.head_dim + x] = q;
+    }
+  }
 }
 
 // Rows of single elements, a warp each; forward (BWD false) or backward.
@@ -314,22 +327,28 @@ __global__ void __launch_bounds__(kThreads) qk_rope_any_kernel(const __grid_cons
   }
 }
 
-// dw of both parts from the CTAs' sums: a warp per column, 32 partial sums of every 32nd CTA, in order.
-__global__ void __launch_bounds__(kThreads) qk_rope_dw_kernel(const float* sums, int ctas, int dim, float* dw_q, float* dw_k) {
+// dw of both parts from the CTAs' sums: a CTA for 32 columns, a warp for every 32nd CTA's sums (8 loads on their way at a time), then
+// the warps' in order.
+__global__ void __launch_bounds__(1024) qk_rope_dw_kernel(const float* sums, int ctas, int dim, float* dw_q, float* dw_k) {
+  __shared__ float share[32][33];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, x = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (x >= 2 * dim) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = blockIdx.x * 32 + lane;
+  float q = 0.0f;
+#pragma unroll 8
+  for (int c = warp; c < ctas; c += 32) q += x < 2 * dim ? __ldcg(sums + static_cast<int64_t>(c) * 2 * dim + x) : 0.0f;
+  share[warp][lane] = q;
+  __syncthreads();
+  if (warp > 0 || x >= 2 * dim) return;
   float* out = x < dim ? dw_q : dw_k;
   if (out == nullptr) return;
-  float q = 0.0f;
-#pragma unroll 4
-  for (int c = lane; c < ctas; c += 32) q += sums[static_cast<int64_t>(c) * 2 * dim + x];
-  q = row_sum<32>(q);
-  if (lane == 0) out[x < dim ? x : x - dim] = q;
+  q = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) q += share[w][lane];
+  out[x < dim ? x : x - dim] = q;
 }
 
-int bwd_ctas() { return 3 * num_sms(); }
+int bwd_ctas(const Turn& f) { return (f.f32 ? kBwdCtas<float> : kBwdCtas<bf16>)*num_sms(); }
 
 bool chunks_of(const void* p, int64_t ld, int64_t hs, int64_t bytes, int64_t elem) {
   return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * elem % bytes == 0 && hs * elem % bytes == 0);
@@ -350,8 +369,9 @@ void set_items(Args& g, int64_t want, int least) {
   const int64_t runs = min(static_cast<int64_t>((heads + least - 1) / least), max(int64_t{1}, (want + g.t.tokens - 1) / g.t.tokens));
   g.per = static_cast<int>((heads + runs - 1) / runs);
   g.items0 = (g.part[0].n + g.per - 1) / g.per;
-  g.items = g.items0 + (g.part[1].n + g.per - 1) / g.per;
-  g.total = g.t.tokens * g.items;
+  g.items1 = (g.part[1].n + g.per - 1) / g.per;
+  g.total0 = g.t.tokens * g.items0;
+  g.total = g.total0 + g.t.tokens * g.items1;
 }
 
 struct FwdLaunch {
@@ -359,7 +379,7 @@ struct FwdLaunch {
   cudaStream_t s;
   template <typename T, bool I, int L>
   cudaError_t operator()() const {
-    return launch_pdl(qk_rope_fwd_kernel<T, I, L>, dim3(static_cast<unsigned>((g.total + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, g);
+    return launch_pdl(g.t.norm ? qk_rope_fwd_kernel<T, I, L, true> : qk_rope_fwd_kernel<T, I, L, false>, dim3(static_cast<unsigned>((g.total + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, g);
   }
 };
 
@@ -392,7 +412,7 @@ cudaError_t launch_qk_rope_fwd(const Turn& f, const Heads (&part)[2], cudaStream
                : launch_pdl(qk_rope_any_kernel<bf16, false>, dim3(ctas), dim3(kThreads), 0, stream, g);
 }
 
-int64_t qk_rope_bwd_workspace_bytes(const Turn& f) { return static_cast<int64_t>(bwd_ctas()) * 2 * f.head_dim * 4; }
+int64_t qk_rope_bwd_workspace_bytes(const Turn& f) { return static_cast<int64_t>(bwd_ctas(f)) * 2 * f.head_dim * 4; }
 
 cudaError_t launch_qk_rope_bwd(const Turn& f, const Heads (&part)[2], const TurnGrad (&grad)[2], void* ws, cudaStream_t stream) {
   Args g{};
@@ -406,10 +426,15 @@ cudaError_t launch_qk_rope_bwd(const Turn& f, const Heads (&part)[2], const Turn
     vec = vec && chunks_of(grad[p].dy, grad[p].ld_dy, grad[p].hs_dy, bytes, elem) && chunks_of(grad[p].dx, grad[p].ld_dx, grad[p].hs_dx, bytes, elem) &&
           (!f.norm || chunks_of(part[p].in, part[p].ld_in, part[p].hs_in, bytes, elem));
   }
+  for (int p = 0; p < 2; ++p) {
+    auto together = [&](const void* x, int64_t ld, int64_t hs) { return x != nullptr && hs == f.head_dim && f.head_dim * elem % 16 == 0 && chunks_of(x, ld, hs, 16, elem); };
+    g.fetch_dy[p] = together(grad[p].dy, grad[p].ld_dy, grad[p].hs_dy);
+    g.fetch_in[p] = together(part[p].in, part[p].ld_in, part[p].hs_in);
+  }
   const bool dw = grad[0].dw != nullptr || grad[1].dw != nullptr;
   if (dw) g.sums = static_cast<float*>(ws);
-  set_items(g, int64_t{8} * bwd_ctas() * kWarps, 8);
-  const int ctas = static_cast<int>(min((g.total + kWarps - 1) / kWarps, static_cast<int64_t>(bwd_ctas())));
+  set_items(g, int64_t{8} * bwd_ctas(f) * kWarps, 8);
+  const int ctas = static_cast<int>(min((g.total + kWarps - 1) / kWarps, static_cast<int64_t>(bwd_ctas(f))));
   cudaError_t e;
   if (vec)
     e = by_kind(f, BwdLaunch{g, stream, ctas});
@@ -418,7 +443,7 @@ cudaError_t launch_qk_rope_bwd(const Turn& f, const Heads (&part)[2], const Turn
               : launch_pdl(qk_rope_any_kernel<bf16, true>, dim3(ctas), dim3(kThreads), 0, stream, g);
   if (e != cudaSuccess || !dw) return e;
   const float* sums = g.sums;
-  return launch_pdl(qk_rope_dw_kernel, dim3((2 * f.head_dim + kWarps - 1) / kWarps), dim3(kThreads), 0, stream, sums, ctas, f.head_dim, grad[0].dw, grad[1].dw);
+  return launch_pdl(qk_rope_dw_kernel, dim3((2 * f.head_dim + 31) / 32), dim3(1024), 0, stream, sums, ctas, f.head_dim, grad[0].dw, grad[1].dw);
 }
 
 }  // namespace fp8gb
