@@ -8,7 +8,7 @@
 //   0-3 (and 4-7)  weights, one thread per row: 128 rows of a tile each
 //   4-11 or 8-11   keys and values on their way: 8-bit codes into bf16 (exactly: a code times a power of two), and what must not be
 //                  multiplied by a weight of zero out of the last tiles (below)
-//   12, 13         copies (TMA, one box per page), tensor-core instructions
+//   the last ones  copies (TMA, one box per page), tensor-core instructions (a thread per tile of rows)
 // Two forms (NQ): 2 tiles of rows over the same keys, one's weights worked out while the other is on the tensor cores, where units
 // have more than 128 rows; 1 tile of rows with two S in turn where they have fewer (single tokens), twice the warps for the 8-bit conversion.
 //
@@ -37,7 +37,6 @@ namespace {
 using namespace attend;
 using heads::bf16;
 
-constexpr int kThreads = 512;
 constexpr int kPanel = 16384;        // 128 rows of 128 bytes
 constexpr int kCounterBytes = 4096;  // of the workspace: two counters per CTA
 constexpr int kMaxCtas = kCounterBytes / 8;
@@ -52,8 +51,10 @@ struct Form {
   static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 4 : 8);
   static constexpr int RAW = 128 * D + 4 * D;   // 128 rows of codes and their units
   static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 8 : 6)) : 0;
-  static constexpr int PREP_WARP = NQ == 1 ? 4 : 8;  // the first of them
-  static constexpr int PREP_WARPS = 12 - PREP_WARP;
+  // warps: weights, then those that work on keys and values on their way, one for the copies, one or two for the tensor cores
+  static constexpr int PREP_WARP = NQ == 1 ? 4 : 8, PREP_WARPS = 12 - PREP_WARP;
+  static constexpr int GROUP_WARPS = 4;  // on one 8-bit tile
+  static constexpr int COPY_WARP = PREP_WARP + PREP_WARPS, MMA_WARP = COPY_WARP + 1, WARPS = MMA_WARP + NQ, THREADS = 32 * WARPS;
   static_assert(NQ == 2 || NQ == 1, "tiles");
   static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
   static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
@@ -105,6 +106,7 @@ struct Sequences {
 };
 
 // ---- where this CTA's run begins -------------------------------------------------------------------------------------
+template <int kThreads>
 __device__ void find_start(const Params& p, const Sequences& src, int per, uint32_t* cost, Misc* misc, int64_t* share) {
   constexpr uint32_t kLong = 0xFFFFFFFFu;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seqs = src.seqs;
@@ -288,7 +290,7 @@ __device__ float unusual(const Params& p, int64_t row, int64_t unit, int d) {
 }
 
 template <int D, bool MX, int NQ, bool SPREAD>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ Params p) {
   using F = Form<D, MX, NQ, SPREAD>;
@@ -314,13 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_done + 8 * i, 1);
     }
     for (int i = 0; i < F::STAGES; ++i) {
-      mbar_init(kv_full + 8 * i, MX ? 4 : 1);
+      mbar_init(kv_full + 8 * i, MX ? F::GROUP_WARPS : 1);
       mbar_init(kv_empty + 8 * i, NQ);
       mbar_init(v_fixed + 8 * i, F::PREP_WARPS);
     }
     for (int i = 0; i < F::RAWS; ++i) {
       mbar_init(raw_full + 8 * i, 1);
-      mbar_init(raw_empty + 8 * i, 4);
+      mbar_init(raw_empty + 8 * i, F::GROUP_WARPS);
     }
     mbar_init(bar_final, NQ);
     fence_mbar_init();
@@ -329,14 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == 13) {
+  if (warp == F::MMA_WARP) {
     tmem_alloc(smem_u32(&misc->tmem), 512);
     tmem_relinquish();
   }
   pdl_wait();
   pdl_trigger();
   // (the costs lie where the tiles will: written before the barrier, fenced against the copies)
-  find_start(p, src, per, reinterpret_cast<uint32_t*>(smem), misc, reinterpret_cast<int64_t*>(smem + F::OFF_MISC - 8 * F::NBAR - 8 * (kThreads / 32)));
+  find_start<F::THREADS>(p, src, per, reinterpret_cast<uint32_t*>(smem), misc, reinterpret_cast<int64_t*>(smem + F::OFF_MISC - 8 * F::NBAR - 256));
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto scores_at = [&](int slot) { return tmem + (SPREAD ? 128 : 64) * slot; };
   auto weights_at = [&](int slot) { return SPREAD ? tmem + 384 + 64 * slot : scores_at(slot) + 32; };
 
-  if (warp == 12) {
+  if (warp == F::COPY_WARP) {
     // ---- copies ------------------------------------------------------------------------------------------------------
     const int rows = min(p.c.page_size, kTile);  // of a box
     bool ok = true;
@@ -426,11 +428,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (globaltimer_ns() - t0 < 200000ull) {
       }
     }
-  } else if (warp >= 13 && warp < 13 + NQ) {
+  } else if (warp >= F::MMA_WARP) {
     // ---- tensor-core instructions --------------------------------------------------------------------------------------
     // One thread for each tile of rows: with the whole warp walking along and electing a thread for each group of instructions, votes and
     // convergence took some 1700 clocks of an item's 5000 (two tiles of 128 wide heads; 4380 so).
-    const int q = warp - 13;
+    const int q = warp - F::MMA_WARP;
     if (elect_one()) {
       constexpr uint32_t kScores = idesc_bf16(128, SPREAD ? 128 : 64, false), kValues = idesc_bf16(128, D, true);
       bool ok = true;
@@ -569,10 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp >= F::PREP_WARP && warp < 12) {
+  } else if (warp >= F::PREP_WARP) {
     // ---- keys and values on their way ----------------------------------------------------------------------------------
-    // (one tile of rows: 8-bit keys in the first four warps, values in the others)
-    const int mine = MX && NQ == 1 ? (warp - F::PREP_WARP) >> 2 : -1, tid = (threadIdx.x - 32 * F::PREP_WARP) % (MX ? 128 : 32 * F::PREP_WARPS), rows = min(p.c.page_size, kTile);
+    // (one tile of rows: 8-bit keys in the first half of the warps, values in the others)
+    constexpr int kGroup = 32 * (MX ? F::GROUP_WARPS : F::PREP_WARPS);
+    const int mine = MX && NQ == 1 ? (warp - F::PREP_WARP) / F::GROUP_WARPS : -1, tid = (threadIdx.x - 32 * F::PREP_WARP) % kGroup, rows = min(p.c.page_size, kTile);
     bool ok = true;
     int n = 0;
     for (; ok && k.live(); k.next()) {
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* v = smem + F::OFF_KV + (u % F::STAGES) * F::TILE;
           bool bad = false;
 #pragma unroll 4
-          for (int i = tid; (SPREAD || edge) && i < F::PANELS * 1024; i += 32 * F::PREP_WARPS) {
+          for (int i = tid; (SPREAD || edge) && i < F::PANELS * 1024; i += kGroup) {
             uint4* at = reinterpret_cast<uint4*>(v) + i;
             const uint4 x = *at;
             if ((i / (F::GROUP / 16)) * 8 + ((i >> 3) & 7) >= live) {
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lost = misc->bad[raw];
             bool bad = false;
             // a thread's 16 columns of every kStep-th row; the swizzle's place is the same in all of them
-            constexpr int kLanes = D / 16, kStep = 128 / kLanes, kRows = 128 / kStep;
+            constexpr int kLanes = D / 16, kStep = kGroup / kLanes, kRows = 128 / kStep;
             const int row0 = tid / kLanes, c = tid % kLanes;
             uint8_t* panel = out + (row0 >> 3) * F::GROUP + (c >> 2) * 1024 + (row0 & 7) * 128;
             const int flip = (c >> 2) & 1;  // (the panels' lanes take their two stores in opposite order: other banks)
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t unit[kRows], largest = 0u;
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
-              x[j] = reinterpret_cast<const uint4*>(codes)[tid + 128 * j];
+              x[j] = reinterpret_cast<const uint4*>(codes)[tid + kGroup * j];
               unit[j] = units[(row0 + j * kStep) * (D / 32) + c / 2];
             }
 #pragma unroll
@@ -1013,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == F::MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1036,7 +1039,7 @@ cudaError_t launch_form(const CUtensorMap& q, const CUtensorMap& k, const CUtens
   auto* kernel = paged_attention_kernel<D, MX, NQ, SPREAD>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(ctas()), dim3(kThreads), F::SMEM, stream, q, k, v, p);
+  return launch_pdl(kernel, dim3(ctas()), dim3(F::THREADS), F::SMEM, stream, q, k, v, p);
 }
 
 }  // namespace
