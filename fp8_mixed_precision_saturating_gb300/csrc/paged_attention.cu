@@ -53,7 +53,10 @@ struct Form {
   static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 8 : 6)) : 0;
   // warps: weights, then those that work on keys and values on their way, one for the copies, one or two for the tensor cores
   static constexpr int PREP_WARP = NQ == 1 ? 4 : 8, PREP_WARPS = 12 - PREP_WARP;
-  static constexpr int GROUP_WARPS = 4;  // on one 8-bit tile
+  // On one 8-bit tile; one tile of rows: keys and values side by side (64 tokens over 4096 keys: 167 us). Not better: 8 warps on each
+  // tile and three stages in turn, queries in one buffer, 182 us; stages of 64 rows, two for the keys and two for the values,
+  // 185 us. Shared memory is what they all wait for: the codes in and out, the bf16 in, and each read once by the tensor cores.
+  static constexpr int GROUP_WARPS = 4;
   static constexpr int COPY_WARP = PREP_WARP + PREP_WARPS, MMA_WARP = COPY_WARP + 1, WARPS = MMA_WARP + NQ, THREADS = 32 * WARPS;
   static_assert(NQ == 2 || NQ == 1, "tiles");
   static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       mbar_init(v_fixed + 8 * i, F::PREP_WARPS);
     }
     for (int i = 0; i < F::RAWS; ++i) {
-      mbar_init(raw_full + 8 * i, 1);
+      mbar_init(raw_full + 8 * i, 33);  // each lane's copies of units, and the codes'
       mbar_init(raw_empty + 8 * i, F::GROUP_WARPS);
     }
     mbar_init(bar_final, NQ);
@@ -373,19 +376,33 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
                         k.s.first + t0 + (SPREAD ? 0 : i * p.tokens_per_tile));
       }
       __syncwarp();
+      // 64 pages of the table ahead, a lane 2 of them: pages[0] from page index `window` on, pages[1] the 32 after
       const int32_t* table = p.b.page_table + k.at.seq * p.b.ld_table;
-      auto page_of = [&](int t) {  // lane l: the tile's page l, -1 outside the cache or past the end
-        const int key = t * kTile + lane * rows;
-        int page = -1;
-        if (t < k.b && lane * rows < kTile && key < k.s.seen) page = __ldg(table + (key >> p.c.page_bits));
-        return page;
+      const int ends = ((k.s.seen - 1) >> p.c.page_bits) + 1;  // pages of the sequence
+      auto page_at = [&](int i) {  // -1 outside the cache
+        const int page = i < ends ? __ldg(table + i) : -1;
+        return page >= 0 && page < p.c.pages ? page : -1;
       };
-      int next = page_of(k.a);
+      int window = (k.a * kTile) >> p.c.page_bits;
+      int pages0 = page_at(window + lane), pages1 = page_at(window + 32 + lane);
+      auto page_of = [&](int i) {  // page i of the sequence, each lane its own i, all within the window
+        const int at = i - window, lo = __shfl_sync(0xFFFFFFFFu, pages0, at & 31), hi = __shfl_sync(0xFFFFFFFFu, pages1, at & 31);
+        return at < 32 ? lo : hi;
+      };
       for (int t = k.a; t < k.b; ++t, ++n) {
-        const int page = next, boxes = min(kTile / rows, (min(k.s.seen - t * kTile, kTile) + rows - 1) / rows);
-        next = page_of(t + 1);
-        const int within = (t * kTile + lane * rows) & (p.c.page_size - 1);
-        const bool good = page >= 0 && page < p.c.pages;
+        const int key = t * kTile, left = min(k.s.seen - key, kTile), boxes = min(kTile / rows, (left + rows - 1) / rows);
+        const int first = key >> p.c.page_bits;
+        if (first >= window + 32) {
+          window += 32;
+          pages0 = pages1;
+          pages1 = page_at(window + 32 + lane);
+        }
+        const int page = page_of(first + min(lane, 15)), within = (key + lane * rows) & (p.c.page_size - 1);
+        // 8-bit: the page of this lane's 16 bytes of units, kUnitRows rows
+        constexpr int kUnitRows = 512 / D;
+        const int unit_row = lane * kUnitRows, unit_page = MX ? page_of(first + (min(unit_row, kTile - 1) / rows)) : 0;
+        const int64_t unit_at = MX ? ((static_cast<int64_t>(unit_page) * p.c.heads + k.at.head) * p.c.page_size + ((key + unit_row) & (p.c.page_size - 1))) * (D / 32) : 0;
+        const uint32_t found = __ballot_sync(0xFFFFFFFFu, lane < boxes && page >= 0);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int u = 2 * n + kv;
@@ -397,26 +414,21 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
             if (!ok) break;
             if (elect_one()) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * D * 2));
             __syncwarp();
-            if (lane < boxes) tma_load_5d(dst + lane * rows * D * 2, map, bar, 0, 0, 0, within >> 3, good ? page * p.page_steps + k.at.head * p.head_steps : -1);
+            if (lane < boxes) tma_load_5d(dst + lane * rows * D * 2, map, bar, 0, 0, 0, within >> 3, page >= 0 ? page * p.page_steps + k.at.head * p.head_steps : -1);
           } else {
             const int slot = u % F::RAWS;
             const uint32_t bar = raw_full + 8 * slot, dst = base + F::OFF_RAW + slot * F::RAW;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_empty + 8 * slot, ((u / F::RAWS) & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
             if (!ok) break;
             // the codes of a page outside the cache are zeros (the copy's fill); its units are not copied
-            const uint32_t found = __ballot_sync(0xFFFFFFFFu, lane < boxes && good);
             if (elect_one()) {
               misc->bad[slot] = ~found & ((1u << boxes) - 1u);
-              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * D + __popc(found) * rows * (D / 32)));
+              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * D));
             }
             __syncwarp();
-            if (lane < boxes) {
-              tma_load_4d(dst + lane * rows * D, map, bar, 0, within, k.at.head, good ? page : -1);
-              if (good) {
-                const uint8_t* units = (kv == 0 ? p.c.k_scale : p.c.v_scale) + ((static_cast<int64_t>(page) * p.c.heads + k.at.head) * p.c.page_size + within) * (D / 32);
-                bulk_load(dst + 128 * D + lane * rows * (D / 32), units, rows * (D / 32), bar);
-              }
-            }
+            if (lane < boxes) tma_load_4d(dst + lane * rows * D, map, bar, 0, within, k.at.head, page);
+            if (unit_row < left && unit_page >= 0) async_load16(dst + 128 * D + 16 * lane, (kv == 0 ? p.c.k_scale : p.c.v_scale) + unit_at);
+            async_arrive(bar);
           }
           __syncwarp();
         }
@@ -607,8 +619,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
 #pragma unroll 1
           for (int kv = mine < 0 ? 0 : mine; kv <= (mine < 0 ? 1 : mine); ++kv) {
             const int u = 2 * n + kv, raw = u % F::RAWS, slot = u % F::STAGES;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_full + 8 * raw, (u / F::RAWS) & 1, p.w, DEV_ERR_WAIT_EPILOGUE) &&
-                                             mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_full + 8 * raw, (u / F::RAWS) & 1, p.w, DEV_ERR_WAIT_EPILOGUE));
             if (!ok) break;
             const uint8_t* codes = smem + F::OFF_RAW + raw * F::RAW;
             const uint8_t* units = codes + 128 * D;
@@ -618,15 +629,6 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
             // a thread's 16 columns of every kStep-th row; the swizzle's place is the same in all of them
             constexpr int kLanes = D / 16, kStep = kGroup / kLanes, kRows = 128 / kStep;
             const int row0 = tid / kLanes, c = tid % kLanes;
-            uint8_t* panel = out + (row0 >> 3) * F::GROUP + (c >> 2) * 1024 + (row0 & 7) * 128;
-            const int flip = (c >> 2) & 1;  // (the panels' lanes take their two stores in opposite order: other banks)
-            uint4* first = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + flip) ^ (row0 & 7)) << 4));
-            uint4* second = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + 1 - flip) ^ (row0 & 7)) << 4));
-            auto store = [&](int j, const uint32_t (&y)[8]) {
-              const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-              first[j * (kStep / 8) * (F::GROUP / 16)] = flip ? hi : lo;
-              second[j * (kStep / 8) * (F::GROUP / 16)] = flip ? lo : hi;
-            };
             uint4 x[kRows];
             uint32_t unit[kRows], largest = 0u;
 #pragma unroll
@@ -634,6 +636,15 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
               x[j] = reinterpret_cast<const uint4*>(codes)[tid + kGroup * j];
               unit[j] = units[(row0 + j * kStep) * (D / 32) + c / 2];
             }
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
+            if (!ok) break;
+            uint8_t* panel = out + (row0 >> 3) * F::GROUP + (c >> 2) * 1024 + (row0 & 7) * 128;
+            uint4* first = reinterpret_cast<uint4*>(panel + (((2 * (c & 3)) ^ (row0 & 7)) << 4));
+            uint4* second = reinterpret_cast<uint4*>(panel + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4));
+            auto store = [&](int j, const uint32_t (&y)[8]) {
+              first[j * (kStep / 8) * (F::GROUP / 16)] = make_uint4(y[0], y[1], y[2], y[3]);
+              second[j * (kStep / 8) * (F::GROUP / 16)] = make_uint4(y[4], y[5], y[6], y[7]);
+            };
 #pragma unroll
             for (int j = 0; j < kRows; ++j) largest = max(largest, unit[j]);
             if (largest < 135u && lost == 0u && (kv == 0 || !edge)) {  // 2^(unit - 127) 2^120 is a bf16
@@ -644,14 +655,15 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
                 store(j, y);
               }
             } else {
-#pragma unroll
+#pragma unroll 1
               for (int j = 0; j < kRows; ++j) {
                 const int row = row0 + j * kStep;
+                const uint32_t at = units[row * (D / 32) + c / 2];
                 uint32_t y[8], any = 0u;
-                decode16(x[j], bf16_pair(0x7B80u), y);  // in two factors
+                decode16(reinterpret_cast<const uint4*>(codes)[tid + kGroup * j], bf16_pair(0x7B80u), y);  // in two factors
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  y[e] = times(y[e], bf16_pair(unit[j] == 255u ? 0x7FC0u : unit[j] == 0u ? 0x0040u : unit[j] << 7));
+                  y[e] = times(y[e], bf16_pair(at == 255u ? 0x7FC0u : at == 0u ? 0x0040u : at << 7));
                   if ((lost >> (row / rows) & 1u) || (kv == 1 && row >= live)) y[e] = 0u;
                   any |= not_finite(y[e]);
                 }

@@ -343,6 +343,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// 16 bytes from global to shared memory, and an arrival on `bar` (one of its count) when all of this thread's so far have landed.
+__device__ __forceinline__ void async_load16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_arrive(uint32_t bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
+
 // Shared-memory descriptor of a tile without swizzle whose 8-row core matrices (8 rows of 16
 // bytes, 128 contiguous bytes) follow each other every 128 bytes (stride byte offset 128).
 __device__ __forceinline__ uint64_t smem_desc_plain128(uint32_t saddr) {
