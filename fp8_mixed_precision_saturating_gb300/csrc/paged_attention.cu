@@ -6,11 +6,12 @@
 // weights in registers, P = bf16(weights) back to tensor memory over S, O += P V with P read from there. A CTA stays on its
 // SM and works through a run of tiles (attend_walk.cuh); its warps divide the work:
 //   0-3 (and 4-7)  weights, one thread per row: 128 rows of a tile each
-//   4-11 or 8-11   keys and values on their way: 8-bit codes into bf16 (exactly: a code times a power of two), and what must not be
+//   the next 4 or 8  keys and values on their way: 8-bit codes into bf16 (exactly: a code times a power of two), and what must not be
 //                  multiplied by a weight of zero out of the last tiles (below)
 //   the last ones  copies (TMA, one box per page), tensor-core instructions (a thread per tile of rows)
-// Two forms (NQ): 2 tiles of rows over the same keys, one's weights worked out while the other is on the tensor cores, where units
-// have more than 128 rows; 1 tile of rows with two S in turn where they have fewer (single tokens), twice the warps for the 8-bit conversion.
+// Three forms (chosen at the end of this file): two tiles of rows over the same keys, one's weights worked out while the other is on the tensor cores (NQ 2);
+// one tile (NQ 1, bf16 only); and SPREAD, 32 rows four times in a tile, whose copies weigh a quarter of a tile's keys each (the other
+// keys' weights stay zero) and are added up at the unit's end, so that a single token's few rows still have four warps.
 //
 // The reference moves only where a row's maximum passes it by more than 8 (in log2 of the weights; below, exp cannot overflow
 // and fp32 sums lose nothing): then O in tensor memory and the sum are scaled, otherwise O is never touched.
@@ -39,7 +40,8 @@ using heads::bf16;
 
 constexpr int kPanel = 16384;        // 128 rows of 128 bytes
 constexpr int kCounterBytes = 4096;  // of the workspace: two counters per CTA
-constexpr int kMaxCtas = kCounterBytes / 8;
+constexpr int kMaxCtas = 160;        // (152 SMs; what a join holds of each part has to fit into shared memory)
+constexpr int kJoinBytes = 200 * 1024;  // of shared memory
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
 template <int D, bool MX, int NQ, bool SPREAD>
@@ -62,10 +64,10 @@ struct Form {
   static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
   static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
   static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
-  static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
-  static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 12 + 1;
+  static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW > kJoinBytes ? OFF_RAW + RAWS * RAW : kJoinBytes;
+  static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 12 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int OFF_STATS = OFF_MISC + 256;  // (reference, sum) of each row, SPREAD: of each warp's rows
+  static constexpr int OFF_STATS = OFF_MISC + 512;  // (reference, sum) of each row, SPREAD: of each warp's rows
   static constexpr int SMEM = OFF_STATS + 1024 * NQ + 1024;
   // A wait names a phase by its parity, so whoever waits on a barrier has to see all of its phases. Where keys and values have
   // different waiters (the warps that look at bf16 values, the two groups that convert 8-bit tiles) a stage is always
@@ -80,6 +82,7 @@ struct Params {
   Cache c;
   Batch b;
   int group, tokens_per_tile, capacity;
+  int group_inverse;  // ceil(2^16 / group): (r * group_inverse) >> 16 is r / group for r < 128
   float c2;   // |scale| log2 e
   bool flip;  // scale < 0
   int page_steps, head_steps;  // of a bf16 cache's pages and heads in its tensor maps' last dimension
@@ -88,17 +91,24 @@ struct Params {
   WaitCtl w;
 };
 
+// A cut tile of rows whose parts are all there: rows `rows` from token `token` and head `head` on, of CTAs c0 .. c1.
+struct Join {
+  int64_t token;
+  int head, rows, c0, c1;
+};
+
 // What is not in rings, at OFF_MISC.
 struct Misc {
   Place start;
   int64_t total;
   int runs;
   uint32_t tmem;
-  int last[2];
+  Join join[4];     // what this CTA adds up at its end: of each tile of rows, the run's first unit and its last
   uint32_t bad[8];  // of each raw tile, the boxes whose page is outside the cache
   int dirty[16];  // the last segment with tiles, of those with this number modulo 16, that holds values that are not finite in edge tiles
 };
-static_assert(sizeof(Misc) <= 256, "misc");
+static_assert(sizeof(Misc) <= 512 && 8 * kMaxCtas <= kCounterBytes, "misc");
+static_assert(kJoinBytes >= kMaxCtas * (256 + 2 * 512), "eight columns of a block of all parts");
 
 struct Sequences {
   const Batch& b;
@@ -109,9 +119,50 @@ struct Sequences {
 };
 
 // ---- where this CTA's run begins -------------------------------------------------------------------------------------
+// Few sequences of few blocks: a lane for each, every warp for itself (one token over 1000: 2 us of 12 with
+// the general way below).
+__device__ bool find_start_of_few(const Params& p, const Sequences& src, int per, Misc* misc) {
+  const int lane = threadIdx.x & 31;
+  if (src.seqs > 32) return false;
+  Seq q{0, 0, 0, 0};
+  if (lane < src.seqs) q = src.seq(lane);
+  if (__syncthreads_or(q.n > 4 * per)) return false;  // (all of the CTA alike, whatever a length does meanwhile)
+  int mine = 0;
+  for (int b = 0; b * per < q.n; ++b) mine += items_of(q, b, per, p.a.window);
+  const int64_t all = static_cast<int64_t>(mine) * p.c.heads;
+  int64_t upto = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  const int runs = static_cast<int>(min(total, static_cast<int64_t>(gridDim.x)));  // none of them empty
+  const bool works = static_cast<int>(blockIdx.x) < runs;
+  const int64_t begin = works ? begin_of(total, blockIdx.x, runs) : 0, end = works ? begin_of(total, blockIdx.x + 1, runs) : 0;
+  if (threadIdx.x == 0) {
+    misc->total = total;
+    misc->runs = runs;
+    misc->start.item = begin;
+    misc->start.end = end;
+  }
+  if (threadIdx.x < 32 && works && upto - all <= begin && begin < upto) {
+    const int64_t at = begin - (upto - all);
+    const int head = static_cast<int>(quotient(at, mine));
+    int off = static_cast<int>(at - static_cast<int64_t>(head) * mine), block = 0;
+    for (int n; off >= (n = items_of(q, block, per, p.a.window)); ++block) off -= n;
+    misc->start.seq = lane;
+    misc->start.head = head;
+    misc->start.block = block;
+    misc->start.off = off;
+  }
+  return true;
+}
+
 template <int kThreads>
 __device__ void find_start(const Params& p, const Sequences& src, int per, uint32_t* cost, Misc* misc, int64_t* share) {
   constexpr uint32_t kLong = 0xFFFFFFFFu;
+  if (find_start_of_few(p, src, per, misc)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seqs = src.seqs;
   bool some_long = false;
   for (int s = tid; s < seqs; s += kThreads) {
@@ -292,6 +343,148 @@ __device__ float unusual(const Params& p, int64_t row, int64_t unit, int d) {
   return isfinite(v) ? 0.0f : v;
 }
 
+// After a wait that ran out: time for the copies in flight to land (microseconds) before the CTA can exit.
+__device__ __noinline__ void settle() {
+  const unsigned long long t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 200000ull) {
+  }
+}
+
+// ---- a tile's rows, and its parts ------------------------------------------------------------------------------------
+// Row r of a tile that begins at a token and query head.
+__device__ __forceinline__ bf16* row_of(const Params& p, int64_t token, int head, int r) {
+  const int tk = (r * p.group_inverse) >> 16, hd = r - tk * p.group;
+  return static_cast<bf16*>(p.a.out) + (token + tk) * p.a.ld_out + (static_cast<int64_t>(head) + hd) * p.a.hs_out;
+}
+__device__ __forceinline__ void put_lse(const Params& p, int64_t token, int head, int r, float reference, float sum) {
+  if (p.a.lse == nullptr) return;
+  const int tk = (r * p.group_inverse) >> 16, hd = r - tk * p.group;
+  p.a.lse[(token + tk) * p.a.q_heads + head + hd] = sum == 0.0f ? -INFINITY : (reference + log2f(sum)) * kLn2;
+}
+// The part of a cut unit (its first CTA c0) that a CTA leaves in the workspace: (reference, sum) of each row, then O by
+// blocks of 32 rows, in a block four columns of all its rows after the other (a warp, a thread per row, writes without gaps).
+template <int D, int NQ>
+__device__ __forceinline__ char* part_at(const Params& p, int c0, int cta, int q) {
+  return p.parts + (static_cast<int64_t>(2 * cta + (cta == c0 ? 1 : 0)) * NQ + q) * (128 * (D + 2) * 4);
+}
+
+// A unit's parts added up, in their order, by the whole CTA at its end, when shared memory is free: for as many blocks of 32 rows of all
+// parts as fit (or some columns of one) their references and sums become weights, then the rows' elements are added. What bounds it is the
+// way to L2 and back, and code that comes once and from far: short loops over bulk copies.
+template <int D, int NQ, int kThreads>
+__device__ __noinline__ bool join_parts(const Params& p, const Join u, int q, uint8_t* smem, float* inverse, uint32_t bar, uint32_t& phase) {
+  constexpr int kAll = D / 4, kLanes = 8;  // columns by fours; threads for a row's statistics
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, parts = u.c1 - u.c0 + 1;
+  const int whole = kJoinBytes / (parts * (256 + kAll * 512)), step = 32 * most(whole, 1);
+  const int wide = whole > 0 ? kAll : (kJoinBytes / parts - 256) / 512 & ~1;  // columns by fours at once, an even number
+  __threadfence();
+  if (u.rows * kAll <= kThreads && parts <= 32) {  // few rows: a thread for four elements, its reference and sum on the way
+    if (tid >= u.rows * kAll) return true;
+    const int d = tid / u.rows, r = tid - d * u.rows;  // (at most 14 rows: one block)
+    float top = -INFINITY, sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int c = 0; c < parts; c += 8) {
+      float2 x[8];
+      float4 y[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const char* at = part_at<D, NQ>(p, u.c0, u.c0 + least(c + b, parts - 1), q);
+        x[b] = __ldcg(reinterpret_cast<const float2*>(at) + r);
+        y[b] = __ldcg(reinterpret_cast<const float4*>(at + 1024) + tid);
+      }
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (c + b >= parts || x[b].y == 0.0f) continue;  // 0: a part that saw nothing
+        const float to = fmaxf(top, x[b].x), f = exp2_of(top - to), w = exp2_of(x[b].x - to);
+        top = to;
+        sum = fmaf(w, x[b].y, sum * f);
+        o.x = fmaf(w, y[b].x, o.x * f), o.y = fmaf(w, y[b].y, o.y * f), o.z = fmaf(w, y[b].z, o.z * f), o.w = fmaf(w, y[b].w, o.w * f);
+      }
+    }
+    if (d == 0) put_lse(p, u.token, u.head, r, top, sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<uint2*>(row_of(p, u.token, u.head, r) + 4 * d) =
+        inv == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
+    return true;
+  }
+  const uint32_t base = smem_u32(smem);
+  const float2* ml = reinterpret_cast<const float2*>(smem);  // [parts][rows of this step, up to 32 more of them]
+#pragma unroll 1
+  for (int r0 = 0; r0 < u.rows; r0 += step) {
+    const int rows = least(step, u.rows - r0), ml_rows = (rows + 1) & ~1;
+#pragma unroll 1
+    for (int d0 = 0; d0 < kAll; d0 += wide) {
+      const int columns = least(wide, kAll - d0), o_bytes = rows * columns * 16, o_at = parts * ml_rows * 8;
+      fence_proxy_async();
+      __syncthreads();
+      if (warp == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts * (o_bytes + ml_rows * 8)));
+        __syncwarp();
+#pragma unroll 1
+        for (int c = lane; c < parts; c += 32) {
+          const char* at = part_at<D, NQ>(p, u.c0, u.c0 + c, q);
+          bulk_load(base + c * ml_rows * 8, at + 8 * r0, ml_rows * 8, bar);
+          bulk_load(base + o_at + c * o_bytes, at + 1024 + (r0 * kAll + d0 * rows) * 16, o_bytes, bar);
+        }
+      }
+      const bool ok = mbar_wait(bar, phase, p.w, DEV_ERR_WAIT_EPILOGUE);
+      if (!__syncthreads_and(ok)) return false;
+      phase ^= 1u;
+      float2* weight = const_cast<float2*>(ml);
+#pragma unroll 1
+      for (int r1 = 0; r1 < rows; r1 += kThreads / kLanes) {
+        const int r = r1 + tid / kLanes, l = tid % kLanes;
+        float top = -INFINITY, sum = 0.0f;
+        if (r < rows) {
+#pragma unroll 2
+          for (int c = l; c < parts; c += kLanes) top = fmaxf(top, ml[c * ml_rows + r].x);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (top == -INFINITY) top = 0.0f;
+        if (r < rows) {
+#pragma unroll 2
+          for (int c = l; c < parts; c += kLanes) {
+            const float2 x = ml[c * ml_rows + r];
+            const float w = exp2_of(x.x - top);
+            weight[c * ml_rows + r].x = w;
+            sum = fmaf(w, x.y, sum);
+          }
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (r < rows && l == 0) {
+          if (d0 == 0) put_lse(p, u.token, u.head, r0 + r, top, sum);
+          inverse[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        }
+      }
+      __syncthreads();
+      const int pairs = columns / 2, blocks = (rows + 31) / 32;
+#pragma unroll 1
+      for (int x = warp; x < blocks * pairs; x += kThreads / 32) {  // 8 columns of a block, a lane per row
+        const int block = x / pairs, d = x - block * pairs, across = least(rows - 32 * block, 32), r = lane;
+        if (r >= across) continue;
+        const float4* from = reinterpret_cast<const float4*>(smem + o_at) + 32 * block * columns + 2 * d * across + r;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), e = o;
+#pragma unroll 2
+        for (int c = 0; c < parts; ++c) {
+          const float2 w = ml[c * ml_rows + 32 * block + r];
+          const float4 a = from[c * (o_bytes / 16)], b = from[c * (o_bytes / 16) + across];
+          if (w.y == 0.0f) continue;  // a part that saw nothing
+          o.x = fmaf(w.x, a.x, o.x), o.y = fmaf(w.x, a.y, o.y), o.z = fmaf(w.x, a.z, o.z), o.w = fmaf(w.x, a.w, o.w);
+          e.x = fmaf(w.x, b.x, e.x), e.y = fmaf(w.x, b.y, e.y), e.z = fmaf(w.x, b.z, e.z), e.w = fmaf(w.x, b.w, e.w);
+        }
+        const float inv = inverse[32 * block + r];
+        uint4 packed = make_uint4(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv), heads::pack(e.x * inv, e.y * inv), heads::pack(e.z * inv, e.w * inv));
+        if (inv == 0.0f) packed = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(row_of(p, u.token, u.head, r0 + 32 * block + r) + 4 * d0 + 8 * d) = packed;
+      }
+    }
+  }
+  return true;
+}
+
 template <int D, bool MX, int NQ, bool SPREAD>
 __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -304,7 +497,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
   Misc* misc = reinterpret_cast<Misc*>(smem + F::OFF_MISC);
   const uint32_t q_full = base + F::OFF_BAR, q_empty = q_full + 16, kv_full = q_empty + 16, kv_empty = kv_full + 8 * F::STAGES;
   const uint32_t raw_full = kv_empty + 8 * F::STAGES, raw_empty = raw_full + 8 * F::RAWS, s_full = raw_empty + 8 * F::RAWS;
-  const uint32_t p_ready = s_full + 32, o_done = p_ready + 32, v_fixed = o_done + 32, bar_final = v_fixed + 8 * F::STAGES;
+  const uint32_t p_ready = s_full + 32, o_done = p_ready + 32, v_fixed = o_done + 32, bar_final = v_fixed + 8 * F::STAGES, bar_join = bar_final + 8;
   const int per = NQ * p.tokens_per_tile;
   const Sequences src{p.b, p.capacity, p.b.seqs};
 
@@ -328,8 +521,10 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       mbar_init(raw_empty + 8 * i, F::GROUP_WARPS);
     }
     mbar_init(bar_final, NQ);
+    mbar_init(bar_join, 1);
     fence_mbar_init();
     for (int i = 0; i < 16; ++i) misc->dirty[i] = -1;
+    for (int i = 0; i < 4; ++i) misc->join[i].rows = 0;
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -363,6 +558,15 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
     int n = 0;  // items so far
     for (; ok && k.live(); k.next()) {
       if (k.a >= k.b) continue;
+      // 64 pages of the table ahead, a lane 2 of them: pages[0] from page index `window` on, pages[1] the 32 after
+      const int32_t* table = p.b.page_table + k.at.seq * p.b.ld_table;
+      const int ends = ((k.s.seen - 1) >> p.c.page_bits) + 1;  // pages of the sequence
+      auto page_at = [&](int i) {  // -1 outside the cache
+        const int page = i < ends ? __ldg(table + i) : -1;
+        return page >= 0 && page < p.c.pages ? page : -1;
+      };
+      int window = (k.a * kTile) >> p.c.page_bits;
+      int pages0 = page_at(window + lane), pages1 = page_at(window + 32 + lane);
       const int buf = NQ == 1 ? k.filled & 1 : 0, use = NQ == 1 ? k.filled >> 1 : k.filled;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty + 8 * buf, (use & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
       if (!ok) break;
@@ -376,15 +580,6 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
                         k.s.first + t0 + (SPREAD ? 0 : i * p.tokens_per_tile));
       }
       __syncwarp();
-      // 64 pages of the table ahead, a lane 2 of them: pages[0] from page index `window` on, pages[1] the 32 after
-      const int32_t* table = p.b.page_table + k.at.seq * p.b.ld_table;
-      const int ends = ((k.s.seen - 1) >> p.c.page_bits) + 1;  // pages of the sequence
-      auto page_at = [&](int i) {  // -1 outside the cache
-        const int page = i < ends ? __ldg(table + i) : -1;
-        return page >= 0 && page < p.c.pages ? page : -1;
-      };
-      int window = (k.a * kTile) >> p.c.page_bits;
-      int pages0 = page_at(window + lane), pages1 = page_at(window + 32 + lane);
       auto page_of = [&](int i) {  // page i of the sequence, each lane its own i, all within the window
         const int at = i - window, lo = __shfl_sync(0xFFFFFFFFu, pages0, at & 31), hi = __shfl_sync(0xFFFFFFFFu, pages1, at & 31);
         return at < 32 ? lo : hi;
@@ -436,9 +631,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       }
     }
     if (!ok) {  // let the copies in flight land (microseconds) before the CTA can exit
-      const unsigned long long t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 200000ull) {
-      }
+      settle();
     }
   } else if (warp >= F::MMA_WARP) {
     // ---- tensor-core instructions --------------------------------------------------------------------------------------
@@ -647,7 +840,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
             };
 #pragma unroll
             for (int j = 0; j < kRows; ++j) largest = max(largest, unit[j]);
-            if (largest < 135u && lost == 0u && (kv == 0 || !edge)) {  // 2^(unit - 127) 2^120 is a bf16
+            if (largest < 135u && lost == 0u && (kv == 0 || live >= kTile)) {  // 2^(unit - 127) 2^120 is a bf16, and all values are finite
 #pragma unroll
               for (int j = 0; j < kRows; ++j) {
                 uint32_t y[8];
@@ -692,7 +885,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
     constexpr int HALVES = SPREAD ? 1 : 2, KEYS = SPREAD ? 32 : 64;  // steps of a tile, a thread's keys of a step
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_at = tmem + lanes + 256 + 128 * q;
-    const int token = row / p.group;
+    const int token = (row * p.group_inverse) >> 16;
     const float c2 = p.c2, slack = fminf(kSlack / c2, 3.0e38f);
     bool ok = true;
     int n = 0;  // tiles of this warpgroup so far
@@ -815,29 +1008,24 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       const bool some = part.lo < part.hi, alone = k.first() && k.last();
       const int64_t unit0 = k.at.item - k.at.off;
       const int c0 = alone ? 0 : cta_of(total, unit0, runs), c1 = alone ? 0 : cta_of(total, unit0 + k.items - 1, runs);
-      constexpr int64_t kPart = 128 * (D + 2) * 4;  // bytes of one tile's part: (reference, sum) of each row, then O
-      auto part_at = [&](int cta) { return p.parts + (static_cast<int64_t>(2 * cta + (cta == c0 ? 1 : 0)) * NQ + q) * kPart; };
-      char* to = alone ? nullptr : part_at(blockIdx.x);
+      char* to = alone ? nullptr : part_at<D, NQ>(p, c0, blockIdx.x, q);
       const int rows = least(k.s.n - i0, p.tokens_per_tile) * p.group;  // of this tile
-      auto out_at = [&](int r) {
-        const int tk = r / p.group, hd = r - tk * p.group;
-        return static_cast<bf16*>(p.a.out) + (static_cast<int64_t>(k.s.first) + i0 + tk) * p.a.ld_out + (static_cast<int64_t>(k.at.head) * p.group + hd) * p.a.hs_out;
-      };
-      auto set_lse = [&](int r, float reference, float sum) {
-        if (p.a.lse == nullptr) return;
-        const int tk = r / p.group, hd = r - tk * p.group;
-        p.a.lse[(static_cast<int64_t>(k.s.first) + i0 + tk) * p.a.q_heads + k.at.head * p.group + hd] = sum == 0.0f ? -INFINITY : (reference + log2f(sum)) * kLn2;
-      };
-      auto put8 = [&](int r, int d, const float (&y)[8], float sum, float inv) {  // 8 elements of a row, done or as they are
+      auto set_lse = [&](int r, float reference, float sum) { put_lse(p, static_cast<int64_t>(k.s.first) + i0, k.at.head * p.group, r, reference, sum); };
+      // where this thread puts elements of its row (SPREAD: of the row that it adds up), done or as they are
+      const int own = SPREAD ? static_cast<int>(threadIdx.x) >> 2 : row, block = own & ~31, across = least(rows - block, 32);
+      char* const place = own >= rows ? nullptr
+                          : alone     ? reinterpret_cast<char*>(row_of(p, static_cast<int64_t>(k.s.first) + i0, k.at.head * p.group, own))
+                                      : to + 1024 + 16 * (block * (D / 4) + own - block);
+      auto put8 = [&](int d, const float (&y)[8], float sum, float inv) {
         if (alone) {
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = sum == 0.0f ? 0u : heads::pack(y[2 * j] * inv, y[2 * j + 1] * inv);
-          *reinterpret_cast<uint4*>(out_at(r) + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(place + 2 * d) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-          float4* o = reinterpret_cast<float4*>(to + 1024 + (static_cast<int64_t>(r) * D + d) * 4);
+          float4* o = reinterpret_cast<float4*>(place) + (d / 4) * across;
           __stcg(o, make_float4(y[0], y[1], y[2], y[3]));
-          __stcg(o + 1, make_float4(y[4], y[5], y[6], y[7]));
+          __stcg(o + across, make_float4(y[4], y[5], y[6], y[7]));
         }
       };
       auto add_unusual = [&](int d, float (&x)[8]) {  // what was taken out of the values that this thread's row sees
@@ -906,7 +1094,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
                 y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w, y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
               }
             }
-            put8(r, d + 8 * e0, y, s.y, inv);
+            put8(d + 8 * e0, y, s.y, inv);
           }
           bar_sync(1, 128);
         }
@@ -941,7 +1129,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(x[8 * e + j]);
             if (dirty) add_unusual(d + 8 * e, y);
-            put8(row, d + 8 * e, y, l, inv);
+            put8(d + 8 * e, y, l, inv);
           }
         }
         if (valid && alone) set_lse(row, m * c2, l);
@@ -951,77 +1139,9 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       if (!alone) {
         __threadfence();
         bar_sync(1 + q, 128);
-        if ((threadIdx.x & 127) == 0) {
-          const unsigned before = atomicAdd(p.counters + 2 * c0 + q, 1u);
-          misc->last[q] = before == static_cast<unsigned>(c1 - c0);
-          if (misc->last[q]) p.counters[2 * c0 + q] = 0u;
-        }
-        bar_sync(1 + q, 128);
-        if (misc->last[q]) {
-          __threadfence();
-          // first each row's reference and sum over the parts, then the rows' elements, 16 bytes a thread: several parts' loads at
-          // once where there are few rows and many parts, several rows' otherwise (one after the other an end took 50 us
-          // of two tiles' 256 rows)
-          float2* stats = reinterpret_cast<float2*>(smem + F::OFF_STATS) + 128 * q;
-          const int t = threadIdx.x & 127;
-          if (t < rows) {
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(part_at(c)) + t).x);
-            if (top == -INFINITY) top = 0.0f;
-#pragma unroll 8
-            for (int c = c0; c <= c1; ++c) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_at(c)) + t);
-              sum = fmaf(exp2_of(ml.x - top), ml.y, sum);
-            }
-            set_lse(t, top, sum);
-            stats[t] = make_float2(top, sum == 0.0f ? 0.0f : 1.0f / sum);
-          }
-          bar_sync(1 + q, 128);
-          const int all = rows * (D / 4);
-          auto add = [&](float4& o, const float2& ml, const float4& y, float top) {
-            const float w = exp2_of(ml.x - top);
-            if (ml.y != 0.0f) o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);  // (0: a part that saw nothing)
-          };
-          auto ml_at = [&](int c, int x) { return __ldcg(reinterpret_cast<const float2*>(part_at(c)) + x / (D / 4)); };
-          auto o_at_part = [&](int c, int x) { return __ldcg(reinterpret_cast<const float4*>(part_at(c) + 1024) + x); };
-          auto finish = [&](int x, const float4& o) {
-            const int r = x / (D / 4);
-            const float inv = stats[r].y;
-            *reinterpret_cast<uint2*>(out_at(r) + 4 * (x - r * (D / 4))) =
-                inv == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
-          };
-          if (all <= 512) {
-#pragma unroll 1
-            for (int x = t; x < all; x += 128) {
-              const float top = stats[x / (D / 4)].x;
-              float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-              for (int c = c0; c <= c1; ++c) add(o, ml_at(c, x), o_at_part(c, x), top);
-              finish(x, o);
-            }
-          } else {
-            constexpr int kBatch = 8;
-#pragma unroll 1
-            for (int x0 = t; x0 < all; x0 += 128 * kBatch) {
-              float4 o[kBatch] = {};
-#pragma unroll 1
-              for (int c = c0; c <= c1; ++c) {
-                float4 y[kBatch];
-                float2 ml[kBatch];
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                  ml[b] = ml_at(c, least(x0 + 128 * b, all - 1));
-                  y[b] = o_at_part(c, least(x0 + 128 * b, all - 1));
-                }
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) add(o[b], ml[b], y[b], stats[least(x0 + 128 * b, all - 1) / (D / 4)].x);
-              }
-#pragma unroll
-              for (int b = 0; b < kBatch; ++b)
-                if (x0 + 128 * b < all) finish(x0 + 128 * b, o[b]);
-            }
-          }
+        if ((threadIdx.x & 127) == 0 && atomicAdd(p.counters + 2 * c0 + q, 1u) == static_cast<unsigned>(c1 - c0)) {
+          p.counters[2 * c0 + q] = 0u;
+          misc->join[2 * q + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)] = Join{static_cast<int64_t>(k.s.first) + i0, k.at.head * p.group, rows, c0, c1};
         }
       }
     }
@@ -1032,17 +1152,30 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  uint32_t phase = 0;
+  bool joined = true;
+#pragma unroll 1
+  for (int i = 0; i < 2 * NQ && joined; ++i)
+    if (misc->join[i].rows > 0) joined = join_parts<D, NQ, F::THREADS>(p, misc->join[i], i >> 1, smem, reinterpret_cast<float*>(smem + F::OFF_STATS), bar_join, phase);
+  if (!joined) settle();  // (copies may be in flight)
 }
 
 int ctas() { return min(num_sms(), kMaxCtas); }
 
-// Two tiles of rows where units have more than one tile's on average.
-bool two_tiles(const Attention& a, const Cache& c, const Batch& b) { return b.tokens * (a.q_heads / c.heads) > static_cast<int64_t>(b.seqs) * kTile; }
-
-// And one tile of 32 rows, four times over, where they have fewer still.
+// Which form, by the rows that a sequence has for a cache head on average (the lengths are on the device). Measured with 64 sequences
+// over 4096 keys, 8 heads, D 128, in us:
+//   rows              4     16     32     36     64    128    132    192    256
+//   32, four times  174.5  179.9  181.7  336.5  339.1                              (8-bit: 167  180  181  327  338)
+//   one tile        176.6  182.0  182.9  186.0  190.0  200.4  358.2  361.2  365.7  (8-bit: 221  235  235  240  242  251  450)
+//   two tiles       177.7  184.6  186.5  189.3  193.2  204.4  229.1  235.6  243.3  (8-bit: 204  215  214  215  217  224  255)
+// (D 64: 94, 134 and 144 with 4 rows; one token over 100 keys, D 64: 6.1, 6.6 and 6.8). So up to 32 rows: a tile of 32, each of the
+// four warps of weights with its own quarter of the keys. Above: two tiles, but one in bf16 where units do not fill it.
 bool spread(const Attention& a, const Cache& c, const Batch& b) {
   const int64_t group = a.q_heads / c.heads;
   return group <= 32 && b.tokens * group <= static_cast<int64_t>(b.seqs) * 32;
+}
+bool two_tiles(const Attention& a, const Cache& c, const Batch& b) {
+  return !spread(a, c, b) && (c.mx || b.tokens * (a.q_heads / c.heads) > static_cast<int64_t>(b.seqs) * kTile);
 }
 
 template <int D, bool MX, int NQ, bool SPREAD>
@@ -1066,6 +1199,7 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
   p.c = c;
   p.b = b;
   p.group = a.q_heads / c.heads;
+  p.group_inverse = (65536 + p.group - 1) / p.group;
   const bool two = two_tiles(a, c, b), four = spread(a, c, b);
   p.tokens_per_tile = (four ? 32 : kTile) / p.group;
   // (a cache without pages holds nothing, and the tensor maps need an address)
@@ -1117,12 +1251,13 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-#define FP8GB_FORM(D, MX)                                          \
-  (two    ? launch_form<D, MX, 2, false>(mq, mk, mv, p, stream)      \
-   : four ? launch_form<D, MX, 1, true>(mq, mk, mv, p, stream)       \
-          : launch_form<D, MX, 1, false>(mq, mk, mv, p, stream))
-  if (c.head_dim == 64) return c.mx ? FP8GB_FORM(64, true) : FP8GB_FORM(64, false);
-  return c.mx ? FP8GB_FORM(128, true) : FP8GB_FORM(128, false);
+#define FP8GB_FORM(D, MX, NQ, SPREAD) launch_form<D, MX, NQ, SPREAD>(mq, mk, mv, p, stream)
+  if (c.mx) {
+    if (c.head_dim == 64) return four ? FP8GB_FORM(64, true, 1, true) : FP8GB_FORM(64, true, 2, false);
+    return four ? FP8GB_FORM(128, true, 1, true) : FP8GB_FORM(128, true, 2, false);
+  }
+  if (c.head_dim == 64) return two ? FP8GB_FORM(64, false, 2, false) : four ? FP8GB_FORM(64, false, 1, true) : FP8GB_FORM(64, false, 1, false);
+  return two ? FP8GB_FORM(128, false, 2, false) : four ? FP8GB_FORM(128, false, 1, true) : FP8GB_FORM(128, false, 1, false);
 #undef FP8GB_FORM
 }
 
