@@ -138,6 +138,8 @@ Cache to_cache(const fp8_kv_cache_t* c) {
 }
 Batch to_batch(const fp8_kv_batch_t* b) { return Batch{b->tokens, b->ld_table, b->seqs, b->table_width, b->q_start, b->kv_len, b->page_table}; }
 
+Attention to_attention(const fp8_paged_attention_t* a) { return Attention{a->q_heads, a->window, a->scale, a->q, a->out, a->ld_q, a->hs_q, a->ld_out, a->hs_out, a->lse}; }
+
 fp8_status_t check_attention(const fp8_paged_attention_t* a, const fp8_kv_cache_t* c, const fp8_kv_batch_t* b, const char* who) {
   if (a == nullptr) return fail(FP8_ERR_INVALID_ARG, "%s: null arguments", who);
   FP8GB_TRY(check_cache(c, who));
@@ -152,16 +154,17 @@ fp8_status_t check_attention(const fp8_paged_attention_t* a, const fp8_kv_cache_
   if (b->tokens > 0 && (a->q == nullptr || a->out == nullptr)) return fail(FP8_ERR_INVALID_ARG, "%s: null q or out", who);
   FP8GB_TRY(check_heads(a->q, a->ld_q, a->hs_q, b->tokens, a->q_heads, c->head_dim, 2, who, "q"));
   FP8GB_TRY(check_heads(a->out, a->ld_out, a->hs_out, b->tokens, a->q_heads, c->head_dim, 2, who, "out"));
+  FP8GB_TRY(check_in_place(a->q, a->ld_q, a->hs_q, a->out, a->ld_out, a->hs_out, b->tokens, a->q_heads, who, "q"));
   const int64_t limit = 1ll << 40;
   if (a->ld_q > limit || a->hs_q > limit) return fail(FP8_ERR_UNSUPPORTED, "%s: a stride of q above 2^40", who);
   auto whole = [&](int64_t ld, int64_t hs) { return (b->tokens <= 1 || ld % 8 == 0) && (a->q_heads <= 1 || hs % 8 == 0); };
   if (!aligned16(a->q) || !aligned16(a->out) || !whole(a->ld_q, a->hs_q) || !whole(a->ld_out, a->hs_out))
     return fail(FP8_ERR_ALIGNMENT, "%s: q and out must be 16-byte aligned with strides of multiples of 8", who);
   if (!aligned_to(a->lse, 4)) return fail(FP8_ERR_ALIGNMENT, "%s: lse is not aligned to its elements", who);
+  const char* why = paged_attention_refusal(to_attention(a), to_cache(c), to_batch(b));
+  if (why != nullptr) return fail(FP8_ERR_UNSUPPORTED, "%s: %s", who, why);
   return FP8_OK;
 }
-
-Attention to_attention(const fp8_paged_attention_t* a) { return Attention{a->q_heads, a->window, a->scale, a->q, a->out, a->ld_q, a->hs_q, a->ld_out, a->hs_out, a->lse}; }
 
 }  // namespace
 

@@ -276,5 +276,6 @@ constexpr int kAttendMaxSeqs = 16384;  // sequences of one call (their costs are
 // tokens, seqs > 0
 cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Batch& b, void* ws, cudaStream_t stream, const char** why);
 int64_t paged_attention_workspace_bytes(const Attention& a, const Cache& c, const Batch& b);
+const char* paged_attention_refusal(const Attention& a, const Cache& c, const Batch& b);  // why sizes or strides are not supported, or null
 
 }  // namespace fp8gb

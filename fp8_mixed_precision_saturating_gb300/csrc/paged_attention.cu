@@ -329,6 +329,9 @@ __device__ __forceinline__ __nv_bfloat162 bf16_pair(uint32_t bits) {
   return v;
 }
 
+// What a row's elements are divided by: 0 for a row that saw nothing, NaN under a score of +infinity (infinity over infinity).
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.0f ? 0.0f : isinf(sum) ? __int_as_float(0x7FFFFFFF) : 1.0f / sum; }
+
 // A value of the cache that is not finite, or 0.
 template <bool MX, int D>
 __device__ float unusual(const Params& p, int64_t row, int64_t unit, int d) {
@@ -403,7 +406,7 @@ __device__ __noinline__ bool join_parts(const Params& p, const Join u, int q, ui
       }
     }
     if (d == 0) put_lse(p, u.token, u.head, r, top, sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = inverse_of(sum);
     *reinterpret_cast<uint2*>(row_of(p, u.token, u.head, r) + 4 * d) =
         inv == 0.0f ? make_uint2(0u, 0u) : make_uint2(heads::pack(o.x * inv, o.y * inv), heads::pack(o.z * inv, o.w * inv));
     return true;
@@ -456,7 +459,7 @@ __device__ __noinline__ bool join_parts(const Params& p, const Join u, int q, ui
         for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (r < rows && l == 0) {
           if (d0 == 0) put_lse(p, u.token, u.head, r0 + r, top, sum);
-          inverse[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+          inverse[r] = inverse_of(sum);
         }
       }
       __syncthreads();
@@ -886,7 +889,8 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_at = tmem + lanes + 256 + 128 * q;
     const int token = (row * p.group_inverse) >> 16;
-    const float c2 = p.c2, slack = fminf(kSlack / c2, 3.0e38f);
+    // (a score of +infinity: the reference stays finite, so that the weight and the sum become infinite and not NaN)
+    const float c2 = p.c2, slack = fminf(kSlack / c2, 3.0e38f), highest = fminf(3.0e38f / c2, 3.0e38f);
     bool ok = true;
     int n = 0;  // tiles of this warpgroup so far
     // A step's slot, and its barriers' phase. When the scores of a step are there, the product with the values of the last step but one is
@@ -954,7 +958,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
             top = fmaxf(top, top1);
             const bool move = valid && top > limit;
             if (__any_sync(0xFFFFFFFFu, move)) {  // the reference moves
-              const float to = move ? top : m;
+              const float to = move ? fminf(top, highest) : m;
               if (t > part.lo || half > 0) {
                 const float f = move ? exp2_of((m - to) * c2) : 1.0f;
                 l *= f;
@@ -1066,7 +1070,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
         const float f = exp2_of(m * c2 - joined(lane).x);
         const int r = threadIdx.x >> 2, e0 = threadIdx.x & 3;  // a row and 8 of 32 columns
         const float2 s = joined(r);
-        const float inv = s.y == 0.0f ? 0.0f : 1.0f / s.y;
+        const float inv = inverse_of(s.y);
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           if (some) {
@@ -1110,7 +1114,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
           if (threadIdx.x == 0) mbar_arrive(q_empty + 8 * (k.filled & 1));
         }
       } else if (any) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = inverse_of(l);
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t x[32];
@@ -1178,6 +1182,19 @@ bool two_tiles(const Attention& a, const Cache& c, const Batch& b) {
   return !spread(a, c, b) && (c.mx || b.tokens * (a.q_heads / c.heads) > static_cast<int64_t>(b.seqs) * kTile);
 }
 
+// A bf16 cache's pages and heads as one dimension of its tensor maps, at the strides' common part.
+struct Steps {
+  int64_t unit, page, head, all;
+};
+Steps steps_of(const Cache& c) {
+  const int64_t ps = c.pages > 1 ? c.page_stride : 0, hs = c.heads > 1 ? c.head_stride : 0, both = std::gcd(ps, hs), unit = both != 0 ? both : c.token_stride;
+  return Steps{unit, ps / unit, hs / unit, (static_cast<int64_t>(max(c.pages, 1)) - 1) * (ps / unit) + (c.heads - 1) * (hs / unit) + 1};
+}
+
+int tokens_of_tile(const Attention& a, const Cache& c, const Batch& b) { return (spread(a, c, b) ? 32 : kTile) / (a.q_heads / c.heads); }
+// (a cache without pages holds nothing, and the tensor maps need an address)
+int reach_of(const Cache& c, const Batch& b) { return static_cast<int>(min(c.pages > 0 ? static_cast<int64_t>(b.table_width) << c.page_bits : 0, int64_t{0x7FFFFF00})); }
+
 template <int D, bool MX, int NQ, bool SPREAD>
 cudaError_t launch_form(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Params& p, cudaStream_t stream) {
   using F = Form<D, MX, NQ, SPREAD>;
@@ -1188,6 +1205,18 @@ cudaError_t launch_form(const CUtensorMap& q, const CUtensorMap& k, const CUtens
 }
 
 }  // namespace
+
+const char* paged_attention_refusal(const Attention& a, const Cache& c, const Batch& b) {
+  if (!c.mx && steps_of(c).all > 0x7FFFFFFF) return "pages and heads of the cache lie at strides whose common part is too small";
+  const int64_t limit = int64_t{1} << 39;  // tensor maps' strides are below 2^40 bytes, the widest one here 16 tokens of bf16
+  auto far = [&](int64_t n, int64_t stride) { return n > 1 && stride >= limit; };
+  if (c.token_stride >= limit / 16 || far(c.heads, c.head_stride) || far(c.pages, c.page_stride) || far(b.tokens, a.ld_q) || far(a.q_heads, a.hs_q)) return "a stride of 2^39 elements or more (2^35 between a cache's tokens)";
+  // tiles of keys over blocks of rows, counted in 32 bits per sequence and in 64 over all of them (times the CTAs)
+  const int64_t per = (two_tiles(a, c, b) ? 2 : 1) * tokens_of_tile(a, c, b);
+  const __int128 tiles = static_cast<__int128>(b.tokens / per + 1) * (reach_of(c, b) / kTile + 1);
+  if (tiles >= 0xFFFFFFFF || tiles * max(b.seqs, 1) * c.heads >= (static_cast<__int128>(1) << 54)) return "more tokens over a longer table than a call counts";
+  return nullptr;
+}
 
 int64_t paged_attention_workspace_bytes(const Attention& a, const Cache& c, const Batch& b) {
   return kCounterBytes + static_cast<int64_t>(ctas()) * 2 * (two_tiles(a, c, b) ? 2 : 1) * 128 * (c.head_dim + 2) * 4;
@@ -1201,10 +1230,8 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
   p.group = a.q_heads / c.heads;
   p.group_inverse = (65536 + p.group - 1) / p.group;
   const bool two = two_tiles(a, c, b), four = spread(a, c, b);
-  p.tokens_per_tile = (four ? 32 : kTile) / p.group;
-  // (a cache without pages holds nothing, and the tensor maps need an address)
-  const int64_t reach = c.pages > 0 ? static_cast<int64_t>(b.table_width) << c.page_bits : 0;
-  p.capacity = static_cast<int>(min(reach, int64_t{0x7FFFFF00}));
+  p.tokens_per_tile = tokens_of_tile(a, c, b);
+  p.capacity = reach_of(c, b);
   // scale 0: every weight is 1, and -infinity times it stays -infinity
   p.c2 = max(std::fabs(a.scale) * kLog2e, 1.0e-44f);
   p.flip = a.scale < 0.0f;
@@ -1234,16 +1261,11 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
   } else {
     // a tile's rows by groups of 8, both panels of a group one after the other: with a box for each panel the two halves of
     // a row's 256 bytes were fetched far apart (64 tokens over 4096: 1.0 TB/s with 128 rows a box, 5.8 with 16, 6.1 so)
-    const int64_t ps = c.pages > 1 ? c.page_stride : 0, hs = c.heads > 1 ? c.head_stride : 0, both = std::gcd(ps, hs), unit = both != 0 ? both : c.token_stride;
-    const int64_t steps = (static_cast<int64_t>(pages) - 1) * (ps / unit) + (c.heads - 1) * (hs / unit) + 1;
-    if (steps > 0x7FFFFFFF) {
-      *why = "pages and heads of the cache lie at strides whose common part is too small";
-      return cudaErrorInvalidValue;
-    }
-    p.page_steps = static_cast<int>(ps / unit);
-    p.head_steps = static_cast<int>(hs / unit);
-    const uint64_t dims[5] = {64, 8, D / 64, static_cast<uint64_t>(c.page_size / 8), static_cast<uint64_t>(steps)};
-    const uint64_t strides[4] = {static_cast<uint64_t>(2 * c.token_stride), 128, static_cast<uint64_t>(16 * c.token_stride), static_cast<uint64_t>(2 * unit)};
+    const Steps steps = steps_of(c);
+    p.page_steps = static_cast<int>(steps.page);
+    p.head_steps = static_cast<int>(steps.head);
+    const uint64_t dims[5] = {64, 8, D / 64, static_cast<uint64_t>(c.page_size / 8), static_cast<uint64_t>(steps.all)};
+    const uint64_t strides[4] = {static_cast<uint64_t>(2 * c.token_stride), 128, static_cast<uint64_t>(16 * c.token_stride), static_cast<uint64_t>(2 * steps.unit)};
     const uint32_t box[5] = {64, 8, static_cast<uint32_t>(D / 64), rows / 8, 1};
     made = made && encode_tmap_nd(&mk, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, dims, strides, box, 128) && encode_tmap_nd(&mv, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, dims, strides, box, 128);
   }

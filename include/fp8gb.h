@@ -650,6 +650,7 @@ int64_t fp8_qk_rope_bwd_workspace_bytes(const fp8_qk_rope_t* f, const fp8_qk_rop
  *                   448 * 2^e >= the group's amax (0 for a zero amax, at least -127), in k_scale and v_scale as the byte e + 127,
  *                   [pages, heads, page_size, head_dim / 32] contiguous. An infinity saturates (it counts as the
  *                   largest finite bf16); a group that holds a NaN has the scale 0xFF and stands for NaNs.
+ *                   (Codes 0x7F and 0xFF, which fp8_kv_append never writes, read as +-480 units.)
  * page_size: a power of two, 8 .. 4096. All buffers 16-byte aligned, strides of whole 16 bytes. */
 typedef enum { FP8_KV_BF16 = 0, FP8_KV_MX_E4M3 = 1 } fp8_kv_format_t;
 typedef struct {
@@ -691,8 +692,9 @@ fp8_status_t fp8_kv_append(const fp8_qk_rope_t* f, const fp8_kv_cache_t* c, cons
  * A row that sees nothing, or only keys of weight 0, gets out = 0 and lse = -infinity. Keys and values in masked places do not
  * touch a row, whatever they are. Products with fp32 accumulation, statistics in fp32; the weights are rounded to bf16 for the second
  * product (their sum is not). q, out: bf16 head tensors [tokens, q_heads, head_dim], 16-byte aligned, strides multiples of 8;
- * lse [tokens, q_heads] fp32. head_dim 64 or 128; q_heads a multiple of the cache's heads, at most 128 times as many; at most 16384
- * sequences. */
+ * lse [tokens, q_heads] fp32; out may be q itself with the same strides. head_dim 64 or 128; q_heads a multiple of the cache's heads,
+ * at most 128 times as many; at most 16384 sequences; strides below 2^39 elements (2^35 between a cache's tokens), those of a bf16 cache's
+ * pages and heads with a common part of which they hold no more than 2^31 together; tokens times the table's reach of some 10^13. */
 typedef struct {
   int32_t q_heads;
   int32_t window;

@@ -175,6 +175,21 @@ def test_attention(g):
         g.fp8_paged_attention_workspace_bytes(attn(window=-1), cache(g), batch(g))
 
 
+def test_attention_out_of_reach(g):
+    def attn(**kw):
+        return g.paged_attention(kw.pop("q_heads", 4), 0.125, **{**dict(q=A, ld_q=256, hs_q=64, out=B, ld_out=256, hs_out=64), **kw})
+    name, ws, un = "fp8_paged_attention", (S, 1 << 50), g.FP8_ERR_UNSUPPORTED
+    odd = dict(heads=2, head_stride=1024, pages=32768, page_stride=8 * 131101)  # a common part of 8: 2^32 of them
+    refused(g, un, "common part", name, attn(), cache(g, **odd), batch(g), *ws)
+    for kw in (dict(page_stride=1 << 39), dict(token_stride=1 << 35, page_stride=1 << 40)):
+        refused(g, un, "2^39", name, attn(), cache(g, pages=2, **kw), batch(g), *ws)
+    refused(g, un, "2^39", name, attn(ld_q=1 << 39), cache(g), batch(g), *ws)
+    refused(g, g.FP8_ERR_INVALID_ARG, "in place", name, attn(out=A, ld_out=512), cache(g), batch(g), *ws)
+    refused(g, un, "longer table", name, attn(), cache(g), batch(g, tokens=1 << 30, table_width=1 << 30, ld_table=1 << 30), *ws)
+    a, c, b = attn(ld_q=1 << 39, hs_q=1 << 39, q_heads=1), cache(g, pages=1, page_stride=1 << 39, head_stride=1 << 39), batch(g, tokens=1)  # (strides that nothing uses)
+    assert g.lib.fp8_paged_attention_workspace_bytes(a, c, b) >= 0
+
+
 def test_blocks_of_tensors(g):
     z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
     x = z(4, 6, 64)
