@@ -6,7 +6,7 @@
 // weights in registers, P = bf16(weights) back to tensor memory over S, O += P V with P read from there. A CTA stays on its
 // SM and works through a run of tiles (attend_walk.cuh); its warps divide the work:
 //   0-3 (and 4-7)  weights, one thread per row: 128 rows of a tile each
-//   the next 4 or 8  keys and values on their way: 8-bit codes into bf16 (exactly: a code times a power of two), and what must not be
+//   the next 4 or 8  keys and values on their way: 8-bit codes into bf16 (a code times a power of two: exact down to bf16's smallest numbers), and what must not be
 //                  multiplied by a weight of zero out of the last tiles (below)
 //   the last ones  copies (TMA, one box per page), tensor-core instructions (a thread per tile of rows)
 // Three forms (chosen at the end of this file): two tiles of rows over the same keys, one's weights worked out while the other is on the tensor cores (NQ 2);
@@ -633,9 +633,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
         if (!ok) break;
       }
     }
-    if (!ok) {  // let the copies in flight land (microseconds) before the CTA can exit
-      settle();
-    }
+    if (!ok) settle();
   } else if (warp >= F::MMA_WARP) {
     // ---- tensor-core instructions --------------------------------------------------------------------------------------
     // One thread for each tile of rows: with the whole warp walking along and electing a thread for each group of instructions, votes and

@@ -707,7 +707,7 @@ typedef struct {
 } fp8_paged_attention_t;
 
 /* workspace: device, 16-byte aligned, fp8_paged_attention_workspace_bytes(a, c, b) bytes (which does not depend on the lengths), zero-filled before
- * its first use and left reusable by every successful call; calls that may overlap need their own. The result
+ * its first use and left reusable by every successful call (of this function: others leave other things); calls that may overlap need their own. The result
  * depends on nothing but the inputs. */
 fp8_status_t fp8_paged_attention(const fp8_paged_attention_t* a, const fp8_kv_cache_t* c, const fp8_kv_batch_t* b, void* workspace,
                                  int64_t workspace_bytes, void* stream);

@@ -1,5 +1,6 @@
 """Refusals of the heads', cache's and attention's entry points, on CPU: every call below is refused before it touches the GPU, the same
 way through both bindings. Device addresses are made-up numbers; nothing is dereferenced."""
+import ctypes
 import math
 
 import pytest
@@ -233,3 +234,14 @@ def test_blocks_of_tensors(g):
     for kw in (dict(q=z(6, 4, 64)), dict(out=z(7, 4, 32)), dict(lse=torch.zeros(6, 4))):
         with pytest.raises(ValueError):
             g.fp8_paged_attention_workspace_bytes(g.paged_attention(4, 1.0, **{**dict(q=z(7, 4, 64), out=z(7, 4, 64)), **kw}), cc, b)
+
+
+def test_blocks_exchanged(g):
+    f, c, b, a = g.qk_rope(0, 1, 1, 64, 0, 0), g.fp8_kv_cache_t(), g.fp8_kv_batch_t(), g.paged_attention(1, 1.0)
+    grad = g.qk_rope_grad()
+    for name, calls in (("fp8_kv_append", ((f, b, c), (c, c, b), (f, c, f), (bytes(512), c, b))), ("fp8_paged_attention", ((a, b, c, None, 0), (f, c, b, None, 0), (a, c, a, None, 0))),
+                        ("fp8_qk_rope_fwd", ((grad,), (c,))), ("fp8_qk_rope_bwd", ((grad, f, None, 0), (f, f, None, 0)))):
+        for fn in {getattr(g, name), getattr(g, "_by_ctypes", {}).get(name, getattr(g, name))}:
+            for args in calls:
+                with pytest.raises((TypeError, ctypes.ArgumentError)):
+                    fn(*args)
