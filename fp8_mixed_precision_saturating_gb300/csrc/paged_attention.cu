@@ -16,6 +16,14 @@
 // The reference moves only where a row's maximum passes it by more than 8 (in log2 of the weights; below, exp cannot overflow
 // and fp32 sums lose nothing): then O in tensor memory and the sum are scaled, otherwise O is never touched.
 //
+// P is rounded to bf16 because the tensor cores take both operands of the second product in 16 bits; the sum of the weights is of the unrounded ones, so
+// that the roundings (half a step, 2^-9 on average) stay independent errors of the terms and not of the whole.
+//
+// Measured (4 query heads to each of 8 cache heads, D 128): 64 tokens over 4096 keys each 170 us, 6.3 TB/s, 0.93 of a copy's rate: memory; the
+// same in 8 bits 156 us, 3.5 TB/s: shared memory's bandwidth (the conversion's and the tensor cores' together 0.8 of it). A chunk
+// of 2048 tokens over 16384 keys 361 us, 1430 TFLOP/s, 0.75 of a large product's rate: the weights' arithmetic, of which a tile's 64 keys take
+// some 1700 clocks and their products 1370. One token over 100 keys 7 us: the chain launch, lengths, page table, keys, scores, weights, output.
+//
 // Masked places. Weights are set, not added to, so keys may be anything. A value that is not finite would make 0 * inf of a
 // weight of zero: in tiles with keys that some row does not see (the last ones, and the first ones of a window) values
 // behind the end become zero, and others that are not finite become zero as well and are added at the end to the rows that see them.
@@ -51,20 +59,22 @@ struct Form {
   // keys and values: groups of 8 rows, each panel's 8 x 128 bytes after the other (queries: a panel's 128 rows together)
   static constexpr int GROUP = PANELS * 1024;
   static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 4 : 8);
-  static constexpr int RAW = 128 * D + 4 * D;   // 128 rows of codes and their units
+  static constexpr int RAW = 128 * D, UNITS = 4 * D;  // 128 rows of codes (rows of 128: their 16-byte pieces in the copy's swizzle), and their units
   static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 8 : 6)) : 0;
   // warps: weights, then those that work on keys and values on their way, one for the copies, one or two for the tensor cores
   static constexpr int PREP_WARP = NQ == 1 ? 4 : 8, PREP_WARPS = 12 - PREP_WARP;
-  // On one 8-bit tile; one tile of rows: keys and values side by side (64 tokens over 4096 keys: 167 us). Not better: 8 warps on each
-  // tile and three stages in turn, queries in one buffer, 182 us; stages of 64 rows, two for the keys and two for the values,
-  // 185 us. Shared memory is what they all wait for: the codes in and out, the bf16 in, and each read once by the tensor cores.
+  // On one 8-bit tile; one tile of rows: keys and values side by side (64 tokens over 4096 keys of 8 heads of 128: 156 us; 165 while the
+  // lanes that read a row's codes and write its panels met in the banks). Not better, measured then: 8 warps on each tile and three stages in turn,
+  // queries in one buffer, 174 us; stages of 64 rows, two for the keys and two for the values, 185. Shared memory is what they all
+  // wait for: the codes in and out, the bf16 in, and each read once by the tensor cores.
   static constexpr int GROUP_WARPS = 4;
   static constexpr int COPY_WARP = PREP_WARP + PREP_WARPS, MMA_WARP = COPY_WARP + 1, WARPS = MMA_WARP + NQ, THREADS = 32 * WARPS;
   static_assert(NQ == 2 || NQ == 1, "tiles");
   static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
   static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
   static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
-  static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW > kJoinBytes ? OFF_RAW + RAWS * RAW : kJoinBytes;
+  static constexpr int OFF_UNITS = OFF_RAW + RAWS * RAW, OFF_END = OFF_UNITS + RAWS * UNITS;
+  static constexpr int OFF_BAR = OFF_END > kJoinBytes ? OFF_END : kJoinBytes;
   static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 12 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int OFF_STATS = OFF_MISC + 512;  // (reference, sum) of each row, SPREAD: of each warp's rows
@@ -73,7 +83,7 @@ struct Form {
   // different waiters (the warps that look at bf16 values, the two groups that convert 8-bit tiles) a stage is always
   // one or the other's.
   static_assert(MX ? NQ == 2 || (STAGES % 2 == 0 && RAWS % 2 == 0) : STAGES % 2 == 0, "stages");
-  static_assert(RAW % 128 == 0 && OFF_RAW % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
+  static_assert(RAW % 1024 == 0 && OFF_RAW % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
   static_assert(OFF_RAW >= 4 * kAttendMaxSeqs, "room for the sequences' costs");
 };
 
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
             }
             __syncwarp();
             if (lane < boxes) tma_load_4d(dst + lane * rows * D, map, bar, 0, within, k.at.head, page);
-            if (unit_row < left && unit_page >= 0) async_load16(dst + 128 * D + 16 * lane, (kv == 0 ? p.c.k_scale : p.c.v_scale) + unit_at);
+            if (unit_row < left && unit_page >= 0) async_load16(base + F::OFF_UNITS + slot * F::UNITS + 16 * lane, (kv == 0 ? p.c.k_scale : p.c.v_scale) + unit_at);
             async_arrive(bar);
           }
           __syncwarp();
@@ -816,18 +826,20 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_full + 8 * raw, (u / F::RAWS) & 1, p.w, DEV_ERR_WAIT_EPILOGUE));
             if (!ok) break;
             const uint8_t* codes = smem + F::OFF_RAW + raw * F::RAW;
-            const uint8_t* units = codes + 128 * D;
+            const uint8_t* units = smem + F::OFF_UNITS + raw * F::UNITS;
             uint8_t* out = smem + F::OFF_KV + slot * F::TILE;
             const uint32_t lost = misc->bad[raw];
             bool bad = false;
-            // a thread's 16 columns of every kStep-th row; the swizzle's place is the same in all of them
+            // A thread's 16 columns (number c) of every kStep-th row; the swizzles' places are the same in all of them. Rows of 128: eight
+            // lanes take four c of rows r and r ^ 5, which meet in no bank, neither in the codes nor in the panels.
             constexpr int kLanes = D / 16, kStep = kGroup / kLanes, kRows = 128 / kStep;
-            const int row0 = tid / kLanes, c = tid % kLanes;
+            const int pair = (tid >> 4) & 3, row0 = D == 128 ? 8 * (tid >> 6) + (tid & 4 ? pair ^ 5 : pair) : tid / kLanes;
+            const int c = D == 128 ? (tid & 3) + ((tid >> 1) & 4) : tid % kLanes, at = row0 * kLanes + (D == 128 ? c ^ (row0 & 7) : c);
             uint4 x[kRows];
             uint32_t unit[kRows], largest = 0u;
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
-              x[j] = reinterpret_cast<const uint4*>(codes)[tid + kGroup * j];
+              x[j] = reinterpret_cast<const uint4*>(codes)[at + kGroup * j];
               unit[j] = units[(row0 + j * kStep) * (D / 32) + c / 2];
             }
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
@@ -852,12 +864,12 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
 #pragma unroll 1
               for (int j = 0; j < kRows; ++j) {
                 const int row = row0 + j * kStep;
-                const uint32_t at = units[row * (D / 32) + c / 2];
+                const uint32_t byte = units[row * (D / 32) + c / 2];
                 uint32_t y[8], any = 0u;
-                decode16(reinterpret_cast<const uint4*>(codes)[tid + kGroup * j], bf16_pair(0x7B80u), y);  // in two factors
+                decode16(reinterpret_cast<const uint4*>(codes)[at + kGroup * j], bf16_pair(0x7B80u), y);  // in two factors
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  y[e] = times(y[e], bf16_pair(at == 255u ? 0x7FC0u : at == 0u ? 0x0040u : at << 7));
+                  y[e] = times(y[e], bf16_pair(byte == 255u ? 0x7FC0u : byte == 0u ? 0x0040u : byte << 7));
                   if ((lost >> (row / rows) & 1u) || (kv == 1 && row >= live)) y[e] = 0u;
                   any |= not_finite(y[e]);
                 }
@@ -1255,7 +1267,8 @@ cudaError_t launch_paged_attention(const Attention& a, const Cache& c, const Bat
     const uint64_t dims[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads), pages};
     const uint64_t strides[3] = {static_cast<uint64_t>(c.token_stride), or_row(c.heads, c.head_stride, D), or_row(c.pages, c.page_stride, D)};
     const uint32_t box[4] = {static_cast<uint32_t>(D), rows, 1, 1};
-    made = made && encode_tmap_nd(&mk, k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box, 0) && encode_tmap_nd(&mv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box, 0);
+    made = made && encode_tmap_nd(&mk, k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box, D == 128 ? 128 : 0) &&
+           encode_tmap_nd(&mv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box, D == 128 ? 128 : 0);
   } else {
     // a tile's rows by groups of 8, both panels of a group one after the other: with a box for each panel the two halves of
     // a row's 256 bytes were fetched far apart (64 tokens over 4096: 1.0 TB/s with 128 rows a box, 5.8 with 16, 6.1 so)
