@@ -2,6 +2,9 @@
 tensor's beginning, units cut into few and into many parts, pages of several sequences, output over the queries, calls at once and
 captured ones, values of every 8-bit unit and infinities among the keys that all rows see. Bounds: as in the operators' own tests;
 where the same numbers go through the same operations the results are the same bits."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -220,3 +223,20 @@ def test_calls_at_once_and_captured_ones(g):
                 for x, y in zip(la.results(), w):
                     assert torch.equal(x, y), way
     g.fp8_poll_device_error()
+
+
+def test_the_usage_example_runs():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    block = next(b for b in re.findall(r"```python\n(.*?)```", open(path).read(), re.S) if "fp8_kv_append" in b)
+    import fp8_mixed_precision_saturating_gb300 as m
+    env = {"torch": torch, "g": m}
+    torch.manual_seed(0)
+    exec(compile(block, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    m.fp8_poll_device_error()
+    # a sequence of one token sees itself alone; one of zeros and a new token the new token's part of its values
+    new = env["qkv"][:, 40:].repeat_interleave(4, dim=1)
+    assert torch.equal(env["o"][2], new[2])
+    o, v = env["o"].float(), new.float()
+    share = (o * v).sum(-1) / (v * v).sum(-1)
+    assert torch.all((share > 0) & (share <= 1.01)) and torch.allclose(o, share[..., None] * v, atol=0.05)
