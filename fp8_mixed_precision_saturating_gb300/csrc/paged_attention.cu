@@ -58,7 +58,13 @@ struct Form {
   static constexpr int TILE = PANELS * kPanel;  // 128 rows of bf16
   // keys and values: groups of 8 rows, each panel's 8 x 128 bytes after the other (queries: a panel's 128 rows together)
   static constexpr int GROUP = PANELS * 1024;
-  static constexpr int STAGES = MX ? (D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 4 : 6)) : (D == 128 ? 4 : 8);
+  // Stages of keys and values: in turn, or (8-bit, one tile of rows: two groups of warps convert them side by side) each their own. Values
+  // wait for their weights and are held three times as long as keys.
+  static constexpr bool APART = MX && NQ == 1;
+  static constexpr int KEYS = D == 128 ? 1 : 2, STAGES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+  static constexpr int QBUFS = APART && D == 128 ? 1 : 2;  // buffers of queries (NQ 2: one for each tile)
+  static __device__ __forceinline__ int stage_of(int n, int kv) { return !APART ? (2 * n + kv) % STAGES : kv == 0 ? n % KEYS : KEYS + n % (STAGES - KEYS); }
+  static __device__ __forceinline__ uint32_t phase_of(int n, int kv) { return (!APART ? (2 * n + kv) / STAGES : kv == 0 ? n / KEYS : n / (STAGES - KEYS)) & 1; }
   static constexpr int RAW = 128 * D, UNITS = 4 * D;  // 128 rows of codes (rows of 128: their 16-byte pieces in the copy's swizzle), and their units
   static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 8 : 6)) : 0;
   // warps: weights, then those that work on keys and values on their way, one for the copies, one or two for the tensor cores
@@ -71,9 +77,11 @@ struct Form {
   static constexpr int COPY_WARP = PREP_WARP + PREP_WARPS, MMA_WARP = COPY_WARP + 1, WARPS = MMA_WARP + NQ, THREADS = 32 * WARPS;
   static_assert(NQ == 2 || NQ == 1, "tiles");
   static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
-  static constexpr int OFF_KV = 2 * TILE;       // two tiles of queries before
+  static constexpr int OFF_KV = QBUFS * TILE;
   static constexpr int OFF_RAW = OFF_KV + STAGES * TILE;
-  static constexpr int OFF_UNITS = OFF_RAW + RAWS * RAW, OFF_END = OFF_UNITS + RAWS * UNITS;
+  static constexpr int OFF_UNITS = OFF_RAW + RAWS * RAW;
+  // where the four copies of spread rows are added up: in their queries' buffer, or beside it where the next unit's come into it
+  static constexpr int OFF_SHARE = OFF_UNITS + RAWS * UNITS, SHARE = SPREAD && QBUFS == 1 ? 16384 : 0, OFF_END = OFF_SHARE + SHARE;
   static constexpr int OFF_BAR = OFF_END > kJoinBytes ? OFF_END : kJoinBytes;
   static constexpr int NBAR = 4 + 3 * STAGES + 2 * RAWS + 12 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
@@ -82,7 +90,7 @@ struct Form {
   // A wait names a phase by its parity, so whoever waits on a barrier has to see all of its phases. Where keys and values have
   // different waiters (the warps that look at bf16 values, the two groups that convert 8-bit tiles) a stage is always
   // one or the other's.
-  static_assert(MX ? NQ == 2 || (STAGES % 2 == 0 && RAWS % 2 == 0) : STAGES % 2 == 0, "stages");
+  static_assert(APART ? RAWS % 2 == 0 : MX || STAGES % 2 == 0, "stages");
   static_assert(RAW % 1024 == 0 && OFF_RAW % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
   static_assert(OFF_RAW >= 4 * kAttendMaxSeqs, "room for the sequences' costs");
 };
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
-      mbar_init(q_empty + 8 * i, SPREAD ? 2 : NQ);
+      mbar_init(q_empty + 8 * i, F::SHARE == 0 && SPREAD ? 2 : NQ);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -580,19 +588,23 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       };
       int window = (k.a * kTile) >> p.c.page_bits;
       int pages0 = page_at(window + lane), pages1 = page_at(window + 32 + lane);
-      const int buf = NQ == 1 ? k.filled & 1 : 0, use = NQ == 1 ? k.filled >> 1 : k.filled;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty + 8 * buf, (use & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
-      if (!ok) break;
-      const int t0 = k.at.block * per, tiles = NQ == 2 && t0 + p.tokens_per_tile < k.s.n ? 2 : 1;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(q_full + 8 * buf, static_cast<uint32_t>((SPREAD ? 4 : tiles) * p.tokens_per_tile * p.group * D * 2));
-        for (int i = 0; i < (SPREAD ? 4 : tiles); ++i)
+      auto load_queries = [&]() {
+        const int buf = NQ == 1 ? k.filled % F::QBUFS : 0, use = NQ == 1 ? k.filled / F::QBUFS : k.filled;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty + 8 * buf, (use & 1) ^ 1u, p.w, DEV_ERR_WAIT_PRODUCER));
+        if (!ok) return;
+        const int t0 = k.at.block * per, tiles = NQ == 2 && t0 + p.tokens_per_tile < k.s.n ? 2 : 1;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(q_full + 8 * buf, static_cast<uint32_t>((SPREAD ? 4 : tiles) * p.tokens_per_tile * p.group * D * 2));
+          for (int i = 0; i < (SPREAD ? 4 : tiles); ++i)
 #pragma unroll
-          for (int j = 0; j < F::PANELS; ++j)
-            tma_load_3d(base + (NQ == 1 ? buf : i) * F::TILE + j * kPanel + (SPREAD ? i * 4096 : 0), &tm_q, q_full + 8 * buf, 64 * j, k.at.head * p.group,
-                        k.s.first + t0 + (SPREAD ? 0 : i * p.tokens_per_tile));
-      }
-      __syncwarp();
+            for (int j = 0; j < F::PANELS; ++j)
+              tma_load_3d(base + (NQ == 1 ? buf : i) * F::TILE + j * kPanel + (SPREAD ? i * 4096 : 0), &tm_q, q_full + 8 * buf, 64 * j, k.at.head * p.group,
+                          k.s.first + t0 + (SPREAD ? 0 : i * p.tokens_per_tile));
+        }
+        __syncwarp();
+      };
+      if (F::QBUFS == 2) load_queries();
+      if (!ok) break;
       auto page_of = [&](int i) {  // page i of the sequence, each lane its own i, all within the window
         const int at = i - window, lo = __shfl_sync(0xFFFFFFFFu, pages0, at & 31), hi = __shfl_sync(0xFFFFFFFFu, pages1, at & 31);
         return at < 32 ? lo : hi;
@@ -640,6 +652,8 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
           }
           __syncwarp();
         }
+        // (one buffer of queries: this unit's first tile is on its way before the last unit's queries have been read)
+        if (ok && F::QBUFS == 1 && t == k.a) load_queries();
         if (!ok) break;
       }
     }
@@ -677,11 +691,11 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       Part s, v;  // the scores' place, one item ahead, and the values'
       part_of(ahead, s);
       part_of(k, v);
-      int k_stage = 0, v_stage = 1;
+      int k_stage = 0, v_stage = F::APART ? F::KEYS : 1;
       uint32_t k_phase = 0, v_phase = 0, q_phase = 0, p_phase = 0, s_slot = 0, v_slot = 0;  // q_phase, p_phase: a bit per buffer or slot
       auto await_keys = [&]() {
         if (s.fresh) {
-          const uint32_t buf = NQ == 1 ? s.filled & 1 : 0;
+          const uint32_t buf = NQ == 1 ? s.filled % F::QBUFS : 0;
           wait(q_full + 8 * buf, (q_phase >> buf) & 1u);
           q_phase ^= 1u << buf;
           s.fresh = false;
@@ -697,7 +711,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       const uint64_t q_desc = smem_desc_sw128(base), k_desc = smem_desc_sw128(base + F::OFF_KV, F::GROUP, 16), v_desc = smem_desc_sw128(base + F::OFF_KV, F::GROUP, 1024);
       auto scores = [&](int half) {  // S = Q K^T
         const int slot = SPREAD ? s_slot : 2 * q + half;
-        const uint64_t qd = q_desc + (((NQ == 2 ? q : s.filled & 1) * F::TILE) >> 4), kd = k_desc + ((k_stage * F::TILE + half * 8 * F::GROUP) >> 4);
+        const uint64_t qd = q_desc + (((NQ == 2 ? q : s.filled % F::QBUFS) * F::TILE) >> 4), kd = k_desc + ((k_stage * F::TILE + half * 8 * F::GROUP) >> 4);
         const uint32_t to = scores_at(slot);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) mma_bf16(to, qd + (((i >> 2) * kPanel + (i & 3) * 32) >> 4), kd + (((i >> 2) * 1024 + (i & 3) * 32) >> 4), kScores, i > 0);
@@ -717,23 +731,23 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       };
       auto scores_done = [&]() {
         mma_commit(kv_empty + 8 * k_stage);
-        k_stage += 2;
-        if (k_stage >= F::STAGES) {
-          k_stage -= F::STAGES;
+        k_stage += F::APART ? 1 : 2;
+        if (k_stage >= (F::APART ? F::KEYS : F::STAGES)) {
+          k_stage -= F::APART ? F::KEYS : F::STAGES;
           k_phase ^= 1;
         }
         s_slot ^= 1;
         if (++s.t == s.end) {
-          mma_commit(q_empty + 8 * (NQ == 1 ? s.filled & 1 : 0));
+          mma_commit(q_empty + 8 * (NQ == 1 ? s.filled % F::QBUFS : 0));
           ahead.next();
           part_of(ahead, s);
         }
       };
       auto values_done = [&]() {
         mma_commit(kv_empty + 8 * v_stage);
-        v_stage += 2;
+        v_stage += F::APART ? 1 : 2;
         if (v_stage >= F::STAGES) {
-          v_stage -= F::STAGES;
+          v_stage -= F::APART ? F::STAGES - F::KEYS : F::STAGES;
           v_phase ^= 1;
         }
         v_slot ^= 1;
@@ -822,7 +836,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
         } else {
 #pragma unroll 1
           for (int kv = mine < 0 ? 0 : mine; kv <= (mine < 0 ? 1 : mine); ++kv) {
-            const int u = 2 * n + kv, raw = u % F::RAWS, slot = u % F::STAGES;
+            const int u = 2 * n + kv, raw = u % F::RAWS, slot = F::stage_of(n, kv);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_full + 8 * raw, (u / F::RAWS) & 1, p.w, DEV_ERR_WAIT_EPILOGUE));
             if (!ok) break;
             const uint8_t* codes = smem + F::OFF_RAW + raw * F::RAW;
@@ -842,7 +856,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
               x[j] = reinterpret_cast<const uint4*>(codes)[at + kGroup * j];
               unit[j] = units[(row0 + j * kStep) * (D / 32) + c / 2];
             }
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(kv_empty + 8 * slot, ((u / F::STAGES) & 1) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(kv_empty + 8 * slot, F::phase_of(n, kv) ^ 1u, p.w, DEV_ERR_WAIT_EPILOGUE));
             if (!ok) break;
             uint8_t* panel = out + (row0 >> 3) * F::GROUP + (c >> 2) * 1024 + (row0 & 7) * 128;
             uint4* first = reinterpret_cast<uint4*>(panel + (((2 * (c & 3)) ^ (row0 & 7)) << 4));
@@ -1065,7 +1079,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       if constexpr (SPREAD) {
         // the four warps' copies of a row, each over its own keys, are brought to one reference and added
         float2* stats = reinterpret_cast<float2*>(smem + F::OFF_STATS);
-        float4* share = reinterpret_cast<float4*>(smem + (k.filled & 1) * F::TILE);  // (the unit's queries, which nothing reads any more)
+        float4* share = reinterpret_cast<float4*>(smem + (F::SHARE != 0 ? F::OFF_SHARE : (k.filled & 1) * F::TILE));  // (the unit's queries, which nothing reads any more)
         stats[threadIdx.x] = make_float2(m * c2, l);
         bar_sync(1, 128);
         auto joined = [&](int r) {
@@ -1118,7 +1132,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
           else
             __stcg(reinterpret_cast<float2*>(to) + r, make_float2(s.y == 0.0f ? -INFINITY : s.x, s.y));
         }
-        if (some) {
+        if (F::SHARE == 0 && some) {
           fence_proxy_async_smem();
           bar_sync(1, 128);
           if (threadIdx.x == 0) mbar_arrive(q_empty + 8 * (k.filled & 1));
