@@ -74,7 +74,10 @@ struct Form {
   // queries in one buffer, 174 us; stages of 64 rows, two for the keys and two for the values, 185. Shared memory is what they all
   // wait for: the codes in and out, the bf16 in, and each read once by the tensor cores.
   static constexpr int GROUP_WARPS = 4;
-  static constexpr int COPY_WARP = PREP_WARP + PREP_WARPS, MMA_WARP = COPY_WARP + 1, WARPS = MMA_WARP + NQ, THREADS = 32 * WARPS;
+  // Copies: one tile of rows: a warp for the keys and one for the values (8-bit: one warp for both took 2180 clocks an item, of which
+  // the conversion took 790). Two: keys and values share stages, so one.
+  static constexpr int COPY_WARPS = NQ == 1 ? 2 : 1;
+  static constexpr int COPY_WARP = PREP_WARP + PREP_WARPS, MMA_WARP = COPY_WARP + COPY_WARPS, WARPS = MMA_WARP + NQ, THREADS = 32 * WARPS;
   static_assert(NQ == 2 || NQ == 1, "tiles");
   static_assert(NQ == 1 || !SPREAD, "one tile of spread rows");
   static constexpr int OFF_KV = QBUFS * TILE;
@@ -572,9 +575,10 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
   auto scores_at = [&](int slot) { return tmem + (SPREAD ? 128 : 64) * slot; };
   auto weights_at = [&](int slot) { return SPREAD ? tmem + 384 + 64 * slot : scores_at(slot) + 32; };
 
-  if (warp == F::COPY_WARP) {
+  if (warp >= F::COPY_WARP && warp < F::MMA_WARP) {
     // ---- copies ------------------------------------------------------------------------------------------------------
-    const int rows = min(p.c.page_size, kTile);  // of a box
+    const int row_bits = least(p.c.page_bits, 7), rows = 1 << row_bits;  // of a box
+    const int kv0 = F::COPY_WARPS == 2 ? warp - F::COPY_WARP : 0, kv1 = F::COPY_WARPS == 2 ? kv0 + 1 : 2;
     bool ok = true;
     int n = 0;  // items so far
     for (; ok && k.live(); k.next()) {
@@ -603,14 +607,14 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
         }
         __syncwarp();
       };
-      if (F::QBUFS == 2) load_queries();
+      if (F::QBUFS == 2 && kv0 == 0) load_queries();
       if (!ok) break;
       auto page_of = [&](int i) {  // page i of the sequence, each lane its own i, all within the window
         const int at = i - window, lo = __shfl_sync(0xFFFFFFFFu, pages0, at & 31), hi = __shfl_sync(0xFFFFFFFFu, pages1, at & 31);
         return at < 32 ? lo : hi;
       };
       for (int t = k.a; t < k.b; ++t, ++n) {
-        const int key = t * kTile, left = min(k.s.seen - key, kTile), boxes = min(kTile / rows, (left + rows - 1) / rows);
+        const int key = t * kTile, left = min(k.s.seen - key, kTile), boxes = (left + rows - 1) >> row_bits;
         const int first = key >> p.c.page_bits;
         if (first >= window + 32) {
           window += 32;
@@ -620,11 +624,11 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
         const int page = page_of(first + min(lane, 15)), within = (key + lane * rows) & (p.c.page_size - 1);
         // 8-bit: the page of this lane's 16 bytes of units, kUnitRows rows
         constexpr int kUnitRows = 512 / D;
-        const int unit_row = lane * kUnitRows, unit_page = MX ? page_of(first + (min(unit_row, kTile - 1) / rows)) : 0;
+        const int unit_row = lane * kUnitRows, unit_page = MX ? page_of(first + (min(unit_row, kTile - 1) >> row_bits)) : 0;
         const int64_t unit_at = MX ? ((static_cast<int64_t>(unit_page) * p.c.heads + k.at.head) * p.c.page_size + ((key + unit_row) & (p.c.page_size - 1))) * (D / 32) : 0;
         const uint32_t found = __ballot_sync(0xFFFFFFFFu, lane < boxes && page >= 0);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll 1
+        for (int kv = kv0; kv < kv1; ++kv) {
           const int u = 2 * n + kv;
           const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
           if constexpr (!MX) {
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
           __syncwarp();
         }
         // (one buffer of queries: this unit's first tile is on its way before the last unit's queries have been read)
-        if (ok && F::QBUFS == 1 && t == k.a) load_queries();
+        if (ok && F::QBUFS == 1 && kv0 == 0 && t == k.a) load_queries();
         if (!ok) break;
       }
     }
