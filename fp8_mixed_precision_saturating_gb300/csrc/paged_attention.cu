@@ -20,7 +20,7 @@
 // that the roundings (half a step, 2^-9 on average) stay independent errors of the terms and not of the whole.
 //
 // Measured (4 query heads to each of 8 cache heads, D 128): 64 tokens over 4096 keys each 170 us, 6.3 TB/s, 0.93 of a copy's rate: memory; the
-// same in 8 bits 156 us, 3.5 TB/s: shared memory's bandwidth (the conversion's and the tensor cores' together 0.8 of it). A chunk
+// same in 8 bits 144 us, 3.9 TB/s: shared memory's bandwidth (copies, conversion and tensor cores together use 0.85 of it). A chunk
 // of 2048 tokens over 16384 keys 361 us, 1430 TFLOP/s, 0.75 of a large product's rate: the weights' arithmetic, of which a tile's 64 keys take
 // some 1700 clocks and their products 1370. One token over 100 keys 7 us: the chain launch, lengths, page table, keys, scores, weights, output.
 //
@@ -69,10 +69,9 @@ struct Form {
   static constexpr int RAWS = MX ? (D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 8 : 6)) : 0;
   // warps: weights, then those that work on keys and values on their way, one for the copies, one or two for the tensor cores
   static constexpr int PREP_WARP = NQ == 1 ? 4 : 8, PREP_WARPS = 12 - PREP_WARP;
-  // On one 8-bit tile; one tile of rows: keys and values side by side (64 tokens over 4096 keys of 8 heads of 128: 156 us; 165 while the
-  // lanes that read a row's codes and write its panels met in the banks). Not better, measured then: 8 warps on each tile and three stages in turn,
-  // queries in one buffer, 174 us; stages of 64 rows, two for the keys and two for the values, 185. Shared memory is what they all
-  // wait for: the codes in and out, the bf16 in, and each read once by the tensor cores.
+  // On one 8-bit tile; one tile of rows: keys and values side by side (64 tokens over 4096 keys of 8 heads of 128: 144 us; with one stage for
+  // each 156, and 165 while the lanes that read a row's codes and write its panels met in the banks; 8 warps on each tile, three stages in turn,
+  // 174 beside 170 then). Shared memory is what they wait for: the codes in and out, the bf16 in, and each read once by the tensor cores.
   static constexpr int GROUP_WARPS = 4;
   // Copies: one tile of rows: a warp for the keys and one for the values (8-bit: one warp for both took 2180 clocks an item, of which
   // the conversion took 790). Two: keys and values share stages, so one.
