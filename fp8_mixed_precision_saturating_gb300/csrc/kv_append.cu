@@ -3,8 +3,8 @@
 //
 // What bounds it: memory, each element in once and out once; for a few tokens the chain of loads (the token's sequence, its length, its page,
 // then the rows). A warp takes a token and a run of its heads, so that this chain and the angles are paid once per run.
-// Measured, 32 + 8 + 8 heads of 128, bf16 cache: a prompt of 8192 tokens 42.4 us, 4.75 TB/s (the rotation alone runs at 6.1: each warp waits for its chain
-// once; runs of 32 heads 45.3, 4 CTAs an SM 42.2, 8 rows at once on 2 CTAs 58); one token of 64 sequences 3.8 us, the launch and the chain.
+// Measured, 32 + 8 + 8 heads of 128, bf16 cache: a prompt of 8192 tokens 37.3 us, 5.4 TB/s (the rotation alone runs at 6.35: each warp waits for its chain
+// once; runs of 32 heads 40; 8 rows at once half as fast); one token of 64 sequences 3.7 us, the launch and the chain.
 #include "heads.cuh"
 
 namespace fp8gb {
@@ -12,7 +12,9 @@ namespace {
 
 using namespace heads;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Small CTAs: a warp's slot is free again when its CTA's last warp is done (a prompt of 8192 tokens, items in the tokens'
+// order: 39.0 us; CTAs of 128 threads 39.5, of 256 42.6).
+constexpr int kThreads = 64, kWarps = kThreads / 32;
 
 struct Args {
   Turn t;
@@ -75,16 +77,18 @@ __device__ __forceinline__ int64_t unit_at(const Slot& s, const Cache& c, int h)
   return ((s.page * c.heads + h) * c.page_size + s.at) * (c.head_dim / 32);
 }
 
+// All tokens' queries come first, then the keys, then the values: the warps of a CTA have the same work (in the order of the tokens: 39.0 us).
 struct Item {
   int64_t token;
   int part, h0, h1;
 };
 __device__ __forceinline__ Item item_of(int64_t i, const Args& g) {
   Item m;
-  m.token = g.items == 1 ? i : i >> 32 == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(g.items) : i / g.items;
-  const int j = static_cast<int>(i - m.token * g.items);
-  m.part = j >= g.first[2] ? 2 : j >= g.first[1] ? 1 : 0;
-  m.h0 = (j - g.first[m.part]) * g.per;
+  m.part = i >= g.b.tokens * g.first[2] ? 2 : i >= g.b.tokens * g.first[1] ? 1 : 0;
+  i -= g.b.tokens * g.first[m.part];
+  const int items = (m.part == 2 ? g.items : g.first[m.part + 1]) - g.first[m.part];
+  m.token = items == 1 ? i : i >> 32 == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(items) : i / items;
+  m.h0 = static_cast<int>(i - m.token * items) * g.per;
   m.h1 = min(m.h0 + g.per, g.part[m.part].n);
   return m;
 }
@@ -106,7 +110,7 @@ __device__ __forceinline__ void store_mx(const float (&x)[8], bool live, int d, 
 }
 
 template <bool INTER, int LPR, bool MX>
-__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(kThreads, 12) kv_append_kernel(const __grid_constant__ Args g) {
   constexpr int RPW = 32 / LPR, U = 4;
   // keys on their way into 8 bits: a warp's rows, turned, to be read 8 consecutive elements a lane
   __shared__ __align__(16) float share[MX ? kWarps : 1][MX ? RPW : 1][MX ? LPR * 8 : 4];
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
   const Lane a = lane_of<INTER>(l, g.t.head_dim, g.t.rot_dims);
   pdl_wait();
   pdl_trigger();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kWarps + warp;
   if (i >= g.total) return;
   const Item m = item_of(i, g);
   const Heads& p = g.part[m.part];
@@ -286,7 +290,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_any_kernel(const __grid_co
 template <bool I, int L>
 cudaError_t launch_one(const Args& g, cudaStream_t s) {
   auto* k = g.c.mx ? kv_append_kernel<I, L, true> : kv_append_kernel<I, L, false>;
-  return launch_pdl(k, dim3(static_cast<unsigned>((g.total + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, g);
+  const int64_t ctas = (g.total + kWarps - 1) / kWarps, most = int64_t{1} << 30;  // (2^31 tokens have more than a grid's first dimension holds)
+  return launch_pdl(k, dim3(static_cast<unsigned>(min(ctas, most)), static_cast<unsigned>((ctas + most - 1) / most)), dim3(kThreads), 0, s, g);
 }
 
 bool whole(const void* p, int64_t ld, int64_t hs, int64_t bytes) {
@@ -318,7 +323,7 @@ cudaError_t launch_kv_append(const Turn& f, const Heads (&part)[3], const Cache&
   }
   g.total = f.tokens * g.items;
   if (!vec) {
-    const unsigned ctas = static_cast<unsigned>(min((g.total + kWarps - 1) / kWarps, int64_t{8} * num_sms()));
+    const unsigned ctas = static_cast<unsigned>(min((g.total + kWarps - 1) / kWarps, int64_t{32} * num_sms()));
     return c.mx ? launch_pdl(kv_append_any_kernel<true>, dim3(ctas), dim3(kThreads), 0, stream, g) : launch_pdl(kv_append_any_kernel<false>, dim3(ctas), dim3(kThreads), 0, stream, g);
   }
   if (f.head_dim <= 64) return f.interleaved ? launch_one<true, 8>(g, stream) : launch_one<false, 8>(g, stream);

@@ -5,8 +5,8 @@
 // input, and writes one gradient. A token's angles are worked out once per item (a token and a run of its heads)
 // and serve all its rows; a lane's norm weight, angle and amplitude are one factor per member of a pair
 //   y_u = r (u uc - v vs),  y_v = r (u us + v vc),   uc = w_u cos a, us = w_u sin a, vs = w_v sin a, vc = w_v cos a,
-// and the arithmetic works on two pairs at once (fp32x2). Measured, 16384 tokens of 32 + 8 heads of 128 in bf16 with norms: forward 54.7 us,
-// 6.1 TB/s (0.9 of a copy); backward 95 us, 5.3 TB/s, some 4 of them the sum of the weights' gradients: rows in registers are what it
+// and the arithmetic works on two pairs at once (fp32x2). Measured, 16384 tokens of 32 + 8 heads of 128 in bf16 with norms: forward 52.8 us,
+// 6.35 TB/s (0.94 of a copy); backward 95 us, 5.3 TB/s, some 4 of them the sum of the weights' gradients: rows in registers are what it
 // has too few of on their way.
 // Backward: with (du, dv) the incoming pair turned back, z = x r, dz = w d:
 //   dx = r (dz - z mean(dz z)),   dw = sum over tokens and heads of d z.
@@ -18,6 +18,9 @@ namespace {
 using namespace heads;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Of the forward: small CTAs, a warp's slot is free again when its CTA's last warp is done (16384 tokens of 40 heads of 128: 52.8 us;
+// CTAs of 128 threads 53.3, of 256 54.6).
+constexpr int kFwdThreads = 64, kFwdWarps = kFwdThreads / 32;
 
 struct Args {
   Turn t;
@@ -61,13 +64,13 @@ template <typename T>
 constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
 
 template <typename T, bool INTER, int LPR, bool NORM>
-__global__ void __launch_bounds__(kThreads, 3) qk_rope_fwd_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(kFwdThreads, 12) qk_rope_fwd_kernel(const __grid_constant__ Args g) {
   constexpr int RPW = 32 / LPR, U = kRows<T>;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane a = lane_of<INTER>(lane % LPR, g.t.head_dim, g.t.rot_dims);
   pdl_wait();
   pdl_trigger();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFwdWarps + (threadIdx.x >> 5);
   if (i >= g.total) return;
   const Item m = item_of(i, g);
   const Heads& p = g.part[m.part];
@@ -365,7 +368,7 @@ struct FwdLaunch {
   cudaStream_t s;
   template <typename T, bool I, int L>
   cudaError_t operator()() const {
-    return launch_pdl(g.t.norm ? qk_rope_fwd_kernel<T, I, L, true> : qk_rope_fwd_kernel<T, I, L, false>, dim3(static_cast<unsigned>((g.total + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, g);
+    return launch_pdl(g.t.norm ? qk_rope_fwd_kernel<T, I, L, true> : qk_rope_fwd_kernel<T, I, L, false>, dim3(static_cast<unsigned>((g.total + kFwdWarps - 1) / kFwdWarps)), dim3(kFwdThreads), 0, s, g);
   }
 };
 
