@@ -72,9 +72,9 @@ FP8GB_HD int items_of(const Seq& s, int block, int per, int window) {
 }
 
 // CTA c of `ctas` takes items begin_of(c) .. begin_of(c + 1) - 1 of `total`; cta_of is the one that takes item x.
-// (Small numbers in 32 bits: a division in 64 takes some hundred instructions.)
+// (Small numbers in 32 bits: a division in 64 takes some hundred instructions. Both have to be: a long prompt's items pass 32 bits.)
 FP8GB_HD int64_t quotient(int64_t a, int64_t b) {
-  return static_cast<uint64_t>(a) >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+  return (static_cast<uint64_t>(a) | static_cast<uint64_t>(b)) >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 FP8GB_HD int64_t begin_of(int64_t total, int c, int ctas) { return quotient(total * c, ctas); }
 FP8GB_HD int cta_of(int64_t total, int64_t x, int ctas) { return static_cast<int>(quotient((x + 1) * ctas - 1, total)); }
