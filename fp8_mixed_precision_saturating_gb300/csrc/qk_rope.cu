@@ -184,13 +184,18 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_rope_bwd_kernel(const _
           }
           // dx = r (t - z mean(t z)) = r t - x r^3 mean(t x)
           const float r = rsqrtf(fmaf(q, inv_dim, g.t.eps));
-          const Pair rr = both(r), rw = both(live ? r : 0.0f), f = both(-r * r * r * e * inv_dim);
+          const Pair rr = both(r), f = both(-r * r * r * e * inv_dim);
+          if constexpr (DW) {
+            if (live) {  // (not a factor of 0 for the others: they repeat the last row, and an infinity of it times 0 is no 0)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                au[k] = fma2(yu[k], mul2(u[k], rr), au[k]);
+                av[k] = fma2(yv[k], mul2(v[k], rr), av[k]);
+              }
+            }
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if constexpr (DW) {
-              au[k] = fma2(yu[k], mul2(u[k], rw), au[k]);
-              av[k] = fma2(yv[k], mul2(v[k], rw), av[k]);
-            }
             yu[k] = fma2(u[k], f, mul2(tu[k], rr));
             yv[k] = fma2(v[k], f, mul2(tv[k], rr));
           }
