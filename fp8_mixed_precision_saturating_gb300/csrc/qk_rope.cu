@@ -182,22 +182,21 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_rope_bwd_kernel(const _
             q += __shfl_xor_sync(0xFFFFFFFFu, q, x);
             e += __shfl_xor_sync(0xFFFFFFFFu, e, x);
           }
-          // dx = r (t - z mean(t z)) = r t - x r^3 mean(t x)
+          // dx = r (t - z mean(t z)) with z = x r first: r^3 leaves fp32's range where rows are beyond 10^13 or below 10^-13
           const float r = rsqrtf(fmaf(q, inv_dim, g.t.eps));
-          const Pair rr = both(r), f = both(-r * r * r * e * inv_dim);
+          const Pair rr = both(r), m = both(-(e * r) * inv_dim);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) u[k] = mul2(u[k], rr), v[k] = mul2(v[k], rr);
           if constexpr (DW) {
             if (live) {  // (not a factor of 0 for the others: they repeat the last row, and an infinity of it times 0 is no 0)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                au[k] = fma2(yu[k], mul2(u[k], rr), au[k]);
-                av[k] = fma2(yv[k], mul2(v[k], rr), av[k]);
-              }
+              for (int k = 0; k < 2; ++k) au[k] = fma2(yu[k], u[k], au[k]), av[k] = fma2(yv[k], v[k], av[k]);
             }
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            yu[k] = fma2(u[k], f, mul2(tu[k], rr));
-            yv[k] = fma2(v[k], f, mul2(tv[k], rr));
+            yu[k] = mul2(fma2(u[k], m, tu[k]), rr);
+            yv[k] = mul2(fma2(v[k], m, tv[k]), rr);
           }
         }
         if (live && b.dx != nullptr) Raw<T, INTER>::put(dx + h * b.hs_dx, a.o0, a.o1, yu, yv);
