@@ -109,7 +109,7 @@ __device__ __forceinline__ void store_mx(const float (&x)[8], bool live, int d, 
   if ((d & 31) == 0) units[d >> 5] = static_cast<uint8_t>(u.byte);
 }
 
-template <bool INTER, int LPR, bool MX>
+template <bool INTER, int LPR, bool MX, bool PARTIAL>
 __global__ void __launch_bounds__(kThreads, 12) kv_append_kernel(const __grid_constant__ Args g) {
   constexpr int RPW = 32 / LPR, U = 4;
   // keys on their way into 8 bits: a warp's rows, turned, to be read 8 consecutive elements a lane
@@ -188,9 +188,9 @@ __global__ void __launch_bounds__(kThreads, 12) kv_append_kernel(const __grid_co
       const bool live = a.in && h < m.h1;
       raw[j].get(u, v);
       if (g.t.norm)
-        turn<LPR, true>(f, inv_dim, g.t.eps, u, v, yu, yv);
+        turn<LPR, true, INTER, PARTIAL>(a, f, inv_dim, g.t.eps, u, v, yu, yv);
       else
-        turn<LPR, false>(f, inv_dim, g.t.eps, u, v, yu, yv);
+        turn<LPR, false, INTER, PARTIAL>(a, f, inv_dim, g.t.eps, u, v, yu, yv);
       if (m.part == 0) {
         if (live) Raw<bf16, INTER>::put(out + h * p.hs_out, a.o0, a.o1, yu, yv);
       } else if constexpr (MX) {
@@ -289,7 +289,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_any_kernel(const __grid_co
 
 template <bool I, int L>
 cudaError_t launch_one(const Args& g, cudaStream_t s) {
-  auto* k = g.c.mx ? kv_append_kernel<I, L, true> : kv_append_kernel<I, L, false>;
+  const bool partial = g.t.rot_dims < g.t.head_dim;  // (heads that turn in part have kernels of their own)
+  auto* k = g.c.mx ? (partial ? kv_append_kernel<I, L, true, true> : kv_append_kernel<I, L, true, false>)
+                   : (partial ? kv_append_kernel<I, L, false, true> : kv_append_kernel<I, L, false, false>);
   const int64_t ctas = (g.total + kWarps - 1) / kWarps, most = int64_t{1} << 30;  // (2^31 tokens have more than a grid's first dimension holds)
   return launch_pdl(k, dim3(static_cast<unsigned>(min(ctas, most)), static_cast<unsigned>((ctas + most - 1) / most)), dim3(kThreads), 0, s, g);
 }
