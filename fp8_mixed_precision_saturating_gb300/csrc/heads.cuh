@@ -248,16 +248,21 @@ __device__ __forceinline__ float element(const float* p) { return *p; }
 __device__ __forceinline__ void set_element(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void set_element(float* p, float v) { *p = v; }
 
-// The sequence that row t of a batch belongs to, and its position there; position -1 where there is none. A
-// whole warp searches: 32 of the beginnings at a time.
+// The sequence that row t of a batch belongs to, and its position there; sequence and position -1 where there is none. A
+// whole warp searches: 32 of the beginnings at a time, as if they rise. A row that is not found so (a row of nobody is not, either) is looked for in
+// every sequence, since beginnings may fall, as in the zeros of unused entries.
 struct Place {
   int seq;
   int64_t pos;
 };
 
+__device__ __forceinline__ bool holds(const Batch& b, int seq, int64_t t) {
+  return static_cast<int64_t>(__ldg(b.q_start + seq)) <= t && t < static_cast<int64_t>(__ldg(b.q_start + seq + 1));
+}
+
 __device__ __forceinline__ Place place_of(int64_t t, const Batch& b, int lane) {
   Place r{-1, -1};
-  if (b.seqs <= 0 || static_cast<int64_t>(__ldg(b.q_start)) > t) return r;
+  if (b.seqs <= 0) return r;
   int lo = 0, hi = b.seqs;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) >> 5;
@@ -267,8 +272,16 @@ __device__ __forceinline__ Place place_of(int64_t t, const Batch& b, int lane) {
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
   }
+  if (!holds(b, lo, t)) {
+    lo = -1;
+#pragma unroll 1
+    for (int64_t s = 0; s < b.seqs && lo < 0; s += 32) {
+      const uint32_t found = __ballot_sync(0xFFFFFFFFu, s + lane < b.seqs && holds(b, static_cast<int>(s) + lane, t));
+      if (found != 0u) lo = static_cast<int>(s) + __ffs(found) - 1;
+    }
+    if (lo < 0) return r;
+  }
   const int64_t first = max(0, __ldg(b.q_start + lo)), end = __ldg(b.q_start + lo + 1);
-  if (t >= end || t < first) return r;
   r.seq = lo;
   r.pos = static_cast<int64_t>(max(0, __ldg(b.kv_len + lo))) - (min(end, b.tokens) - first) + (t - first);
   return r;

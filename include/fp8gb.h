@@ -667,8 +667,8 @@ typedef struct {
  * sequence s are rows q_start[s] .. q_start[s + 1] - 1 of the head tensors; its cache holds kv_len[s] tokens with the new ones,
  * which come last: row i of them is at position kv_len[s] - (q_start[s + 1] - q_start[s]) + i. Position p lies in page
  * page_table[s * ld_table + p / page_size]. Rows from q_start[seqs] on belong to nobody: they are neither read nor written.
- * Values out of range stay harmless: q_start is taken within 0 .. tokens (and as no new tokens where it falls), a negative
- * kv_len as 0; positions below 0 or from table_width * page_size on are neither stored nor seen; a page outside
+ * Values out of range stay harmless: q_start is taken within 0 .. tokens (and as no new tokens where it falls, as in unused
+ * entries of 0 at the end; rows that two sequences name, once it has fallen, are either's), a negative kv_len as 0; positions below 0 or from table_width * page_size on are neither stored nor seen; a page outside
  * the cache holds zeros and takes nothing. */
 typedef struct {
   int64_t tokens;            /* rows of the head tensors */
