@@ -666,9 +666,11 @@ typedef struct {
 /* A batch of sequences, their lengths on the device (so that a captured call serves other lengths): the new tokens of
  * sequence s are rows q_start[s] .. q_start[s + 1] - 1 of the head tensors; its cache holds kv_len[s] tokens with the new ones,
  * which come last: row i of them is at position kv_len[s] - (q_start[s + 1] - q_start[s]) + i. Position p lies in page
- * page_table[s * ld_table + p / page_size]. Rows from q_start[seqs] on belong to nobody: they are neither read nor written.
+ * page_table[s * ld_table + p / page_size]. Rows that no sequence names (from the last one's end on, say) belong to nobody: they
+ * have to be there, as tokens counts them, and may be read, but touch no result and are not written.
  * Values out of range stay harmless: q_start is taken within 0 .. tokens (and as no new tokens where it falls, as in unused
- * entries of 0 at the end; rows that two sequences name, once it has fallen, are either's), a negative kv_len as 0; positions below 0 or from table_width * page_size on are neither stored nor seen; a page outside
+ * entries of 0 at the end; rows that two sequences name, once it has fallen, are written for both, in no order), a negative
+ * kv_len as 0; positions below 0 or from table_width * page_size on are neither stored nor seen; a page outside
  * the cache holds zeros and takes nothing. */
 typedef struct {
   int64_t tokens;            /* rows of the head tensors */
