@@ -11,8 +11,8 @@
 // lane l holding elements l + 32 i, partners read through shared memory.
 //
 // Angles. p * turns[i] modulo 2^64 is the angle as a fraction of a turn with nothing lost; its top 32 bits are split into a quarter
-// turn and a rest x within an eighth of a turn either way (exact to 2^-33 turns), whose sine and cosine are their Taylor series up to x^9
-// and x^10: what is left out is below 2 10^-9 and 2 10^-10, fp32 rounds at 3 10^-8. The groups of lanes that hold different rows at
+// turn and a rest x within an eighth of a turn either way (the lower bits are dropped: at most 2^-32 turns, 1.5 10^-9, one way), whose sine and
+// cosine are their Taylor series up to x^9 and x^10: what is left out is below 2 10^-9 and 2 10^-10, fp32 rounds at 3 10^-8. The groups of lanes that hold different rows at
 // once share a token's angles: each works out its part of the four and they exchange them.
 #pragma once
 #include <cuda_bf16.h>

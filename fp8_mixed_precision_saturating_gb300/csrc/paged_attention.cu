@@ -403,7 +403,8 @@ __device__ __noinline__ bool join_parts(const Params& p, const Join u, int q, ui
   __threadfence();
   if (u.rows * kAll <= kThreads && parts <= 32) {  // few rows: a thread for four elements, its reference and sum on the way
     if (tid >= u.rows * kAll) return true;
-    const int d = tid / u.rows, r = tid - d * u.rows;  // (at most 14 rows: one block)
+    static_assert(kThreads / kAll <= 32, "rows of one block, as they lie in the parts");
+    const int d = tid / u.rows, r = tid - d * u.rows;
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
