@@ -667,7 +667,7 @@ def _check_rope_grads(f, b):
 def kv_cache(k, v, k_scale=None, v_scale=None):
     """An fp8_kv_cache_t of tensors [pages, heads, page_size, head_dim] (any strides but the last: keys and values alike): bf16, or
     uint8 codes with uint8 scales [pages, heads, page_size, head_dim / 32], contiguous."""
-    if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
+    if k.dim() != 4 or v.shape != k.shape or any(a != b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1):
         raise ValueError("k and v: [pages, heads, page_size, head_dim], of the same shape and strides")
     if k.shape[3] > 1 and k.stride(3) != 1:
         raise ValueError("k: the elements of a head are not next to each other")
