@@ -1039,7 +1039,7 @@ __global__ void __launch_bounds__(Form<D, MX, NQ, SPREAD>::THREADS, 1)
       // ---- the unit's end, or this CTA's part's ------------------------------------------------------------------------
       const bool some = part.lo < part.hi, alone = k.first() && k.last();
       const int64_t unit0 = k.at.item - k.at.off;
-      const int c0 = alone ? 0 : cta_of(total, unit0, runs), c1 = alone ? 0 : cta_of(total, unit0 + k.items - 1, runs);
+      const int c0 = alone ? 0 : cta_of(total, unit0, runs), c1 = alone ? 0 : least(cta_of(total, unit0 + k.items - 1, runs), runs - 1);  // (lengths that changed under the call)
       char* to = alone ? nullptr : part_at<D, NQ>(p, c0, blockIdx.x, q);
       const int rows = least(k.s.n - i0, p.tokens_per_tile) * p.group;  // of this tile
       auto set_lse = [&](int r, float reference, float sum) { put_lse(p, static_cast<int64_t>(k.s.first) + i0, k.at.head * p.group, r, reference, sum); };
