@@ -275,9 +275,18 @@ __device__ __forceinline__ Place place_of(int64_t t, const Batch& b, int lane) {
   if (!holds(b, lo, t)) {
     lo = -1;
 #pragma unroll 1
-    for (int64_t s = 0; s < b.seqs && lo < 0; s += 32) {
-      const uint32_t found = __ballot_sync(0xFFFFFFFFu, s + lane < b.seqs && holds(b, static_cast<int>(s) + lane, t));
-      if (found != 0u) lo = static_cast<int>(s) + __ffs(found) - 1;
+    for (int64_t s = 0; s < b.seqs && lo < 0; s += 256) {  // 8 of a lane's at a time, their loads together (past the end: an empty sequence)
+      const int32_t* q = b.q_start + s;
+      const int left = static_cast<int>(min(b.seqs - s, int64_t{512})), row = static_cast<int>(t);
+      int32_t from[8], to[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) from[j] = __ldg(q + min(32 * j + lane, left)), to[j] = __ldg(q + min(32 * j + lane + 1, left));
+      uint32_t at = 256;
+#pragma unroll
+      for (int j = 7; j >= 0; --j)
+        if (from[j] <= row && row < to[j]) at = 32 * j + lane;
+      at = __reduce_min_sync(0xFFFFFFFFu, at);
+      if (at < 256) lo = static_cast<int>(s) + static_cast<int>(at);
     }
     if (lo < 0) return r;
   }
