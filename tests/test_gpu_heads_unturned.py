@@ -157,3 +157,35 @@ def test_append(g, D, rot, inter, off, mx):
         # 448 * 2^120 and its negative; the others of the group are below half of the smallest step there
         assert torch.all(last[:, 0, 29] == 0x7E) and torch.all(last[:, 1, 29] == 0xFE)
         assert not (last[:, 2] & 127).any() and not (last[:, :2, others[D - 32:]] & 127).any()
+
+
+@pytest.mark.parametrize("case", CASES, ids=case_ids)
+@pytest.mark.parametrize("norm", [False, True])
+def test_in_place_and_captured(g, case, norm):
+    """Heads that turn in part over their own rows, forward and gradient, from a graph: the bits of calls with an output of their own."""
+    D, rot, inter, dt, off = case
+    x, dy = rows(70, 5, D, dt, off, 1), rows(70, 5, D, dt, off, 2)
+    work, back = (torch.empty(x.numel() + off, dtype=dt, device="cuda")[off:].view(x.shape) for _ in range(2))
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(2, 2, D, device="cuda")
+    kw = lambda i: dict(dw_q=dw[i, 0], dw_k=dw[i, 1]) if norm else {}  # noqa: E731
+    f, _ = block(g, case, x, norm, q_out=y[:, :4], k_out=y[:, 4:])
+    f_in, _ = block(g, case, work, norm, q_out=work[:, :4], k_out=work[:, 4:])
+    b = g.qk_rope_grad(dq_out=dy[:, :4], dk_out=dy[:, 4:], dq=dx[:, :4], dk=dx[:, 4:], **kw(0))
+    b_in = g.qk_rope_grad(dq_out=back[:, :4], dk_out=back[:, 4:], dq=back[:, :4], dk=back[:, 4:], **kw(1))
+    n = g.fp8_qk_rope_bwd_workspace_bytes(f, b)
+    ws = [torch.empty(max(n, 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    g.fp8_qk_rope_fwd(f)
+    g.fp8_qk_rope_bwd(f, b, ws[0], n)
+    g.fp8_qk_rope_fwd(f_in)  # (the first call of the capture's kernels)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.fp8_qk_rope_fwd(f_in)
+        g.fp8_qk_rope_bwd(f, b_in, ws[1], n)
+    for _ in range(2):
+        work.copy_(x)
+        back.copy_(dy)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(work), bits(y)) and torch.equal(bits(back), bits(dx))
+        assert not norm or torch.equal(dw[0], dw[1])
