@@ -19,10 +19,11 @@
 // P is rounded to bf16 because the tensor cores take both operands of the second product in 16 bits; the sum of the weights is of the unrounded ones, so
 // that the roundings (half a step, 2^-9 on average) stay independent errors of the terms and not of the whole.
 //
-// Measured (4 query heads to each of 8 cache heads, D 128): 64 tokens over 4096 keys each 170 us, 6.3 TB/s, 0.93 of a copy's rate: memory; the
-// same in 8 bits 144 us, 3.9 TB/s: shared memory's bandwidth (copies, conversion and tensor cores together use 0.85 of it). A chunk
-// of 2048 tokens over 16384 keys 361 us, 1430 TFLOP/s, 0.75 of a large product's rate: the weights' arithmetic, of which a tile's 64 keys take
-// some 1700 clocks and their products 1370. One token over 100 keys 7 us: the chain launch, lengths, page table, keys, scores, weights, output.
+// Measured (4 query heads to each of 8 cache heads, D 128): 64 tokens over 4096 keys each 172 us, 6.2 TB/s, 0.92 of a copy's rate: memory; the
+// same in 8 bits 147 us, 3.8 TB/s: shared memory's bandwidth (copies, conversion and tensor cores together use 0.85 of it). A chunk
+// of 2048 tokens over 16384 keys 364 us by itself, 382 in a loop under the power limit, 1416 and 1350 TFLOP/s, 0.74 and 0.71 of a large product's
+// rate: the weights' arithmetic, of which a tile's 64 keys take some 1700 clocks and their products 1370. One token over 100 keys 8 us
+// (D 64: 7): the chain launch, lengths, page table, keys, scores, weights, output.
 //
 // Masked places. Weights are set, not added to, so keys may be anything. A value that is not finite would make 0 * inf of a
 // weight of zero: in tiles with keys that some row does not see (the last ones, and the first ones of a window) values
@@ -1197,11 +1198,15 @@ int ctas() { return min(num_sms(), kMaxCtas); }
 // Which form, by the rows that a sequence has for a cache head on average (the lengths are on the device). Measured with 64 sequences
 // over 4096 keys, 8 heads, D 128, in us:
 //   rows              4     16     32     36     64    128    132    192    256
-//   32, four times  174.5  179.9  181.7  336.5  339.1                              (8-bit: 167  180  181  327  338)
-//   one tile        176.6  182.0  182.9  186.0  190.0  200.4  358.2  361.2  365.7  (8-bit: 221  235  235  240  242  251  450)
-//   two tiles       177.7  184.6  186.5  189.3  193.2  204.4  229.1  235.6  243.3  (8-bit: 204  215  214  215  217  224  255)
-// (D 64: 94, 134 and 144 with 4 rows; one token over 100 keys, D 64: 6.1, 6.6 and 6.8). So up to 32 rows: a tile of 32, each of the
-// four warps of weights with its own quarter of the keys. Above: two tiles, but one in bf16 where units do not fill it.
+//   32, four times  174    177    179    332    337                              (8-bit: 147  149  151  279  281)
+//   one tile        175    179    183    183    186    193    349    356    359
+//   two tiles       177    181    183    185    188    193    219    234    243  (8-bit: 175  178  178  179  180  183  227  234  243)
+// (D 64, 4 rows: 94, 133 and 148, 8-bit 98 and 156; one token over 100 keys, D 64: 7.0, 7.4 and 8.0.) So up to 32 rows: a tile of 32, each of the
+// four warps of weights with its own quarter of the keys. Above: two tiles, but one in bf16 where units do not fill it (8-bit caches
+// have no such form: with earlier stages it took 221 to 251 us for 4 to 128 rows, with the present ones it has not been measured).
+// What an average does not see is a batch of many short sequences and a long one: 255 single tokens over 4096 keys and a chunk of 1793 over
+// 16384 (32 rows on average) take 2100 us in the first form, of which the chunk's blocks of 8 tokens are two thirds, and 1035 in the second;
+// by themselves the tokens take 632 and the chunk, in the third form, 337. Calls of their own for long chunks are faster there.
 bool spread(const Attention& a, const Cache& c, const Batch& b) {
   const int64_t group = a.q_heads / c.heads;
   return group <= 32 && b.tokens * group <= static_cast<int64_t>(b.seqs) * 32;

@@ -6,7 +6,7 @@
 // and serve all its rows; a lane's norm weight, angle and amplitude are one factor per member of a pair
 //   y_u = r (u uc - v vs),  y_v = r (u us + v vc),   uc = w_u cos a, us = w_u sin a, vs = w_v sin a, vc = w_v cos a,
 // and the arithmetic works on two pairs at once (fp32x2). Measured, 16384 tokens of 32 + 8 heads of 128 in bf16 with norms: forward 52.8 us,
-// 6.35 TB/s (0.94 of a copy); backward 95 us, 5.3 TB/s, some 4 of them the sum of the weights' gradients: rows in registers are what it
+// 6.35 TB/s (0.94 of a copy; 54.0 on another box); backward 96 us, 5.2 TB/s, some 4 of them the sum of the weights' gradients: rows in registers are what it
 // has too few of on their way.
 // Backward: with (du, dv) the incoming pair turned back, z = x r, dz = w d:
 //   dx = r (dz - z mean(dz z)),   dw = sum over tokens and heads of d z.

@@ -576,7 +576,8 @@ int64_t fp8_block_norm_bwd_workspace_bytes(const fp8_block_norm_t* f, const fp8_
  *   BASE     PLAIN with base * factor^(rot_dims / (rot_dims - 2))
  *   PARTS    with r = original f_i / 2 pi, the turns over the original length: f_i / factor for r <= low, f_i for r >= high,
  *            (1 - s) f_i / factor + s f_i with s = (r - low) / (high - low) between
- *   PARTS_BY_INDEX  the same with s linear in i between the (real) indices where r is low and high */
+ *   PARTS_BY_INDEX  the same with s linear in i between the (real) indices where r is low and high
+ * turns is the caller's memory: models that round those two indices, or turn by other frequencies, bring a table of their own. */
 typedef enum { FP8_ROPE_HALF = 0, FP8_ROPE_INTERLEAVED = 1 } fp8_rope_layout_t;
 typedef enum {
   FP8_ROPE_PLAIN = 0,
