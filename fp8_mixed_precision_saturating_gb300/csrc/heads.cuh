@@ -209,18 +209,19 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// x's members as a pair's other ones take them: nothing of those that do not turn, whose sine of 0 times an infinity or a NaN would be no 0.
+// x's members as a pair's other ones take them: nothing of those that do not turn, whose sine of 0 times an infinity or a NaN would be no 0
+// (`nothing`: a zero whose product with the sine is -0, so that a -0 stays one).
 // A lane's pairs turn together with HALF. (PARTIAL: kernels of heads that turn in part, so that the others do without the selections. 8192 tokens of 40
 // heads of 128 in bf16 with norms, halves and interleaved: forward 29.4 and 28.6 us, half of each head turning 30.5 and 29.3; gradient
 // 53.4 and 54.5, 53.9 and 62.1.)
 template <bool INTER, bool PARTIAL>
-__device__ __forceinline__ void turning(int turned, const Pair (&x)[2], Pair (&t)[2]) {
+__device__ __forceinline__ void turning(int turned, float nothing, const Pair (&x)[2], Pair (&t)[2]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     t[k] = x[k];
     if constexpr (PARTIAL) {
       const float2 a = split(x[k]);
-      t[k] = pair((INTER ? 2 * k < turned : turned > 0) ? a.x : 0.0f, (INTER ? 2 * k + 1 < turned : turned > 0) ? a.y : 0.0f);
+      t[k] = pair((INTER ? 2 * k < turned : turned > 0) ? a.x : nothing, (INTER ? 2 * k + 1 < turned : turned > 0) ? a.y : nothing);
     }
   }
 }
@@ -228,8 +229,8 @@ __device__ __forceinline__ void turning(int turned, const Pair (&x)[2], Pair (&t
 template <int LPR, bool NORM, bool INTER, bool PARTIAL>
 __device__ __forceinline__ void turn(const Lane& a, const Factors& f, float inv_dim, float eps, const Pair (&u)[2], const Pair (&v)[2], Pair (&yu)[2], Pair (&yv)[2]) {
   Pair tu[2], tv[2];
-  turning<INTER, PARTIAL>(a.turned, u, tu);
-  turning<INTER, PARTIAL>(a.turned, v, tv);
+  turning<INTER, PARTIAL>(a.turned, -0.0f, u, tu);  // (times us)
+  turning<INTER, PARTIAL>(a.turned, 0.0f, v, tv);   // (times nvs)
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     yu[k] = fma2(u[k], f.uc[k], mul2(tv[k], f.nvs[k]));

@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_rope_bwd_kernel(const _
         const bool live = a.in && h < m.h1;
         rd[j].get(du, dv);
         Pair tu[2], tv[2];
-        turning<INTER, PARTIAL>(a.turned, du, tu);
-        turning<INTER, PARTIAL>(a.turned, dv, tv);
+        turning<INTER, PARTIAL>(a.turned, 0.0f, du, tu);   // (times -sin)
+        turning<INTER, PARTIAL>(a.turned, -0.0f, dv, tv);  // (times sin)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           yu[k] = fma2(du[k], pc[k], mul2(tv[k], ps[k]));

@@ -665,8 +665,9 @@ typedef struct {
 } fp8_kv_cache_t;
 
 /* A batch of sequences, their lengths on the device (so that a captured call serves other lengths; they stay as they are while
- * a call runs): the new tokens of sequence s are rows q_start[s] .. q_start[s + 1] - 1 of the head tensors; its cache holds kv_len[s] tokens with the new ones,
- * which come last: row i of them is at position kv_len[s] - (q_start[s + 1] - q_start[s]) + i. Position p lies in page
+ * a call runs): the new tokens of sequence s are rows q_start[s] .. q_start[s + 1] - 1 of the head tensors; its cache holds
+ * kv_len[s] tokens with the new ones, which come last: row i of them is at position
+ * kv_len[s] - (q_start[s + 1] - q_start[s]) + i. Position p lies in page
  * page_table[s * ld_table + p / page_size]. Rows that no sequence names (from the last one's end on, say) belong to nobody: they
  * have to be there, as tokens counts them, and may be read, but touch no result and are not written.
  * Values out of range stay harmless: q_start is taken within 0 .. tokens (and as no new tokens where it falls, as in unused

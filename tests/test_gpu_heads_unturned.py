@@ -117,6 +117,22 @@ def test_gradient(g, case, value):
                 assert torch.equal(a[rot:][same], (value * signs.sum(1))[same]) and torch.all(torch.isnan(a[rot:][~same]))
 
 
+@pytest.mark.parametrize("case", CASES, ids=case_ids)
+def test_a_copy_without_a_norm(g, case):
+    """What does not turn comes through by the bit, zeros of both signs and the smallest numbers among it, forward and backward."""
+    D, rot, inter, dt, off = case
+    x = rows(9, 4, D, dt, off, 1)
+    x[::2, :, rot:] *= torch.randint(0, 2, (5, 4, D - rot), device="cuda").to(dt)  # (a product: -0 where x is negative)
+    x[1, :, rot:] *= 2.0 ** -126
+    assert torch.any(bits(x[..., rot:]) == bits(torch.tensor([-0.0], dtype=dt, device="cuda")))
+    y, dx = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    f, _ = block(g, case, x, False, q_out=y[:, :3], k_out=y[:, 3:])
+    g.fp8_qk_rope_fwd(f)
+    g.fp8_qk_rope_bwd(f, g.qk_rope_grad(dq_out=x[:, :3], dk_out=x[:, 3:], dq=dx[:, :3], dk=dx[:, 3:]), None, 0)
+    for out in (y, dx):
+        assert torch.equal(bits(out[..., rot:].contiguous()), bits(x[..., rot:].contiguous()))
+
+
 @pytest.mark.parametrize("D, rot, inter, off", [(128, 64, False, 0), (128, 64, True, 0), (64, 32, False, 1), (96, 32, True, 3), (128, 0, False, 0), (64, 0, True, 1), (256, 128, False, 0)])
 @pytest.mark.parametrize("mx", [False, True])
 def test_append(g, D, rot, inter, off, mx):
